@@ -662,6 +662,83 @@ psk_status dequantize_and_gather_k_cache_dense(
     const int32_t* base_offsets, int32_t compress_ratio, int32_t width,
     const uint8_t* is_valid_token, psk_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Batch metadata from request lengths                                        */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * compute_slot_mappings -- positions, the token-to-request map and the cache
+ * slots of a batch from its request lengths: the inputs that the inserts
+ * (slot_mapping), the index builders (token_to_req, positions) and the
+ * compressed-row writers (compressed slots) take.  Rules of [BE]
+ * _decode_positions_from_metadata and [MDL] _deepseek_v4_swa_slot_mapping; the
+ * pages print no kernel that forms them together.
+ *
+ *   query_start_loc int32 [num_reqs + 1], non-decreasing; seq_lens int32
+ *                   [num_reqs].  Token t of request r, qsl[r] <= t < qsl[r+1],
+ *                   sits at pos = seq_lens[r] - (qsl[r+1] - qsl[r]) + (t - qsl[r]).
+ *                   A token outside [qsl[0], qsl[num_reqs]) is padding: every
+ *                   output of it is -1.
+ *   block_table     int32 [num_reqs, >= bt_width] with base_offsets as in
+ *                   compute_global_topk_indices_and_lens.
+ *   comp_block_table the compressed cache's table; NULL means the main table
+ *                   with its stride and width (comp_base_offsets and
+ *                   comp_block_size stay independent).
+ *   positions       nullable int64 [num_tokens]: pos.
+ *   token_to_req    nullable int32 [num_tokens]: r.
+ *   slot_mapping    nullable int64 [num_tokens]: page * block_size + pos %
+ *                   block_size, page = block_table[r][pos/block_size - base];
+ *                   -1 when pos < 0, the logical page is outside [0, bt_width)
+ *                   or the page is < 0.
+ *   comp_slot_mapping nullable int64 [num_tokens]: the slot of compressed entry
+ *                   pos / compress_ratio where the token closes its group
+ *                   ((pos + 1) % compress_ratio == 0), through the compressed
+ *                   table; else -1.
+ *   Outputs are 16-byte aligned for the widest stores and 8-byte (int64) or
+ *   4-byte (int32) aligned at least.
+ */
+psk_status compute_slot_mappings(
+    const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_reqs,
+    int64_t num_tokens, const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t block_size, const int32_t* comp_block_table,
+    int64_t comp_bt_stride, int32_t comp_bt_width, const int32_t* comp_base_offsets,
+    int32_t comp_block_size, int32_t compress_ratio, int64_t* positions, int32_t* token_to_req,
+    int64_t* slot_mapping, int64_t* comp_slot_mapping, psk_stream_t stream);
+
+/*
+ * extend_block_tables -- block tables grown from request lengths with pages
+ * from a list of unused ones (the pages take block tables as given; this is
+ * the step that makes them).
+ *
+ *   seq_lens        int32 [num_reqs]; row r needs ceil(floor(max(seq_lens[r], 0)
+ *                   / compress_ratio) / block_size) pages (compress_ratio 1: the
+ *                   table of a cache with one entry per token).
+ *   page_counts     nullable int32 [num_reqs]: pages row r already holds, in
+ *                   its first columns (clamped to [0, bt_width]; 0 when null).
+ *   page_pool       int32 [pool_size] page numbers, of which those from
+ *                   *pool_head on are unused (pool_head nullable: 0; clamped at 0).
+ *   block_table     int32 [num_reqs, >= bt_width], row stride bt_stride (in and
+ *                   out).  Columns a row holds are kept; the missing ones take
+ *                   page_pool[start_r], page_pool[start_r + 1], ... with start_r =
+ *                   head + the demand of all earlier rows; columns past the row's
+ *                   pages are -1.  A row is never shortened.
+ *   page_counts_out int32 [num_reqs]: pages row r holds now.
+ *   pool_head_out   int32 [1]: first page of the pool that is still unused.
+ *   err_count       nullable int32 [1], incremented for every row that is not
+ *                   extended and keeps the pages it holds: one that needs more
+ *                   than bt_width pages (it demands none), or one whose pages
+ *                   would end past pool_size (it keeps its place in the sums).
+ *   The inputs are not changed apart from block_table, so a repeated call gives
+ *   the same result; page_counts_out and pool_head_out must not overlap the
+ *   other arrays or each other.  pool_size <= INT32_MAX.  With num_reqs = 0
+ *   nothing is written, pool_head_out included.
+ */
+psk_status extend_block_tables(
+    const int32_t* seq_lens, int32_t num_reqs, int32_t block_size, int32_t compress_ratio,
+    const int32_t* page_counts, const int32_t* page_pool, int64_t pool_size,
+    const int32_t* pool_head, int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    int32_t* page_counts_out, int32_t* pool_head_out, int32_t* err_count, psk_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -83,6 +83,11 @@ SIGNATURES = {
     "compress_kv_cache_insert": (
         _I32, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _I32, _P, _I32, _I64, _I32, _I32, _P,
                ctypes.c_float, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "compute_slot_mappings": (
+        _I32, [_P, _P, _I32, _I64, _P, _I64, _I32, _P, _I32, _P, _I64, _I32, _P, _I32, _I32, _P, _P,
+               _P, _P, _P]),
+    "extend_block_tables": (
+        _I32, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _I64, _I32, _P, _P, _P, _P]),
     "indexer_k_norm_rope_store": (
         _I32, [_P, _I64, _P, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I32, _I32, _P, _I64,
                _I64, _I32, _P, _P]),

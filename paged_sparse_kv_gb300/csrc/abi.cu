@@ -10,6 +10,7 @@
 #include <cstring>
 #include <string>
 
+#include "batch_meta.h"
 #include "compressor.h"
 #include "gather.h"
 #include "index_build.h"
@@ -79,7 +80,7 @@ extern "C" {
 
 const char* psk_last_error(void) { return g_last_error.c_str(); }
 
-int32_t psk_abi_version(void) { return 5; }
+int32_t psk_abi_version(void) { return 6; }
 
 psk_status psk_device_wait_timeouts(uint32_t* count) {
     CHECK(count != nullptr, "count must be non-null");
@@ -831,6 +832,92 @@ psk_status dequantize_and_gather_k_cache_dense(
                         bt_width, base_offsets, compress_ratio};
     return cuda_status(psk::launch_gather_dense(p, ds, reinterpret_cast<cudaStream_t>(stream)),
                        "dequantize_and_gather_k_cache_dense launch");
+}
+
+psk_status compute_slot_mappings(
+    const int32_t* query_start_loc, const int32_t* seq_lens, int32_t num_reqs,
+    int64_t num_tokens, const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t block_size, const int32_t* comp_block_table,
+    int64_t comp_bt_stride, int32_t comp_bt_width, const int32_t* comp_base_offsets,
+    int32_t comp_block_size, int32_t compress_ratio, int64_t* positions, int32_t* token_to_req,
+    int64_t* slot_mapping, int64_t* comp_slot_mapping, psk_stream_t stream) {
+    CHECK(num_tokens >= 0, "num_tokens must be >= 0");
+    CHECK(block_size >= 1 && comp_block_size >= 1, "block sizes must be >= 1");
+    CHECK(compress_ratio >= 1, "compress_ratio must be >= 1");
+    CHECK(bt_width >= 0 && bt_stride >= bt_width, "need 0 <= bt_width <= bt_stride");
+    if (comp_block_table != nullptr) {
+        CHECK(comp_bt_width >= 0 && comp_bt_stride >= comp_bt_width,
+              "need 0 <= comp_bt_width <= comp_bt_stride");
+    }
+    if (num_tokens == 0 || !(positions || token_to_req || slot_mapping || comp_slot_mapping))
+        return ok();
+    CHECK(num_tokens <= (int64_t)INT32_MAX, "num_tokens must fit in int32 (query_start_loc is)");
+    CHECK(num_reqs >= 1, "num_reqs must be >= 1");
+    CHECK(query_start_loc && seq_lens, "query_start_loc and seq_lens must be non-null");
+    CHECK(bt_width == 0 || block_table, "block_table must be non-null");
+    CHECK(aligned(query_start_loc, 4) && aligned(seq_lens, 4) && aligned(block_table, 4) &&
+              aligned(base_offsets, 4) && aligned(comp_block_table, 4) &&
+              aligned(comp_base_offsets, 4) && aligned(token_to_req, 4),
+          "int32 arrays must be 4-byte aligned");
+    CHECK(aligned(positions, 8) && aligned(slot_mapping, 8) && aligned(comp_slot_mapping, 8),
+          "int64 arrays must be 8-byte aligned");
+    psk::SlotMapParams p{};
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.num_reqs = num_reqs;
+    p.num_tokens = num_tokens;
+    p.main = {block_table, bt_stride, bt_width, base_offsets, block_size, -1};
+    p.comp = comp_block_table == nullptr
+                 ? psk::SlotMapTable{block_table, bt_stride, bt_width, comp_base_offsets,
+                                     comp_block_size, -1}
+                 : psk::SlotMapTable{comp_block_table, comp_bt_stride, comp_bt_width,
+                                     comp_base_offsets, comp_block_size, -1};
+    p.compress_ratio = compress_ratio;
+    p.positions = positions;
+    p.token_to_req = token_to_req;
+    p.slots = slot_mapping;
+    p.comp_slots = comp_slot_mapping;
+    return cuda_status(psk::launch_slot_mappings(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "compute_slot_mappings launch");
+}
+
+psk_status extend_block_tables(
+    const int32_t* seq_lens, int32_t num_reqs, int32_t block_size, int32_t compress_ratio,
+    const int32_t* page_counts, const int32_t* page_pool, int64_t pool_size,
+    const int32_t* pool_head, int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    int32_t* page_counts_out, int32_t* pool_head_out, int32_t* err_count, psk_stream_t stream) {
+    CHECK(num_reqs >= 0, "num_reqs must be >= 0");
+    CHECK(block_size >= 1, "block_size must be >= 1");
+    CHECK(compress_ratio >= 1, "compress_ratio must be >= 1");
+    CHECK(bt_width >= 0 && bt_stride >= bt_width, "need 0 <= bt_width <= bt_stride");
+    CHECK(pool_size >= 0 && pool_size <= (int64_t)INT32_MAX,
+          "pool_size must be in [0, INT32_MAX]");
+    if (num_reqs == 0) return ok();
+    CHECK(seq_lens && page_counts_out && pool_head_out,
+          "seq_lens, page_counts_out and pool_head_out must be non-null");
+    CHECK(pool_size == 0 || page_pool, "page_pool must be non-null");
+    CHECK(bt_width == 0 || block_table, "block_table must be non-null");
+    CHECK(aligned(seq_lens, 4) && aligned(page_counts, 4) && aligned(page_pool, 4) &&
+              aligned(pool_head, 4) && aligned(block_table, 4) && aligned(page_counts_out, 4) &&
+              aligned(pool_head_out, 4) && aligned(err_count, 4),
+          "int32 arrays must be 4-byte aligned");
+    // every CTA reads all counts and the head: they are not updated in place
+    const auto overlap = [](const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+        return a != nullptr && b != nullptr && a < b + m && b < a + n;
+    };
+    CHECK(!overlap(page_counts, num_reqs, page_counts_out, num_reqs) &&
+              !overlap(pool_head, 1, pool_head_out, 1) &&
+              !overlap(page_counts, num_reqs, pool_head_out, 1) &&
+              !overlap(pool_head, 1, page_counts_out, num_reqs) &&
+              !overlap(page_counts_out, num_reqs, pool_head_out, 1) &&
+              !overlap(seq_lens, num_reqs, page_counts_out, num_reqs) &&
+              !overlap(seq_lens, num_reqs, pool_head_out, 1),
+          "page_counts_out and pool_head_out must not overlap the inputs or each other");
+    psk::ExtendParams p{seq_lens, num_reqs, block_size, compress_ratio, page_counts, page_pool,
+                        pool_size, pool_head, block_table, bt_stride, bt_width, page_counts_out,
+                        pool_head_out, err_count, 0};
+    return cuda_status(psk::launch_extend_block_tables(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "extend_block_tables launch");
 }
 
 }  // extern "C"

@@ -572,3 +572,99 @@ def dequantize_and_gather_k_cache_dense(out: torch.Tensor, cache: torch.Tensor,
           _rows(block_table, "block_table"), block_table.shape[1], _ptr(base_offsets),
           compress_ratio, out.shape[1], _ptr(valid))
     return out
+
+
+# ---- batch metadata from request lengths ------------------------------------------------
+
+def _vec(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, size: Optional[int] = None):
+    """A 1-D contiguous tensor of ``dtype`` (``size`` entries at least), or None."""
+    if t is None:
+        return
+    _need(t, dtype, name)
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be 1-D contiguous")
+    if size is not None and t.shape[0] < size:
+        raise ValueError(f"{name} must have at least {size} entries, got {t.shape[0]}")
+
+
+def _table(t: torch.Tensor, name: str, rows: int):
+    """Row stride and width of an int32 block table with at least ``rows`` rows."""
+    _need(t, torch.int32, name)
+    stride = _rows(t, name)
+    if t.shape[0] < rows:
+        raise ValueError(f"{name} must have at least {rows} rows, got {t.shape[0]}")
+    return max(stride, t.shape[1]), t.shape[1]
+
+
+def compute_slot_mappings(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                          block_table: torch.Tensor, block_size: int, num_tokens: int, *,
+                          base_offsets: Optional[torch.Tensor] = None,
+                          compressed_block_table: Optional[torch.Tensor] = None,
+                          compressed_block_size: Optional[int] = None,
+                          compressed_base_offsets: Optional[torch.Tensor] = None,
+                          compress_ratio: int = 1,
+                          positions: Optional[torch.Tensor] = None,
+                          token_to_req: Optional[torch.Tensor] = None,
+                          slot_mapping: Optional[torch.Tensor] = None,
+                          compressed_slot_mapping: Optional[torch.Tensor] = None):
+    """Batch metadata from request lengths; returns (positions [T] int64, token_to_req [T]
+    int32, slot_mapping [T] int64, compressed_slot_mapping [T] int64), -1 for padding tokens."""
+    _need_cuda(query_start_loc, seq_lens, block_table, base_offsets, compressed_block_table,
+               compressed_base_offsets, positions, token_to_req, slot_mapping,
+               compressed_slot_mapping)
+    dev, T, R = seq_lens.device, int(num_tokens), seq_lens.shape[0]
+    _vec(seq_lens, torch.int32, "seq_lens")
+    _vec(query_start_loc, torch.int32, "query_start_loc", R + 1)
+    _vec(base_offsets, torch.int32, "base_offsets", R)
+    _vec(compressed_base_offsets, torch.int32, "compressed_base_offsets", R)
+    stride, width = _table(block_table, "block_table", R)
+    cbt = compressed_block_table
+    cstride, cwidth = (0, 0) if cbt is None else _table(cbt, "compressed_block_table", R)
+    outs = []
+    for t, dt, n in ((positions, torch.int64, "positions"), (token_to_req, torch.int32, "token_to_req"),
+                     (slot_mapping, torch.int64, "slot_mapping"),
+                     (compressed_slot_mapping, torch.int64, "compressed_slot_mapping")):
+        _vec(t, dt, n, T)
+        outs.append(torch.empty((max(T, 0),), dtype=dt, device=dev) if t is None else t)
+    _call(dev, "compute_slot_mappings", _ptr(query_start_loc), _ptr(seq_lens), R, T,
+          _ptr(block_table), stride, width, _ptr(base_offsets), block_size, _ptr(cbt), cstride,
+          cwidth, _ptr(compressed_base_offsets),
+          block_size if compressed_block_size is None else compressed_block_size, compress_ratio,
+          *(_ptr(t) for t in outs))
+    return tuple(outs)
+
+
+def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
+                        block_table: torch.Tensor, block_size: int, *,
+                        page_counts: Optional[torch.Tensor] = None,
+                        pool_head: Optional[torch.Tensor] = None, compress_ratio: int = 1,
+                        page_counts_out: Optional[torch.Tensor] = None,
+                        pool_head_out: Optional[torch.Tensor] = None,
+                        err_count: Optional[torch.Tensor] = None):
+    """Grow ``block_table`` [R, width] int32 (in place) to the pages ``seq_lens`` needs, with
+    pages of ``page_pool`` from ``pool_head`` on; returns (block_table, page_counts [R],
+    pool_head [1]).  The inputs but the table are left as they were."""
+    _need_cuda(seq_lens, page_pool, block_table, page_counts, pool_head, page_counts_out,
+               pool_head_out, err_count)
+    dev, R = seq_lens.device, seq_lens.shape[0]
+    _vec(seq_lens, torch.int32, "seq_lens")
+    _vec(page_pool, torch.int32, "page_pool")
+    _vec(page_counts, torch.int32, "page_counts", R)
+    _vec(page_counts_out, torch.int32, "page_counts_out", R)
+    for t, n in ((pool_head, "pool_head"), (pool_head_out, "pool_head_out"),
+                 (err_count, "err_count")):
+        _vec(t, torch.int32, n, 1)
+    stride, width = _table(block_table, "block_table", R)
+    if R > 1 and block_table.stride(0) < width:
+        raise ValueError("rows of block_table must not overlap")
+    if page_counts_out is None:
+        page_counts_out = torch.empty((R,), dtype=torch.int32, device=dev)
+    if pool_head_out is None:
+        pool_head_out = torch.empty((1,), dtype=torch.int32, device=dev)
+    if R == 0:  # no launch: the head stays where it is
+        pool_head_out.fill_(0) if pool_head is None else pool_head_out.copy_(pool_head)
+    _call(dev, "extend_block_tables", _ptr(seq_lens), R, block_size, compress_ratio,
+          _ptr(page_counts), _ptr(page_pool), page_pool.shape[0], _ptr(pool_head),
+          _ptr(block_table), stride, width, _ptr(page_counts_out), _ptr(pool_head_out),
+          _ptr(err_count))
+    return block_table, page_counts_out, pool_head_out
