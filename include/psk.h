@@ -739,6 +739,94 @@ psk_status extend_block_tables(
     const int32_t* pool_head, int32_t* block_table, int64_t bt_stride, int32_t bt_width,
     int32_t* page_counts_out, int32_t* pool_head_out, int32_t* err_count, psk_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Attention over paged fp8_ds_mla caches                                     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * sparse_mla_attention -- attention of new tokens over the cache rows an index
+ * matrix names, without writing the rows out: what [BE]
+ * forward_deepseek_v4_decode (k_cache with extra_k_cache) and the sparse
+ * prefill attention compute from the combined matrix of
+ * combine_topk_swa_indices.  The pages call a library kernel for it; the
+ * formulas below are its definition here.
+ *
+ *   For token t and head h with query q = q[t][h] and the rows k_j = the
+ *   head_dim values that dequantize_and_gather_k_cache_pair gives for column j
+ *   (each row is key and value at once, shared by all heads), over the visible
+ *   columns j, those whose slot lies inside its cache:
+ *     s_j = softmax_scale * q.k_j
+ *     out[t][h] = sum_j exp(s_j) k_j / (sum_j exp(s_j) + exp(sink[h]))
+ *     lse[t][h] = log sum_j exp(s_j)         (natural log, without the sink)
+ *   A row that sees nothing has out = 0 and lse = -inf.  Sums, maxima and
+ *   weights are binary32; a weight is rounded to bf16 where it multiplies k_j
+ *   on the tensor cores (the sums in the denominator and in lse take it
+ *   unrounded).
+ *
+ *   q             bf16; row (t, h) at q + t*q_stride_t + h*q_stride_h (elements,
+ *                 multiples of 8; 16-byte aligned), head_dim values.
+ *   cache         fp8_ds_mla pages with UE8M0 scales, read by columns
+ *                 [0, split); extra_cache by columns [split, cols) (may be NULL
+ *                 when split == cols).  head_dim in {128, 256, 512}, rope_dim a
+ *                 multiple of 64 in [0, head_dim).
+ *   indices       int32 [num_tokens, cols], row stride idx_stride: slot ids; a
+ *                 slot < 0 or >= num_pages * block_size of its cache is not
+ *                 visible.  A slot named twice counts twice.
+ *   softmax_scale finite and > 0.
+ *   sink          nullable binary32 [num_heads] (no sink when null).
+ *   out           bf16; row (t, h) at out + t*out_stride_t + h*out_stride_h
+ *                 (multiples of 8; 16-byte aligned; rows must not overlap).
+ *   lse           nullable binary32; (t, h) at lse + t*lse_stride_t + h.
+ *   workspace     at least sparse_mla_attention_workspace_bytes(...) bytes,
+ *                 16-byte aligned (may be NULL when that is 0).  Scratch for the
+ *                 call: its contents need not be kept between calls, and two
+ *                 calls that can run at the same time need one each.
+ *   A NaN or infinity in a visible row or in q gives what the formulas give; a
+ *   row that is not visible is not read.
+ */
+int64_t sparse_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
+                                             int32_t head_dim, int32_t cols);
+
+psk_status sparse_mla_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const uint8_t* cache, int64_t num_pages, int64_t page_stride,
+    int32_t block_size, const uint8_t* extra_cache, int64_t extra_num_pages,
+    int64_t extra_page_stride, int32_t extra_block_size, int32_t head_dim, int32_t rope_dim,
+    const int32_t* indices, int64_t idx_stride, int32_t cols, int32_t split,
+    float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
+    int64_t workspace_bytes, psk_stream_t stream);
+
+/*
+ * chunk_mla_attention -- causal attention of a chunk of new tokens over the
+ * positions of their own requests through the block table: the attention of a
+ * layer whose visible rows follow from the positions alone (the window layers
+ * without compressed entries, [BE] _update_decode_swa_metadata, and whole
+ * contexts).  Token t of request r sees the positions
+ *   [max(replay_start[r], pos - window + 1, 0), pos],
+ * pos as in combine_topk_swa_indices (window 0: no lower bound from the
+ * window), those of them whose logical page position/block_size -
+ * base_offsets[r] lies in [0, bt_width) and names a page in [0, num_pages).
+ * The new tokens' own rows have to be in the cache already.  Formulas, types
+ * and the other arguments as in sparse_mla_attention.  A padding token
+ * (is_valid_token 0, or a request index outside [0, num_reqs)) sees nothing:
+ * out = 0, lse = -inf.
+ */
+int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
+                                            int32_t head_dim, int32_t bt_width,
+                                            int32_t block_size, int32_t window);
+
+psk_status chunk_mla_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const uint8_t* cache, int64_t num_pages, int64_t page_stride,
+    int32_t block_size, int32_t head_dim, int32_t rope_dim, const int32_t* query_start_loc,
+    const int32_t* seq_lens, const int32_t* token_to_req, const int32_t* replay_start,
+    int32_t num_reqs, const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t window, const uint8_t* is_valid_token,
+    float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
+    int64_t workspace_bytes, psk_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

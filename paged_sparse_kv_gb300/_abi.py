@@ -83,6 +83,15 @@ SIGNATURES = {
     "compress_kv_cache_insert": (
         _I32, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _I32, _P, _I32, _I64, _I32, _I32, _P,
                ctypes.c_float, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P]),
+    "sparse_mla_attention_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32]),
+    "sparse_mla_attention": (
+        _I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I32, _I32,
+               _P, _I64, _I32, _I32, ctypes.c_float, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "chunk_mla_attention_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32, _I32, _I32]),
+    "chunk_mla_attention": (
+        _I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _I32,
+               _P, _I64, _I32, _P, _I32, _P, ctypes.c_float, _P, _P, _I64, _I64, _P, _I64, _P, _I64,
+               _P]),
     "compute_slot_mappings": (
         _I32, [_P, _P, _I32, _I64, _P, _I64, _I32, _P, _I32, _P, _I64, _I32, _P, _I32, _I32, _P, _P,
                _P, _P, _P]),

@@ -5,11 +5,13 @@
 // returns PSK_OK without a launch when there is no work, and otherwise
 // launches exactly one kernel on the caller's stream.  Nothing here
 // allocates, synchronises or keeps state beyond the per-thread error text.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <string>
 
+#include "attention.h"
 #include "batch_meta.h"
 #include "compressor.h"
 #include "gather.h"
@@ -72,6 +74,42 @@ psk_status check_cache(const uint8_t* cache, int64_t num_pages, int64_t page_str
     CHECK(aligned(cache, 16), "cache must be 16-byte aligned");
     CHECK(num_pages <= INT64_MAX / page_stride, "cache size overflows int64");
     return PSK_OK;
+}
+
+bool attn_head_dim_ok(int32_t d) { return d == 128 || d == 256 || d == 512; }
+
+// The arguments both attention entry points share.  `work` = false where the
+// call has no tokens: pointers are not looked at.
+psk_status check_attention(const psk::AttnParams& p, bool work, int64_t workspace_need,
+                           int64_t workspace_bytes) {
+    CHECK(p.num_heads >= 1, "num_heads must be >= 1");
+    CHECK(std::isfinite(p.scale) && p.scale > 0.0f, "softmax_scale must be finite and > 0");
+    CHECK(p.q_stride_t >= 0 && p.q_stride_h >= 0 && p.q_stride_t % 8 == 0 &&
+              p.q_stride_h % 8 == 0,
+          "query strides must be non-negative multiples of 8 elements");
+    CHECK(p.out_stride_t % 8 == 0 && p.out_stride_h % 8 == 0 &&
+              (p.num_tokens <= 1 || p.out_stride_t >= p.head_dim) &&
+              (p.num_heads <= 1 || p.out_stride_h >= p.head_dim) && p.out_stride_t >= 0 &&
+              p.out_stride_h >= 0,
+          "output strides must be multiples of 8 elements and at least head_dim");
+    CHECK(p.lse == nullptr || p.num_tokens <= 1 || p.lse_stride_t >= p.num_heads,
+          "lse_stride_t must be >= num_heads");
+    if (!work) return PSK_OK;
+    CHECK(p.num_tokens <= (int64_t)INT32_MAX, "num_tokens must fit in int32");
+    CHECK(p.q != nullptr && p.out != nullptr, "q and out must be non-null");
+    CHECK(aligned(p.q, 16) && aligned(p.out, 16), "q and out must be 16-byte aligned");
+    CHECK(aligned(p.sink, 4) && aligned(p.lse, 4), "sink and lse must be 4-byte aligned");
+    CHECK(workspace_bytes >= workspace_need, "workspace must hold %lld bytes (got %lld)",
+          (long long)workspace_need, (long long)workspace_bytes);
+    CHECK(workspace_need == 0 || (p.workspace != nullptr && aligned(p.workspace, 16)),
+          "workspace must be non-null and 16-byte aligned");
+    return PSK_OK;
+}
+
+// The largest number of positions a token of a call can see.
+int64_t chunk_max_keys(int32_t bt_width, int32_t block_size, int32_t window) {
+    const int64_t all = (int64_t)bt_width * block_size;
+    return window > 0 && window < all ? window : all;
 }
 
 }  // namespace
@@ -918,6 +956,146 @@ psk_status extend_block_tables(
                         pool_head_out, err_count, 0};
     return cuda_status(psk::launch_extend_block_tables(p, reinterpret_cast<cudaStream_t>(stream)),
                        "extend_block_tables launch");
+}
+
+int64_t sparse_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
+                                             int32_t head_dim, int32_t cols) {
+    if (num_tokens < 1 || num_heads < 1 || !attn_head_dim_ok(head_dim) || cols < 1) return 0;
+    return psk::attention_workspace_bytes(num_tokens, num_heads, head_dim, cols);
+}
+
+psk_status sparse_mla_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const uint8_t* cache, int64_t num_pages, int64_t page_stride,
+    int32_t block_size, const uint8_t* extra_cache, int64_t extra_num_pages,
+    int64_t extra_page_stride, int32_t extra_block_size, int32_t head_dim, int32_t rope_dim,
+    const int32_t* indices, int64_t idx_stride, int32_t cols, int32_t split,
+    float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
+    int64_t workspace_bytes, psk_stream_t stream) {
+    CHECK(num_tokens >= 0 && cols >= 0, "num_tokens and cols must be >= 0");
+    CHECK(split >= 0 && split <= cols, "need 0 <= split <= cols");
+    CHECK(attn_head_dim_ok(head_dim), "head_dim must be one of 128, 256, 512 (got %d)", head_dim);
+    CHECK(rope_dim >= 0 && rope_dim < head_dim && rope_dim % 64 == 0,
+          "rope_dim must be a multiple of 64 in [0, head_dim) (got %d)", rope_dim);
+    const int64_t rec = fp8_record_bytes(head_dim, rope_dim, 1);
+    psk_status st = check_cache(cache, num_pages, page_stride, block_size, rec);
+    if (st != PSK_OK) return st;
+    if (split < cols || extra_cache != nullptr) {
+        st = check_cache(extra_cache, extra_num_pages, extra_page_stride, extra_block_size, rec);
+        if (st != PSK_OK) return st;
+    }
+    CHECK(idx_stride >= cols, "idx_stride must be >= cols");
+    psk::AttnParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride_t = q_stride_t;
+    p.q_stride_h = q_stride_h;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.head_dim = head_dim;
+    p.rope_dim = rope_dim;
+    p.cache = {cache, num_pages, page_stride, block_size, -1};
+    p.scale = softmax_scale;
+    p.sink = sink;
+    p.out = static_cast<uint16_t*>(out);
+    p.out_stride_t = out_stride_t;
+    p.out_stride_h = out_stride_h;
+    p.lse = lse;
+    p.lse_stride_t = lse_stride_t;
+    p.workspace = workspace;
+    p.extra = extra_cache == nullptr
+                  ? p.cache
+                  : psk::AttnCache{extra_cache, extra_num_pages, extra_page_stride,
+                                   extra_block_size, -1};
+    p.idx = indices;
+    p.idx_stride = idx_stride;
+    p.cols = cols;
+    p.split = split;
+    st = check_attention(
+        p, num_tokens > 0,
+        sparse_mla_attention_workspace_bytes(num_tokens, num_heads, head_dim, cols),
+        workspace_bytes);
+    if (st != PSK_OK) return st;
+    if (num_tokens == 0) return ok();
+    CHECK(cols == 0 || indices != nullptr, "indices must be non-null");
+    CHECK(aligned(indices, 4), "indices must be 4-byte aligned");
+    return cuda_status(psk::launch_attention_indexed(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "sparse_mla_attention launch");
+}
+
+int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
+                                            int32_t head_dim, int32_t bt_width,
+                                            int32_t block_size, int32_t window) {
+    if (num_tokens < 1 || num_heads < 1 || !attn_head_dim_ok(head_dim) || bt_width < 1 ||
+        block_size < 1 || window < 0)
+        return 0;
+    return psk::attention_workspace_bytes(num_tokens, num_heads, head_dim,
+                                          chunk_max_keys(bt_width, block_size, window));
+}
+
+psk_status chunk_mla_attention(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const uint8_t* cache, int64_t num_pages, int64_t page_stride,
+    int32_t block_size, int32_t head_dim, int32_t rope_dim, const int32_t* query_start_loc,
+    const int32_t* seq_lens, const int32_t* token_to_req, const int32_t* replay_start,
+    int32_t num_reqs, const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t window, const uint8_t* is_valid_token,
+    float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
+    int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
+    int64_t workspace_bytes, psk_stream_t stream) {
+    CHECK(num_tokens >= 0, "num_tokens must be >= 0");
+    CHECK(window >= 0, "window must be >= 0");
+    CHECK(attn_head_dim_ok(head_dim), "head_dim must be one of 128, 256, 512 (got %d)", head_dim);
+    CHECK(rope_dim >= 0 && rope_dim < head_dim && rope_dim % 64 == 0,
+          "rope_dim must be a multiple of 64 in [0, head_dim) (got %d)", rope_dim);
+    psk_status st = check_cache(cache, num_pages, page_stride, block_size,
+                                fp8_record_bytes(head_dim, rope_dim, 1));
+    if (st != PSK_OK) return st;
+    CHECK(bt_width >= 0 && bt_stride >= bt_width, "need 0 <= bt_width <= bt_stride");
+    psk::AttnParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride_t = q_stride_t;
+    p.q_stride_h = q_stride_h;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.head_dim = head_dim;
+    p.rope_dim = rope_dim;
+    p.cache = {cache, num_pages, page_stride, block_size, -1};
+    p.scale = softmax_scale;
+    p.sink = sink;
+    p.out = static_cast<uint16_t*>(out);
+    p.out_stride_t = out_stride_t;
+    p.out_stride_h = out_stride_h;
+    p.lse = lse;
+    p.lse_stride_t = lse_stride_t;
+    p.workspace = workspace;
+    p.extra = p.cache;
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.t2r = token_to_req;
+    p.replay = replay_start;
+    p.valid = is_valid_token;
+    p.num_reqs = num_reqs;
+    p.bt = block_table;
+    p.bt_stride = bt_stride;
+    p.bt_width = bt_width;
+    p.base_off = base_offsets;
+    p.window = window;
+    st = check_attention(p, num_tokens > 0,
+                         chunk_mla_attention_workspace_bytes(num_tokens, num_heads, head_dim,
+                                                             bt_width, block_size, window),
+                         workspace_bytes);
+    if (st != PSK_OK) return st;
+    if (num_tokens == 0) return ok();
+    CHECK(num_reqs >= 1, "num_reqs must be >= 1");
+    CHECK(query_start_loc && seq_lens && token_to_req,
+          "query_start_loc, seq_lens and token_to_req must be non-null");
+    CHECK(bt_width == 0 || block_table, "block_table must be non-null");
+    CHECK(aligned(query_start_loc, 4) && aligned(seq_lens, 4) && aligned(token_to_req, 4) &&
+              aligned(replay_start, 4) && aligned(block_table, 4) && aligned(base_offsets, 4),
+          "int32 arrays must be 4-byte aligned");
+    return cuda_status(psk::launch_attention_chunk(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "chunk_mla_attention launch");
 }
 
 }  // extern "C"

@@ -668,3 +668,121 @@ def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
           _ptr(block_table), stride, width, _ptr(page_counts_out), _ptr(pool_head_out),
           _ptr(err_count))
     return block_table, page_counts_out, pool_head_out
+
+
+# ---- attention over paged fp8_ds_mla caches ------------------------------------------------
+
+def _heads(t: torch.Tensor, name: str):
+    """[T, H, D] bf16 with unit inner stride: its strides (a size-1 dim may carry any)."""
+    _need(t, torch.bfloat16, name)
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [T, H, D] with unit inner stride")
+    T, H, D = t.shape
+    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+
+
+def _attention_outputs(q, sink, out, lse, workspace, need):
+    """Checked or allocated outputs and workspace of an attention call."""
+    T, H, D = q.shape
+    if sink is not None:
+        _vec(sink, torch.float32, "sink", H)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError(f"out {tuple(out.shape)} does not match q {tuple(q.shape)}")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _need(lse, torch.float32, "lse")
+    if lse.shape != (T, H) or (H > 1 and lse.stride(1) != 1):
+        raise ValueError(f"lse must be [{T}, {H}] with unit inner stride")
+    if workspace is None:
+        if need > 0:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    return out, lse, (lse.stride(0) if T > 1 else H), workspace
+
+
+def _on(dev: torch.device, fn, *args):
+    """A size query that depends on the device: asked with ``dev`` current."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return fn(*args)
+
+
+def sparse_mla_attention(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
+                         block_size: int, *, extra_cache: Optional[torch.Tensor] = None,
+                         extra_block_size: Optional[int] = None, split: Optional[int] = None,
+                         softmax_scale: Optional[float] = None,
+                         sink: Optional[torch.Tensor] = None, rope_dim: int = 64,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None):
+    """Attention of ``q`` [T, H, D] over the fp8_ds_mla rows ``indices`` [T, C] names: slots of
+    ``cache`` in columns [0, split), of ``extra_cache`` in the others (``split`` defaults to all
+    columns).  Returns (out [T, H, D] bf16, lse [T, H] binary32); scale defaults to D^-1/2.
+    ``workspace`` (uint8) is scratch; two calls that can run at once need one each."""
+    _need_cuda(q, cache, indices, extra_cache, sink, out, lse, workspace)
+    qt, qh = _heads(q, "q")
+    T, H, D = q.shape
+    _need(indices, torch.int32, "indices")
+    if indices.dim() != 2 or indices.shape[0] != T:
+        raise ValueError(f"indices must be [{T}, C]")
+    C = indices.shape[1]
+    split = C if split is None else split
+    np_a, ps_a = _pages(cache)
+    np_b, ps_b = (0, 0) if extra_cache is None else _pages(extra_cache)
+    lib = _abi.lib()
+    need = _on(q.device, lib.sparse_mla_attention_workspace_bytes, T, H, D, C)
+    out, lse, ls, workspace = _attention_outputs(q, sink, out, lse, workspace, need)
+    ot, oh = _heads(out, "out")
+    _call(q.device, "sparse_mla_attention", _ptr(q), qt, qh, T, H, _ptr(cache), np_a, ps_a,
+          block_size, _ptr(extra_cache), np_b, ps_b,
+          block_size if extra_block_size is None else extra_block_size, D, rope_dim,
+          _ptr(indices), max(_rows(indices, "indices"), C), C, split,
+          D ** -0.5 if softmax_scale is None else softmax_scale, _ptr(sink), _ptr(out), ot, oh,
+          _ptr(lse), ls, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out, lse
+
+
+def chunk_mla_attention(q: torch.Tensor, cache: torch.Tensor, query_start_loc: torch.Tensor,
+                        seq_lens: torch.Tensor, token_to_req: torch.Tensor,
+                        block_table: torch.Tensor, block_size: int, *, window_size: int = 0,
+                        replay_start: Optional[torch.Tensor] = None,
+                        base_offsets: Optional[torch.Tensor] = None,
+                        is_valid_token: Optional[torch.Tensor] = None,
+                        softmax_scale: Optional[float] = None,
+                        sink: Optional[torch.Tensor] = None, rope_dim: int = 64,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Causal attention of a chunk of new tokens ``q`` [T, H, D] over their requests' positions
+    through ``block_table`` (whole context, or the last ``window_size`` positions); rows of the
+    new tokens must be in the cache.  Returns (out [T, H, D] bf16, lse [T, H] binary32)."""
+    _need_cuda(q, cache, query_start_loc, seq_lens, token_to_req, block_table, replay_start,
+               base_offsets, is_valid_token, sink, out, lse, workspace)
+    qt, qh = _heads(q, "q")
+    T, H, D = q.shape
+    R = seq_lens.shape[0]
+    _vec(seq_lens, torch.int32, "seq_lens")
+    _vec(query_start_loc, torch.int32, "query_start_loc", R + 1)
+    _vec(token_to_req, torch.int32, "token_to_req", T)
+    _vec(replay_start, torch.int32, "replay_start", R)
+    _vec(base_offsets, torch.int32, "base_offsets", R)
+    stride, width = _table(block_table, "block_table", R)
+    valid = None if is_valid_token is None else is_valid_token.to(torch.uint8)
+    _vec(valid, torch.uint8, "is_valid_token", T)
+    pages, page_stride = _pages(cache)
+    lib = _abi.lib()
+    need = _on(q.device, lib.chunk_mla_attention_workspace_bytes, T, H, D, width, block_size,
+               window_size)
+    out, lse, ls, workspace = _attention_outputs(q, sink, out, lse, workspace, need)
+    ot, oh = _heads(out, "out")
+    _call(q.device, "chunk_mla_attention", _ptr(q), qt, qh, T, H, _ptr(cache), pages, page_stride,
+          block_size, D, rope_dim, _ptr(query_start_loc), _ptr(seq_lens), _ptr(token_to_req),
+          _ptr(replay_start), R, _ptr(block_table), stride, width, _ptr(base_offsets),
+          window_size, _ptr(valid), D ** -0.5 if softmax_scale is None else softmax_scale,
+          _ptr(sink), _ptr(out), ot, oh, _ptr(lse), ls, _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    return out, lse
