@@ -94,8 +94,9 @@ int32_t psk_abi_version(void);
 /*
  * psk_device_wait_timeouts -- diagnostic of the pipelined kernels.
  * Kernels that wait on shared-memory barriers (the TMA-fed gather, the
- * index builders that stage top-k rows by bulk copies and the long-window
- * compressed-row kernel of compress_kv_cache_insert) bound every wait to
+ * index builders that stage top-k rows by bulk copies, the long-window
+ * compressed-row kernel of compress_kv_cache_insert and the attention kernels)
+ * bound every wait to
  * 2 s of wall time; a wait that expires is counted in a per-device counter,
  * the kernel stops its remaining work instead of hanging, and the output of
  * that launch is incomplete.  This call copies the current device's count
@@ -781,8 +782,9 @@ psk_status extend_block_tables(
  *                 16-byte aligned (may be NULL when that is 0).  Scratch for the
  *                 call: its contents need not be kept between calls, and two
  *                 calls that can run at the same time need one each.
- *   A NaN or infinity in a visible row or in q gives what the formulas give; a
- *   row that is not visible is not read.
+ *   A NaN in q or in a visible row, or a score that is NaN or +infinity, makes
+ *   that (t, h) NaN; what is not visible to a token has no influence on it,
+ *   whatever it holds.
  */
 int64_t sparse_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
                                              int32_t head_dim, int32_t cols);
@@ -808,13 +810,15 @@ psk_status sparse_mla_attention(
  * window), those of them whose logical page position/block_size -
  * base_offsets[r] lies in [0, bt_width) and names a page in [0, num_pages).
  * The new tokens' own rows have to be in the cache already.  Formulas, types
- * and the other arguments as in sparse_mla_attention.  A padding token
+ * and the other arguments as in sparse_mla_attention; a token that sees a row
+ * with an infinity in it may get NaN in every dim.  A padding token
  * (is_valid_token 0, or a request index outside [0, num_reqs)) sees nothing:
  * out = 0, lse = -inf.
  */
-int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
-                                            int32_t head_dim, int32_t bt_width,
-                                            int32_t block_size, int32_t window);
+int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_reqs,
+                                            int32_t num_heads, int32_t head_dim,
+                                            int32_t bt_width, int32_t block_size,
+                                            int32_t window);
 
 psk_status chunk_mla_attention(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,

@@ -87,7 +87,7 @@ SIGNATURES = {
     "sparse_mla_attention": (
         _I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I32, _I32,
                _P, _I64, _I32, _I32, ctypes.c_float, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
-    "chunk_mla_attention_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32, _I32, _I32]),
+    "chunk_mla_attention_workspace_bytes": (_I64, [_I64, _I32, _I32, _I32, _I32, _I32, _I32]),
     "chunk_mla_attention": (
         _I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _I32,
                _P, _I64, _I32, _P, _I32, _P, ctypes.c_float, _P, _P, _I64, _I64, _P, _I64, _P, _I64,

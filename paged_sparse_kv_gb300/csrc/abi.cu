@@ -122,14 +122,17 @@ int32_t psk_abi_version(void) { return 6; }
 
 psk_status psk_device_wait_timeouts(uint32_t* count) {
     CHECK(count != nullptr, "count must be non-null");
-    uint32_t gather = 0, index = 0, compress = 0;
+    uint32_t gather = 0, index = 0, compress = 0, attention = 0;
     psk_status st = cuda_status(psk::read_wait_timeouts(&gather), "reading the wait-timeout counter");
     if (st != PSK_OK) return st;
     st = cuda_status(psk::read_index_wait_timeouts(&index), "reading the wait-timeout counter");
     if (st != PSK_OK) return st;
     st = cuda_status(psk::read_compress_wait_timeouts(&compress), "reading the wait-timeout counter");
     if (st != PSK_OK) return st;
-    *count = gather + index + compress;
+    st = cuda_status(psk::read_attention_wait_timeouts(&attention),
+                     "reading the wait-timeout counter");
+    if (st != PSK_OK) return st;
+    *count = gather + index + compress + attention;
     return PSK_OK;
 }
 
@@ -961,7 +964,7 @@ psk_status extend_block_tables(
 int64_t sparse_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
                                              int32_t head_dim, int32_t cols) {
     if (num_tokens < 1 || num_heads < 1 || !attn_head_dim_ok(head_dim) || cols < 1) return 0;
-    return psk::attention_workspace_bytes(num_tokens, num_heads, head_dim, cols);
+    return psk::attention_workspace_bytes(num_tokens, num_heads, head_dim, cols, true, 0);
 }
 
 psk_status sparse_mla_attention(
@@ -1023,14 +1026,16 @@ psk_status sparse_mla_attention(
                        "sparse_mla_attention launch");
 }
 
-int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
-                                            int32_t head_dim, int32_t bt_width,
-                                            int32_t block_size, int32_t window) {
-    if (num_tokens < 1 || num_heads < 1 || !attn_head_dim_ok(head_dim) || bt_width < 1 ||
+int64_t chunk_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_reqs,
+                                            int32_t num_heads, int32_t head_dim,
+                                            int32_t bt_width, int32_t block_size,
+                                            int32_t window) {
+    if (num_tokens < 1 || num_reqs < 1 || num_heads < 1 || !attn_head_dim_ok(head_dim) || bt_width < 1 ||
         block_size < 1 || window < 0)
         return 0;
     return psk::attention_workspace_bytes(num_tokens, num_heads, head_dim,
-                                          chunk_max_keys(bt_width, block_size, window));
+                                          chunk_max_keys(bt_width, block_size, window), false,
+                                          num_reqs);
 }
 
 psk_status chunk_mla_attention(
@@ -1082,7 +1087,7 @@ psk_status chunk_mla_attention(
     p.base_off = base_offsets;
     p.window = window;
     st = check_attention(p, num_tokens > 0,
-                         chunk_mla_attention_workspace_bytes(num_tokens, num_heads, head_dim,
+                         chunk_mla_attention_workspace_bytes(num_tokens, num_reqs, num_heads, head_dim,
                                                              bt_width, block_size, window),
                          workspace_bytes);
     if (st != PSK_OK) return st;

@@ -49,12 +49,15 @@ struct AttnParams {
     int32_t window;           // 0: the whole context
 };
 
-// Bytes of workspace a call of these sizes needs on the current device;
-// max_keys is the largest number of keys one token can see.
+// Bytes of workspace a call of these sizes needs on the current device; max_keys
+// is the largest number of rows one token can see.
 int64_t attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_dim,
-                                  int64_t max_keys);
+                                  int64_t max_keys, bool indexed, int32_t num_reqs);
 
 cudaError_t launch_attention_indexed(AttnParams p, cudaStream_t stream);
 cudaError_t launch_attention_chunk(AttnParams p, cudaStream_t stream);
+
+// Count of expired bounded waits in the attention kernels.
+cudaError_t read_attention_wait_timeouts(uint32_t* count);
 
 }  // namespace psk

@@ -775,8 +775,8 @@ def chunk_mla_attention(q: torch.Tensor, cache: torch.Tensor, query_start_loc: t
     _vec(valid, torch.uint8, "is_valid_token", T)
     pages, page_stride = _pages(cache)
     lib = _abi.lib()
-    need = _on(q.device, lib.chunk_mla_attention_workspace_bytes, T, H, D, width, block_size,
-               window_size)
+    need = _on(q.device, lib.chunk_mla_attention_workspace_bytes, T, R, H, D, width,
+               block_size, window_size)
     out, lse, ls, workspace = _attention_outputs(q, sink, out, lse, workspace, need)
     ot, oh = _heads(out, "out")
     _call(q.device, "chunk_mla_attention", _ptr(q), qt, qh, T, H, _ptr(cache), pages, page_stride,

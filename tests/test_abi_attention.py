@@ -76,9 +76,10 @@ def test_workspace_sizes(psk_lib):
     s, c = psk_lib.sparse_mla_attention_workspace_bytes, psk_lib.chunk_mla_attention_workspace_bytes
     for bad in ((0, 64, 512, 640), (4, 0, 512, 640), (4, 64, 96, 640), (4, 64, 512, 0)):
         assert s(*bad) == 0
-    for bad in ((0, 64, 512, 16, 64, 0), (4, 64, 512, 0, 64, 0), (4, 64, 512, 16, 64, -1)):
+    for bad in ((0, 2, 64, 512, 16, 64, 0), (4, 0, 64, 512, 16, 64, 0), (4, 2, 64, 512, 0, 64, 0),
+                (4, 2, 64, 512, 16, 64, -1)):
         assert c(*bad) == 0
-    for n in (s(1, 16, 512, 640), c(2, 64, 512, 2048, 64, 0)):
+    for n in (s(1, 16, 512, 640), c(2, 2, 64, 512, 2048, 64, 0)):
         assert n >= 0 and n % 16 == 0
 
 
