@@ -770,10 +770,10 @@ psk_status extend_block_tables(
  *                 [0, split); extra_cache by columns [split, cols) (may be NULL
  *                 when split == cols).  head_dim in {128, 256, 512}, rope_dim a
  *                 multiple of 64 in [0, head_dim).
- *   indices       int32 [num_tokens, cols], row stride idx_stride: slot ids; a
+ *   indices       int32 [num_tokens, cols], row stride idx_stride, cols <= 2^30: slot ids; a
  *                 slot < 0 or >= num_pages * block_size of its cache is not
  *                 visible.  A slot named twice counts twice.
- *   softmax_scale finite and > 0.
+ *   softmax_scale a normal number in (0, 1e38].
  *   sink          nullable binary32 [num_heads] (no sink when null).
  *   out           bf16; row (t, h) at out + t*out_stride_t + h*out_stride_h
  *                 (multiples of 8; 16-byte aligned; rows must not overlap).

@@ -83,7 +83,8 @@ bool attn_head_dim_ok(int32_t d) { return d == 128 || d == 256 || d == 512; }
 psk_status check_attention(const psk::AttnParams& p, bool work, int64_t workspace_need,
                            int64_t workspace_bytes) {
     CHECK(p.num_heads >= 1, "num_heads must be >= 1");
-    CHECK(std::isfinite(p.scale) && p.scale > 0.0f, "softmax_scale must be finite and > 0");
+    CHECK(std::isnormal(p.scale) && p.scale > 0.0f && p.scale <= 1e38f,
+          "softmax_scale must be a normal number in (0, 1e38]");
     CHECK(p.q_stride_t >= 0 && p.q_stride_h >= 0 && p.q_stride_t % 8 == 0 &&
               p.q_stride_h % 8 == 0,
           "query strides must be non-negative multiples of 8 elements");
@@ -976,7 +977,8 @@ psk_status sparse_mla_attention(
     float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
     int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
     int64_t workspace_bytes, psk_stream_t stream) {
-    CHECK(num_tokens >= 0 && cols >= 0, "num_tokens and cols must be >= 0");
+    CHECK(num_tokens >= 0 && cols >= 0 && cols <= (1 << 30),
+          "num_tokens must be >= 0 and cols in [0, 2^30]");
     CHECK(split >= 0 && split <= cols, "need 0 <= split <= cols");
     CHECK(attn_head_dim_ok(head_dim), "head_dim must be one of 128, 256, 512 (got %d)", head_dim);
     CHECK(rope_dim >= 0 && rope_dim < head_dim && rope_dim % 64 == 0,

@@ -19,11 +19,13 @@
 // operand of the first, as the M-major A operand of the second.
 //
 // Roles.  16 worker warps dequantise a tile, take the softmax of S^T and at the
-// end of a unit write O^T; one thread issues the MMAs; one warp looks one unit
-// ahead (which tiles hold anything visible, which tokens and positions).  The
-// tile is handed over in chunks of 64 dims: the first product follows the
-// dequantisation chunk by chunk, and the next tile is dequantised into the
-// chunks the second product has finished with.  Every wait is bounded (2 s of
+// end of a unit write O^T; one thread issues the MMAs; one warp plans ahead: it
+// finds the tiles that hold anything visible and puts the addresses and scales
+// of their rows into a ring, across units.  The tile is handed over in blocks of
+// 128 dims: the first product follows the dequantisation block by block, and
+// the next tile is dequantised into the blocks the second product has finished
+// with.  The first loads of a tile are in flight during the softmax of the one
+// before.  Every wait is bounded (2 s of
 // wall time, counted in psk_device_wait_timeouts).
 //
 // Softmax in one pass: a running reference m per column.  It follows the
@@ -49,7 +51,7 @@ constexpr int kWorkers = 16;          // worker warps
 constexpr int kMmaWarp = kWorkers;
 constexpr int kPlanWarp = kWorkers + 1;
 constexpr int kThreads = (kWorkers + 2) * kWarp;
-constexpr int kMaxChunks = 8;         // 64-dim chunks of a row (head_dim 512)
+constexpr int kMaxBlocks = 4;         // 128-dim blocks of a row (head_dim 512)
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -61,34 +63,49 @@ __device__ unsigned int g_attn_wait_timeouts = 0;
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
-// What a CTA does next: a set of tiles for a set of columns.
+// A set of columns; its tiles follow one another in the stream of tiles.
 struct Unit {
-    int32_t done;
-    int32_t ntiles;
-    int32_t first;        // the tiles are first, first + 1, ... where mask is 0
-    int32_t part;         // which part of the split work (row of the workspace)
-    uint64_t mask;        // index form with at most 64 tiles: those with a visible row
-    int32_t lo, hi;       // position form: the positions of all columns
-    int32_t req;
-    int32_t pad;
-    int32_t col_token[kMaxCols];  // -1: column not in use
+    int32_t part;                  // which part of the split work (row of the workspace)
+    int32_t pad[3];
+    int64_t col_q[kMaxCols];       // element offset of the column's query
+    int64_t col_out[kMaxCols];     // and of its output row
+    int32_t col_token[kMaxCols];   // -1: column not in use
     int32_t col_head[kMaxCols];
-    int32_t col_lo[kMaxCols], col_hi[kMaxCols];  // kTokens: positions a column sees
+    int32_t col_lo[kMaxCols], col_hi[kMaxCols];  // kTokens: positions the column sees
 };
 
+struct alignas(16) Row {
+    const uint8_t* data;  // null: the row does not exist or is not visible
+    uint2 scales;         // its UE8M0 bytes
+};
+
+constexpr int kFirst = 1, kLast = 2, kEmpty = 4, kDone = 8;
+
+// One step of the stream: a tile's rows, and where it stands in its unit.
+struct Tile {
+    int32_t flags;
+    int32_t unit;   // slot of its unit
+    int32_t pos;    // position form: position of row 0
+    int32_t pad;
+    Row row[kTile];
+};
+
+constexpr int kTiles = 3;  // tiles the planning warp may be ahead, the current one included
+
 struct Shared {
+    Tile tile[kTiles];
     Unit unit[2];
-    uint64_t unit_full[2], unit_empty[2];
-    uint64_t full[kMaxChunks];         // chunk c of the tile is dequantised
-    uint64_t freed[kMaxChunks / 2];    // the second product is done with chunks 2j, 2j + 1
-    uint64_t s_ready, p_ready, drain;
-    uint64_t group_bar[4];
-    uint32_t tmem;
-    uint8_t row_ok[2][kTile];          // the row exists (and is visible where one token is at work)
-    uint8_t row_bad[2][kTile];         // kTokens: it holds a NaN or an infinity
     alignas(16) float red[4][2][4][16];  // [group][exchange parity][lane quarter][column]
     alignas(16) float ref[kWorkers][16];
     alignas(16) float aux[kWorkers][16];
+    uint64_t tile_full[kTiles], tile_empty[kTiles];
+    uint64_t unit_empty[2];
+    uint64_t full[kMaxBlocks];     // 128 dims of the tile are dequantised
+    uint64_t freed[kMaxBlocks];    // the second product is done with them
+    uint64_t s_ready, p_ready, drain;
+    uint64_t group_bar[4];
+    uint32_t tmem;
+    uint8_t row_bad[2][kTile];     // kTokens: the row holds a NaN or an infinity
 };
 
 struct LaunchShape {
@@ -107,6 +124,14 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait_bounded(bar, parity, kWaitLimitNs);
     return __all_sync(0xFFFFFFFFu, ok);
 }
+
+// Blocks (128 dims) in the order both products take them: those with rope dims
+// first, since their copies take longest, then the others downwards.
+struct Order {
+    int blocks, rope_from;  // blocks >= rope_from hold rope dims
+    __device__ __forceinline__ explicit Order(const AttnParams& p)
+        : blocks(p.head_dim / 128), rope_from((p.head_dim - p.rope_dim) / 128) {}
+};
 
 // ---- the planning warp -------------------------------------------------------------
 
@@ -135,32 +160,155 @@ __device__ __forceinline__ TokenRange token_range(const AttnParams& p, int64_t t
     return x;
 }
 
-__device__ __forceinline__ bool slot_ok(const AttnParams& p, int32_t col, int32_t slot) {
-    const AttnCache& c = col < p.split ? p.cache : p.extra;
-    return slot >= 0 && slot < c.num_pages * c.block_size;
-}
-
-// Even share `part` of n tiles: [first, first + count).
+// Even share `part` of n tiles: [first, end).
 __device__ __forceinline__ void share(int32_t n, int32_t part, int32_t parts, int32_t& first,
-                                      int32_t& count) {
+                                      int32_t& end) {
     first = (int32_t)((int64_t)n * part / parts);
-    count = (int32_t)((int64_t)n * (part + 1) / parts) - first;
+    end = (int32_t)((int64_t)n * (part + 1) / parts);
 }
 
-// Waits for the slot of unit `seq`, which two units before it have used.
-__device__ __forceinline__ bool unit_slot(Shared& sh, int seq) {
-    return seq < 2 || wait_all(&sh.unit_empty[seq & 1], ((seq >> 1) - 1) & 1);
+// What the rows of a unit are looked up by.
+struct Source {
+    int64_t token;           // index form
+    int32_t req, lo, hi;     // position form
+};
+
+constexpr int kRowsPerLane = kTile / kWarp;
+
+// Cache entries of a tile's rows lane, lane + 32, ...: slots (index form) or
+// pages, -1 for none.  True if any row of the tile has one.
+template <int kSrc>
+__device__ __forceinline__ bool tile_entries(const AttnParams& p, const Source& src, int32_t tile, int lane,
+                                             int32_t (&entry)[kRowsPerLane]) {
+    bool any = false;
+    int32_t x[kRowsPerLane];
+#pragma unroll
+    for (int j = 0; j < kRowsPerLane; ++j) {
+        x[j] = -1;
+        const int64_t i = (int64_t)tile * kTile + j * kWarp + lane;
+        if (kSrc == kIndexed) {
+            if (i < p.cols) x[j] = p.idx[src.token * p.idx_stride + i];
+        } else {
+            const int64_t pos = src.lo + i;
+            if (pos <= src.hi) {
+                int32_t off;
+                const int32_t logical = div_block32((int32_t)pos, p.cache.block_size, p.cache.shift, off) -
+                                        (p.base_off ? p.base_off[src.req] : 0);
+                if (logical >= 0 && logical < p.bt_width) x[j] = p.bt[(int64_t)src.req * p.bt_stride + logical];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsPerLane; ++j) {
+        const int32_t c = tile * kTile + j * kWarp + lane;
+        const AttnCache& k = kSrc == kIndexed && c >= p.split ? p.extra : p.cache;
+        const int64_t limit = kSrc == kIndexed ? k.num_pages * k.block_size : k.num_pages;
+        entry[j] = x[j] >= 0 && x[j] < limit ? x[j] : -1;
+        any |= entry[j] >= 0;
+    }
+    return __any_sync(0xFFFFFFFFu, any);
 }
 
-__device__ __forceinline__ void unit_publish(Shared& sh, int seq, int lane) {
+// Fills `rows` with the addresses and scales of the entries.
+template <int kSrc>
+__device__ __forceinline__ void tile_rows(const AttnParams& p, const Source& src, int32_t tile, int lane,
+                                          const int32_t (&entry)[kRowsPerLane], Row* rows) {
+    const int32_t token_stride = p.head_dim + p.rope_dim, nsc = p.head_dim / 64;
+    Row r[kRowsPerLane];
+#pragma unroll
+    for (int j = 0; j < kRowsPerLane; ++j) {
+        r[j] = Row{nullptr, make_uint2(0, 0)};
+        if (entry[j] < 0) continue;
+        const int32_t i = tile * kTile + j * kWarp + lane;
+        const AttnCache& c = kSrc == kIndexed && i >= p.split ? p.extra : p.cache;
+        int32_t page = entry[j], off;
+        if (kSrc == kIndexed)
+            page = div_block32(entry[j], c.block_size, c.shift, off);
+        else
+            div_block32(src.lo + i, c.block_size, c.shift, off);
+        const uint8_t* pg = c.base + (int64_t)page * c.page_stride;
+        r[j].data = pg + (int64_t)off * token_stride;
+        const uint8_t* sc = pg + (int64_t)c.block_size * token_stride + (int64_t)off * nsc;
+        if (nsc == 8) {
+            r[j].scales = ld_nc_v2(sc);
+        } else if (nsc == 4) {
+            r[j].scales.x = ld_nc_u32(sc);
+        } else {
+            r[j].scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsPerLane; ++j) rows[j * kWarp + lane] = r[j];
+}
+
+struct Stream {
+    int tiles = 0, units = 0;  // published so far
+};
+
+// Waits for the tile slot the next record takes.
+__device__ __forceinline__ bool tile_slot(Shared& sh, const Stream& st) {
+    return st.tiles < kTiles || wait_all(&sh.tile_empty[st.tiles % kTiles], (st.tiles / kTiles - 1) & 1);
+}
+
+__device__ __forceinline__ void publish(Shared& sh, Stream& st, int lane, int32_t flags, int32_t pos) {
+    Tile& t = sh.tile[st.tiles % kTiles];
+    if (lane == 0) {
+        t.flags = flags;
+        t.unit = st.units & 1;
+        t.pos = pos;
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.unit_full[seq & 1]);
+    if (lane == 0) mbar_arrive(&sh.tile_full[st.tiles % kTiles]);
+    ++st.tiles;
+}
+
+// The tiles [first, end) of a unit that hold anything.
+template <int kSrc>
+__device__ __forceinline__ bool stream_unit(const AttnParams& p, Shared& sh, Stream& st, const Source& src,
+                                            int32_t first, int32_t end, int lane) {
+    int32_t entry[kRowsPerLane], ahead[kRowsPerLane];
+    int32_t tile = first;
+    while (tile < end && !tile_entries<kSrc>(p, src, tile, lane, entry)) ++tile;
+    int32_t flags = kFirst;
+    if (tile >= end) {
+        if (!tile_slot(sh, st)) return false;
+        publish(sh, st, lane, kFirst | kLast | kEmpty, 0);
+    }
+    while (tile < end) {
+        int32_t next = tile + 1;
+        while (next < end && !tile_entries<kSrc>(p, src, next, lane, ahead)) ++next;
+        if (!tile_slot(sh, st)) return false;
+        tile_rows<kSrc>(p, src, tile, lane, entry, sh.tile[st.tiles % kTiles].row);
+        if (next >= end) flags |= kLast;
+        publish(sh, st, lane, flags, kSrc == kIndexed ? 0 : src.lo + tile * kTile);
+        flags = 0;
+        tile = next;
+#pragma unroll
+        for (int j = 0; j < kRowsPerLane; ++j) entry[j] = ahead[j];
+    }
+    ++st.units;
+    return true;
+}
+
+// Waits for the slot of the next unit, which two units before it have used.
+__device__ __forceinline__ bool unit_slot(Shared& sh, const Stream& st) {
+    return st.units < 2 || wait_all(&sh.unit_empty[st.units & 1], ((st.units >> 1) - 1) & 1);
+}
+
+__device__ __forceinline__ void set_column(const AttnParams& p, Unit& un, int c, int64_t t, int32_t h,
+                                           bool used, int32_t lo, int32_t hi) {
+    un.col_token[c] = used ? (int32_t)t : -1;
+    un.col_head[c] = h;
+    un.col_q[c] = t * p.q_stride_t + h * p.q_stride_h;
+    un.col_out[c] = t * p.out_stride_t + h * p.out_stride_h;
+    un.col_lo[c] = used ? lo : 0;
+    un.col_hi[c] = used ? hi : -1;
 }
 
 template <int kSrc>
 __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
     const int lane = threadIdx.x % kWarp;
-    int seq = 0;
+    Stream st;
     for (int64_t u = blockIdx.x; u < ls.units; u += gridDim.x) {
         const int32_t part = (int32_t)(u % ls.splits);
         const int64_t v = u / ls.splits;
@@ -168,55 +316,24 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
             const int64_t t = v / ls.head_groups;
             const int32_t h0 = (int32_t)(v % ls.head_groups) * ls.heads_per_unit;
             const int32_t heads = min(ls.heads_per_unit, p.num_heads - h0);
-            uint64_t mask = 0;
-            int32_t first = 0, count = 0;
-            TokenRange x{0, 0, -1};
+            Source src{t, 0, 0, -1};
+            int32_t n, first, end;
             if (kSrc == kIndexed) {
-                const int32_t n = p.cols / kTile + (p.cols % kTile != 0);
-                if (n <= 64) {
-                    const int32_t* row = p.idx + t * p.idx_stride;
-                    for (int32_t i = 0; i < n; ++i) {
-                        bool any = false;
-#pragma unroll
-                        for (int j = 0; j < kTile / kWarp; ++j) {
-                            const int32_t c = i * kTile + j * kWarp + lane;
-                            if (c < p.cols) any |= slot_ok(p, c, row[c]);
-                        }
-                        if (__any_sync(0xFFFFFFFFu, any)) mask |= 1ull << i;
-                    }
-                    share(__popcll(mask), part, ls.splits, first, count);
-                    for (int32_t k = 0; k < first; ++k) mask &= mask - 1;
-                    uint64_t rest = mask;
-                    for (int32_t k = 0; k < count; ++k) rest &= rest - 1;
-                    mask ^= rest;
-                } else {
-                    share(n, part, ls.splits, first, count);
-                }
+                n = p.cols / kTile + (p.cols % kTile != 0);
             } else {
-                x = token_range(p, t);
-                const int32_t n = x.hi < x.lo ? 0 : (int32_t)(((int64_t)x.hi - x.lo) / kTile) + 1;
-                share(n, part, ls.splits, first, count);
+                const TokenRange x = token_range(p, t);
+                src.req = x.req;
+                src.lo = x.lo;
+                src.hi = x.hi;
+                n = x.hi < x.lo ? 0 : (x.hi - x.lo) / kTile + 1;
             }
-            if (!unit_slot(sh, seq)) return false;
-            Unit& un = sh.unit[seq & 1];
-            if (lane == 0) {
-                un.done = 0;
-                un.ntiles = count;
-                un.first = first;
-                un.part = part;
-                un.mask = mask;
-                un.lo = x.lo;
-                un.hi = x.hi;
-                un.req = x.req;
-            }
+            share(n, part, ls.splits, first, end);
+            if (!unit_slot(sh, st)) return false;
+            Unit& un = sh.unit[st.units & 1];
+            if (lane == 0) un.part = part;
 #pragma unroll
-            for (int k = 0; k < kMaxCols / kWarp; ++k) {
-                const int c = lane + k * kWarp;
-                un.col_token[c] = c < heads ? (int32_t)t : -1;
-                un.col_head[c] = h0 + c;
-            }
-            unit_publish(sh, seq, lane);
-            ++seq;
+            for (int c = lane; c < kMaxCols; c += kWarp) set_column(p, un, c, t, h0 + c, c < heads, 0, 0);
+            if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
         } else {
             // a run of neighbouring tokens of one request is a unit
             const int64_t t0 = v * ls.tokens_per_unit;
@@ -230,44 +347,31 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 starts &= starts - 1;
                 const int32_t b = starts ? __ffs(starts) - 1 : n;
                 const bool in = lane >= a && lane < b && x.lo <= x.hi;
-                const int32_t lo = __reduce_min_sync(0xFFFFFFFFu, in ? x.lo : INT32_MAX);
-                const int32_t hi = __reduce_max_sync(0xFFFFFFFFu, in ? x.hi : -1);
-                const int32_t tiles = hi < lo ? 0 : (int32_t)(((int64_t)hi - lo) / kTile) + 1;
-                int32_t first, count;
-                share(tiles, part, ls.splits, first, count);
-                if (!unit_slot(sh, seq)) return false;
-                Unit& un = sh.unit[seq & 1];
-                const int32_t req = __shfl_sync(0xFFFFFFFFu, x.req, a);
-                if (lane == 0) {
-                    un.done = 0;
-                    un.ntiles = count;
-                    un.first = first;
-                    un.part = part;
-                    un.mask = 0;
-                    un.lo = lo;
-                    un.hi = hi;
-                    un.req = req;
-                }
+                Source src;
+                src.token = 0;
+                src.req = __shfl_sync(0xFFFFFFFFu, x.req, a);
+                src.lo = __reduce_min_sync(0xFFFFFFFFu, in ? x.lo : INT32_MAX);
+                src.hi = __reduce_max_sync(0xFFFFFFFFu, in ? x.hi : -1);
+                const int32_t tiles = src.hi < src.lo ? 0 : (src.hi - src.lo) / kTile + 1;
+                int32_t first, end;
+                share(tiles, part, ls.splits, first, end);
+                if (!unit_slot(sh, st)) return false;
+                Unit& un = sh.unit[st.units & 1];
+                if (lane == 0) un.part = part;
 #pragma unroll
                 for (int k = 0; k < kMaxCols / kWarp; ++k) {
                     const int c = lane + k * kWarp;
                     const int tok = a + c / p.num_heads;
-                    const bool used = tok < b;
-                    const int32_t clo = __shfl_sync(0xFFFFFFFFu, x.lo, tok & 31);
-                    const int32_t chi = __shfl_sync(0xFFFFFFFFu, x.hi, tok & 31);
-                    un.col_token[c] = used ? (int32_t)(t0 + tok) : -1;
-                    un.col_head[c] = c % p.num_heads;
-                    un.col_lo[c] = used ? clo : 0;
-                    un.col_hi[c] = used ? chi : -1;
+                    const int32_t lo = __shfl_sync(0xFFFFFFFFu, x.lo, tok & 31);
+                    const int32_t hi = __shfl_sync(0xFFFFFFFFu, x.hi, tok & 31);
+                    set_column(p, un, c, t0 + tok, c % p.num_heads, tok < b, lo, hi);
                 }
-                unit_publish(sh, seq, lane);
-                ++seq;
+                if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
             }
         }
     }
-    if (!unit_slot(sh, seq)) return false;
-    if (lane == 0) sh.unit[seq & 1].done = 1;
-    unit_publish(sh, seq, lane);
+    if (!tile_slot(sh, st)) return false;
+    publish(sh, st, lane, kDone, 0);
     return true;
 }
 
@@ -276,140 +380,100 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
 template <int N>
 __device__ bool issue(const AttnParams& p, Shared& sh, uint32_t k_tile, uint32_t q_tile,
                       uint32_t p_tile, uint32_t tmem) {
-    const int chunks = p.head_dim / 64, blocks = p.head_dim / 128;
-    constexpr uint32_t kFirst = umma_idesc(kTile, N, false), kSecond = umma_idesc(128, N, true);
+    const Order ord(p);
+    constexpr uint32_t kS = umma_idesc(kTile, N, false), kO = umma_idesc(128, N, true);
     uint32_t step = 0;
     for (int seq = 0;; ++seq) {
-        if (!mbar_wait_bounded(&sh.unit_full[seq & 1], (seq >> 1) & 1, kWaitLimitNs)) return false;
-        const Unit& un = sh.unit[seq & 1];
-        const int32_t done = un.done, ntiles = un.ntiles;
-        mbar_arrive(&sh.unit_empty[seq & 1]);
-        if (done) return true;
-        for (int32_t i = 0; i < ntiles; ++i, ++step) {
-            for (int c = 0; c < chunks; ++c) {
-                if (!mbar_wait_bounded(&sh.full[c], step & 1, kWaitLimitNs)) return false;
-                tmem_fence_after();
-                // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart, 32 bytes a step
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_bf16(tmem, umma_desc(k_tile + c * kChunkBytes + k * 32, 16, 1024, kSwizzle128),
-                              umma_desc(q_tile + c * (N * 128) + k * 32, 16, 1024, kSwizzle128), kFirst,
-                              c > 0 || k > 0);
-            }
-            umma_commit(&sh.s_ready);
-            if (!mbar_wait_bounded(&sh.p_ready, step & 1, kWaitLimitNs)) return false;
+        const int slot = seq % kTiles;
+        if (!mbar_wait_bounded(&sh.tile_full[slot], (seq / kTiles) & 1, kWaitLimitNs)) return false;
+        const int32_t flags = sh.tile[slot].flags;
+        mbar_arrive(&sh.tile_empty[slot]);
+        if (flags & kDone) return true;
+        if (flags & kEmpty) continue;
+        // the blocks without rope dims are ready first
+        for (int i = 0; i < ord.blocks; ++i) {
+            const int j = i < ord.rope_from ? ord.rope_from - 1 - i : ord.blocks - 1 - (i - ord.rope_from);
+            if (!mbar_wait_bounded(&sh.full[j], step & 1, kWaitLimitNs)) return false;
             tmem_fence_after();
-            for (int j = 0; j < blocks; ++j) {
-                // A: M-major, 128-byte swizzle: 64-dim chunks kChunkBytes apart, 8-row groups
-                // 1024 bytes apart.  B: N-major, no swizzle: 8-column groups 2048 bytes
-                // apart, 8-row groups 128 bytes apart.
+            // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart, 32 bytes a step
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_bf16(tmem + N + j * N,
-                              umma_desc(k_tile + j * 2 * kChunkBytes + k * 2048, kChunkBytes, 1024,
-                                        kSwizzle128),
-                              umma_desc(p_tile + k * 256, 128, 2048, kSwizzleNone), kSecond,
-                              i > 0 || k > 0);
-                umma_commit(&sh.freed[j]);
+            for (int k = 0; k < 8; ++k) {
+                const int c = 2 * j + k / 4;
+                umma_bf16(tmem, umma_desc(k_tile + c * kChunkBytes + (k % 4) * 32, 16, 1024, kSwizzle128),
+                          umma_desc(q_tile + c * (N * 128) + (k % 4) * 32, 16, 1024, kSwizzle128), kS,
+                          i > 0 || k > 0);
             }
         }
+        umma_commit(&sh.s_ready);
+        if (!mbar_wait_bounded(&sh.p_ready, step & 1, kWaitLimitNs)) return false;
+        tmem_fence_after();
+        for (int j = ord.blocks - 1; j >= 0; --j) {
+            // A: M-major, 128-byte swizzle: 64-dim chunks kChunkBytes apart, 8-row groups
+            // 1024 bytes apart.  B: N-major, no swizzle: 8-column groups 2048 bytes
+            // apart, 8-row groups 128 bytes apart.
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                umma_bf16(tmem + N + j * N,
+                          umma_desc(k_tile + j * 2 * kChunkBytes + k * 2048, kChunkBytes, 1024, kSwizzle128),
+                          umma_desc(p_tile + k * 256, 128, 2048, kSwizzleNone), kO,
+                          !(flags & kFirst) || k > 0);
+            umma_commit(&sh.freed[j]);
+        }
+        ++step;
     }
 }
 
 // ---- the worker warps ----------------------------------------------------------------
 
-struct Row {
-    const uint8_t* data;  // null: the row does not exist
-    uint2 scales;
-};
-
-// The cache entry of tile row `row`: a slot (index form) or a page, -1 for none.
-template <int kSrc>
-__device__ __forceinline__ int32_t row_entry(const AttnParams& p, const Unit& un, int32_t tile, int row) {
-    if (kSrc == kIndexed) {
-        const int64_t c = (int64_t)tile * kTile + row;
-        if (c >= p.cols) return -1;
-        const int32_t s = p.idx[(int64_t)un.col_token[0] * p.idx_stride + c];
-        return slot_ok(p, (int32_t)c, s) ? s : -1;
-    }
-    const int64_t pos = (int64_t)un.lo + (int64_t)tile * kTile + row;
-    if (pos > un.hi) return -1;
-    int32_t off;
-    const int32_t logical = div_block32((int32_t)pos, p.cache.block_size, p.cache.shift, off) -
-                            (p.base_off ? p.base_off[un.req] : 0);
-    if (logical < 0 || logical >= p.bt_width) return -1;
-    const int32_t page = p.bt[(int64_t)un.req * p.bt_stride + logical];
-    return page >= 0 && page < p.cache.num_pages ? page : -1;
+// Two E4M3 bytes in the upper bytes of each half of t -> the bf16 pair of their
+// values times 2^-120: sign, exponent and mantissa moved to their bf16 places
+// (bias 127 against 7), which holds for zeros and subnormals too; the caller's
+// factor is 2^120 times the scale.  NaN codes are not handled.
+__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) {
+    return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
 }
 
-template <int kSrc>
-__device__ __forceinline__ Row row_of(const AttnParams& p, const Unit& un, int32_t tile, int row,
-                                      int32_t entry) {
-    Row r{nullptr, make_uint2(0, 0)};
-    if (entry < 0) return r;
-    const AttnCache& c = kSrc == kIndexed && tile * kTile + row >= p.split ? p.extra : p.cache;
-    int32_t page = entry, off;
-    if (kSrc == kIndexed)
-        page = div_block32(entry, c.block_size, c.shift, off);
-    else
-        div_block32((int32_t)((int64_t)un.lo + (int64_t)tile * kTile + row), c.block_size, c.shift, off);
-    const int32_t token_stride = p.head_dim + p.rope_dim, nsc = p.head_dim / 64;
-    const uint8_t* pg = c.base + (int64_t)page * c.page_stride;
-    r.data = pg + (int64_t)off * token_stride;
-    const uint8_t* sc = pg + (int64_t)c.block_size * token_stride + (int64_t)off * nsc;
-    if (nsc == 8) {
-        r.scales = ld_nc_v2(sc);
-    } else if (nsc == 4) {
-        r.scales.x = ld_nc_u32(sc);
-    } else {
-        r.scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
-    }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// The quarter (16 dims) of chunk c that a thread dequantises: 16 E4M3 bytes, or
-// 32 bytes of bf16 where the chunk lies in the rope dims.
-__device__ __forceinline__ void load_quarter(const AttnParams& p, const Row& r, int c, int quarter,
-                                             uint4 (&raw)[2]) {
-    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-    if (r.data == nullptr) return;
-    const int nope = p.head_dim - p.rope_dim;
-    if (c * 64 < nope) {
-        raw[0] = ld_stream_v4(r.data + c * 64 + quarter * 16);
-    } else {
-        const uint8_t* b = r.data + nope + (c * 64 - nope) * 2 + quarter * 32;
-        raw[0] = ld_stream_v4(b);
-        raw[1] = ld_stream_v4(b + 16);
+// 16 E4M3 bytes of UE8M0 scale byte b as eight bf16 pairs, by the rule of the
+// gather: the product with a power of two, rounded to bf16 once.  One packed
+// multiply by 2^(120 + b - 127) does it where that factor is a bf16 number
+// (b <= 134: values up to 448 * 2^7); a larger scale takes a second one (both
+// exact but for an overflow).  A NaN code goes through the converter.
+__device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8]) {
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    const uint32_t f = (b <= 134u ? b + 120u : 247u) * 0x00800080u;
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
+        w[2 * i] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x1404)), f);
+        w[2 * i + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x3424)), f);
     }
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(uint32_t bytes, uint64_t scale2) {
-    return scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(bytes), scale2);
-}
-
-// 16 dims as eight bf16 pairs, by the rule of the gather.
-__device__ __forceinline__ void dequant_quarter(const AttnParams& p, const Row& r, int c,
-                                                const uint4 (&raw)[2], uint32_t (&w)[8]) {
-    if (c * 64 < p.head_dim - p.rope_dim) {
-        const uint32_t b = ((c < 4 ? r.scales.x : r.scales.y) >> (8 * (c & 3))) & 0xFFu;
-        const uint64_t s2 = splat_f32x2(r.data == nullptr ? 0.0f : ue8m0_scale(b));
-        const uint32_t in[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+    if (b > 134u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
+    }
+    if (nan & 0x80808080u) {
+        const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[2 * i] = bf16_pair(in[i] & 0xFFFFu, s2);
-            w[2 * i + 1] = bf16_pair(in[i] >> 16, s2);
+            w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
+            w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
         }
-    } else {
-        w[0] = raw[0].x; w[1] = raw[0].y; w[2] = raw[0].z; w[3] = raw[0].w;
-        w[4] = raw[1].x; w[5] = raw[1].y; w[6] = raw[1].z; w[7] = raw[1].w;
     }
 }
 
 // Clears the non-finite values of w; true if there were any.
-__device__ __forceinline__ bool clear_non_finite(uint32_t (&w)[8]) {
+template <int K>
+__device__ __forceinline__ bool clear_non_finite(uint32_t (&w)[K]) {
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < K; ++i) {
         const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
         if (lo) w[i] &= 0xFFFF0000u;
         if (hi) w[i] &= 0x0000FFFFu;
@@ -418,240 +482,327 @@ __device__ __forceinline__ bool clear_non_finite(uint32_t (&w)[8]) {
     return bad;
 }
 
+// 16-byte copy global -> shared; `bytes` 0 writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Queries of a unit into the swizzled B tile of the first product; unused
+// columns are zero.  Asynchronous.
+template <int N>
+__device__ __forceinline__ void load_queries(const AttnParams& p, const Unit& un, uint32_t q_tile, int tid) {
+    const int shift = p.head_dim == 512 ? 3 : p.head_dim == 256 ? 2 : 1;  // log2 of the 64-dim chunks
+#pragma unroll 4
+    for (int i = tid; i < (N * 8) << shift; i += kWorkers * kWarp) {
+        const int part = i & 7, c = (i >> 3) & ((1 << shift) - 1), n = i >> (3 + shift);
+        copy16(q_tile + c * (N * 128) + n * 128 + ((part ^ (n & 7)) * 16), p.q + un.col_q[n] * (un.col_token[n] >= 0) + c * 64 + part * 8,
+               un.col_token[n] >= 0 ? 16 : 0);
+    }
+}
+
+constexpr int kAhead = 4;  // E4M3 chunks of a row quarter in flight per thread
+
 template <int N, int kSrc>
-__device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint8_t* k_tile,
-                     uint8_t* q_tile, uint8_t* p_tile, uint32_t tmem) {
+__device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint32_t k_tile,
+                     uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
     constexpr int NC = N / 4;  // columns of a worker warp
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     const int quad = warp % 4, group = warp / 4;
-    const int row = tid / 4, quarter = tid % 4;        // dequantisation
+    const int row = tid / 4, quarter = tid % 4;        // dequantisation: 16 dims of a row's chunk
     const int srow = quad * kWarp + lane;              // softmax: the tile row of this lane
-    const int chunks = p.head_dim / 64, blocks = p.head_dim / 128;
-    const uint32_t k_addr = smem_u32(k_tile) + row * 128;
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * kWarp) << 16);
+    const Order ord(p);
+    const int nope = p.head_dim - p.rope_dim, fp8_chunks = nope / 64, chunks = p.head_dim / 64;
+    const uint32_t k_addr = k_tile + row * 128;
+    const uint32_t swz0 = ((2 * quarter) ^ (row & 7)) * 16, swz1 = ((2 * quarter + 1) ^ (row & 7)) * 16;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * kWarp) << 16) + group * NC;
     uint32_t step = 0, exchange = 0;
 
+    float l[NC];
+    float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
+    uint4 raw[kAhead];         // chunks fp8_chunks - 1, - 2, ... of the row
+    Row r{nullptr, make_uint2(0, 0)};
+
+    const auto load = [&](int k) {  // the k-th chunk in that order
+        return r.data != nullptr ? ld_stream_v4(r.data + (fp8_chunks - 1 - k) * 64 + quarter * 16)
+                                 : make_uint4(0, 0, 0, 0);
+    };
+    // takes the next tile's row and starts its first loads
+    const auto start = [&](const Tile& t) {
+        r = t.row[row];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (k < fp8_chunks) raw[k] = load(k);
+    };
+
+    if (!wait_all(&sh.tile_full[0], 0)) return false;
+    int32_t flags = sh.tile[0].flags;
+    if (!(flags & (kDone | kEmpty))) {
+        load_queries<N>(p, sh.unit[sh.tile[0].unit], q_tile, tid);
+        start(sh.tile[0]);
+    }
     for (int seq = 0;; ++seq) {
-        if (!wait_all(&sh.unit_full[seq & 1], (seq >> 1) & 1)) return false;
-        const Unit& un = sh.unit[seq & 1];
-        if (un.done) return true;
-        const int32_t ntiles = un.ntiles;
-        uint64_t mask = un.mask;
-        const bool masked = mask != 0;
-
-        float l[NC];
+        const int slot = seq % kTiles;
+        const Tile& tl = sh.tile[slot];
+        const Unit& un = sh.unit[tl.unit];
+        if (flags & kDone) return true;
+        if (flags & kFirst) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) l[i] = 0.0f;
-        float m_used = -INFINITY;  // of column `lane`, for lane < NC
-
-        if (ntiles > 0) {
-            // queries of the unit into the swizzled B tile; unused columns are zero
-            for (int i = tid; i < N * chunks * 8; i += kWorkers * kWarp) {
-                const int part = i % 8, c = (i / 8) % chunks, n = i / (8 * chunks);
-                const uint32_t dst = smem_u32(q_tile) + c * (N * 128) + n * 128 + ((part ^ (n & 7)) * 16);
-                const int32_t t = un.col_token[n];
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (t >= 0)
-                    v = ld_nc_v4(p.q + (int64_t)t * p.q_stride_t + (int64_t)un.col_head[n] * p.q_stride_h +
-                                 c * 64 + part * 8);
-                sts_v4(dst, v.x, v.y, v.z, v.w);
+            for (int i = 0; i < NC; ++i) l[i] = 0.0f;
+            m_used = -INFINITY;
+        }
+        const int nslot = (seq + 1) % kTiles;
+        int32_t next_flags = 0;
+        bool next_known = false;
+        if (!(flags & kEmpty)) {
+            const int buf = step & 1;
+            if (kSrc == kTokens) {
+                if (quarter == 0) sh.row_bad[buf][row] = 0;
+                __syncwarp();
             }
-            int32_t tile = masked ? __ffsll(mask) - 1 : un.first;
-            int32_t entry = row_entry<kSrc>(p, un, tile, row);
-            for (int32_t i = 0; i < ntiles; ++i, ++step) {
-                const int buf = step & 1;
-                const Row r = row_of<kSrc>(p, un, tile, row, entry);
-                if (quarter == 0) {
-                    sh.row_ok[buf][row] = r.data != nullptr;
-                    if (kSrc == kTokens) sh.row_bad[buf][row] = 0;
-                }
-                __syncwarp();
-                uint4 raw[4][2];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < chunks) load_quarter(p, r, c, quarter, raw[c]);
-                const int32_t this_tile = tile;
-                if (i + 1 < ntiles) {
-                    mask &= mask - 1;
-                    tile = masked ? __ffsll(mask) - 1 : tile + 1;
-                    entry = row_entry<kSrc>(p, un, tile, row);
-                }
-#pragma unroll
-                for (int c = 0; c < kMaxChunks; ++c) {
-                    if (c >= chunks) break;
-                    if (step > 0 && c % 2 == 0 && !wait_all(&sh.freed[c / 2], (step - 1) & 1)) return false;
-                    uint32_t w[8];
-                    dequant_quarter(p, r, c, raw[c % 4], w);
-                    if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
-                    const uint32_t dst = k_addr + c * kChunkBytes;
-                    sts_v4(dst + (((2 * quarter) ^ (row & 7)) * 16), w[0], w[1], w[2], w[3]);
-                    sts_v4(dst + (((2 * quarter + 1) ^ (row & 7)) * 16), w[4], w[5], w[6], w[7]);
-                    if (c + 4 < chunks) load_quarter(p, r, c + 4, quarter, raw[c % 4]);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.full[c]);
-                }
-
-                // softmax of the tile: this lane's row, NC columns
-                if (!wait_all(&sh.full[chunks - 1], step & 1)) return false;  // row_ok, row_bad
-                if (!wait_all(&sh.s_ready, step & 1)) return false;
-                tmem_fence_after();
-                float s[NC];
-                tmem_ld<NC>(lane_base + group * NC, s);
-                const bool ok = sh.row_ok[buf][srow];
-                const int32_t pos = un.lo + this_tile * kTile + srow;
-                const bool bad = kSrc == kTokens && sh.row_bad[buf][srow];
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    bool see = ok;
-                    if (kSrc == kTokens)
-                        see = see && pos >= un.col_lo[group * NC + k] && pos <= un.col_hi[group * NC + k];
-                    s[k] = see ? (bad ? NAN : s[k] * ls.scale_log2) : -INFINITY;
-                }
-                float mine = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const float x = warp_max(s[k]);
-                    if (lane == k) mine = x;
-                }
-                float(&red)[4][16] = sh.red[group][exchange & 1];
-                if (lane < NC) red[quad][lane] = mine;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-                bool grow = false;
-                if (lane < NC) {
-                    const float top = fmaxf(fmaxf(red[0][lane], red[1][lane]), fmaxf(red[2][lane], red[3][lane]));
-                    float alpha = 1.0f;
-                    if (top > m_used + kLazy) {
-                        alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
-                        grow = alpha != 1.0f;
-                        m_used = top;
+            // ---- dequantisation, block by block from the last dims down
+            int block = ord.blocks;  // blocks >= block are free
+            const auto need = [&](int j) {
+                if (step > 0 && j < block && !wait_all(&sh.freed[j], (step - 1) & 1)) return false;
+                block = j < block ? j : block;
+                return true;
+            };
+            for (int c = chunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
+                if (!need(c / 2)) return false;
+                const uint32_t dst = k_addr + c * kChunkBytes;
+                const uint8_t* src = r.data + nope + (c * 64 - nope) * 2 + quarter * 32;
+                if (kSrc == kTokens) {
+                    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (r.data != nullptr) {
+                        const uint4 x = ld_stream_v4(src), y = ld_stream_v4(src + 16);
+                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
                     }
-                    sh.ref[warp][lane] = m_used == -INFINITY ? 0.0f : m_used;
-                    sh.aux[warp][lane] = alpha;
+                    if (clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+                    sts_v4(dst + swz0, w[0], w[1], w[2], w[3]);
+                    sts_v4(dst + swz1, w[4], w[5], w[6], w[7]);
+                } else {
+                    const uint32_t n = r.data != nullptr ? 16 : 0;
+                    const void* from = r.data != nullptr ? src : p.cache.base;
+                    copy16(dst + swz0, from, n);
+                    copy16(dst + swz1, r.data != nullptr ? src + 16 : p.cache.base, n);
                 }
+            }
+            for (int k0 = 0; k0 < fp8_chunks; k0 += kAhead) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int k = k0 + u, c = fp8_chunks - 1 - k;
+                    if (c < 0) break;
+                    const uint32_t b = ((c < 4 ? r.scales.x : r.scales.y) >> (8 * (c & 3))) & 0xFFu;
+                    uint32_t w[8];
+                    dequant16(raw[u], b, w);
+                    if (c - kAhead >= 0) raw[u] = load(k + kAhead);
+                    if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+                    if (!need(c / 2)) return false;
+                    const uint32_t dst = k_addr + c * kChunkBytes;
+                    sts_v4(dst + swz0, w[0], w[1], w[2], w[3]);
+                    sts_v4(dst + swz1, w[4], w[5], w[6], w[7]);
+                    if (c % 2 == 0 && c / 2 < ord.rope_from) {
+                        // the first hand-over of a unit covers its queries
+                        if ((flags & kFirst) && c / 2 == ord.rope_from - 1) copies_done();
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.full[c / 2]);
+                    }
+                }
+            }
+            if (ord.rope_from < ord.blocks) {
+                copies_done();
+                fence_async_smem();
                 __syncwarp();
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-                    // the previous tile's second product is done: s_ready came after it
-                    float a[NC];
+                if (lane == 0)
+                    for (int j = ord.rope_from; j < ord.blocks; ++j) mbar_arrive(&sh.full[j]);
+            }
+
+            // ---- the next tile's loads, in flight during the softmax
+            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
+            next_flags = sh.tile[nslot].flags;
+            next_known = true;
+            if (!(next_flags & (kDone | kEmpty))) start(sh.tile[nslot]);
+
+            // ---- softmax of the tile: this lane's row, NC columns
+            if (!wait_all(&sh.s_ready, step & 1)) return false;
+            tmem_fence_after();
+            float s[NC];
+            tmem_ld<NC>(lane_base, s);
+            bool ok = tl.row[srow].data != nullptr;
+            if (kSrc == kTokens) {
+                // every worker has handed over its share of the tile: its flags are there
+                if (!wait_all(&sh.full[0], step & 1)) return false;
+                if (ord.rope_from < ord.blocks && !wait_all(&sh.full[ord.blocks - 1], step & 1)) return false;
+                const int32_t pos = tl.pos + srow;
+                const bool bad = sh.row_bad[buf][srow];
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const bool see = ok && pos >= un.col_lo[group * NC + k] && pos <= un.col_hi[group * NC + k];
+                    s[k] = see ? (bad ? NAN : s[k]) : -INFINITY;
+                }
+            } else if (!__all_sync(0xFFFFFFFFu, ok)) {
+#pragma unroll
+                for (int k = 0; k < NC; ++k) s[k] = ok ? s[k] : -INFINITY;
+            }
+            float(&red)[4][16] = sh.red[group][exchange & 1];
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+                const float x0 = warp_max(s[k]), x1 = warp_max(s[k + 1]);
+                const float x2 = warp_max(s[k + 2]), x3 = warp_max(s[k + 3]);
+                if (lane == 0) *reinterpret_cast<float4*>(&red[quad][k]) = make_float4(x0, x1, x2, x3);
+            }
+            if (lane == 0) mbar_arrive(&sh.group_bar[group]);
+            if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+            ++exchange;
+            bool grow = false;
+            if (lane < NC) {
+                const float top = ls.scale_log2 * fmaxf(fmaxf(red[0][lane], red[1][lane]),
+                                                        fmaxf(red[2][lane], red[3][lane]));
+                float alpha = 1.0f;
+                if (top > m_used + kLazy) {
+                    alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
+                    grow = alpha != 1.0f;
+                    m_used = top;
+                }
+                sh.ref[warp][lane] = m_used == -INFINITY ? 0.0f : m_used;
+                sh.aux[warp][lane] = alpha;
+            }
+            __syncwarp();
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                // the previous tile's second product is done: s_ready came after it
+#pragma unroll
+                for (int k = 0; k < NC; ++k) l[k] *= sh.aux[warp][k];
+                for (int j = 0; j < ord.blocks; ++j) {
+                    float o[NC];
+                    tmem_ld<NC>(lane_base + N + j * N, o);
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) o[k] *= sh.aux[warp][k];
+                    tmem_st<NC>(lane_base + N + j * N, o);
+                }
+                tmem_wait_st();
+            }
+#pragma unroll
+            for (int k = 0; k < NC; k += 4) {
+                const float4 ref = *reinterpret_cast<const float4*>(&sh.ref[warp][k]);
+                s[k] = ex2_approx(fmaf(s[k], ls.scale_log2, -ref.x));
+                s[k + 1] = ex2_approx(fmaf(s[k + 1], ls.scale_log2, -ref.y));
+                s[k + 2] = ex2_approx(fmaf(s[k + 2], ls.scale_log2, -ref.z));
+                s[k + 3] = ex2_approx(fmaf(s[k + 3], ls.scale_log2, -ref.w));
+            }
+#pragma unroll
+            for (int k = 0; k < NC; ++k) l[k] += s[k];
+            // weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by side
+            if constexpr (NC >= 8) {
+#pragma unroll
+                for (int k = 0; k < NC; k += 8)
+                    sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
+                           pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
+                           pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
+            } else {
+                sts_v2(p_tile + (group / 2) * (kTile * 16) + srow * 16 + (group & 1) * 8,
+                       pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+            }
+            fence_async_smem();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_ready);
+            ++step;
+        }
+        if (!next_known) {
+            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
+            next_flags = sh.tile[nslot].flags;
+            if (!(next_flags & (kDone | kEmpty))) start(sh.tile[nslot]);
+        }
+        // the first product of this unit is done with its queries
+        if ((flags & kLast) && !(next_flags & (kDone | kEmpty)))
+            load_queries<N>(p, sh.unit[sh.tile[nslot].unit], q_tile, tid);
+        if (flags & kLast) {
+            // ---- the unit's sums: over the lanes, then over the group's four warps
+            float mine = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                float x = l[k];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+                if (lane == k) mine = x;
+            }
+            float(&red)[4][16] = sh.red[group][exchange & 1];
+            if (lane < NC) red[quad][lane] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.group_bar[group]);
+            if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+            ++exchange;
+            if (lane < NC) {
+                const float total = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+                const int n = group * NC + lane;
+                const int32_t t = un.col_token[n], h = un.col_head[n];
+                float inv = 1.0f;
+                if (t >= 0) {
+                    if (ls.splits > 1) {
+                        if (quad == 0) {
+                            float* ml = ls.part_ml + (((int64_t)t * p.num_heads + h) * ls.splits + un.part) * 2;
+                            ml[0] = m_used;
+                            ml[1] = total;
+                        }
+                    } else {
+                        const float ref = m_used == -INFINITY ? 0.0f : m_used;
+                        const float den = total + (p.sink ? ex2_approx(p.sink[h] * kLog2e - ref) : 0.0f);
+                        inv = total == 0.0f ? 0.0f : 1.0f / den;
+                        if (p.lse && quad == 0)
+                            p.lse[(int64_t)t * p.lse_stride_t + h] =
+                                total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                    }
+                }
+                sh.aux[warp][lane] = inv;
+            }
+            __syncwarp();
+            if (!(flags & kEmpty)) {
+                if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
+                tmem_fence_after();
+            }
+            for (int j = 0; j < ord.blocks; ++j) {
+                float o[NC];
+                if (!(flags & kEmpty)) {
+                    tmem_ld<NC>(lane_base + N + j * N, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                }
+                const int d = j * 128 + srow;
+                if (ls.splits > 1) {
 #pragma unroll
                     for (int k = 0; k < NC; ++k) {
-                        a[k] = sh.aux[warp][k];
-                        l[k] *= a[k];
-                    }
-                    for (int j = 0; j < blocks; ++j) {
-                        float o[NC];
-                        tmem_ld<NC>(lane_base + N + j * N + group * NC, o);
-#pragma unroll
-                        for (int k = 0; k < NC; ++k) o[k] *= a[k];
-                        tmem_st<NC>(lane_base + N + j * N + group * NC, o);
-                    }
-                    tmem_wait_st();
-                }
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    s[k] = ex2_approx(s[k] - sh.ref[warp][k]);
-                    l[k] += s[k];
-                }
-                // weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by side
-                if constexpr (NC >= 8) {
-#pragma unroll
-                    for (int k = 0; k < NC; k += 8)
-                        sts_v4(smem_u32(p_tile) + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
-                               pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
-                               pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
-                } else {
-                    sts_v2(smem_u32(p_tile) + (group / 2) * (kTile * 16) + srow * 16 + (group & 1) * 8,
-                           pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
-                }
-                fence_async_smem();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready);
-            }
-        }
-
-        // the unit's sums: over the lanes, then over the group's four warps
-        float mine = 0.0f;
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            float x = l[k];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-            if (lane == k) mine = x;
-        }
-        float(&red)[4][16] = sh.red[group][exchange & 1];
-        if (lane < NC) red[quad][lane] = mine;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-        if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-        ++exchange;
-        if (lane < NC) {
-            const float total = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-            const int n = group * NC + lane;
-            const int32_t t = un.col_token[n];
-            float inv = 1.0f;
-            if (t >= 0) {
-                const int32_t h = un.col_head[n];
-                if (ls.splits > 1) {
-                    if (quad == 0) {
-                        float* ml = ls.part_ml + (((int64_t)t * p.num_heads + h) * ls.splits + un.part) * 2;
-                        ml[0] = m_used;
-                        ml[1] = total;
+                        const int32_t t = un.col_token[group * NC + k], h = un.col_head[group * NC + k];
+                        if (t >= 0)
+                            ls.part_o[(((int64_t)t * p.num_heads + h) * ls.splits + un.part) * p.head_dim + d] = o[k];
                     }
                 } else {
-                    const float ref = m_used == -INFINITY ? 0.0f : m_used;
-                    const float den = total + (p.sink ? ex2_approx(p.sink[h] * kLog2e - ref) : 0.0f);
-                    inv = total == 0.0f ? 0.0f : 1.0f / den;
-                    if (p.lse && quad == 0)
-                        p.lse[(int64_t)t * p.lse_stride_t + h] =
-                            total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                    // 4 x 4 exchange among four lanes: each then holds four dims of one column
+#pragma unroll
+                    for (int k = 0; k < NC; k += 4) {
+                        const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k]);
+                        const bool odd = lane & 1, upper = lane & 2;
+                        const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
+                        const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
+                        const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
+                        const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
+                        const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
+                        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                        const int n = group * NC + k + (upper ? 2 : 0) + (odd ? 1 : 0);
+                        if (un.col_token[n] >= 0)
+                            st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
+                    }
                 }
             }
-            sh.aux[warp][lane] = inv;
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.unit_empty[tl.unit]);
         }
         __syncwarp();
-        if (ntiles > 0) {
-            if (!wait_all(&sh.freed[blocks - 1], (step - 1) & 1)) return false;
-            tmem_fence_after();
-        }
-        for (int j = 0; j < blocks; ++j) {
-            float o[NC];
-            if (ntiles > 0) {
-                tmem_ld<NC>(lane_base + N + j * N + group * NC, o);
-            } else {
-#pragma unroll
-                for (int k = 0; k < NC; ++k) o[k] = 0.0f;
-            }
-            const int d = j * 128 + srow;
-            if (ls.splits > 1) {
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const int32_t t = un.col_token[group * NC + k], h = un.col_head[group * NC + k];
-                    if (t >= 0)
-                        ls.part_o[(((int64_t)t * p.num_heads + h) * ls.splits + un.part) * p.head_dim + d] = o[k];
-                }
-            } else {
-                // two dims a store: even lanes take column k, odd lanes column k + 1
-#pragma unroll
-                for (int k = 0; k < NC; k += 2) {
-                    const float a = o[k] * sh.aux[warp][k], b = o[k + 1] * sh.aux[warp][k + 1];
-                    const bool odd = lane & 1;
-                    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
-                    const uint32_t w = odd ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
-                    const int n = group * NC + k + (odd ? 1 : 0);
-                    const int32_t t = un.col_token[n];
-                    if (t >= 0)
-                        *reinterpret_cast<uint32_t*>(p.out + (int64_t)t * p.out_stride_t +
-                                                     (int64_t)un.col_head[n] * p.out_stride_h + (d & ~1)) = w;
-                }
-            }
-        }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.unit_empty[seq & 1]);
+        if (lane == 0) mbar_arrive(&sh.tile_empty[slot]);
+        flags = next_flags;
     }
 }
 
@@ -676,11 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.unit_full[i], 1);
-            mbar_init(&sh.unit_empty[i], kWorkers + 1);
+            mbar_init(&sh.unit_empty[i], kWorkers);
         }
-        for (int i = 0; i < kMaxChunks; ++i) mbar_init(&sh.full[i], kWorkers);
-        for (int i = 0; i < kMaxChunks / 2; ++i) mbar_init(&sh.freed[i], 1);
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(&sh.tile_full[i], 1);
+            mbar_init(&sh.tile_empty[i], kWorkers + 1);
+        }
+        for (int i = 0; i < kMaxBlocks; ++i) {
+            mbar_init(&sh.full[i], kWorkers);
+            mbar_init(&sh.freed[i], 1);
+        }
         mbar_init(&sh.s_ready, 1);
         mbar_init(&sh.p_ready, kWorkers);
         mbar_init(&sh.drain, 1);
@@ -697,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool ok = true;
     if (warp < kWorkers) {
-        ok = work<N, kSrc>(p, ls, sh, k_tile, q_tile, p_tile, tmem);
+        ok = work<N, kSrc>(p, ls, sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
     } else if (warp == kPlanWarp) {
         ok = plan<kSrc>(p, ls, sh);
     } else if (lane == 0) {
