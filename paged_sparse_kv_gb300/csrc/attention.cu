@@ -18,10 +18,10 @@
 // tile that both products read: with the dims contiguous as the K-major A
 // operand of the first, as the M-major A operand of the second.
 //
-// Roles.  16 worker warps dequantise a tile, take the softmax of S^T and at the
+// Roles.  8 worker warps dequantise a tile, take the softmax of S^T and at the
 // end of a unit write O^T; one thread issues the MMAs; one warp plans ahead: it
-// finds the tiles that hold anything visible and puts the addresses and scales
-// of their rows into a ring, across units.  The tile is handed over in blocks of
+// finds the tiles that hold anything visible and puts the addresses of their
+// rows into a ring, across units.  The tile is handed over in blocks of
 // 128 dims: the first product follows the dequantisation block by block, and
 // the next tile is dequantised into the blocks the second product has finished
 // with.  The first loads of a tile are in flight during the softmax of the one
@@ -29,9 +29,9 @@
 // wall time, counted in psk_device_wait_timeouts).
 //
 // Softmax in one pass: a running reference m per column.  It follows the
-// maximum lazily, only when a tile's maximum lies more than 2^8 above it, so
-// that O^T is rescaled on few tiles and a weight is at most 2^8; the reference
-// cancels in out and in lse.  Sums and weights are binary32; the weights are
+// maximum lazily: the first tile sets it, and later ones raise it only where a
+// weight would exceed 2^16, so that O^T is hardly ever rescaled and the maxima
+// of most tiles are never formed; the reference cancels in out and in lse.  Sums and weights are binary32; the weights are
 // rounded to bf16 for the second product alone (the operands of one MMA share a
 // type, and a row's bf16 values do not fit fp16's range), while l sums them
 // unrounded, so that lse keeps binary32 accuracy and the roundings in out, being
@@ -47,7 +47,8 @@ namespace psk {
 namespace {
 
 constexpr int kTile = 128;            // rows of a tile (M of the first product)
-constexpr int kWorkers = 16;          // worker warps
+constexpr int kWorkers = 8;           // worker warps
+constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 32 rows
 constexpr int kMmaWarp = kWorkers;
 constexpr int kPlanWarp = kWorkers + 1;
 constexpr int kThreads = (kWorkers + 2) * kWarp;
@@ -56,7 +57,8 @@ constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;         // log2 units the maximum may run ahead of the reference
+constexpr float kLazy = 16.0f;        // log2 units the maximum may run ahead of the reference
+constexpr float kNone = -3.0e38f;     // reference of a column that has seen nothing
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_attn_wait_timeouts = 0;
@@ -68,15 +70,15 @@ struct Unit {
     int32_t part;                  // which part of the split work (row of the workspace)
     int32_t pad[3];
     int64_t col_q[kMaxCols];       // element offset of the column's query
-    int64_t col_out[kMaxCols];     // and of its output row
+    int64_t col_out[kMaxCols];     // and of its output row (of its part, where the work is split)
     int32_t col_token[kMaxCols];   // -1: column not in use
     int32_t col_head[kMaxCols];
     int32_t col_lo[kMaxCols], col_hi[kMaxCols];  // kTokens: positions the column sees
 };
 
 struct alignas(16) Row {
-    const uint8_t* data;  // null: the row does not exist or is not visible
-    uint2 scales;         // its UE8M0 bytes
+    const uint8_t* data;    // null: the row does not exist or is not visible
+    const uint8_t* scales;  // its UE8M0 bytes
 };
 
 constexpr int kFirst = 1, kLast = 2, kEmpty = 4, kDone = 8;
@@ -95,15 +97,16 @@ constexpr int kTiles = 3;  // tiles the planning warp may be ahead, the current 
 struct Shared {
     Tile tile[kTiles];
     Unit unit[2];
-    alignas(16) float red[4][2][4][16];  // [group][exchange parity][lane quarter][column]
-    alignas(16) float ref[kWorkers][16];
-    alignas(16) float aux[kWorkers][16];
+    alignas(16) float red[kGroups][2][4][kMaxCols / kGroups];  // [group][exchange parity][quad][column]
+    alignas(16) float ref[kWorkers][kMaxCols / kGroups];
+    alignas(16) float aux[kWorkers][kMaxCols / kGroups];
+    int32_t over[kGroups][2][4];
     uint64_t tile_full[kTiles], tile_empty[kTiles];
     uint64_t unit_empty[2];
     uint64_t full[kMaxBlocks];     // 128 dims of the tile are dequantised
     uint64_t freed[kMaxBlocks];    // the second product is done with them
     uint64_t s_ready, p_ready, drain;
-    uint64_t group_bar[4];
+    uint64_t group_bar[kGroups];
     uint32_t tmem;
     uint8_t row_bad[2][kTile];     // kTokens: the row holds a NaN or an infinity
 };
@@ -124,14 +127,6 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait_bounded(bar, parity, kWaitLimitNs);
     return __all_sync(0xFFFFFFFFu, ok);
 }
-
-// Blocks (128 dims) in the order both products take them: those with rope dims
-// first, since their copies take longest, then the others downwards.
-struct Order {
-    int blocks, rope_from;  // blocks >= rope_from hold rope dims
-    __device__ __forceinline__ explicit Order(const AttnParams& p)
-        : blocks(p.head_dim / 128), rope_from((p.head_dim - p.rope_dim) / 128) {}
-};
 
 // ---- the planning warp -------------------------------------------------------------
 
@@ -209,36 +204,28 @@ __device__ __forceinline__ bool tile_entries(const AttnParams& p, const Source& 
     return __any_sync(0xFFFFFFFFu, any);
 }
 
-// Fills `rows` with the addresses and scales of the entries.
+// Fills `rows` with the addresses of the entries' data and scales.
 template <int kSrc>
 __device__ __forceinline__ void tile_rows(const AttnParams& p, const Source& src, int32_t tile, int lane,
                                           const int32_t (&entry)[kRowsPerLane], Row* rows) {
-    const int32_t token_stride = p.head_dim + p.rope_dim, nsc = p.head_dim / 64;
-    Row r[kRowsPerLane];
+    const int32_t token_stride = p.head_dim + p.rope_dim;
 #pragma unroll
     for (int j = 0; j < kRowsPerLane; ++j) {
-        r[j] = Row{nullptr, make_uint2(0, 0)};
-        if (entry[j] < 0) continue;
-        const int32_t i = tile * kTile + j * kWarp + lane;
-        const AttnCache& c = kSrc == kIndexed && i >= p.split ? p.extra : p.cache;
-        int32_t page = entry[j], off;
-        if (kSrc == kIndexed)
-            page = div_block32(entry[j], c.block_size, c.shift, off);
-        else
-            div_block32(src.lo + i, c.block_size, c.shift, off);
-        const uint8_t* pg = c.base + (int64_t)page * c.page_stride;
-        r[j].data = pg + (int64_t)off * token_stride;
-        const uint8_t* sc = pg + (int64_t)c.block_size * token_stride + (int64_t)off * nsc;
-        if (nsc == 8) {
-            r[j].scales = ld_nc_v2(sc);
-        } else if (nsc == 4) {
-            r[j].scales.x = ld_nc_u32(sc);
-        } else {
-            r[j].scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
+        Row r{nullptr, nullptr};
+        if (entry[j] >= 0) {
+            const int32_t i = tile * kTile + j * kWarp + lane;
+            const AttnCache& c = kSrc == kIndexed && i >= p.split ? p.extra : p.cache;
+            int32_t page = entry[j], off;
+            if (kSrc == kIndexed)
+                page = div_block32(entry[j], c.block_size, c.shift, off);
+            else
+                div_block32(src.lo + i, c.block_size, c.shift, off);
+            const uint8_t* pg = c.base + (int64_t)page * c.page_stride;
+            r.data = pg + (int64_t)off * token_stride;
+            r.scales = pg + (int64_t)c.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
         }
+        rows[j * kWarp + lane] = r;
     }
-#pragma unroll
-    for (int j = 0; j < kRowsPerLane; ++j) rows[j * kWarp + lane] = r[j];
 }
 
 struct Stream {
@@ -295,12 +282,14 @@ __device__ __forceinline__ bool unit_slot(Shared& sh, const Stream& st) {
     return st.units < 2 || wait_all(&sh.unit_empty[st.units & 1], ((st.units >> 1) - 1) & 1);
 }
 
-__device__ __forceinline__ void set_column(const AttnParams& p, Unit& un, int c, int64_t t, int32_t h,
-                                           bool used, int32_t lo, int32_t hi) {
+__device__ __forceinline__ void set_column(const AttnParams& p, const LaunchShape& ls, Unit& un, int c,
+                                           int32_t part, int64_t t, int32_t h, bool used, int32_t lo,
+                                           int32_t hi) {
     un.col_token[c] = used ? (int32_t)t : -1;
     un.col_head[c] = h;
     un.col_q[c] = t * p.q_stride_t + h * p.q_stride_h;
-    un.col_out[c] = t * p.out_stride_t + h * p.out_stride_h;
+    un.col_out[c] = ls.splits > 1 ? ((t * p.num_heads + h) * ls.splits + part) * p.head_dim
+                                  : t * p.out_stride_t + h * p.out_stride_h;
     un.col_lo[c] = used ? lo : 0;
     un.col_hi[c] = used ? hi : -1;
 }
@@ -332,7 +321,8 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
             Unit& un = sh.unit[st.units & 1];
             if (lane == 0) un.part = part;
 #pragma unroll
-            for (int c = lane; c < kMaxCols; c += kWarp) set_column(p, un, c, t, h0 + c, c < heads, 0, 0);
+            for (int c = lane; c < kMaxCols; c += kWarp) 
+                set_column(p, ls, un, c, part, t, h0 + c, c < heads, 0, 0);
             if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
         } else {
             // a run of neighbouring tokens of one request is a unit
@@ -364,7 +354,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                     const int tok = a + c / p.num_heads;
                     const int32_t lo = __shfl_sync(0xFFFFFFFFu, x.lo, tok & 31);
                     const int32_t hi = __shfl_sync(0xFFFFFFFFu, x.hi, tok & 31);
-                    set_column(p, un, c, t0 + tok, c % p.num_heads, tok < b, lo, hi);
+                    set_column(p, ls, un, c, part, t0 + tok, c % p.num_heads, tok < b, lo, hi);
                 }
                 if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
             }
@@ -376,12 +366,25 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
 }
 
 // ---- the MMA thread ------------------------------------------------------------------
+//
+// Both products take the 128-dim blocks in one order: first those without rope
+// dims, from the last one down, then those with rope dims, whose copies take
+// longest.  The second product frees them from the last block down, the order
+// they are dequantised in.
 
-template <int N>
-__device__ bool issue(const AttnParams& p, Shared& sh, uint32_t k_tile, uint32_t q_tile,
-                      uint32_t p_tile, uint32_t tmem) {
-    const Order ord(p);
+template <int N, int D>
+__device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_tile, uint32_t p_tile,
+                      uint32_t tmem) {
+    constexpr int kBlocks = D / 128;
     constexpr uint32_t kS = umma_idesc(kTile, N, false), kO = umma_idesc(128, N, true);
+    // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart, 32 bytes a step of 16 dims
+    const uint64_t k_desc = umma_desc(k_tile, 16, 1024, kSwizzle128);
+    const uint64_t q_desc = umma_desc(q_tile, 16, 1024, kSwizzle128);
+    // A of the second product: M-major, 128-byte swizzle: 64-dim chunks kChunkBytes apart,
+    // 8-row groups 1024 bytes apart.  B: N-major, no swizzle: 8-column groups 2048 bytes
+    // apart, 8-row groups 128 bytes apart.
+    const uint64_t v_desc = umma_desc(k_tile, kChunkBytes, 1024, kSwizzle128);
+    const uint64_t p_desc = umma_desc(p_tile, 128, 2048, kSwizzleNone);
     uint32_t step = 0;
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles;
@@ -390,33 +393,25 @@ __device__ bool issue(const AttnParams& p, Shared& sh, uint32_t k_tile, uint32_t
         mbar_arrive(&sh.tile_empty[slot]);
         if (flags & kDone) return true;
         if (flags & kEmpty) continue;
-        // the blocks without rope dims are ready first
-        for (int i = 0; i < ord.blocks; ++i) {
-            const int j = i < ord.rope_from ? ord.rope_from - 1 - i : ord.blocks - 1 - (i - ord.rope_from);
+        for (int i = 0; i < kBlocks; ++i) {
+            const int j = i < rope_from ? rope_from - 1 - i : kBlocks - 1 - (i - rope_from);
             if (!mbar_wait_bounded(&sh.full[j], step & 1, kWaitLimitNs)) return false;
             tmem_fence_after();
-            // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart, 32 bytes a step
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = 2 * j + k / 4;
-                umma_bf16(tmem, umma_desc(k_tile + c * kChunkBytes + (k % 4) * 32, 16, 1024, kSwizzle128),
-                          umma_desc(q_tile + c * (N * 128) + (k % 4) * 32, 16, 1024, kSwizzle128), kS,
+            for (int k = 0; k < 8; ++k)
+                umma_bf16(tmem, k_desc + ((j * 2 * kChunkBytes + (k / 4) * kChunkBytes + (k % 4) * 32) >> 4),
+                          q_desc + ((j * 2 * (N * 128) + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), kS,
                           i > 0 || k > 0);
-            }
         }
         umma_commit(&sh.s_ready);
         if (!mbar_wait_bounded(&sh.p_ready, step & 1, kWaitLimitNs)) return false;
         tmem_fence_after();
-        for (int j = ord.blocks - 1; j >= 0; --j) {
-            // A: M-major, 128-byte swizzle: 64-dim chunks kChunkBytes apart, 8-row groups
-            // 1024 bytes apart.  B: N-major, no swizzle: 8-column groups 2048 bytes
-            // apart, 8-row groups 128 bytes apart.
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-                umma_bf16(tmem + N + j * N,
-                          umma_desc(k_tile + j * 2 * kChunkBytes + k * 2048, kChunkBytes, 1024, kSwizzle128),
-                          umma_desc(p_tile + k * 256, 128, 2048, kSwizzleNone), kO,
-                          !(flags & kFirst) || k > 0);
+                umma_bf16(tmem + N + j * N, v_desc + ((j * 2 * kChunkBytes + k * 2048) >> 4),
+                          p_desc + ((k * 256) >> 4), kO, !(flags & kFirst) || k > 0);
             umma_commit(&sh.freed[j]);
         }
         ++step;
@@ -439,29 +434,29 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// 16 E4M3 bytes of UE8M0 scale byte b as eight bf16 pairs, by the rule of the
+// 32 E4M3 bytes of UE8M0 scale byte b as sixteen bf16 pairs, by the rule of the
 // gather: the product with a power of two, rounded to bf16 once.  One packed
 // multiply by 2^(120 + b - 127) does it where that factor is a bf16 number
 // (b <= 134: values up to 448 * 2^7); a larger scale takes a second one (both
 // exact but for an overflow).  A NaN code goes through the converter.
-__device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8]) {
-    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ void dequant32(const uint4 (&raw)[2], uint32_t b, uint32_t (&w)[16]) {
+    const uint32_t in[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
     const uint32_t f = (b <= 134u ? b + 120u : 247u) * 0x00800080u;
     uint32_t nan = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
         w[2 * i] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x1404)), f);
         w[2 * i + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x3424)), f);
     }
     if (b > 134u) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
+        for (int i = 0; i < 16; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
     }
     if (nan & 0x80808080u) {
         const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
             w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
         }
@@ -490,59 +485,101 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;
 
 // Queries of a unit into the swizzled B tile of the first product; unused
 // columns are zero.  Asynchronous.
-template <int N>
+template <int N, int D>
 __device__ __forceinline__ void load_queries(const AttnParams& p, const Unit& un, uint32_t q_tile, int tid) {
-    const int shift = p.head_dim == 512 ? 3 : p.head_dim == 256 ? 2 : 1;  // log2 of the 64-dim chunks
-#pragma unroll 4
-    for (int i = tid; i < (N * 8) << shift; i += kWorkers * kWarp) {
-        const int part = i & 7, c = (i >> 3) & ((1 << shift) - 1), n = i >> (3 + shift);
-        copy16(q_tile + c * (N * 128) + n * 128 + ((part ^ (n & 7)) * 16), p.q + un.col_q[n] * (un.col_token[n] >= 0) + c * 64 + part * 8,
-               un.col_token[n] >= 0 ? 16 : 0);
+    const int part = tid & 7;
+#pragma unroll
+    for (int n0 = 0; n0 < N; n0 += kWorkers * kWarp / 8) {
+        const int n = n0 + (tid >> 3);
+        if (n >= N) break;
+        const bool used = un.col_token[n] >= 0;
+        const uint16_t* src = used ? p.q + un.col_q[n] + part * 8 : p.q;
+        const uint32_t dst = q_tile + n * 128 + ((part ^ (n & 7)) * 16);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) copy16(dst + c * (N * 128), used ? src + c * 64 : src, used ? 16 : 0);
     }
 }
 
-constexpr int kAhead = 4;  // E4M3 chunks of a row quarter in flight per thread
+// Sum of v[k] over the 32 lanes: lane i gets the sum of column i % K.  Halves the
+// columns a lane holds at each exchange (K - 1 shuffles instead of 5 K).
+template <int K>
+__device__ __forceinline__ float column_sums(float (&v)[K], int lane) {
+#pragma unroll
+    for (int w = K / 2; w >= 1; w /= 2) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float send = up ? v[i] : v[i + w];
+            v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+        }
+    }
+    float x = v[0];
+#pragma unroll
+    for (int o = K; o < kWarp; o *= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
 
-template <int N, int kSrc>
+constexpr int kAhead = 4;  // 64-dim E4M3 chunks of a row half in flight per thread
+
+template <int N, int kSrc, int D>
 __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint32_t k_tile,
                      uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
-    constexpr int NC = N / 4;  // columns of a worker warp
+    constexpr int NC = N / kGroups;  // columns of a worker warp
+    constexpr int kChunks = D / 64, kBlocks = D / 128;
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     const int quad = warp % 4, group = warp / 4;
-    const int row = tid / 4, quarter = tid % 4;        // dequantisation: 16 dims of a row's chunk
+    const int row = tid / 2, half = tid % 2;           // dequantisation: 32 dims of a row's chunk
     const int srow = quad * kWarp + lane;              // softmax: the tile row of this lane
-    const Order ord(p);
-    const int nope = p.head_dim - p.rope_dim, fp8_chunks = nope / 64, chunks = p.head_dim / 64;
+    const int nope = D - p.rope_dim, fp8_chunks = nope / 64;
+    const int rope_from = nope / 128;                  // blocks from here on hold rope dims
     const uint32_t k_addr = k_tile + row * 128;
-    const uint32_t swz0 = ((2 * quarter) ^ (row & 7)) * 16, swz1 = ((2 * quarter + 1) ^ (row & 7)) * 16;
+    uint32_t swz[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) swz[i] = ((4 * half + i) ^ (row & 7)) * 16;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * kWarp) << 16) + group * NC;
     uint32_t step = 0, exchange = 0;
 
     float l[NC];
     float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
-    uint4 raw[kAhead];         // chunks fp8_chunks - 1, - 2, ... of the row
-    Row r{nullptr, make_uint2(0, 0)};
+    uint4 raw[kAhead][2];      // chunks fp8_chunks - 1, - 2, ... of the row
+    const uint8_t* data = nullptr;
+    uint2 scales = make_uint2(0, 0);
 
-    const auto load = [&](int k) {  // the k-th chunk in that order
-        return r.data != nullptr ? ld_stream_v4(r.data + (fp8_chunks - 1 - k) * 64 + quarter * 16)
-                                 : make_uint4(0, 0, 0, 0);
+    const auto load = [&](uint4(&x)[2], int k) {  // the k-th chunk in that order
+        x[0] = x[1] = make_uint4(0, 0, 0, 0);
+        if (data != nullptr) {
+            const uint8_t* src = data + (fp8_chunks - 1 - k) * 64 + half * 32;
+            x[0] = ld_stream_v4(src);
+            x[1] = ld_stream_v4(src + 16);
+        }
     };
     // takes the next tile's row and starts its first loads
     const auto start = [&](const Tile& t) {
-        r = t.row[row];
+        const Row r = t.row[row];
+        data = r.data;
+        scales = make_uint2(0, 0);
+        if (data != nullptr) {
+            if (D == 512) {
+                scales = ld_nc_v2(r.scales);
+            } else if (D == 256) {
+                scales.x = ld_nc_u32(r.scales);
+            } else {
+                scales.x = ld_nc_u8(r.scales) | (ld_nc_u8(r.scales + 1) << 8);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (k < fp8_chunks) raw[k] = load(k);
+            if (k < fp8_chunks) load(raw[k], k);
     };
 
     if (!wait_all(&sh.tile_full[0], 0)) return false;
     int32_t flags = sh.tile[0].flags;
     if (!(flags & (kDone | kEmpty))) {
-        load_queries<N>(p, sh.unit[sh.tile[0].unit], q_tile, tid);
+        load_queries<N, D>(p, sh.unit[sh.tile[0].unit], q_tile, tid);
         start(sh.tile[0]);
     }
     for (int seq = 0;; ++seq) {
-        const int slot = seq % kTiles;
+        const int slot = seq % kTiles, nslot = (seq + 1) % kTiles;
         const Tile& tl = sh.tile[slot];
         const Unit& un = sh.unit[tl.unit];
         if (flags & kDone) return true;
@@ -551,90 +588,88 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             for (int i = 0; i < NC; ++i) l[i] = 0.0f;
             m_used = -INFINITY;
         }
-        const int nslot = (seq + 1) % kTiles;
-        int32_t next_flags = 0;
-        bool next_known = false;
         if (!(flags & kEmpty)) {
             const int buf = step & 1;
             if (kSrc == kTokens) {
-                if (quarter == 0) sh.row_bad[buf][row] = 0;
+                if (half == 0) sh.row_bad[buf][row] = 0;
                 __syncwarp();
             }
-            // ---- dequantisation, block by block from the last dims down
-            int block = ord.blocks;  // blocks >= block are free
+            // ---- dequantisation, from the last chunk down
+            int block = kBlocks;  // blocks from here on are free
             const auto need = [&](int j) {
-                if (step > 0 && j < block && !wait_all(&sh.freed[j], (step - 1) & 1)) return false;
-                block = j < block ? j : block;
-                return true;
+                if (j >= block) return true;
+                block = j;
+                return step == 0 || wait_all(&sh.freed[j], (step - 1) & 1);
             };
-            for (int c = chunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
+            for (int c = kChunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
                 if (!need(c / 2)) return false;
                 const uint32_t dst = k_addr + c * kChunkBytes;
-                const uint8_t* src = r.data + nope + (c * 64 - nope) * 2 + quarter * 32;
+                const uint8_t* src = data == nullptr ? p.cache.base : data + nope + (c * 64 - nope) * 2 + half * 64;
                 if (kSrc == kTokens) {
-                    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (r.data != nullptr) {
-                        const uint4 x = ld_stream_v4(src), y = ld_stream_v4(src + 16);
-                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                        w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-                    }
-                    if (clear_non_finite(w)) sh.row_bad[buf][row] = 1;
-                    sts_v4(dst + swz0, w[0], w[1], w[2], w[3]);
-                    sts_v4(dst + swz1, w[4], w[5], w[6], w[7]);
-                } else {
-                    const uint32_t n = r.data != nullptr ? 16 : 0;
-                    const void* from = r.data != nullptr ? src : p.cache.base;
-                    copy16(dst + swz0, from, n);
-                    copy16(dst + swz1, r.data != nullptr ? src + 16 : p.cache.base, n);
-                }
-            }
-            for (int k0 = 0; k0 < fp8_chunks; k0 += kAhead) {
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int k = k0 + u, c = fp8_chunks - 1 - k;
-                    if (c < 0) break;
-                    const uint32_t b = ((c < 4 ? r.scales.x : r.scales.y) >> (8 * (c & 3))) & 0xFFu;
-                    uint32_t w[8];
-                    dequant16(raw[u], b, w);
-                    if (c - kAhead >= 0) raw[u] = load(k + kAhead);
-                    if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
-                    if (!need(c / 2)) return false;
-                    const uint32_t dst = k_addr + c * kChunkBytes;
-                    sts_v4(dst + swz0, w[0], w[1], w[2], w[3]);
-                    sts_v4(dst + swz1, w[4], w[5], w[6], w[7]);
-                    if (c % 2 == 0 && c / 2 < ord.rope_from) {
-                        // the first hand-over of a unit covers its queries
-                        if ((flags & kFirst) && c / 2 == ord.rope_from - 1) copies_done();
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.full[c / 2]);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4] = {0, 0, 0, 0};
+                        if (data != nullptr) {
+                            const uint4 x = ld_stream_v4(src + i * 16);
+                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        }
+                        if (clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+                        sts_v4(dst + swz[i], w[0], w[1], w[2], w[3]);
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        copy16(dst + swz[i], data == nullptr ? src : src + i * 16, data == nullptr ? 0 : 16);
                 }
             }
-            if (ord.rope_from < ord.blocks) {
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                const int c = fp8_chunks - 1 - k;
+                if (c < 0) break;
+                const uint32_t b = ((c < 4 ? scales.x : scales.y) >> (8 * (c & 3))) & 0xFFu;
+                uint32_t w[16];
+                dequant32(raw[k % kAhead], b, w);
+                if (c - kAhead >= 0) load(raw[k % kAhead], k + kAhead);
+                if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+                if (!need(c / 2)) return false;
+                const uint32_t dst = k_addr + c * kChunkBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sts_v4(dst + swz[i], w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (c % 2 == 0 && c / 2 < rope_from) {
+                    // the first hand-over of a unit covers its queries
+                    if ((flags & kFirst) && c / 2 == rope_from - 1) copies_done();
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.full[c / 2]);
+                }
+            }
+            if (rope_from < kBlocks) {
                 copies_done();
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    for (int j = ord.rope_from; j < ord.blocks; ++j) mbar_arrive(&sh.full[j]);
+                    for (int j = rope_from; j < kBlocks; ++j) mbar_arrive(&sh.full[j]);
             }
+        }
+        // ---- the next tile's loads, in flight during the softmax
+        if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
+        const int32_t next_flags = sh.tile[nslot].flags;
+        const bool next_rows = !(next_flags & (kDone | kEmpty));
+        if (next_rows) start(sh.tile[nslot]);
 
-            // ---- the next tile's loads, in flight during the softmax
-            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
-            next_flags = sh.tile[nslot].flags;
-            next_known = true;
-            if (!(next_flags & (kDone | kEmpty))) start(sh.tile[nslot]);
-
+        if (!(flags & kEmpty)) {
             // ---- softmax of the tile: this lane's row, NC columns
+            const int buf = step & 1;
             if (!wait_all(&sh.s_ready, step & 1)) return false;
             tmem_fence_after();
             float s[NC];
             tmem_ld<NC>(lane_base, s);
-            bool ok = tl.row[srow].data != nullptr;
+            const bool ok = tl.row[srow].data != nullptr;
             if (kSrc == kTokens) {
                 // every worker has handed over its share of the tile: its flags are there
                 if (!wait_all(&sh.full[0], step & 1)) return false;
-                if (ord.rope_from < ord.blocks && !wait_all(&sh.full[ord.blocks - 1], step & 1)) return false;
+                if (rope_from < kBlocks && !wait_all(&sh.full[kBlocks - 1], step & 1)) return false;
                 const int32_t pos = tl.pos + srow;
                 const bool bad = sh.row_bad[buf][srow];
 #pragma unroll
@@ -646,63 +681,86 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 #pragma unroll
                 for (int k = 0; k < NC; ++k) s[k] = ok ? s[k] : -INFINITY;
             }
-            float(&red)[4][16] = sh.red[group][exchange & 1];
+            // The reference of a column only has to lie near its maximum: it is set by
+            // the first tile and raised where a score lies far above it, which the
+            // group's four warps have to agree on.
+            bool raise = flags & kFirst;
+            float* ref = sh.ref[warp];
+            if (!raise) {
+                float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-                const float x0 = warp_max(s[k]), x1 = warp_max(s[k + 1]);
-                const float x2 = warp_max(s[k + 2]), x3 = warp_max(s[k + 3]);
-                if (lane == 0) *reinterpret_cast<float4*>(&red[quad][k]) = make_float4(x0, x1, x2, x3);
-            }
-            if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-            if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-            ++exchange;
-            bool grow = false;
-            if (lane < NC) {
-                const float top = ls.scale_log2 * fmaxf(fmaxf(red[0][lane], red[1][lane]),
-                                                        fmaxf(red[2][lane], red[3][lane]));
-                float alpha = 1.0f;
-                if (top > m_used + kLazy) {
-                    alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
-                    grow = alpha != 1.0f;
-                    m_used = top;
+                for (int k = 0; k < NC; k += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(&ref[k]);
+                    top = fmaxf(top, fmaf(s[k], ls.scale_log2, -m.x));
+                    top = fmaxf(top, fmaf(s[k + 1], ls.scale_log2, -m.y));
+                    top = fmaxf(top, fmaf(s[k + 2], ls.scale_log2, -m.z));
+                    top = fmaxf(top, fmaf(s[k + 3], ls.scale_log2, -m.w));
                 }
-                sh.ref[warp][lane] = m_used == -INFINITY ? 0.0f : m_used;
-                sh.aux[warp][lane] = alpha;
-            }
-            __syncwarp();
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-                // the previous tile's second product is done: s_ready came after it
-#pragma unroll
-                for (int k = 0; k < NC; ++k) l[k] *= sh.aux[warp][k];
-                for (int j = 0; j < ord.blocks; ++j) {
-                    float o[NC];
-                    tmem_ld<NC>(lane_base + N + j * N, o);
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) o[k] *= sh.aux[warp][k];
-                    tmem_st<NC>(lane_base + N + j * N, o);
+                const bool over = __any_sync(0xFFFFFFFFu, top > kLazy);
+                int32_t(&flag)[4] = sh.over[group][exchange & 1];
+                if (lane == 0) {
+                    flag[quad] = over;
+                    mbar_arrive(&sh.group_bar[group]);
                 }
-                tmem_wait_st();
+                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+                ++exchange;
+                raise = flag[0] | flag[1] | flag[2] | flag[3];
             }
+            if (raise) {
+                float* red = sh.red[group][exchange & 1][quad];
 #pragma unroll
-            for (int k = 0; k < NC; k += 4) {
-                const float4 ref = *reinterpret_cast<const float4*>(&sh.ref[warp][k]);
-                s[k] = ex2_approx(fmaf(s[k], ls.scale_log2, -ref.x));
-                s[k + 1] = ex2_approx(fmaf(s[k + 1], ls.scale_log2, -ref.y));
-                s[k + 2] = ex2_approx(fmaf(s[k + 2], ls.scale_log2, -ref.z));
-                s[k + 3] = ex2_approx(fmaf(s[k + 3], ls.scale_log2, -ref.w));
+                for (int k = 0; k < NC; k += 4) {
+                    const float x0 = warp_max(s[k]), x1 = warp_max(s[k + 1]);
+                    const float x2 = warp_max(s[k + 2]), x3 = warp_max(s[k + 3]);
+                    if (lane == 0) *reinterpret_cast<float4*>(&red[k]) = make_float4(x0, x1, x2, x3);
+                }
+                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
+                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+                if (lane < NC) {
+                    const float(&all)[4][kMaxCols / kGroups] = sh.red[group][exchange & 1];
+                    const float top = ls.scale_log2 * fmaxf(fmaxf(all[0][lane], all[1][lane]),
+                                                            fmaxf(all[2][lane], all[3][lane]));
+                    float alpha = 1.0f;
+                    if (top > m_used) {
+                        alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
+                        m_used = top;
+                    }
+                    ref[lane] = m_used == -INFINITY ? kNone : m_used;
+                    sh.aux[warp][lane] = alpha;
+                }
+                ++exchange;
+                __syncwarp();
+                if (!(flags & kFirst)) {
+                    // the previous tile's second product is done: s_ready came after it
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) l[k] *= sh.aux[warp][k];
+                    for (int j = 0; j < kBlocks; ++j) {
+#pragma unroll
+                        for (int k0 = 0; k0 < NC; k0 += 8) {
+                            float o[8];
+                            tmem_ld<8>(lane_base + N + j * N + k0, o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] *= sh.aux[warp][k0 + k];
+                            tmem_st8(lane_base + N + j * N + k0, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
             }
-#pragma unroll
-            for (int k = 0; k < NC; ++k) l[k] += s[k];
             // weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by side
-            if constexpr (NC >= 8) {
 #pragma unroll
-                for (int k = 0; k < NC; k += 8)
-                    sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
-                           pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
-                           pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
-            } else {
-                sts_v2(p_tile + (group / 2) * (kTile * 16) + srow * 16 + (group & 1) * 8,
-                       pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+            for (int k = 0; k < NC; k += 8) {
+                const float4 m0 = *reinterpret_cast<const float4*>(&ref[k]);
+                const float4 m1 = *reinterpret_cast<const float4*>(&ref[k + 4]);
+                const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[k + i] = ex2_approx(fmaf(s[k + i], ls.scale_log2, -m[i]));
+                    l[k + i] += s[k + i];
+                }
+                sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
+                       pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
+                       pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
             }
             fence_async_smem();
             tmem_fence_before();
@@ -710,25 +768,12 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             if (lane == 0) mbar_arrive(&sh.p_ready);
             ++step;
         }
-        if (!next_known) {
-            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
-            next_flags = sh.tile[nslot].flags;
-            if (!(next_flags & (kDone | kEmpty))) start(sh.tile[nslot]);
-        }
-        // the first product of this unit is done with its queries
-        if ((flags & kLast) && !(next_flags & (kDone | kEmpty)))
-            load_queries<N>(p, sh.unit[sh.tile[nslot].unit], q_tile, tid);
         if (flags & kLast) {
+            // the first product of this unit is done with its queries
+            if (next_rows) load_queries<N, D>(p, sh.unit[sh.tile[nslot].unit], q_tile, tid);
             // ---- the unit's sums: over the lanes, then over the group's four warps
-            float mine = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                float x = l[k];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-                if (lane == k) mine = x;
-            }
-            float(&red)[4][16] = sh.red[group][exchange & 1];
+            const float mine = column_sums<NC>(l, lane);
+            float(&red)[4][kMaxCols / kGroups] = sh.red[group][exchange & 1];
             if (lane < NC) red[quad][lane] = mine;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.group_bar[group]);
@@ -747,12 +792,12 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                             ml[1] = total;
                         }
                     } else {
-                        const float ref = m_used == -INFINITY ? 0.0f : m_used;
-                        const float den = total + (p.sink ? ex2_approx(p.sink[h] * kLog2e - ref) : 0.0f);
+                        const float m = m_used == -INFINITY ? 0.0f : m_used;
+                        const float den = total + (p.sink ? ex2_approx(p.sink[h] * kLog2e - m) : 0.0f);
                         inv = total == 0.0f ? 0.0f : 1.0f / den;
                         if (p.lse && quad == 0)
                             p.lse[(int64_t)t * p.lse_stride_t + h] =
-                                total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                                total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
                     }
                 }
                 sh.aux[warp][lane] = inv;
@@ -762,37 +807,39 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
                 tmem_fence_after();
             }
-            for (int j = 0; j < ord.blocks; ++j) {
-                float o[NC];
-                if (!(flags & kEmpty)) {
-                    tmem_ld<NC>(lane_base + N + j * N, o);
-                } else {
+            for (int j = 0; j < kBlocks; ++j) {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
-                }
-                const int d = j * 128 + srow;
-                if (ls.splits > 1) {
+                for (int k0 = 0; k0 < NC; k0 += 8) {
+                    float o[8];
+                    if (!(flags & kEmpty)) {
+                        tmem_ld<8>(lane_base + N + j * N + k0, o);
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const int32_t t = un.col_token[group * NC + k], h = un.col_head[group * NC + k];
-                        if (t >= 0)
-                            ls.part_o[(((int64_t)t * p.num_heads + h) * ls.splits + un.part) * p.head_dim + d] = o[k];
+                        for (int k = 0; k < 8; ++k) o[k] = 0.0f;
                     }
-                } else {
-                    // 4 x 4 exchange among four lanes: each then holds four dims of one column
+                    const int d = j * 128 + srow;
+                    if (ls.splits > 1) {
 #pragma unroll
-                    for (int k = 0; k < NC; k += 4) {
-                        const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k]);
-                        const bool odd = lane & 1, upper = lane & 2;
-                        const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
-                        const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
-                        const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
-                        const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
-                        const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
-                        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
-                        const int n = group * NC + k + (upper ? 2 : 0) + (odd ? 1 : 0);
-                        if (un.col_token[n] >= 0)
-                            st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
+                        for (int k = 0; k < 8; ++k) {
+                            const int n = group * NC + k0 + k;
+                            if (un.col_token[n] >= 0) ls.part_o[un.col_out[n] + d] = o[k];
+                        }
+                    } else {
+                        // 4 x 4 exchange among four lanes: each then holds four dims of one column
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k0 + k]);
+                            const bool odd = lane & 1, upper = lane & 2;
+                            const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
+                            const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
+                            const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
+                            const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
+                            const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
+                            const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                            const int n = group * NC + k0 + k + (lane & 1) + (lane & 2);
+                            if (un.col_token[n] >= 0)
+                                st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
+                        }
                     }
                 }
             }
@@ -813,15 +860,14 @@ size_t smem_bytes(int n, int head_dim) {
            (size_t)n / 8 * kTile * 16 + sizeof(Shared);
 }
 
-template <int N, int kSrc>
+template <int N, int kSrc, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ LaunchShape ls) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((kAlign - (smem_u32(smem_raw) & (kAlign - 1))) & (kAlign - 1));
-    const int chunks = p.head_dim / 64;
     uint8_t* k_tile = base;
-    uint8_t* q_tile = k_tile + chunks * kChunkBytes;
-    uint8_t* p_tile = q_tile + chunks * (N * 128);
+    uint8_t* q_tile = k_tile + D / 64 * kChunkBytes;
+    uint8_t* p_tile = q_tile + D / 64 * (N * 128);
     Shared& sh = *reinterpret_cast<Shared*>(p_tile + N / 8 * kTile * 16);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
@@ -840,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.s_ready, 1);
         mbar_init(&sh.p_ready, kWorkers);
         mbar_init(&sh.drain, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&sh.group_bar[i], 4);
+        for (int i = 0; i < kGroups; ++i) mbar_init(&sh.group_bar[i], 4);
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(&sh.tmem, ls.tmem_cols);
@@ -853,11 +899,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool ok = true;
     if (warp < kWorkers) {
-        ok = work<N, kSrc>(p, ls, sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
+        ok = work<N, kSrc, D>(p, ls, sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
     } else if (warp == kPlanWarp) {
         ok = plan<kSrc>(p, ls, sh);
     } else if (lane == 0) {
-        ok = issue<N>(p, sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
+        ok = issue<N, D>(sh, (D - p.rope_dim) / 128, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
         if (!ok) {  // wait for the MMAs in flight before the operands go
             umma_commit(&sh.drain);
             mbar_wait_bounded(&sh.drain, 0, kWaitLimitNs);
@@ -954,20 +1000,26 @@ int64_t part_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int3
     return splits <= 1 ? 0 : num_tokens * num_heads * splits * (head_dim + 4) * (int64_t)sizeof(float);
 }
 
-template <int N, int kSrc>
+template <int N, int kSrc, int D>
 cudaError_t launch(const AttnParams& p, const LaunchShape& ls, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_smem_limit_per_device(attention_kernel<N, kSrc>, (int)smem_bytes(N, 512), done);
+    const int smem = (int)smem_bytes(N, D);
+    const cudaError_t e = set_smem_limit_per_device(attention_kernel<N, kSrc, D>, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = ls.units < sm_count() ? ls.units : sm_count();
-    return launch_pdl(attention_kernel<N, kSrc>, dim3((unsigned)grid), dim3(kThreads), smem_bytes(N, p.head_dim),
-                      stream, p, ls);
+    return launch_pdl(attention_kernel<N, kSrc, D>, dim3((unsigned)grid), dim3(kThreads), smem, stream, p, ls);
+}
+
+template <int kSrc, int D>
+cudaError_t launch_n(const AttnParams& p, const Plan& pl, cudaStream_t stream) {
+    return pl.n == 16 ? launch<16, kSrc, D>(p, pl.ls, stream)
+                      : pl.n == 32 ? launch<32, kSrc, D>(p, pl.ls, stream) : launch<64, kSrc, D>(p, pl.ls, stream);
 }
 
 template <int kSrc>
-cudaError_t launch_n(const AttnParams& p, const Plan& pl, cudaStream_t stream) {
-    return pl.n == 16 ? launch<16, kSrc>(p, pl.ls, stream)
-                      : pl.n == 32 ? launch<32, kSrc>(p, pl.ls, stream) : launch<64, kSrc>(p, pl.ls, stream);
+cudaError_t launch_d(const AttnParams& p, const Plan& pl, cudaStream_t stream) {
+    return p.head_dim == 512 ? launch_n<kSrc, 512>(p, pl, stream)
+                             : p.head_dim == 256 ? launch_n<kSrc, 256>(p, pl, stream) : launch_n<kSrc, 128>(p, pl, stream);
 }
 
 cudaError_t run(AttnParams p, int64_t max_keys, bool indexed, cudaStream_t stream) {
@@ -977,9 +1029,9 @@ cudaError_t run(AttnParams p, int64_t max_keys, bool indexed, cudaStream_t strea
     pl.ls.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
     pl.ls.part_o = static_cast<float*>(p.workspace);
     pl.ls.part_ml = pl.ls.part_o + p.num_tokens * p.num_heads * pl.ls.splits * p.head_dim;
-    cudaError_t e = pl.src == kIndexed ? launch_n<kIndexed>(p, pl, stream)
-                    : pl.src == kOneToken ? launch_n<kOneToken>(p, pl, stream)
-                                          : launch_n<kTokens>(p, pl, stream);
+    cudaError_t e = pl.src == kIndexed ? launch_d<kIndexed>(p, pl, stream)
+                    : pl.src == kOneToken ? launch_d<kOneToken>(p, pl, stream)
+                                          : launch_d<kTokens>(p, pl, stream);
     if (e != cudaSuccess || pl.ls.splits == 1) return e;
     return launch_pdl(attention_join_kernel, dim3((unsigned)(p.num_tokens * p.num_heads)), dim3(128),
                       (size_t)pl.ls.splits * 2 * sizeof(float), stream, p, pl.ls);
