@@ -71,6 +71,7 @@ struct Unit {
     int32_t pad[3];
     int64_t col_q[kMaxCols];       // element offset of the column's query
     int64_t col_out[kMaxCols];     // and of its output row (of its part, where the work is split)
+    float col_sink[kMaxCols];      // log2 units; -infinity without one
     int32_t col_token[kMaxCols];   // -1: column not in use
     int32_t col_head[kMaxCols];
     int32_t col_lo[kMaxCols], col_hi[kMaxCols];  // kTokens: positions the column sees
@@ -108,6 +109,7 @@ struct Shared {
     uint64_t s_ready, p_ready, drain;
     uint64_t group_bar[kGroups];
     uint32_t tmem;
+    uint2 scales[2][kTile];        // UE8M0 bytes of the rows
     uint8_t row_bad[2][kTile];     // kTokens: the row holds a NaN or an infinity
 };
 
@@ -166,17 +168,16 @@ __device__ __forceinline__ void share(int32_t n, int32_t part, int32_t parts, in
 struct Source {
     int64_t token;           // index form
     int32_t req, lo, hi;     // position form
+    int32_t base;            // logical page of the table row's first entry
 };
 
 constexpr int kRowsPerLane = kTile / kWarp;
 
-// Cache entries of a tile's rows lane, lane + 32, ...: slots (index form) or
-// pages, -1 for none.  True if any row of the tile has one.
+// What a tile's rows lane, lane + 32, ... are looked up in: slots (index form) or
+// pages, -1 past the end.  The loads are left in flight.
 template <int kSrc>
-__device__ __forceinline__ bool tile_entries(const AttnParams& p, const Source& src, int32_t tile, int lane,
-                                             int32_t (&entry)[kRowsPerLane]) {
-    bool any = false;
-    int32_t x[kRowsPerLane];
+__device__ __forceinline__ void tile_lookup(const AttnParams& p, const Source& src, int32_t tile, int lane,
+                                            int32_t (&x)[kRowsPerLane]) {
 #pragma unroll
     for (int j = 0; j < kRowsPerLane; ++j) {
         x[j] = -1;
@@ -187,19 +188,26 @@ __device__ __forceinline__ bool tile_entries(const AttnParams& p, const Source& 
             const int64_t pos = src.lo + i;
             if (pos <= src.hi) {
                 int32_t off;
-                const int32_t logical = div_block32((int32_t)pos, p.cache.block_size, p.cache.shift, off) -
-                                        (p.base_off ? p.base_off[src.req] : 0);
+                const int32_t logical =
+                    div_block32((int32_t)pos, p.cache.block_size, p.cache.shift, off) - src.base;
                 if (logical >= 0 && logical < p.bt_width) x[j] = p.bt[(int64_t)src.req * p.bt_stride + logical];
             }
         }
     }
+}
+
+// The entries among them that exist, the others -1.  True if any row has one.
+template <int kSrc>
+__device__ __forceinline__ bool tile_entries(const AttnParams& p, int32_t tile, int lane,
+                                             int32_t (&x)[kRowsPerLane]) {
+    bool any = false;
 #pragma unroll
     for (int j = 0; j < kRowsPerLane; ++j) {
         const int32_t c = tile * kTile + j * kWarp + lane;
         const AttnCache& k = kSrc == kIndexed && c >= p.split ? p.extra : p.cache;
         const int64_t limit = kSrc == kIndexed ? k.num_pages * k.block_size : k.num_pages;
-        entry[j] = x[j] >= 0 && x[j] < limit ? x[j] : -1;
-        any |= entry[j] >= 0;
+        if (x[j] >= limit) x[j] = -1;
+        any |= x[j] >= 0;
     }
     return __any_sync(0xFFFFFFFFu, any);
 }
@@ -249,29 +257,41 @@ __device__ __forceinline__ void publish(Shared& sh, Stream& st, int lane, int32_
     ++st.tiles;
 }
 
-// The tiles [first, end) of a unit that hold anything.
+// The tiles [first, end) of a unit that hold anything.  Look-ups run two tiles
+// ahead; a tile is published once it is known whether another one follows.
 template <int kSrc>
 __device__ __forceinline__ bool stream_unit(const AttnParams& p, Shared& sh, Stream& st, const Source& src,
                                             int32_t first, int32_t end, int lane) {
-    int32_t entry[kRowsPerLane], ahead[kRowsPerLane];
-    int32_t tile = first;
-    while (tile < end && !tile_entries<kSrc>(p, src, tile, lane, entry)) ++tile;
-    int32_t flags = kFirst;
-    if (tile >= end) {
-        if (!tile_slot(sh, st)) return false;
-        publish(sh, st, lane, kFirst | kLast | kEmpty, 0);
-    }
-    while (tile < end) {
-        int32_t next = tile + 1;
-        while (next < end && !tile_entries<kSrc>(p, src, next, lane, ahead)) ++next;
-        if (!tile_slot(sh, st)) return false;
-        tile_rows<kSrc>(p, src, tile, lane, entry, sh.tile[st.tiles % kTiles].row);
-        if (next >= end) flags |= kLast;
-        publish(sh, st, lane, flags, kSrc == kIndexed ? 0 : src.lo + tile * kTile);
-        flags = 0;
-        tile = next;
+    int32_t cur[kRowsPerLane], ahead[2][kRowsPerLane];
 #pragma unroll
-        for (int j = 0; j < kRowsPerLane; ++j) entry[j] = ahead[j];
+    for (int i = 0; i < 2; ++i)
+        if (first + i < end) tile_lookup<kSrc>(p, src, first + i, lane, ahead[i]);
+    int32_t flags = kFirst, pending = -1;  // the tile that waits to be published
+    for (int32_t tile = first; tile < end; ++tile) {
+        int32_t x[kRowsPerLane];
+#pragma unroll
+        for (int j = 0; j < kRowsPerLane; ++j) {
+            x[j] = ahead[0][j];
+            ahead[0][j] = ahead[1][j];
+        }
+        if (tile + 2 < end) tile_lookup<kSrc>(p, src, tile + 2, lane, ahead[1]);
+        if (!tile_entries<kSrc>(p, tile, lane, x)) continue;
+        if (pending >= 0) {
+            if (!tile_slot(sh, st)) return false;
+            tile_rows<kSrc>(p, src, pending, lane, cur, sh.tile[st.tiles % kTiles].row);
+            publish(sh, st, lane, flags, kSrc == kIndexed ? 0 : src.lo + pending * kTile);
+            flags = 0;
+        }
+        pending = tile;
+#pragma unroll
+        for (int j = 0; j < kRowsPerLane; ++j) cur[j] = x[j];
+    }
+    if (!tile_slot(sh, st)) return false;
+    if (pending >= 0) {
+        tile_rows<kSrc>(p, src, pending, lane, cur, sh.tile[st.tiles % kTiles].row);
+        publish(sh, st, lane, flags | kLast, kSrc == kIndexed ? 0 : src.lo + pending * kTile);
+    } else {
+        publish(sh, st, lane, kFirst | kLast | kEmpty, 0);
     }
     ++st.units;
     return true;
@@ -285,6 +305,7 @@ __device__ __forceinline__ bool unit_slot(Shared& sh, const Stream& st) {
 __device__ __forceinline__ void set_column(const AttnParams& p, const LaunchShape& ls, Unit& un, int c,
                                            int32_t part, int64_t t, int32_t h, bool used, int32_t lo,
                                            int32_t hi) {
+    un.col_sink[c] = used && p.sink ? p.sink[h] * kLog2e : -INFINITY;
     un.col_token[c] = used ? (int32_t)t : -1;
     un.col_head[c] = h;
     un.col_q[c] = t * p.q_stride_t + h * p.q_stride_h;
@@ -305,7 +326,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
             const int64_t t = v / ls.head_groups;
             const int32_t h0 = (int32_t)(v % ls.head_groups) * ls.heads_per_unit;
             const int32_t heads = min(ls.heads_per_unit, p.num_heads - h0);
-            Source src{t, 0, 0, -1};
+            Source src{t, 0, 0, -1, 0};
             int32_t n, first, end;
             if (kSrc == kIndexed) {
                 n = p.cols / kTile + (p.cols % kTile != 0);
@@ -314,6 +335,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 src.req = x.req;
                 src.lo = x.lo;
                 src.hi = x.hi;
+                if (p.base_off && x.req >= 0) src.base = p.base_off[x.req];
                 n = x.hi < x.lo ? 0 : (x.hi - x.lo) / kTile + 1;
             }
             share(n, part, ls.splits, first, end);
@@ -342,6 +364,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 src.req = __shfl_sync(0xFFFFFFFFu, x.req, a);
                 src.lo = __reduce_min_sync(0xFFFFFFFFu, in ? x.lo : INT32_MAX);
                 src.hi = __reduce_max_sync(0xFFFFFFFFu, in ? x.hi : -1);
+                src.base = p.base_off && src.req >= 0 ? p.base_off[src.req] : 0;
                 const int32_t tiles = src.hi < src.lo ? 0 : (src.hi - src.lo) / kTile + 1;
                 int32_t first, end;
                 share(tiles, part, ls.splits, first, end);
@@ -434,29 +457,29 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// 32 E4M3 bytes of UE8M0 scale byte b as sixteen bf16 pairs, by the rule of the
+// 16 E4M3 bytes of UE8M0 scale byte b as eight bf16 pairs, by the rule of the
 // gather: the product with a power of two, rounded to bf16 once.  One packed
 // multiply by 2^(120 + b - 127) does it where that factor is a bf16 number
 // (b <= 134: values up to 448 * 2^7); a larger scale takes a second one (both
 // exact but for an overflow).  A NaN code goes through the converter.
-__device__ __forceinline__ void dequant32(const uint4 (&raw)[2], uint32_t b, uint32_t (&w)[16]) {
-    const uint32_t in[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+__device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8]) {
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
     const uint32_t f = (b <= 134u ? b + 120u : 247u) * 0x00800080u;
     uint32_t nan = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
         w[2 * i] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x1404)), f);
         w[2 * i + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x3424)), f);
     }
     if (b > 134u) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
+        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
     }
     if (nan & 0x80808080u) {
         const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
             w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
         }
@@ -519,57 +542,74 @@ __device__ __forceinline__ float column_sums(float (&v)[K], int lane) {
     return x;
 }
 
-constexpr int kAhead = 4;  // 64-dim E4M3 chunks of a row half in flight per thread
-
+// Dequantisation: a worker warp owns 16 rows of the tile.  A 128-dim block without
+// rope dims is read by 8 lanes per row, 16 bytes each, so that a load covers 4
+// rows of 128 bytes (a load of 16 rows would take one pass through the L1 tags
+// per row); the two 64-dim chunks and two rows are spread over the lanes so
+// that every eight of them store to eight different 16-byte banks.
 template <int N, int kSrc, int D>
 __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint32_t k_tile,
                      uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
     constexpr int NC = N / kGroups;  // columns of a worker warp
     constexpr int kChunks = D / 64, kBlocks = D / 128;
+    constexpr int kOwn = kTile / kWorkers;             // rows of a warp
+    static_assert(kOwn == 16, "the lane maps below");
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     const int quad = warp % 4, group = warp / 4;
-    const int row = tid / 2, half = tid % 2;           // dequantisation: 32 dims of a row's chunk
     const int srow = quad * kWarp + lane;              // softmax: the tile row of this lane
     const int nope = D - p.rope_dim, fp8_chunks = nope / 64;
     const int rope_from = nope / 128;                  // blocks from here on hold rope dims
-    const uint32_t k_addr = k_tile + row * 128;
-    uint32_t swz[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) swz[i] = ((4 * half + i) ^ (row & 7)) * 16;
+    const bool mixed = fp8_chunks % 2 != 0;            // and the first of them E4M3 dims too
+    const int own = warp * kOwn;
+    // block map: rows b_row + 4 i, 16 bytes at b_byte, in chunk b_chunk of the block
+    const int b_row = own + (lane >> 4) * 2 + ((lane >> 2) & 1), b_chunk = (lane >> 3) & 1;
+    const int b_byte = b_chunk * 64 + (lane & 3) * 16;
+    const uint32_t b_dst = k_tile + b_chunk * kChunkBytes + b_row * 128 + (((2 * (lane & 3)) ^ (b_row & 7)) * 16);
+    // chunk map: rows c_row + 8 i, 16 bytes at 16 (lane % 4)
+    const int c_row = own + (lane >> 2);
+    const uint32_t c_dst = k_tile + c_row * 128 + (((2 * (lane & 3)) ^ (c_row & 7)) * 16);
+    // rope map: rows r_row + 4 i, 16 bytes at 16 (lane % 8)
+    const int r_row = own + (lane >> 3);
+    const uint32_t r_dst = k_tile + r_row * 128 + (((lane & 7) ^ (r_row & 7)) * 16);
     const uint32_t lane_base = tmem + ((uint32_t)(quad * kWarp) << 16) + group * NC;
     uint32_t step = 0, exchange = 0;
 
     float l[NC];
     float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
-    uint4 raw[kAhead][2];      // chunks fp8_chunks - 1, - 2, ... of the row
-    const uint8_t* data = nullptr;
-    uint2 scales = make_uint2(0, 0);
+    uint4 raw[2][4];           // blocks rope_from - 1, rope_from - 2, ... of four rows
+    uint4 raw_chunk[2];        // the E4M3 chunk of a mixed block
+    uint2 scales = make_uint2(0, 0);  // of row own + lane, for lane < 16
 
-    const auto load = [&](uint4(&x)[2], int k) {  // the k-th chunk in that order
-        x[0] = x[1] = make_uint4(0, 0, 0, 0);
-        if (data != nullptr) {
-            const uint8_t* src = data + (fp8_chunks - 1 - k) * 64 + half * 32;
-            x[0] = ld_stream_v4(src);
-            x[1] = ld_stream_v4(src + 16);
-        }
+    const auto load16 = [](const Row& r, int at) {
+        return r.data != nullptr ? ld_stream_v4(r.data + at) : make_uint4(0, 0, 0, 0);
     };
-    // takes the next tile's row and starts its first loads
+    const auto load_block = [&](const Tile& t, uint4(&x)[4], int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = load16(t.row[b_row + 4 * i], j * 128 + b_byte);
+    };
+    // starts the first loads of a tile
     const auto start = [&](const Tile& t) {
-        const Row r = t.row[row];
-        data = r.data;
-        scales = make_uint2(0, 0);
-        if (data != nullptr) {
-            if (D == 512) {
-                scales = ld_nc_v2(r.scales);
-            } else if (D == 256) {
-                scales.x = ld_nc_u32(r.scales);
-            } else {
-                scales.x = ld_nc_u8(r.scales) | (ld_nc_u8(r.scales + 1) << 8);
+        if (lane < kOwn) {
+            const uint8_t* sc = t.row[own + lane].scales;
+            scales = make_uint2(0, 0);
+            if (sc != nullptr) {
+                if (D == 512) {
+                    scales = ld_nc_v2(sc);
+                } else if (D == 256) {
+                    scales.x = ld_nc_u32(sc);
+                } else {
+                    scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
+                }
             }
         }
+        if (mixed) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (k < fp8_chunks) load(raw[k], k);
+            for (int i = 0; i < 2; ++i)
+                raw_chunk[i] = load16(t.row[c_row + 8 * i], (fp8_chunks - 1) * 64 + (lane & 3) * 16);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            if (b < rope_from) load_block(t, raw[b], rope_from - 1 - b);
     };
 
     if (!wait_all(&sh.tile_full[0], 0)) return false;
@@ -590,59 +630,68 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
         }
         if (!(flags & kEmpty)) {
             const int buf = step & 1;
-            if (kSrc == kTokens) {
-                if (half == 0) sh.row_bad[buf][row] = 0;
-                __syncwarp();
+            if (lane < kOwn) {
+                sh.scales[buf][own + lane] = scales;
+                if (kSrc == kTokens) sh.row_bad[buf][own + lane] = 0;
             }
-            // ---- dequantisation, from the last chunk down
+            __syncwarp();
+            const uint8_t* sc = reinterpret_cast<const uint8_t*>(sh.scales[buf]);
+            // ---- dequantisation, from the last dims down
             int block = kBlocks;  // blocks from here on are free
             const auto need = [&](int j) {
                 if (j >= block) return true;
                 block = j;
                 return step == 0 || wait_all(&sh.freed[j], (step - 1) & 1);
             };
+            const auto put = [&](uint4 x, int row, int chunk, uint32_t dst) {
+                uint32_t w[8];
+                dequant16(x, sc[row * 8 + chunk], w);
+                if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+                sts_v4(dst, w[0], w[1], w[2], w[3]);
+                sts_v4(dst ^ 16, w[4], w[5], w[6], w[7]);
+            };
             for (int c = kChunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
                 if (!need(c / 2)) return false;
-                const uint32_t dst = k_addr + c * kChunkBytes;
-                const uint8_t* src = data == nullptr ? p.cache.base : data + nope + (c * 64 - nope) * 2 + half * 64;
-                if (kSrc == kTokens) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* data = tl.row[r_row + 4 * i].data;
+                    const uint8_t* src = data == nullptr ? p.cache.base : data + nope + (c * 64 - nope) * 2 + (lane & 7) * 16;
+                    const uint32_t dst = (r_dst + c * kChunkBytes + i * 512) ^ ((i & 1) * 64);
+                    if (kSrc == kTokens) {
                         uint32_t w[4] = {0, 0, 0, 0};
                         if (data != nullptr) {
-                            const uint4 x = ld_stream_v4(src + i * 16);
+                            const uint4 x = ld_stream_v4(src);
                             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
                         }
-                        if (clear_non_finite(w)) sh.row_bad[buf][row] = 1;
-                        sts_v4(dst + swz[i], w[0], w[1], w[2], w[3]);
+                        if (clear_non_finite(w)) sh.row_bad[buf][r_row + 4 * i] = 1;
+                        sts_v4(dst, w[0], w[1], w[2], w[3]);
+                    } else {
+                        copy16(dst, src, data == nullptr ? 0 : 16);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        copy16(dst + swz[i], data == nullptr ? src : src + i * 16, data == nullptr ? 0 : 16);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-                const int c = fp8_chunks - 1 - k;
-                if (c < 0) break;
-                const uint32_t b = ((c < 4 ? scales.x : scales.y) >> (8 * (c & 3))) & 0xFFu;
-                uint32_t w[16];
-                dequant32(raw[k % kAhead], b, w);
-                if (c - kAhead >= 0) load(raw[k % kAhead], k + kAhead);
-                if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
+            if (mixed) {
+                const int c = fp8_chunks - 1;
                 if (!need(c / 2)) return false;
-                const uint32_t dst = k_addr + c * kChunkBytes;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sts_v4(dst + swz[i], w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (c % 2 == 0 && c / 2 < rope_from) {
-                    // the first hand-over of a unit covers its queries
-                    if ((flags & kFirst) && c / 2 == rope_from - 1) copies_done();
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.full[c / 2]);
-                }
+                for (int i = 0; i < 2; ++i)  // 8 rows on, the swizzle is the same
+                    put(raw_chunk[i], c_row + 8 * i, c, c_dst + c * kChunkBytes + i * 1024);
+            }
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int j = rope_from - 1 - b;
+                if (j < 0) break;
+                if (!need(j)) return false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // 4 rows on, bit 2 of the swizzle turns
+                    put(raw[b % 2][i], b_row + 4 * i, 2 * j + b_chunk,
+                        (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
+                if (j >= 2) load_block(tl, raw[b % 2], j - 2);
+                // the first hand-over of a unit covers its queries
+                if (b == 0 && (flags & kFirst)) copies_done();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[j]);
             }
             if (rope_from < kBlocks) {
                 copies_done();
@@ -793,7 +842,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                         }
                     } else {
                         const float m = m_used == -INFINITY ? 0.0f : m_used;
-                        const float den = total + (p.sink ? ex2_approx(p.sink[h] * kLog2e - m) : 0.0f);
+                        const float den = total + ex2_approx(un.col_sink[n] - m);
                         inv = total == 0.0f ? 0.0f : 1.0f / den;
                         if (p.lse && quad == 0)
                             p.lse[(int64_t)t * p.lse_stride_t + h] =
@@ -808,38 +857,35 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 tmem_fence_after();
             }
             for (int j = 0; j < kBlocks; ++j) {
+                float o[NC];
+                if (!(flags & kEmpty)) {
+                    tmem_ld<NC>(lane_base + N + j * N, o);
+                } else {
 #pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += 8) {
-                    float o[8];
-                    if (!(flags & kEmpty)) {
-                        tmem_ld<8>(lane_base + N + j * N + k0, o);
-                    } else {
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                }
+                const int d = j * 128 + srow;
+                if (ls.splits > 1) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+                    for (int k = 0; k < NC; ++k) {
+                        const int n = group * NC + k;
+                        if (un.col_token[n] >= 0) ls.part_o[un.col_out[n] + d] = o[k];
                     }
-                    const int d = j * 128 + srow;
-                    if (ls.splits > 1) {
+                } else {
+                    // 4 x 4 exchange among four lanes: each then holds four dims of one column
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int n = group * NC + k0 + k;
-                            if (un.col_token[n] >= 0) ls.part_o[un.col_out[n] + d] = o[k];
-                        }
-                    } else {
-                        // 4 x 4 exchange among four lanes: each then holds four dims of one column
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k0 + k]);
-                            const bool odd = lane & 1, upper = lane & 2;
-                            const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
-                            const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
-                            const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
-                            const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
-                            const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
-                            const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
-                            const int n = group * NC + k0 + k + (lane & 1) + (lane & 2);
-                            if (un.col_token[n] >= 0)
-                                st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
-                        }
+                    for (int k = 0; k < NC; k += 4) {
+                        const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k]);
+                        const bool odd = lane & 1, upper = lane & 2;
+                        const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
+                        const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
+                        const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
+                        const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
+                        const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
+                        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                        const int n = group * NC + k + (lane & 3);
+                        if (un.col_token[n] >= 0)
+                            st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
                     }
                 }
             }
