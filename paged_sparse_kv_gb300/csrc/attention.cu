@@ -63,6 +63,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_attn_wait_timeouts = 0;
 
+// What a row that does not exist (or is not visible) is read from: the longest
+// record, all zero, so that the loads of a tile need no conditions.
+__device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
+
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
 // A set of columns; its tiles follow one another in the stream of tiles.
@@ -78,7 +82,7 @@ struct Unit {
 };
 
 struct alignas(16) Row {
-    const uint8_t* data;    // null: the row does not exist or is not visible
+    const uint8_t* data;    // g_zero_row: the row does not exist or is not visible
     const uint8_t* scales;  // its UE8M0 bytes
 };
 
@@ -126,7 +130,7 @@ struct LaunchShape {
 };
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
-    const bool ok = mbar_wait_bounded(bar, parity, kWaitLimitNs);
+    const bool ok = mbar_poll_bounded(bar, parity, kWaitLimitNs);
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -219,7 +223,8 @@ __device__ __forceinline__ void tile_rows(const AttnParams& p, const Source& src
     const int32_t token_stride = p.head_dim + p.rope_dim;
 #pragma unroll
     for (int j = 0; j < kRowsPerLane; ++j) {
-        Row r{nullptr, nullptr};
+        const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+        Row r{zero, zero};
         if (entry[j] >= 0) {
             const int32_t i = tile * kTile + j * kWarp + lane;
             const AttnCache& c = kSrc == kIndexed && i >= p.split ? p.extra : p.cache;
@@ -395,6 +400,8 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
 // longest.  The second product frees them from the last block down, the order
 // they are dequantised in.
 
+// The whole warp walks the pipeline, so that descriptors stay in uniform
+// registers; one elected lane issues.
 template <int N, int D>
 __device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_tile, uint32_t p_tile,
                       uint32_t tmem) {
@@ -408,34 +415,47 @@ __device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_til
     // apart, 8-row groups 128 bytes apart.
     const uint64_t v_desc = umma_desc(k_tile, kChunkBytes, 1024, kSwizzle128);
     const uint64_t p_desc = umma_desc(p_tile, 128, 2048, kSwizzleNone);
+    const uint32_t lead = elect_one();
     uint32_t step = 0;
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles;
-        if (!mbar_wait_bounded(&sh.tile_full[slot], (seq / kTiles) & 1, kWaitLimitNs)) return false;
-        const int32_t flags = sh.tile[slot].flags;
-        mbar_arrive(&sh.tile_empty[slot]);
+        if (!wait_all(&sh.tile_full[slot], (seq / kTiles) & 1)) return false;
+        const int32_t flags = __shfl_sync(0xFFFFFFFFu, sh.tile[slot].flags, 0);
+        if (lead) mbar_arrive(&sh.tile_empty[slot]);
         if (flags & kDone) return true;
         if (flags & kEmpty) continue;
-        for (int i = 0; i < kBlocks; ++i) {
-            const int j = i < rope_from ? rope_from - 1 - i : kBlocks - 1 - (i - rope_from);
-            if (!mbar_wait_bounded(&sh.full[j], step & 1, kWaitLimitNs)) return false;
-            tmem_fence_after();
+        const auto first_product = [&](int j, bool first) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 umma_bf16(tmem, k_desc + ((j * 2 * kChunkBytes + (k / 4) * kChunkBytes + (k % 4) * 32) >> 4),
                           q_desc + ((j * 2 * (N * 128) + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), kS,
-                          i > 0 || k > 0);
+                          !first || k > 0, lead);
+        };
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {  // blocks without rope dims
+            if (j >= rope_from) continue;
+            if (!wait_all(&sh.full[j], step & 1)) return false;
+            tmem_fence_after();
+            first_product(j, j == rope_from - 1);
         }
-        umma_commit(&sh.s_ready);
-        if (!mbar_wait_bounded(&sh.p_ready, step & 1, kWaitLimitNs)) return false;
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {
+            if (j < rope_from) break;
+            if (!wait_all(&sh.full[j], step & 1)) return false;
+            tmem_fence_after();
+            first_product(j, rope_from == 0 && j == kBlocks - 1);
+        }
+        umma_commit(&sh.s_ready, lead);
+        if (!wait_all(&sh.p_ready, step & 1)) return false;
         tmem_fence_after();
+        const bool first_tile = flags & kFirst;
 #pragma unroll
         for (int j = kBlocks - 1; j >= 0; --j) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
                 umma_bf16(tmem + N + j * N, v_desc + ((j * 2 * kChunkBytes + k * 2048) >> 4),
-                          p_desc + ((k * 256) >> 4), kO, !(flags & kFirst) || k > 0);
-            umma_commit(&sh.freed[j]);
+                          p_desc + ((k * 256) >> 4), kO, !first_tile || k > 0, lead);
+            umma_commit(&sh.freed[j], lead);
         }
         ++step;
     }
@@ -443,46 +463,18 @@ __device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_til
 
 // ---- the worker warps ----------------------------------------------------------------
 
-// Two E4M3 bytes in the upper bytes of each half of t -> the bf16 pair of their
-// values times 2^-120: sign, exponent and mantissa moved to their bf16 places
-// (bias 127 against 7), which holds for zeros and subnormals too; the caller's
-// factor is 2^120 times the scale.  NaN codes are not handled.
-__device__ __forceinline__ uint32_t e4m3_bits(uint32_t t) {
-    return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // 16 E4M3 bytes of UE8M0 scale byte b as eight bf16 pairs, by the rule of the
-// gather: the product with a power of two, rounded to bf16 once.  One packed
-// multiply by 2^(120 + b - 127) does it where that factor is a bf16 number
-// (b <= 134: values up to 448 * 2^7); a larger scale takes a second one (both
-// exact but for an overflow).  A NaN code goes through the converter.
+// gather (E4M3 -> fp16 exactly, binary32 product, rounded to bf16).  Per pair that
+// is two conversions on the integer pipe and two on the fp16 one, 2 cycles of a
+// scheduler each: placing the bits with shifts and masks and multiplying bf16
+// pairs took 3 to 4 operations of the integer pipe per pair.
 __device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8]) {
     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    const uint32_t f = (b <= 134u ? b + 120u : 247u) * 0x00800080u;
-    uint32_t nan = 0;
+    const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        nan |= (in[i] & 0x7F7F7F7Fu) + 0x01010101u;
-        w[2 * i] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x1404)), f);
-        w[2 * i + 1] = mul_bf16x2(e4m3_bits(__byte_perm(in[i], 0, 0x3424)), f);
-    }
-    if (b > 134u) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(w[i], b * 0x00800080u);
-    }
-    if (nan & 0x80808080u) {
-        const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
-            w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
-        }
+        w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
+        w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
     }
 }
 
@@ -578,34 +570,31 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
     float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
     uint4 raw[2][4];           // blocks rope_from - 1, rope_from - 2, ... of four rows
     uint4 raw_chunk[2];        // the E4M3 chunk of a mixed block
-    uint2 scales = make_uint2(0, 0);  // of row own + lane, for lane < 16
+    uint2 scales = make_uint2(0, 0);  // of row own + lane % 16
 
-    const auto load16 = [](const Row& r, int at) {
-        return r.data != nullptr ? ld_stream_v4(r.data + at) : make_uint4(0, 0, 0, 0);
-    };
     const auto load_block = [&](const Tile& t, uint4(&x)[4], int j) {
+        const uint8_t* data[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = load16(t.row[b_row + 4 * i], j * 128 + b_byte);
+        for (int i = 0; i < 4; ++i) data[i] = t.row[b_row + 4 * i].data;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ld_stream_v4(data[i] + j * 128 + b_byte);
     };
     // starts the first loads of a tile
     const auto start = [&](const Tile& t) {
-        if (lane < kOwn) {
-            const uint8_t* sc = t.row[own + lane].scales;
-            scales = make_uint2(0, 0);
-            if (sc != nullptr) {
-                if (D == 512) {
-                    scales = ld_nc_v2(sc);
-                } else if (D == 256) {
-                    scales.x = ld_nc_u32(sc);
-                } else {
-                    scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
-                }
-            }
+        const uint8_t* sc = t.row[own + lane % kOwn].scales;
+        if (D == 512) {
+            scales = ld_nc_v2(sc);
+        } else if (D == 256) {
+            scales.x = ld_nc_u32(sc);
+        } else {
+            scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
         }
         if (mixed) {
+            const uint8_t* data[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                raw_chunk[i] = load16(t.row[c_row + 8 * i], (fp8_chunks - 1) * 64 + (lane & 3) * 16);
+            for (int i = 0; i < 2; ++i) data[i] = t.row[c_row + 8 * i].data;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) raw_chunk[i] = ld_stream_v4(data[i] + (fp8_chunks - 1) * 64 + (lane & 3) * 16);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -643,52 +632,58 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 block = j;
                 return step == 0 || wait_all(&sh.freed[j], (step - 1) & 1);
             };
-            const auto put = [&](uint4 x, int row, int chunk, uint32_t dst) {
+            const auto put = [&](uint4 x, uint32_t scale, int row, uint32_t dst) {
                 uint32_t w[8];
-                dequant16(x, sc[row * 8 + chunk], w);
+                dequant16(x, scale, w);
                 if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
                 sts_v4(dst, w[0], w[1], w[2], w[3]);
                 sts_v4(dst ^ 16, w[4], w[5], w[6], w[7]);
             };
-            for (int c = kChunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
-                if (!need(c / 2)) return false;
+            if (fp8_chunks < kChunks) {
+                const uint8_t* data[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* data = tl.row[r_row + 4 * i].data;
-                    const uint8_t* src = data == nullptr ? p.cache.base : data + nope + (c * 64 - nope) * 2 + (lane & 7) * 16;
-                    const uint32_t dst = (r_dst + c * kChunkBytes + i * 512) ^ ((i & 1) * 64);
-                    if (kSrc == kTokens) {
-                        uint32_t w[4] = {0, 0, 0, 0};
-                        if (data != nullptr) {
-                            const uint4 x = ld_stream_v4(src);
-                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                for (int i = 0; i < 4; ++i) data[i] = tl.row[r_row + 4 * i].data;
+                for (int c = kChunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
+                    if (!need(c / 2)) return false;
+                    const int at = nope + (c * 64 - nope) * 2 + (lane & 7) * 16;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t dst = (r_dst + c * kChunkBytes + i * 512) ^ ((i & 1) * 64);
+                        if (kSrc == kTokens) {
+                            const uint4 x = ld_stream_v4(data[i] + at);
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            if (clear_non_finite(w)) sh.row_bad[buf][r_row + 4 * i] = 1;
+                            sts_v4(dst, w[0], w[1], w[2], w[3]);
+                        } else {
+                            copy16(dst, data[i] + at, 16);
                         }
-                        if (clear_non_finite(w)) sh.row_bad[buf][r_row + 4 * i] = 1;
-                        sts_v4(dst, w[0], w[1], w[2], w[3]);
-                    } else {
-                        copy16(dst, src, data == nullptr ? 0 : 16);
                     }
                 }
             }
             if (mixed) {
                 const int c = fp8_chunks - 1;
+                uint32_t scale[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) scale[i] = sc[(c_row + 8 * i) * 8 + c];
                 if (!need(c / 2)) return false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)  // 8 rows on, the swizzle is the same
-                    put(raw_chunk[i], c_row + 8 * i, c, c_dst + c * kChunkBytes + i * 1024);
+                    put(raw_chunk[i], scale[i], c_row + 8 * i, c_dst + c * kChunkBytes + i * 1024);
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int j = rope_from - 1 - b;
                 if (j < 0) break;
+                uint32_t scale[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) scale[i] = sc[(b_row + 4 * i) * 8 + 2 * j + b_chunk];
                 if (!need(j)) return false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // 4 rows on, bit 2 of the swizzle turns
-                    put(raw[b % 2][i], b_row + 4 * i, 2 * j + b_chunk,
+                    put(raw[b % 2][i], scale[i], b_row + 4 * i,
                         (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
                 if (j >= 2) load_block(tl, raw[b % 2], j - 2);
-                // the first hand-over of a unit covers its queries
-                if (b == 0 && (flags & kFirst)) copies_done();
+                if (b == 0 && (flags & kFirst)) copies_done();  // hands over the unit's queries too
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.full[j]);
@@ -714,7 +709,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             tmem_fence_after();
             float s[NC];
             tmem_ld<NC>(lane_base, s);
-            const bool ok = tl.row[srow].data != nullptr;
+            const bool ok = tl.row[srow].data != reinterpret_cast<const uint8_t*>(g_zero_row);
             if (kSrc == kTokens) {
                 // every worker has handed over its share of the tile: its flags are there
                 if (!wait_all(&sh.full[0], step & 1)) return false;
@@ -856,36 +851,55 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
                 tmem_fence_after();
             }
-            for (int j = 0; j < kBlocks; ++j) {
-                float o[NC];
-                if (!(flags & kEmpty)) {
-                    tmem_ld<NC>(lane_base + N + j * N, o);
-                } else {
+            if (ls.splits > 1) {
+                for (int j = 0; j < kBlocks; ++j) {
+                    float o[NC];
 #pragma unroll
                     for (int k = 0; k < NC; ++k) o[k] = 0.0f;
-                }
-                const int d = j * 128 + srow;
-                if (ls.splits > 1) {
+                    if (!(flags & kEmpty)) tmem_ld<NC>(lane_base + N + j * N, o);
+                    const int d = j * 128 + srow;
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const int n = group * NC + k;
-                        if (un.col_token[n] >= 0) ls.part_o[un.col_out[n] + d] = o[k];
+                    for (int k0 = 0; k0 < NC; k0 += 8) {
+                        int64_t at[8];
+                        bool used[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            at[k] = un.col_out[group * NC + k0 + k] + d;
+                            used[k] = un.col_token[group * NC + k0 + k] >= 0;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (used[k]) ls.part_o[at[k]] = o[k0 + k];
                     }
-                } else {
-                    // 4 x 4 exchange among four lanes: each then holds four dims of one column
+                }
+            } else {
+                // 4 x 4 exchanges among four lanes: each then holds four dims of the columns
+                // k + lane % 4, where it stores them
+                uint16_t* dst[NC / 4];
 #pragma unroll
-                    for (int k = 0; k < NC; k += 4) {
-                        const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][k]);
-                        const bool odd = lane & 1, upper = lane & 2;
-                        const float a0 = o[k] * inv.x, a1 = o[k + 1] * inv.y, a2 = o[k + 2] * inv.z, a3 = o[k + 3] * inv.w;
+                for (int k = 0; k < NC / 4; ++k) {
+                    const int n = group * NC + 4 * k + (lane & 3);
+                    dst[k] = un.col_token[n] >= 0 ? p.out + un.col_out[n] + (srow & ~3) : nullptr;
+                }
+                const bool odd = lane & 1, upper = lane & 2;
+                for (int j = 0; j < kBlocks; ++j) {
+                    float o[NC];
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                    if (!(flags & kEmpty)) tmem_ld<NC>(lane_base + N + j * N, o);
+#pragma unroll
+                    for (int k = 0; k < NC / 4; ++k) {
+                        const float4 inv = *reinterpret_cast<const float4*>(&sh.aux[warp][4 * k]);
+                        const float a0 = o[4 * k] * inv.x, a1 = o[4 * k + 1] * inv.y;
+                        const float a2 = o[4 * k + 2] * inv.z, a3 = o[4 * k + 3] * inv.w;
                         const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
                         const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
-                        const uint32_t w0 = odd ? pack_bf16x2(b0, a1) : pack_bf16x2(a0, b0);  // column k (+1 if odd)
-                        const uint32_t w1 = odd ? pack_bf16x2(b1, a3) : pack_bf16x2(a2, b1);  // column k + 2 (+1)
+                        // columns 4 k (+ 1 if odd) and 4 k + 2 (+ 1)
+                        const uint32_t w0 = pack_bf16x2(odd ? b0 : a0, odd ? a1 : b0);
+                        const uint32_t w1 = pack_bf16x2(odd ? b1 : a2, odd ? a3 : b1);
                         const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
-                        const int n = group * NC + k + (lane & 3);
-                        if (un.col_token[n] >= 0)
-                            st_v2(p.out + un.col_out[n] + (d & ~3), upper ? make_uint2(x, w1) : make_uint2(w0, x));
+                        if (dst[k] != nullptr)
+                            st_v2(dst[k] + j * 128, make_uint2(upper ? x : w0, upper ? w1 : x));
                     }
                 }
             }
@@ -948,11 +962,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = work<N, kSrc, D>(p, ls, sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
     } else if (warp == kPlanWarp) {
         ok = plan<kSrc>(p, ls, sh);
-    } else if (lane == 0) {
+    } else {
         ok = issue<N, D>(sh, (D - p.rope_dim) / 128, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
         if (!ok) {  // wait for the MMAs in flight before the operands go
-            umma_commit(&sh.drain);
-            mbar_wait_bounded(&sh.drain, 0, kWaitLimitNs);
+            umma_commit(&sh.drain, elect_one());
+            mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);
         }
     }
     if (!ok && lane == 0) atomicAdd(&g_attn_wait_timeouts, 1u);
