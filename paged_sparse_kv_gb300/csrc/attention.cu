@@ -57,7 +57,7 @@ constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 16.0f;        // log2 units the maximum may run ahead of the reference
+constexpr float kMostWeight = 65536.0f;  // a weight above it has its column's reference raised
 constexpr float kNone = -3.0e38f;     // reference of a column that has seen nothing
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -105,7 +105,7 @@ struct Shared {
     alignas(16) float red[kGroups][2][4][kMaxCols / kGroups];  // [group][exchange parity][quad][column]
     alignas(16) float ref[kWorkers][kMaxCols / kGroups];
     alignas(16) float aux[kWorkers][kMaxCols / kGroups];
-    int32_t over[kGroups][2][4];
+    int32_t over[2];               // a weight of the step is out of range: its reference is raised
     uint64_t tile_full[kTiles], tile_empty[kTiles];
     uint64_t unit_empty[2];
     uint64_t full[kMaxBlocks];     // 128 dims of the tile are dequantised
@@ -393,6 +393,17 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
     return true;
 }
 
+// True once for a step whose weights did not fit, as everyone learns when the
+// first round of them is complete.
+struct Again {
+    uint32_t step = ~0u;
+    __device__ __forceinline__ bool operator()(const Shared& sh, uint32_t now) {
+        if (step == now) return false;
+        step = now;
+        return __shfl_sync(0xFFFFFFFFu, *const_cast<const volatile int32_t*>(&sh.over[now & 1]), 0) != 0;
+    }
+};
+
 // ---- the MMA thread ------------------------------------------------------------------
 //
 // Both products take the 128-dim blocks in one order: first those without rope
@@ -416,7 +427,8 @@ __device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_til
     const uint64_t v_desc = umma_desc(k_tile, kChunkBytes, 1024, kSwizzle128);
     const uint64_t p_desc = umma_desc(p_tile, 128, 2048, kSwizzleNone);
     const uint32_t lead = elect_one();
-    uint32_t step = 0;
+    uint32_t step = 0, round = 0;  // tiles; phases of p_ready
+    Again again;
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles;
         if (!wait_all(&sh.tile_full[slot], (seq / kTiles) & 1)) return false;
@@ -446,9 +458,11 @@ __device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_til
             first_product(j, rope_from == 0 && j == kBlocks - 1);
         }
         umma_commit(&sh.s_ready, lead);
-        if (!wait_all(&sh.p_ready, step & 1)) return false;
-        tmem_fence_after();
         const bool first_tile = flags & kFirst;
+        do {  // a second round of weights follows where a reference had to be raised
+            if (!wait_all(&sh.p_ready, round++ & 1)) return false;
+        } while (!first_tile && again(sh, step));
+        tmem_fence_after();
 #pragma unroll
         for (int j = kBlocks - 1; j >= 0; --j) {
 #pragma unroll
@@ -568,8 +582,10 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 
     float l[NC];
     float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
-    uint4 raw[2][4];           // blocks rope_from - 1, rope_from - 2, ... of four rows
-    uint4 raw_chunk[2];        // the E4M3 chunk of a mixed block
+    // Loads in flight: buffer 0 takes the E4M3 chunk of a mixed block, then every
+    // second pure block, buffer 1 the other pure blocks; each is refilled as soon as
+    // it has been used, across tiles, which spreads the loads evenly.
+    uint4 raw[2][4];
     uint2 scales = make_uint2(0, 0);  // of row own + lane % 16
 
     const auto load_block = [&](const Tile& t, uint4(&x)[4], int j) {
@@ -579,8 +595,14 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = ld_stream_v4(data[i] + j * 128 + b_byte);
     };
-    // starts the first loads of a tile
-    const auto start = [&](const Tile& t) {
+    const auto load_chunk = [&](const Tile& t) {
+        const uint8_t* data[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) data[i] = t.row[c_row + 8 * i].data;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) raw[0][i] = ld_stream_v4(data[i] + (fp8_chunks - 1) * 64 + (lane & 3) * 16);
+    };
+    const auto load_scales = [&](const Tile& t) {
         const uint8_t* sc = t.row[own + lane % kOwn].scales;
         if (D == 512) {
             scales = ld_nc_v2(sc);
@@ -589,24 +611,26 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
         } else {
             scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
         }
-        if (mixed) {
-            const uint8_t* data[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) data[i] = t.row[c_row + 8 * i].data;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) raw_chunk[i] = ld_stream_v4(data[i] + (fp8_chunks - 1) * 64 + (lane & 3) * 16);
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-            if (b < rope_from) load_block(t, raw[b], rope_from - 1 - b);
+    };
+    // the first loads of a tile: what its buffers take first
+    const auto first0 = [&](const Tile& t) {
+        if (mixed)
+            load_chunk(t);
+        else if (rope_from >= 2)
+            load_block(t, raw[0], rope_from - 2);
+    };
+    const auto first1 = [&](const Tile& t) {
+        if (rope_from >= 1) load_block(t, raw[1], rope_from - 1);
     };
 
     if (!wait_all(&sh.tile_full[0], 0)) return false;
     int32_t flags = sh.tile[0].flags;
     if (!(flags & (kDone | kEmpty))) {
         load_queries<N, D>(p, sh.unit[sh.tile[0].unit], q_tile, tid);
-        start(sh.tile[0]);
     }
+    bool loaded = false;  // the tile's first loads are under way
+    uint32_t round = 0;   // phases of p_ready
+    Again again;
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles, nslot = (seq + 1) % kTiles;
         const Tile& tl = sh.tile[slot];
@@ -617,8 +641,24 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             for (int i = 0; i < NC; ++i) l[i] = 0.0f;
             m_used = -INFINITY;
         }
+        // the next tile, looked at when its loads can start
+        int32_t next_flags = 0;
+        bool next_known = false;
+        const auto peek = [&]() {
+            if (next_known) return true;
+            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
+            next_flags = sh.tile[nslot].flags;
+            next_known = true;
+            return true;
+        };
+        const Tile& nt = sh.tile[nslot];
         if (!(flags & kEmpty)) {
             const int buf = step & 1;
+            if (!loaded) {
+                load_scales(tl);
+                first0(tl);
+                first1(tl);
+            }
             if (lane < kOwn) {
                 sh.scales[buf][own + lane] = scales;
                 if (kSrc == kTokens) sh.row_bad[buf][own + lane] = 0;
@@ -668,7 +708,13 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!need(c / 2)) return false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)  // 8 rows on, the swizzle is the same
-                    put(raw_chunk[i], scale[i], c_row + 8 * i, c_dst + c * kChunkBytes + i * 1024);
+                    put(raw[0][i], scale[i], c_row + 8 * i, c_dst + c * kChunkBytes + i * 1024);
+                if (rope_from >= 2) {
+                    load_block(tl, raw[0], rope_from - 2);
+                } else {
+                    if (!peek()) return false;
+                    if (!(next_flags & (kDone | kEmpty))) first0(nt);
+                }
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
@@ -680,77 +726,74 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!need(j)) return false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)  // 4 rows on, bit 2 of the swizzle turns
-                    put(raw[b % 2][i], scale[i], b_row + 4 * i,
+                    put(raw[(b + 1) % 2][i], scale[i], b_row + 4 * i,
                         (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
-                if (j >= 2) load_block(tl, raw[b % 2], j - 2);
-                if (b == 0 && (flags & kFirst)) copies_done();  // hands over the unit's queries too
+                // the rope copies have had time to land: they go along with the last block but one
+                const bool rope_too = rope_from < kBlocks && (j == 1 || rope_from == 1);
+                if (rope_too || (b == 0 && (flags & kFirst))) copies_done();  // queries as well
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[j]);
+                if (lane == 0) {
+                    mbar_arrive(&sh.full[j]);
+                    if (rope_too)
+                        for (int r = rope_from; r < kBlocks; ++r) mbar_arrive(&sh.full[r]);
+                }
+                if (j >= 2) {
+                    load_block(tl, raw[(b + 1) % 2], j - 2);
+                } else {
+                    if (!peek()) return false;
+                    if (!(next_flags & (kDone | kEmpty))) {
+                        if (b % 2 == 0)
+                            first1(nt);
+                        else
+                            first0(nt);
+                    }
+                }
             }
-            if (rope_from < kBlocks) {
+            if (rope_from == 0) {
                 copies_done();
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    for (int j = rope_from; j < kBlocks; ++j) mbar_arrive(&sh.full[j]);
+                    for (int r = 0; r < kBlocks; ++r) mbar_arrive(&sh.full[r]);
             }
         }
-        // ---- the next tile's loads, in flight during the softmax
-        if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
-        const int32_t next_flags = sh.tile[nslot].flags;
+        if (!peek()) return false;
         const bool next_rows = !(next_flags & (kDone | kEmpty));
-        if (next_rows) start(sh.tile[nslot]);
+        if (next_rows && !(flags & kEmpty)) load_scales(nt);
+        loaded = next_rows && !(flags & kEmpty);
 
         if (!(flags & kEmpty)) {
             // ---- softmax of the tile: this lane's row, NC columns
             const int buf = step & 1;
+            const bool ok = tl.row[srow].data != reinterpret_cast<const uint8_t*>(g_zero_row);
             if (!wait_all(&sh.s_ready, step & 1)) return false;
             tmem_fence_after();
-            float s[NC];
-            tmem_ld<NC>(lane_base, s);
-            const bool ok = tl.row[srow].data != reinterpret_cast<const uint8_t*>(g_zero_row);
             if (kSrc == kTokens) {
                 // every worker has handed over its share of the tile: its flags are there
                 if (!wait_all(&sh.full[0], step & 1)) return false;
                 if (rope_from < kBlocks && !wait_all(&sh.full[kBlocks - 1], step & 1)) return false;
-                const int32_t pos = tl.pos + srow;
-                const bool bad = sh.row_bad[buf][srow];
-#pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const bool see = ok && pos >= un.col_lo[group * NC + k] && pos <= un.col_hi[group * NC + k];
-                    s[k] = see ? (bad ? NAN : s[k]) : -INFINITY;
-                }
-            } else if (!__all_sync(0xFFFFFFFFu, ok)) {
-#pragma unroll
-                for (int k = 0; k < NC; ++k) s[k] = ok ? s[k] : -INFINITY;
             }
-            // The reference of a column only has to lie near its maximum: it is set by
-            // the first tile and raised where a score lies far above it, which the
-            // group's four warps have to agree on.
-            bool raise = flags & kFirst;
+            float s[NC];
+            const auto scores = [&]() {
+                tmem_ld<NC>(lane_base, s);
+                if (kSrc == kTokens) {
+                    const int32_t pos = tl.pos + srow;
+                    const bool bad = sh.row_bad[buf][srow];
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) {
+                        const bool see = ok && pos >= un.col_lo[group * NC + k] && pos <= un.col_hi[group * NC + k];
+                        s[k] = see ? (bad ? NAN : s[k]) : -INFINITY;
+                    }
+                } else if (!__all_sync(0xFFFFFFFFu, ok)) {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) s[k] = ok ? s[k] : -INFINITY;
+                }
+            };
+            // The reference of a column only has to lie near its maximum: the first
+            // tile sets it, and it is raised where a weight would exceed 2^kLazy.
             float* ref = sh.ref[warp];
-            if (!raise) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < NC; k += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(&ref[k]);
-                    top = fmaxf(top, fmaf(s[k], ls.scale_log2, -m.x));
-                    top = fmaxf(top, fmaf(s[k + 1], ls.scale_log2, -m.y));
-                    top = fmaxf(top, fmaf(s[k + 2], ls.scale_log2, -m.z));
-                    top = fmaxf(top, fmaf(s[k + 3], ls.scale_log2, -m.w));
-                }
-                const bool over = __any_sync(0xFFFFFFFFu, top > kLazy);
-                int32_t(&flag)[4] = sh.over[group][exchange & 1];
-                if (lane == 0) {
-                    flag[quad] = over;
-                    mbar_arrive(&sh.group_bar[group]);
-                }
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-                raise = flag[0] | flag[1] | flag[2] | flag[3];
-            }
-            if (raise) {
+            const auto set_reference = [&]() {
                 float* red = sh.red[group][exchange & 1][quad];
 #pragma unroll
                 for (int k = 0; k < NC; k += 4) {
@@ -774,42 +817,67 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 }
                 ++exchange;
                 __syncwarp();
-                if (!(flags & kFirst)) {
-                    // the previous tile's second product is done: s_ready came after it
+                return true;
+            };
+            // Weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by
+            // side.  Returns the largest one.
+            const auto weights = [&]() {
+                float most = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < NC; ++k) l[k] *= sh.aux[warp][k];
-                    for (int j = 0; j < kBlocks; ++j) {
+                for (int k = 0; k < NC; k += 8) {
+                    const float4 m0 = *reinterpret_cast<const float4*>(&ref[k]);
+                    const float4 m1 = *reinterpret_cast<const float4*>(&ref[k + 4]);
+                    const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
-                        for (int k0 = 0; k0 < NC; k0 += 8) {
-                            float o[8];
-                            tmem_ld<8>(lane_base + N + j * N + k0, o);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] *= sh.aux[warp][k0 + k];
-                            tmem_st8(lane_base + N + j * N + k0, o);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        s[k + i] = ex2_approx(fmaf(s[k + i], ls.scale_log2, -m[i]));
+                        most = fmaxf(most, s[k + i]);
                     }
-                    tmem_wait_st();
+                    sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
+                           pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
+                           pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
                 }
-            }
-            // weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by side
+                return most;
+            };
+            const auto hand_over = [&]() {
+                fence_async_smem();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready);
+            };
+            scores();
+            if ((flags & kFirst) && !set_reference()) return false;
+            const float most = weights();
+            if (!(flags & kFirst) && __any_sync(0xFFFFFFFFu, most > kMostWeight) && lane == 0)
+                *const_cast<volatile int32_t*>(&sh.over[buf]) = 1;
+            hand_over();
+            if (!wait_all(&sh.p_ready, round++ & 1)) return false;
+            if (!(flags & kFirst) && again(sh, step)) {
+                // once more with raised references; the previous tile's second product is
+                // done (s_ready came after it), this one's has not begun
+                tmem_fence_after();
+                scores();
+                if (!set_reference()) return false;
 #pragma unroll
-            for (int k = 0; k < NC; k += 8) {
-                const float4 m0 = *reinterpret_cast<const float4*>(&ref[k]);
-                const float4 m1 = *reinterpret_cast<const float4*>(&ref[k + 4]);
-                const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                for (int k = 0; k < NC; ++k) l[k] *= sh.aux[warp][k];
+                for (int j = 0; j < kBlocks; ++j) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[k + i] = ex2_approx(fmaf(s[k + i], ls.scale_log2, -m[i]));
-                    l[k + i] += s[k + i];
+                    for (int k0 = 0; k0 < NC; k0 += 8) {
+                        float o[8];
+                        tmem_ld<8>(lane_base + N + j * N + k0, o);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] *= sh.aux[warp][k0 + k];
+                        tmem_st8(lane_base + N + j * N + k0, o);
+                    }
                 }
-                sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
-                       pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
-                       pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
+                tmem_wait_st();
+                weights();
+                hand_over();
+                if (!wait_all(&sh.p_ready, round++ & 1)) return false;
             }
-            fence_async_smem();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_ready);
+            if (tid == 0) sh.over[buf ^ 1] = 0;  // everyone is past the step that used it
+#pragma unroll
+            for (int k = 0; k < NC; ++k) l[k] += s[k];
             ++step;
         }
         if (flags & kLast) {
@@ -947,6 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.p_ready, kWorkers);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < kGroups; ++i) mbar_init(&sh.group_bar[i], 4);
+        sh.over[0] = sh.over[1] = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(&sh.tmem, ls.tmem_cols);
