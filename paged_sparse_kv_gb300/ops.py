@@ -23,15 +23,23 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The handle of a device's current stream and the current device as plain numbers:
+# the torch.cuda objects for them cost 2 us a call, half of what a launch does.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
 def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def _call(dev: torch.device, name: str, *args) -> None:
     """Call a libpsk entry point on ``dev``'s current stream with ``dev`` as
     the current CUDA device (the library launches, sizes grids and sets kernel
     attributes on the current device)."""
-    if torch.cuda.current_device() != dev.index:
+    if _current_device() != dev.index:
         with torch.cuda.device(dev):
             _abi.call(name, *args, _stream(dev))
     else:
@@ -575,25 +583,49 @@ def dequantize_and_gather_k_cache_dense(out: torch.Tensor, cache: torch.Tensor,
 
 
 # ---- batch metadata from request lengths ------------------------------------------------
+#
+# A decode step makes these calls (and the attention ones) once per layer with
+# kernels of a few microseconds, so their argument checks read each property of a
+# tensor once.
 
-def _vec(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, size: Optional[int] = None):
-    """A 1-D contiguous tensor of ``dtype`` (``size`` entries at least), or None."""
+def _index(t: torch.Tensor) -> int:
+    """CUDA device index of the tensor a call takes its device from."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("libpsk operates on CUDA tensors only (no CPU fallback)")
+    return i
+
+
+def _same(t: torch.Tensor, index: int, name: str) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _vec(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, size: int, index: int):
+    """Address of a 1-D contiguous tensor of ``dtype`` with ``size`` entries at least; None for
+    None."""
     if t is None:
-        return
-    _need(t, dtype, name)
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be 1-D contiguous")
-    if size is not None and t.shape[0] < size:
-        raise ValueError(f"{name} must have at least {size} entries, got {t.shape[0]}")
+    if t.numel() < size:
+        raise ValueError(f"{name} must have at least {size} entries, got {t.numel()}")
+    return t.data_ptr()
 
 
-def _table(t: torch.Tensor, name: str, rows: int):
-    """Row stride and width of an int32 block table with at least ``rows`` rows."""
-    _need(t, torch.int32, name)
-    stride = _rows(t, name)
-    if t.shape[0] < rows:
-        raise ValueError(f"{name} must have at least {rows} rows, got {t.shape[0]}")
-    return max(stride, t.shape[1]), t.shape[1]
+def _table(t: torch.Tensor, name: str, rows: int, index: int):
+    """Address, row stride and width of an int32 block table with ``rows`` rows at least."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+    _same(t, index, name)
+    stride, (n, width) = _rows(t, name), t.shape
+    if n < rows:
+        raise ValueError(f"{name} must have at least {rows} rows, got {n}")
+    return t.data_ptr(), max(stride, width), width
 
 
 def compute_slot_mappings(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
@@ -609,29 +641,31 @@ def compute_slot_mappings(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
                           compressed_slot_mapping: Optional[torch.Tensor] = None):
     """Batch metadata from request lengths; returns (positions [T] int64, token_to_req [T]
     int32, slot_mapping [T] int64, compressed_slot_mapping [T] int64), -1 for padding tokens."""
-    _need_cuda(query_start_loc, seq_lens, block_table, base_offsets, compressed_block_table,
-               compressed_base_offsets, positions, token_to_req, slot_mapping,
-               compressed_slot_mapping)
-    dev, T, R = seq_lens.device, int(num_tokens), seq_lens.shape[0]
-    _vec(seq_lens, torch.int32, "seq_lens")
-    _vec(query_start_loc, torch.int32, "query_start_loc", R + 1)
-    _vec(base_offsets, torch.int32, "base_offsets", R)
-    _vec(compressed_base_offsets, torch.int32, "compressed_base_offsets", R)
-    stride, width = _table(block_table, "block_table", R)
+    i, i32, i64 = _index(seq_lens), torch.int32, torch.int64
+    dev, T, R = seq_lens.device, int(num_tokens), seq_lens.numel()
+    if T < 0:
+        raise ValueError("num_tokens must be >= 0")
+    if positions is None:
+        positions = torch.empty((T,), dtype=i64, device=dev)
+    if token_to_req is None:
+        token_to_req = torch.empty((T,), dtype=i32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty((T,), dtype=i64, device=dev)
+    if compressed_slot_mapping is None:
+        compressed_slot_mapping = torch.empty((T,), dtype=i64, device=dev)
     cbt = compressed_block_table
-    cstride, cwidth = (0, 0) if cbt is None else _table(cbt, "compressed_block_table", R)
-    outs = []
-    for t, dt, n in ((positions, torch.int64, "positions"), (token_to_req, torch.int32, "token_to_req"),
-                     (slot_mapping, torch.int64, "slot_mapping"),
-                     (compressed_slot_mapping, torch.int64, "compressed_slot_mapping")):
-        _vec(t, dt, n, T)
-        outs.append(torch.empty((max(T, 0),), dtype=dt, device=dev) if t is None else t)
-    _call(dev, "compute_slot_mappings", _ptr(query_start_loc), _ptr(seq_lens), R, T,
-          _ptr(block_table), stride, width, _ptr(base_offsets), block_size, _ptr(cbt), cstride,
-          cwidth, _ptr(compressed_base_offsets),
+    _call(dev, "compute_slot_mappings",
+          _vec(query_start_loc, i32, "query_start_loc", R + 1, i),
+          _vec(seq_lens, i32, "seq_lens", R, i), R, T,
+          *_table(block_table, "block_table", R, i),
+          _vec(base_offsets, i32, "base_offsets", R, i), block_size,
+          *((None, 0, 0) if cbt is None else _table(cbt, "compressed_block_table", R, i)),
+          _vec(compressed_base_offsets, i32, "compressed_base_offsets", R, i),
           block_size if compressed_block_size is None else compressed_block_size, compress_ratio,
-          *(_ptr(t) for t in outs))
-    return tuple(outs)
+          _vec(positions, i64, "positions", T, i), _vec(token_to_req, i32, "token_to_req", T, i),
+          _vec(slot_mapping, i64, "slot_mapping", T, i),
+          _vec(compressed_slot_mapping, i64, "compressed_slot_mapping", T, i))
+    return positions, token_to_req, slot_mapping, compressed_slot_mapping
 
 
 def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
@@ -644,71 +678,81 @@ def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
     """Grow ``block_table`` [R, width] int32 (in place) to the pages ``seq_lens`` needs, with
     pages of ``page_pool`` from ``pool_head`` on; returns (block_table, page_counts [R],
     pool_head [1]).  The inputs but the table are left as they were."""
-    _need_cuda(seq_lens, page_pool, block_table, page_counts, pool_head, page_counts_out,
-               pool_head_out, err_count)
-    dev, R = seq_lens.device, seq_lens.shape[0]
-    _vec(seq_lens, torch.int32, "seq_lens")
-    _vec(page_pool, torch.int32, "page_pool")
-    _vec(page_counts, torch.int32, "page_counts", R)
-    _vec(page_counts_out, torch.int32, "page_counts_out", R)
-    for t, n in ((pool_head, "pool_head"), (pool_head_out, "pool_head_out"),
-                 (err_count, "err_count")):
-        _vec(t, torch.int32, n, 1)
-    stride, width = _table(block_table, "block_table", R)
+    i, i32 = _index(seq_lens), torch.int32
+    dev, R = seq_lens.device, seq_lens.numel()
+    table, stride, width = _table(block_table, "block_table", R, i)
     if R > 1 and block_table.stride(0) < width:
         raise ValueError("rows of block_table must not overlap")
     if page_counts_out is None:
-        page_counts_out = torch.empty((R,), dtype=torch.int32, device=dev)
+        page_counts_out = torch.empty((R,), dtype=i32, device=dev)
     if pool_head_out is None:
-        pool_head_out = torch.empty((1,), dtype=torch.int32, device=dev)
+        pool_head_out = torch.empty((1,), dtype=i32, device=dev)
     if R == 0:  # no launch: the head stays where it is
         pool_head_out.fill_(0) if pool_head is None else pool_head_out.copy_(pool_head)
-    _call(dev, "extend_block_tables", _ptr(seq_lens), R, block_size, compress_ratio,
-          _ptr(page_counts), _ptr(page_pool), page_pool.shape[0], _ptr(pool_head),
-          _ptr(block_table), stride, width, _ptr(page_counts_out), _ptr(pool_head_out),
-          _ptr(err_count))
+    _call(dev, "extend_block_tables", _vec(seq_lens, i32, "seq_lens", R, i), R, block_size,
+          compress_ratio, _vec(page_counts, i32, "page_counts", R, i),
+          _vec(page_pool, i32, "page_pool", 0, i), page_pool.numel(),
+          _vec(pool_head, i32, "pool_head", 1, i), table, stride, width,
+          _vec(page_counts_out, i32, "page_counts_out", R, i),
+          _vec(pool_head_out, i32, "pool_head_out", 1, i),
+          _vec(err_count, i32, "err_count", 1, i))
     return block_table, page_counts_out, pool_head_out
 
 
 # ---- attention over paged fp8_ds_mla caches ------------------------------------------------
 
-def _heads(t: torch.Tensor, name: str):
-    """[T, H, D] bf16 with unit inner stride: its strides (a size-1 dim may carry any)."""
-    _need(t, torch.bfloat16, name)
+def _heads(t: torch.Tensor, name: str, index: int):
+    """Address and strides of a [T, H, D] bf16 tensor with unit inner stride (a size-1 dim may
+    carry any stride)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    _same(t, index, name)
     if t.dim() != 3 or t.stride(2) != 1:
         raise ValueError(f"{name} must be [T, H, D] with unit inner stride")
     T, H, D = t.shape
-    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+    st, sh, _ = t.stride()
+    return t.data_ptr(), (st if T > 1 else H * D), (sh if H > 1 else D)
 
 
-def _attention_outputs(q, sink, out, lse, workspace, need):
-    """Checked or allocated outputs and workspace of an attention call."""
+def _cache_of(cache: Optional[torch.Tensor], name: str, index: int):
+    if cache is None:
+        return None, 0, 0
+    _same(cache, index, name)
+    return (cache.data_ptr(), *_pages(cache))
+
+
+def _attention_outputs(q, out, lse, workspace, need, index):
+    """Allocated or checked outputs and workspace: (out, lse, the arguments for them)."""
     T, H, D = q.shape
-    if sink is not None:
-        _vec(sink, torch.float32, "sink", H)
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError(f"out {tuple(out.shape)} does not match q {tuple(q.shape)}")
+        o = (out.data_ptr(), H * D, D)
+    else:
+        if out.shape != q.shape:
+            raise ValueError(f"out {tuple(out.shape)} does not match q {tuple(q.shape)}")
+        o = _heads(out, "out", index)
     if lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _need(lse, torch.float32, "lse")
-    if lse.shape != (T, H) or (H > 1 and lse.stride(1) != 1):
-        raise ValueError(f"lse must be [{T}, {H}] with unit inner stride")
+        ls = H
+    else:
+        _need(lse, torch.float32, "lse")
+        _same(lse, index, "lse")
+        if lse.shape != (T, H) or (H > 1 and lse.stride(1) != 1):
+            raise ValueError(f"lse must be [{T}, {H}] with unit inner stride")
+        ls = lse.stride(0) if T > 1 else H
     if workspace is None:
         if need > 0:
             workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
-        _need(workspace, torch.uint8, "workspace")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    return out, lse, (lse.stride(0) if T > 1 else H), workspace
+        _vec(workspace, torch.uint8, "workspace", 0, index)
+    w = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    return out, lse, (*o, lse.data_ptr(), ls, *w)
 
 
-def _on(dev: torch.device, fn, *args):
-    """A size query that depends on the device: asked with ``dev`` current."""
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
+def _on(index: int, fn, *args):
+    """A size query that depends on the device: asked with that device current."""
+    if _current_device() != index:
+        with torch.cuda.device(index):
             return fn(*args)
     return fn(*args)
 
@@ -724,26 +768,22 @@ def sparse_mla_attention(q: torch.Tensor, cache: torch.Tensor, indices: torch.Te
     ``cache`` in columns [0, split), of ``extra_cache`` in the others (``split`` defaults to all
     columns).  Returns (out [T, H, D] bf16, lse [T, H] binary32); scale defaults to D^-1/2.
     ``workspace`` (uint8) is scratch; two calls that can run at once need one each."""
-    _need_cuda(q, cache, indices, extra_cache, sink, out, lse, workspace)
-    qt, qh = _heads(q, "q")
+    i = _index(q)
+    qa = _heads(q, "q", i)
     T, H, D = q.shape
     _need(indices, torch.int32, "indices")
+    _same(indices, i, "indices")
     if indices.dim() != 2 or indices.shape[0] != T:
         raise ValueError(f"indices must be [{T}, C]")
     C = indices.shape[1]
-    split = C if split is None else split
-    np_a, ps_a = _pages(cache)
-    np_b, ps_b = (0, 0) if extra_cache is None else _pages(extra_cache)
-    lib = _abi.lib()
-    need = _on(q.device, lib.sparse_mla_attention_workspace_bytes, T, H, D, C)
-    out, lse, ls, workspace = _attention_outputs(q, sink, out, lse, workspace, need)
-    ot, oh = _heads(out, "out")
-    _call(q.device, "sparse_mla_attention", _ptr(q), qt, qh, T, H, _ptr(cache), np_a, ps_a,
-          block_size, _ptr(extra_cache), np_b, ps_b,
+    need = _on(i, _abi.lib().sparse_mla_attention_workspace_bytes, T, H, D, C)
+    out, lse, oa = _attention_outputs(q, out, lse, workspace, need, i)
+    _call(q.device, "sparse_mla_attention", *qa, T, H, *_cache_of(cache, "cache", i), block_size,
+          *_cache_of(extra_cache, "extra_cache", i),
           block_size if extra_block_size is None else extra_block_size, D, rope_dim,
-          _ptr(indices), max(_rows(indices, "indices"), C), C, split,
-          D ** -0.5 if softmax_scale is None else softmax_scale, _ptr(sink), _ptr(out), ot, oh,
-          _ptr(lse), ls, _ptr(workspace), 0 if workspace is None else workspace.numel())
+          indices.data_ptr(), max(_rows(indices, "indices"), C), C, C if split is None else split,
+          D ** -0.5 if softmax_scale is None else softmax_scale,
+          _vec(sink, torch.float32, "sink", H, i), *oa)
     return out, lse
 
 
@@ -760,29 +800,21 @@ def chunk_mla_attention(q: torch.Tensor, cache: torch.Tensor, query_start_loc: t
     """Causal attention of a chunk of new tokens ``q`` [T, H, D] over their requests' positions
     through ``block_table`` (whole context, or the last ``window_size`` positions); rows of the
     new tokens must be in the cache.  Returns (out [T, H, D] bf16, lse [T, H] binary32)."""
-    _need_cuda(q, cache, query_start_loc, seq_lens, token_to_req, block_table, replay_start,
-               base_offsets, is_valid_token, sink, out, lse, workspace)
-    qt, qh = _heads(q, "q")
+    i, i32 = _index(q), torch.int32
+    qa = _heads(q, "q", i)
     T, H, D = q.shape
-    R = seq_lens.shape[0]
-    _vec(seq_lens, torch.int32, "seq_lens")
-    _vec(query_start_loc, torch.int32, "query_start_loc", R + 1)
-    _vec(token_to_req, torch.int32, "token_to_req", T)
-    _vec(replay_start, torch.int32, "replay_start", R)
-    _vec(base_offsets, torch.int32, "base_offsets", R)
-    stride, width = _table(block_table, "block_table", R)
+    R = seq_lens.numel()
+    table = _table(block_table, "block_table", R, i)
     valid = None if is_valid_token is None else is_valid_token.to(torch.uint8)
-    _vec(valid, torch.uint8, "is_valid_token", T)
-    pages, page_stride = _pages(cache)
-    lib = _abi.lib()
-    need = _on(q.device, lib.chunk_mla_attention_workspace_bytes, T, R, H, D, width,
-               block_size, window_size)
-    out, lse, ls, workspace = _attention_outputs(q, sink, out, lse, workspace, need)
-    ot, oh = _heads(out, "out")
-    _call(q.device, "chunk_mla_attention", _ptr(q), qt, qh, T, H, _ptr(cache), pages, page_stride,
-          block_size, D, rope_dim, _ptr(query_start_loc), _ptr(seq_lens), _ptr(token_to_req),
-          _ptr(replay_start), R, _ptr(block_table), stride, width, _ptr(base_offsets),
-          window_size, _ptr(valid), D ** -0.5 if softmax_scale is None else softmax_scale,
-          _ptr(sink), _ptr(out), ot, oh, _ptr(lse), ls, _ptr(workspace),
-          0 if workspace is None else workspace.numel())
+    need = _on(i, _abi.lib().chunk_mla_attention_workspace_bytes, T, R, H, D, table[2], block_size,
+               window_size)
+    out, lse, oa = _attention_outputs(q, out, lse, workspace, need, i)
+    _call(q.device, "chunk_mla_attention", *qa, T, H, *_cache_of(cache, "cache", i), block_size, D,
+          rope_dim, _vec(query_start_loc, i32, "query_start_loc", R + 1, i),
+          _vec(seq_lens, i32, "seq_lens", R, i), _vec(token_to_req, i32, "token_to_req", T, i),
+          _vec(replay_start, i32, "replay_start", R, i), R, *table,
+          _vec(base_offsets, i32, "base_offsets", R, i), window_size,
+          _vec(valid, torch.uint8, "is_valid_token", T, i),
+          D ** -0.5 if softmax_scale is None else softmax_scale,
+          _vec(sink, torch.float32, "sink", H, i), *oa)
     return out, lse
