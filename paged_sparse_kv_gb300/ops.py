@@ -757,6 +757,24 @@ def _on(index: int, fn, *args):
     return fn(*args)
 
 
+def sparse_mla_attention_workspace_bytes(device: torch.device, num_tokens: int, num_heads: int,
+                                         head_dim: int, cols: int) -> int:
+    """Bytes of ``workspace`` a sparse_mla_attention call of these sizes needs on ``device``."""
+    index = torch.device(device).index
+    return _on(_current_device() if index is None else index,
+               _abi.lib().sparse_mla_attention_workspace_bytes, num_tokens, num_heads, head_dim, cols)
+
+
+def chunk_mla_attention_workspace_bytes(device: torch.device, num_tokens: int, num_reqs: int,
+                                        num_heads: int, head_dim: int, table_width: int,
+                                        block_size: int, window_size: int = 0) -> int:
+    """Bytes of ``workspace`` a chunk_mla_attention call of these sizes needs on ``device``."""
+    index = torch.device(device).index
+    return _on(_current_device() if index is None else index,
+               _abi.lib().chunk_mla_attention_workspace_bytes, num_tokens, num_reqs, num_heads,
+               head_dim, table_width, block_size, window_size)
+
+
 def sparse_mla_attention(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor,
                          block_size: int, *, extra_cache: Optional[torch.Tensor] = None,
                          extra_block_size: Optional[int] = None, split: Optional[int] = None,

@@ -434,7 +434,8 @@ def test_repeatable_and_on_streams(cuda_device):
         for k in set(order):
             assert torch.equal(outs[k][0], want[k][0]) and torch.equal(outs[k][1], want[k][1])
     # one scratch buffer for calls that follow each other on a stream
-    need = max(1, 1 << 24)
+    need = max(ops.sparse_mla_attention_workspace_bytes(d, q.shape[0], q.shape[1], 512, i.shape[1])
+               for q, _, i in cases)
     ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=d)
     for q, c, i in cases * 2:
         k = 0 if q.shape[0] == 24 else 1
