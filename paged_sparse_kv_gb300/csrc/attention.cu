@@ -8,37 +8,34 @@
 //
 // Layout.  All heads of a token share its rows, so the work of a CTA is one
 // token with up to 64 heads (a "unit"; a small head count takes several
-// neighbouring tokens of one request), walked in tiles of 64 rows:
-//   S^T [64 rows x N columns]  = K [64 x D] Q^T          (D/16 MMAs of M = 64)
-//   O^T [D x N]               += K^T [D x 64] P^T        (D/128 x 4 MMAs of M = 128)
-// A column is one (token, head).  O^T for head_dim 512 takes 4 * 64 of the 512
-// columns of tensor memory, which the untransposed form (128 heads x 512 dims)
-// would fill alone.  K is dequantised once per tile into one 128-byte-swizzled
-// bf16 tile that both products read: with the dims contiguous as the K-major A
+// neighbouring tokens of one request), walked in tiles of 128 rows:
+//   S^T [128 rows x N columns]  = K [128 x D] Q^T         (D/16 MMAs of M = 128)
+//   O^T [D x N]                += K^T [D x 128] P^T       (D/128 x 8 MMAs)
+// A column is one (token, head).  Rows on the M side let every head count use
+// full 128-row MMAs and keep O^T for head_dim 512 in 4 * 64 of the 512 columns
+// of tensor memory, which the untransposed form (128 heads x 512 dims) would
+// fill alone.  K is dequantised once per tile into one 128-byte-swizzled bf16
+// tile that both products read: with the dims contiguous as the K-major A
 // operand of the first, as the M-major A operand of the second.
 //
-// Pipeline.  Two tiles are in work: while the workers turn the scores of tile i - 1
-// into weights, the tensor cores form those of tile i; while the workers
-// dequantise tile i + 1, the second product takes tile i - 1.  That is why a tile
-// has 64 rows, although the first product then runs at half rate (34 cycles an MMA
-// against 49 with 128 rows; the second product costs the same per row): two
-// tiles of 128 rows do not fit beside the queries, and with one the workers and
-// the tensor cores wait for each other.
-//
-// Roles.  8 worker warps dequantise and form the weights, and write O^T at the end
-// of a unit; one warp issues the MMAs; one plans ahead: it finds the tiles that hold
-// anything visible and puts the addresses of their rows into a ring, across
-// units.  Every wait is bounded (2 s of wall time, counted in
-// psk_device_wait_timeouts).
+// Roles.  8 worker warps dequantise a tile, take the softmax of S^T and at the
+// end of a unit write O^T; one thread issues the MMAs; one warp plans ahead: it
+// finds the tiles that hold anything visible and puts the addresses of their
+// rows into a ring, across units.  The tile is handed over in blocks of
+// 128 dims: the first product follows the dequantisation block by block, and
+// the next tile is dequantised into the blocks the second product has finished
+// with.  The first loads of a tile are in flight during the softmax of the one
+// before.  Every wait is bounded (2 s of
+// wall time, counted in psk_device_wait_timeouts).
 //
 // Softmax in one pass: a running reference m per column.  It follows the
 // maximum lazily: the first tile sets it, and later ones raise it only where a
 // weight would exceed 2^16, so that O^T is hardly ever rescaled and the maxima
-// of most tiles are never formed; the reference cancels in out and in lse.
-// Sums and weights are binary32; the weights are rounded to bf16 for the second
-// product alone (the operands of one MMA share a type, and a row's bf16 values do
-// not fit fp16's range), while l sums them unrounded, so that lse keeps binary32
-// accuracy and the roundings in out, being unbiased, average out.
+// of most tiles are never formed; the reference cancels in out and in lse.  Sums and weights are binary32; the weights are
+// rounded to bf16 for the second product alone (the operands of one MMA share a
+// type, and a row's bf16 values do not fit fp16's range), while l sums them
+// unrounded, so that lse keeps binary32 accuracy and the roundings in out, being
+// unbiased, average out.
 #include <atomic>
 #include <cmath>
 
@@ -49,17 +46,15 @@
 namespace psk {
 namespace {
 
-constexpr int kTile = 64;             // rows of a tile (M of the first product)
-constexpr int kWorkers = 8;           // worker warps
-constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 16 rows
-constexpr int kMmaWarp = kWorkers;
-constexpr int kPlanWarp = kWorkers + 1;
-constexpr int kThreads = (kWorkers + 2) * kWarp;
-constexpr int kChunkBytes = kTile * 128;  // 64 dims of a tile's rows
+constexpr int kTile = 128;            // rows of a tile (M of the first product)
+constexpr int kMaxWorkers = 16;
+constexpr int kMaxGroups = kMaxWorkers / 4;
+constexpr int kMaxBlocks = 4;         // 128-dim blocks of a row (head_dim 512)
+constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMostWeight = 65536.0f;  // a weight above it has its column's reference raised
+constexpr float kLazy = 16.0f;        // log2 units the maximum may run ahead of the reference
 constexpr float kNone = -3.0e38f;     // reference of a column that has seen nothing
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -71,10 +66,19 @@ __device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
+template <int kSrc>
+struct Roles {
+    static constexpr int kWorkers = kSrc == kTokens ? 16 : 8;  // worker warps
+    static constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 32 rows
+    static constexpr int kMmaWarp = kWorkers, kPlanWarp = kWorkers + 1;
+    static constexpr int kThreads = (kWorkers + 2) * kWarp;
+};
+
 // A set of columns; its tiles follow one another in the stream of tiles.
 struct Unit {
     int32_t part;                  // which part of the split work (row of the workspace)
-    int32_t pad[3];
+    int32_t all_lo, all_hi;        // kTokens: positions that every column in use sees
+    int32_t pad;
     int64_t col_q[kMaxCols];       // element offset of the column's query
     int64_t col_out[kMaxCols];     // and of its output row (of its part, where the work is split)
     float col_sink[kMaxCols];      // log2 units; -infinity without one
@@ -99,21 +103,21 @@ struct Tile {
     Row row[kTile];
 };
 
-constexpr int kTiles = 4;  // tiles the planning warp may be ahead, the current one included
-
-constexpr int kUnits = 3;  // the unit being written out, the one in work, the next one
+constexpr int kTiles = 3;  // tiles the planning warp may be ahead, the current one included
 
 struct Shared {
     Tile tile[kTiles];
-    Unit unit[kUnits];
-    alignas(16) float red[kGroups][2][4][kMaxCols / kGroups];  // [group][exchange parity][quad][column]
-    alignas(16) float aux[kGroups][2][kMaxCols / kGroups];     // factors of the columns
-    int32_t over[2];               // a weight of the step is out of range: its reference is raised
+    Unit unit[2];
+    alignas(16) float red[2][4][kMaxCols];  // [parity of the group's exchange][quad][column]
+    alignas(16) float ref[4 * kMaxCols];    // a copy per quad, by warps
+    alignas(16) float aux[4 * kMaxCols];
+    int32_t over[kMaxGroups][2][4];
     uint64_t tile_full[kTiles], tile_empty[kTiles];
-    uint64_t unit_empty[kUnits];
-    uint64_t full[2], freed[2];    // the tile is dequantised; the second product is done with it
-    uint64_t s_ready[2], p_ready, drain;
-    uint64_t group_bar[kGroups];
+    uint64_t unit_empty[2];
+    uint64_t full[kMaxBlocks];     // 128 dims of the tile are dequantised
+    uint64_t freed[kMaxBlocks];    // the second product is done with them
+    uint64_t s_ready, p_ready, drain;
+    uint64_t group_bar[kMaxGroups];
     uint32_t tmem;
     uint2 scales[2][kTile];        // UE8M0 bytes of the rows
     uint8_t row_bad[2][kTile];     // kTokens: the row holds a NaN or an infinity
@@ -256,7 +260,7 @@ __device__ __forceinline__ void publish(Shared& sh, Stream& st, int lane, int32_
     Tile& t = sh.tile[st.tiles % kTiles];
     if (lane == 0) {
         t.flags = flags;
-        t.unit = st.units % kUnits;
+        t.unit = st.units & 1;
         t.pos = pos;
     }
     __syncwarp();
@@ -304,10 +308,9 @@ __device__ __forceinline__ bool stream_unit(const AttnParams& p, Shared& sh, Str
     return true;
 }
 
-// Waits for the slot of the next unit.
+// Waits for the slot of the next unit, which two units before it have used.
 __device__ __forceinline__ bool unit_slot(Shared& sh, const Stream& st) {
-    return st.units < kUnits ||
-           wait_all(&sh.unit_empty[st.units % kUnits], (st.units / kUnits - 1) & 1);
+    return st.units < 2 || wait_all(&sh.unit_empty[st.units & 1], ((st.units >> 1) - 1) & 1);
 }
 
 __device__ __forceinline__ void set_column(const AttnParams& p, const LaunchShape& ls, Unit& un, int c,
@@ -348,7 +351,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
             }
             share(n, part, ls.splits, first, end);
             if (!unit_slot(sh, st)) return false;
-            Unit& un = sh.unit[st.units % kUnits];
+            Unit& un = sh.unit[st.units & 1];
             if (lane == 0) un.part = part;
 #pragma unroll
             for (int c = lane; c < kMaxCols; c += kWarp) 
@@ -377,8 +380,14 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 int32_t first, end;
                 share(tiles, part, ls.splits, first, end);
                 if (!unit_slot(sh, st)) return false;
-                Unit& un = sh.unit[st.units % kUnits];
-                if (lane == 0) un.part = part;
+                Unit& un = sh.unit[st.units & 1];
+                const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, lane >= a && lane < b ? x.lo : INT32_MIN);
+                const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, lane >= a && lane < b ? x.hi : INT32_MAX);
+                if (lane == 0) {
+                    un.part = part;
+                    un.all_lo = all_lo;
+                    un.all_hi = all_hi;
+                }
 #pragma unroll
                 for (int k = 0; k < kMaxCols / kWarp; ++k) {
                     const int c = lane + k * kWarp;
@@ -396,76 +405,70 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
     return true;
 }
 
-// True once for a step whose weights did not fit, as everyone learns when the
-// first round of them is complete.
-struct Again {
-    uint32_t step = ~0u;
-    __device__ __forceinline__ bool operator()(const Shared& sh, uint32_t now) {
-        if (step == now) return false;
-        step = now;
-        return __shfl_sync(0xFFFFFFFFu, *const_cast<const volatile int32_t*>(&sh.over[now & 1]), 0) != 0;
-    }
-};
-
-// ---- the MMA warp ----------------------------------------------------------------------
+// ---- the MMA thread ------------------------------------------------------------------
 //
-// The first product of a tile is issued before the second one of the tile before.
+// Both products take the 128-dim blocks in one order: first those without rope
+// dims, from the last one down, then those with rope dims, whose copies take
+// longest.  The second product frees them from the last block down, the order
+// they are dequantised in.
+
 // The whole warp walks the pipeline, so that descriptors stay in uniform
 // registers; one elected lane issues.
 template <int N, int D>
-__device__ bool issue(Shared& sh, uint32_t k_tile, uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
-    constexpr int kBlocks = D / 128, kTileBytes = D / 64 * kChunkBytes, kWeightBytes = kTile * N * 2;
+__device__ bool issue(Shared& sh, int rope_from, uint32_t k_tile, uint32_t q_tile, uint32_t p_tile,
+                      uint32_t tmem) {
+    constexpr int kBlocks = D / 128;
     constexpr uint32_t kS = umma_idesc(kTile, N, false), kO = umma_idesc(128, N, true);
     // K-major, 128-byte swizzle: 8-row groups 1024 bytes apart, 32 bytes a step of 16 dims
     const uint64_t k_desc = umma_desc(k_tile, 16, 1024, kSwizzle128);
     const uint64_t q_desc = umma_desc(q_tile, 16, 1024, kSwizzle128);
     // A of the second product: M-major, 128-byte swizzle: 64-dim chunks kChunkBytes apart,
-    // 8-row groups 1024 bytes apart.  B: N-major, no swizzle: 8-column groups a tile's
-    // rows * 16 bytes apart, 8-row groups 128 bytes apart.
+    // 8-row groups 1024 bytes apart.  B: N-major, no swizzle: 8-column groups 2048 bytes
+    // apart, 8-row groups 128 bytes apart.
     const uint64_t v_desc = umma_desc(k_tile, kChunkBytes, 1024, kSwizzle128);
-    const uint64_t p_desc = umma_desc(p_tile, 128, kTile * 16, kSwizzleNone);
+    const uint64_t p_desc = umma_desc(p_tile, 128, 2048, kSwizzleNone);
     const uint32_t lead = elect_one();
-    uint32_t step = 0, round = 0;  // tiles; phases of p_ready
-    Again again;
-    bool pending = false, pending_first = false;  // the second product of tile step - 1
-    const auto second_product = [&]() {
-        do {  // a second round of weights follows where a reference had to be raised
-            if (!wait_all(&sh.p_ready, round++ & 1)) return false;
-        } while (!pending_first && again(sh, step - 1));
-        tmem_fence_after();
-        const uint32_t b = (step - 1) & 1;
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-                umma_bf16(tmem + j * N, v_desc + ((b * kTileBytes + j * 2 * kChunkBytes + k * 2048) >> 4),
-                          p_desc + ((b * kWeightBytes + k * 256) >> 4), kO, !pending_first || k > 0, lead);
-        umma_commit(&sh.freed[b], lead);
-        pending = false;
-        return true;
-    };
+    uint32_t step = 0;
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles;
         if (!wait_all(&sh.tile_full[slot], (seq / kTiles) & 1)) return false;
         const int32_t flags = __shfl_sync(0xFFFFFFFFu, sh.tile[slot].flags, 0);
         if (lead) mbar_arrive(&sh.tile_empty[slot]);
-        if (flags & (kDone | kEmpty)) {
-            if (pending && !second_product()) return false;
-            if (flags & kDone) return true;
-            continue;
-        }
-        const uint32_t b = step & 1;
-        if (!wait_all(&sh.full[b], (step >> 1) & 1)) return false;
-        tmem_fence_after();
+        if (flags & kDone) return true;
+        if (flags & kEmpty) continue;
+        const auto first_product = [&](int j, bool first) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            umma_bf16(tmem + kBlocks * N + b * N,
-                      k_desc + ((b * kTileBytes + k / 4 * kChunkBytes + (k % 4) * 32) >> 4),
-                      q_desc + ((k / 4 * (N * 128) + (k % 4) * 32) >> 4), kS, k > 0, lead);
-        umma_commit(&sh.s_ready[b], lead);
-        if (pending && !second_product()) return false;
-        pending = true;
-        pending_first = flags & kFirst;
+            for (int k = 0; k < 8; ++k)
+                umma_bf16(tmem, k_desc + ((j * 2 * kChunkBytes + (k / 4) * kChunkBytes + (k % 4) * 32) >> 4),
+                          q_desc + ((j * 2 * (N * 128) + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), kS,
+                          !first || k > 0, lead);
+        };
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {  // blocks without rope dims
+            if (j >= rope_from) continue;
+            if (!wait_all(&sh.full[j], step & 1)) return false;
+            tmem_fence_after();
+            first_product(j, j == rope_from - 1);
+        }
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {
+            if (j < rope_from) break;
+            if (!wait_all(&sh.full[j], step & 1)) return false;
+            tmem_fence_after();
+            first_product(j, rope_from == 0 && j == kBlocks - 1);
+        }
+        umma_commit(&sh.s_ready, lead);
+        if (!wait_all(&sh.p_ready, step & 1)) return false;
+        tmem_fence_after();
+        const bool first_tile = flags & kFirst;
+#pragma unroll
+        for (int j = kBlocks - 1; j >= 0; --j) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                umma_bf16(tmem + N + j * N, v_desc + ((j * 2 * kChunkBytes + k * 2048) >> 4),
+                          p_desc + ((k * 256) >> 4), kO, !first_tile || k > 0, lead);
+            umma_commit(&sh.freed[j], lead);
+        }
         ++step;
     }
 }
@@ -485,6 +488,21 @@ __device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8
         w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
         w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
     }
+}
+
+// Whether any of 16 E4M3 bytes of scale byte b may be NaN or overflow bf16: a byte
+// of all ones below its sign, or a scale that takes the largest value, 1.75 * 2^8, past 2^128.
+__device__ __forceinline__ bool may_be_non_finite(uint4 raw, uint32_t b) {
+    const uint32_t ones = ((raw.x & 0x7F7F7F7Fu) + 0x01010101u) | ((raw.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                          ((raw.z & 0x7F7F7F7Fu) + 0x01010101u) | ((raw.w & 0x7F7F7F7Fu) + 0x01010101u);
+    return (ones & 0x80808080u) != 0 || b >= 127 + 128 - 8;
+}
+
+// The same of eight bf16 values: all exponent bits set.
+__device__ __forceinline__ bool any_non_finite(uint4 v) {
+    const uint32_t ones = ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                          ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+    return (ones & 0x80008000u) != 0;
 }
 
 // Clears the non-finite values of w; true if there were any.
@@ -509,7 +527,7 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;
 
 // Queries of a unit into the swizzled B tile of the first product; unused
 // columns are zero.  Asynchronous.
-template <int N, int D>
+template <int N, int D, int kWorkers>
 __device__ __forceinline__ void load_queries(const AttnParams& p, const Unit& un, uint32_t q_tile, int tid) {
     const int part = tid & 7;
 #pragma unroll
@@ -524,132 +542,76 @@ __device__ __forceinline__ void load_queries(const AttnParams& p, const Unit& un
     }
 }
 
-// Closes column n of a unit (reference m, sum of weights `total`): stores its lse, or
-// its reference and sum where the work is split; returns the factor of its O^T.
-__device__ __forceinline__ float finish_column(const AttnParams& p, const LaunchShape& ls, const Unit& un, int n,
-                                               float m, float total) {
-    const int32_t t = un.col_token[n], h = un.col_head[n];
-    if (t < 0) return 0.0f;
-    const bool none = m == kNone;
-    if (ls.splits > 1) {
-        float* ml = ls.part_ml + (((int64_t)t * p.num_heads + h) * ls.splits + un.part) * 2;
-        ml[0] = none ? -INFINITY : m;
-        ml[1] = total;
-        return 1.0f;
-    }
-    const float ref = none ? 0.0f : m;
-    const float den = total + ex2_approx(un.col_sink[n] - ref);
-    if (p.lse)
-        p.lse[(int64_t)t * p.lse_stride_t + h] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
-    return total == 0.0f ? 0.0f : 1.0f / den;
-}
-
-// Writes the NC columns of a warp's group, 32 dims of each block per warp: `srow` is
-// the lane's dim in a block.  Without `sums` the unit saw nothing.
-template <int N, int D, int NC>
-__device__ __forceinline__ void write_out(const AttnParams& p, const LaunchShape& ls, const Unit& un, uint32_t o_base,
-                                          const float* factor, int group, int srow, int lane, bool sums) {
-    constexpr int kBlocks = D / 128;
-    if (ls.splits > 1) {
-        for (int j = 0; j < kBlocks; ++j) {
-            float o[NC];
+// Sum of v[k] over the 32 lanes: lane i gets the sum of column i % K.  Halves the
+// columns a lane holds at each exchange (K - 1 shuffles instead of 5 K).
+template <int K>
+__device__ __forceinline__ float column_sums(float (&v)[K], int lane) {
 #pragma unroll
-            for (int k = 0; k < NC; ++k) o[k] = 0.0f;
-            if (sums) tmem_ld<NC>(o_base + j * N, o);
-            const int d = j * 128 + srow;
+    for (int w = K / 2; w >= 1; w /= 2) {
+        const bool up = lane & w;
 #pragma unroll
-            for (int k0 = 0; k0 < NC; k0 += 8) {
-                int64_t at[8];
-                bool used[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    at[k] = un.col_out[group * NC + k0 + k] + d;
-                    used[k] = un.col_token[group * NC + k0 + k] >= 0;
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (used[k]) ls.part_o[at[k]] = o[k0 + k];
-            }
-        }
-        return;
-    }
-    // 4 x 4 exchanges among four lanes: each then holds four dims of the columns
-    // k + lane % 4, where it stores them
-    uint16_t* dst[NC / 4];
-#pragma unroll
-    for (int k = 0; k < NC / 4; ++k) {
-        const int n = group * NC + 4 * k + (lane & 3);
-        dst[k] = un.col_token[n] >= 0 ? p.out + un.col_out[n] + (srow & ~3) : nullptr;
-    }
-    const bool odd = lane & 1, upper = lane & 2;
-    for (int j = 0; j < kBlocks; ++j) {
-        float o[NC];
-#pragma unroll
-        for (int k = 0; k < NC; ++k) o[k] = 0.0f;
-        if (sums) tmem_ld<NC>(o_base + j * N, o);
-#pragma unroll
-        for (int k = 0; k < NC / 4; ++k) {
-            float4 f = make_float4(0, 0, 0, 0);
-            if (sums) f = *reinterpret_cast<const float4*>(&factor[4 * k]);
-            const float a0 = o[4 * k] * f.x, a1 = o[4 * k + 1] * f.y;
-            const float a2 = o[4 * k + 2] * f.z, a3 = o[4 * k + 3] * f.w;
-            const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
-            const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
-            // columns 4 k (+ 1 if odd) and 4 k + 2 (+ 1)
-            const uint32_t w0 = pack_bf16x2(odd ? b0 : a0, odd ? a1 : b0);
-            const uint32_t w1 = pack_bf16x2(odd ? b1 : a2, odd ? a3 : b1);
-            const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
-            if (dst[k] != nullptr) st_v2(dst[k] + j * 128, make_uint2(upper ? x : w0, upper ? w1 : x));
+        for (int i = 0; i < w; ++i) {
+            const float send = up ? v[i] : v[i + w];
+            v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, w);
         }
     }
+    float x = v[0];
+#pragma unroll
+    for (int o = K; o < kWarp; o *= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
 }
 
-// A worker warp dequantises 8 rows of a tile.  A 128-dim block of E4M3 dims is read
-// by 8 lanes per row, 16 bytes each, so that a load covers 4 rows of 128 bytes (a
-// load of 16 rows would take one pass through the L1 tags per row); the two 64-dim
-// chunks and two rows are spread over the lanes so that every eight of them store
-// to eight different 16-byte banks.
-//
-// Scores come as the fragments of the 16-lane load shape: a lane has rows lane / 4
-// and lane / 4 + 8 of its warp's 16 and columns 2 (lane % 4) + {0, 1} of every 8, so
-// that it keeps the references and sums of few columns in registers.
+// Dequantisation: a worker warp owns 16 rows of the tile.  A 128-dim block without
+// rope dims is read by 8 lanes per row, 16 bytes each, so that a load covers 4
+// rows of 128 bytes (a load of 16 rows would take one pass through the L1 tags
+// per row); the two 64-dim chunks and two rows are spread over the lanes so
+// that every eight of them store to eight different 16-byte banks.
 template <int N, int kSrc, int D>
 __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint32_t k_tile,
                      uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
-    constexpr int NC = N / kGroups;                    // columns of a worker warp
-    constexpr int kPairs = NC / 8, kCols = 2 * kPairs; // column pairs and columns of a lane
+    constexpr int kWorkers = Roles<kSrc>::kWorkers, kGroups = Roles<kSrc>::kGroups;
+    constexpr int NC = N / kGroups;  // columns of a worker warp
     constexpr int kChunks = D / 64, kBlocks = D / 128;
-    constexpr int kTileBytes = kChunks * kChunkBytes, kWeightBytes = kTile * N * 2;
-    constexpr int kOwn = kTile / kWorkers;             // rows a warp dequantises
-    static_assert(kOwn == 8, "the lane maps below");
+    constexpr int kOwn = kTile / kWorkers;             // rows of a warp
+    static_assert(kOwn == 16 || kOwn == 8, "the lane maps below");
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     const int quad = warp % 4, group = warp / 4;
+    const int srow = quad * kWarp + lane;              // softmax: the tile row of this lane
     const int nope = D - p.rope_dim, fp8_chunks = nope / 64;
-    const int pure = nope / 128;                       // blocks from here on hold rope dims
+    const int rope_from = nope / 128;                  // blocks from here on hold rope dims
     const bool mixed = fp8_chunks % 2 != 0;            // and the first of them E4M3 dims too
     const int own = warp * kOwn;
-    // block map: rows own + b_row + 4 i, 16 bytes at b_byte, in chunk b_chunk of the block
-    const int b_row = (lane >> 4) * 2 + ((lane >> 2) & 1), b_chunk = (lane >> 3) & 1;
+    // block map: rows b_row + 4 i, 16 bytes at b_byte, in chunk b_chunk of the block
+    const int b_row = own + (lane >> 4) * 2 + ((lane >> 2) & 1), b_chunk = (lane >> 3) & 1;
     const int b_byte = b_chunk * 64 + (lane & 3) * 16;
-    const uint32_t b_dst = k_tile + b_chunk * kChunkBytes + (own + b_row) * 128 + (((2 * (lane & 3)) ^ b_row) * 16);
-    // chunk map: row own + lane / 4, 16 bytes at 16 (lane % 4)
-    const int c_row = lane >> 2;
-    const uint32_t c_dst = k_tile + (own + c_row) * 128 + (((2 * (lane & 3)) ^ c_row) * 16);
-    // rope map: rows own + r_row + 4 i, 16 bytes at 16 (lane % 8)
-    const int r_row = lane >> 3;
-    const uint32_t r_dst = k_tile + (own + r_row) * 128 + (((lane & 7) ^ r_row) * 16);
-    const uint32_t s_base = tmem + kBlocks * N + ((uint32_t)(quad * kWarp) << 16) + group * NC;
-    const uint32_t o_base = tmem + ((uint32_t)(quad * kWarp) << 16) + group * NC;
-    const int row0 = quad * 16 + (lane >> 2);          // softmax: rows row0 and row0 + 8 of the tile
-    const uint32_t w_dst = p_tile + group * (NC / 8) * (kTile * 16) + row0 * 16 + (lane & 3) * 4;
-    uint32_t step = 0, exchange = 0, round = 0;        // tiles; group exchanges; phases of p_ready
-    Again again;
+    const uint32_t b_dst = k_tile + b_chunk * kChunkBytes + b_row * 128 + (((2 * (lane & 3)) ^ (b_row & 7)) * 16);
+    // chunk map: rows c_row + 8 i, 16 bytes at 16 (lane % 4)
+    const int c_row = own + (lane >> 2);
+    const uint32_t c_dst = k_tile + c_row * 128 + (((2 * (lane & 3)) ^ (c_row & 7)) * 16);
+    // rope map: rows r_row + 4 i, 16 bytes at 16 (lane % 8)
+    const int r_row = own + (lane >> 3);
+    const uint32_t r_dst = k_tile + r_row * 128 + (((lane & 7) ^ (r_row & 7)) * 16);
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * kWarp) << 16) + group * NC;
+    float* const aux = sh.aux + warp * NC;  // factors of the columns
+    uint32_t step = 0, exchange = 0;
 
-    float l[kCols], ref[kCols];
-    uint4 raw[kBlocks][2];     // the tile's blocks as loaded: E4M3 of two rows; [pure][0]: a mixed chunk
-    uint2 scales = make_uint2(0, 0);  // of row own + lane % 8
-    const auto load_tile = [&](const Tile& t) {
-        const uint8_t* sc = t.row[own + (lane & 7)].scales;
+    float l[NC];
+    float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
+    constexpr int kFours = kOwn / 4, kEights = kOwn / 8;
+    uint4 raw[2][kFours];      // blocks rope_from - 1, rope_from - 2, ... of a lane's rows
+    uint4 raw_chunk[kEights];        // the E4M3 chunk of a mixed block
+    uint2 scales = make_uint2(0, 0);  // of row own + lane % 16
+
+    const auto load_block = [&](const Tile& t, uint4(&x)[kFours], int j) {
+        const uint8_t* data[kFours];
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) data[i] = t.row[b_row + 4 * i].data;
+#pragma unroll
+        for (int i = 0; i < kFours; ++i) x[i] = ld_stream_v4(data[i] + j * 128 + b_byte);
+    };
+    // starts the first loads of a tile
+    const auto start = [&](const Tile& t) {
+        const uint8_t* sc = t.row[own + lane % kOwn].scales;
         if (D == 512) {
             scales = ld_nc_v2(sc);
         } else if (D == 256) {
@@ -657,309 +619,325 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
         } else {
             scales.x = ld_nc_u8(sc) | (ld_nc_u8(sc + 1) << 8);
         }
-        const uint8_t* d0 = t.row[own + b_row].data + b_byte;
-        const uint8_t* d1 = t.row[own + b_row + 4].data + b_byte;
+        if (mixed) {
+            const uint8_t* data[kEights];
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            if (j < pure) {
-                raw[j][0] = ld_stream_v4(d0 + j * 128);
-                raw[j][1] = ld_stream_v4(d1 + j * 128);
-            } else if (j == pure && mixed) {
-                raw[j][0] = ld_stream_v4(t.row[own + c_row].data + (fp8_chunks - 1) * 64 + (lane & 3) * 16);
-            }
+            for (int i = 0; i < kEights; ++i) data[i] = t.row[c_row + 8 * i].data;
+#pragma unroll
+            for (int i = 0; i < kEights; ++i) raw_chunk[i] = ld_stream_v4(data[i] + (fp8_chunks - 1) * 64 + (lane & 3) * 16);
         }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            if (b < rope_from) load_block(t, raw[b], rope_from - 1 - b);
     };
 
     if (!wait_all(&sh.tile_full[0], 0)) return false;
     int32_t flags = sh.tile[0].flags;
-    bool loaded = false;           // the tile's loads are under way
-    // the tile whose weights are due
-    int32_t prev = 0, prev_unit = 0, prev_pos = 0;
-    bool due = false, ok0 = false, ok1 = false;
+    if (!(flags & (kDone | kEmpty))) {
+        load_queries<N, D, kWorkers>(p, sh.unit[sh.tile[0].unit], q_tile, tid);
+        start(sh.tile[0]);
+    }
     for (int seq = 0;; ++seq) {
         const int slot = seq % kTiles, nslot = (seq + 1) % kTiles;
         const Tile& tl = sh.tile[slot];
-        const bool rows = !(flags & (kDone | kEmpty));
-        const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
-        bool cur_ok0 = false, cur_ok1 = false;
-        int32_t next_flags = 0;
-        if (rows) {
-            // ---- dequantisation of the tile
+        const Unit& un = sh.unit[tl.unit];
+        if (flags & kDone) return true;
+        if (flags & kFirst) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) l[i] = 0.0f;
+            m_used = -INFINITY;
+        }
+        if (!(flags & kEmpty)) {
             const int buf = step & 1;
-            if (!loaded) load_tile(tl);
-            if (flags & kFirst) {
-                // the queries' place is free when the last tile's first product is done
-                if (step > 0 && !wait_all(&sh.s_ready[buf ^ 1], ((step - 1) >> 1) & 1)) return false;
-                load_queries<N, D>(p, sh.unit[tl.unit], q_tile, tid);
-            }
             if (lane < kOwn) {
                 sh.scales[buf][own + lane] = scales;
                 if (kSrc == kTokens) sh.row_bad[buf][own + lane] = 0;
             }
-            cur_ok0 = tl.row[row0].data != zero;
-            cur_ok1 = tl.row[row0 + 8].data != zero;
             __syncwarp();
-            const uint8_t* sc = reinterpret_cast<const uint8_t*>(sh.scales[buf] + own);
-            const uint32_t at = buf * kTileBytes;
-            bool free = step < 2;  // the second product of two tiles ago is done with the place
-            const auto need = [&]() {
-                if (!free && !wait_all(&sh.freed[buf], ((step >> 1) - 1) & 1)) return false;
-                free = true;
-                return true;
+            const uint8_t* sc = reinterpret_cast<const uint8_t*>(sh.scales[buf]);
+            // ---- dequantisation, from the last dims down
+            int block = kBlocks;  // blocks from here on are free
+            const auto need = [&](int j) {
+                if (j >= block) return true;
+                block = j;
+                return step == 0 || wait_all(&sh.freed[j], (step - 1) & 1);
             };
-            const auto put = [&](uint4 x, int row, int chunk, uint32_t dst) {
+            const auto put = [&](uint4 x, uint32_t scale, int row, uint32_t dst) {
                 uint32_t w[8];
-                dequant16(x, sc[row * 8 + chunk], w);
-                if (kSrc == kTokens && clear_non_finite(w)) sh.row_bad[buf][own + row] = 1;
+                dequant16(x, scale, w);
+                if (kSrc == kTokens && may_be_non_finite(x, scale) && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
                 sts_v4(dst, w[0], w[1], w[2], w[3]);
                 sts_v4(dst ^ 16, w[4], w[5], w[6], w[7]);
             };
-            if (!need()) return false;
-            for (int c = fp8_chunks; c < kChunks; ++c) {  // rope dims: bf16 as stored
-                const int off = nope + (c * 64 - nope) * 2 + (lane & 7) * 16;
+            if (fp8_chunks < kChunks) {
+                const uint8_t* data[kFours];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t* src = tl.row[own + r_row + 4 * i].data + off;
-                    const uint32_t dst = (r_dst + at + c * kChunkBytes + i * 512) ^ (i * 64);
-                    if (kSrc == kTokens) {
-                        const uint4 x = ld_stream_v4(src);
-                        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        if (clear_non_finite(w)) sh.row_bad[buf][own + r_row + 4 * i] = 1;
-                        sts_v4(dst, w[0], w[1], w[2], w[3]);
-                    } else {
-                        copy16(dst, src, 16);
+                for (int i = 0; i < kFours; ++i) data[i] = tl.row[r_row + 4 * i].data;
+                for (int c = kChunks - 1; c >= fp8_chunks; --c) {  // rope dims: bf16 as stored
+                    if (!need(c / 2)) return false;
+                    const int at = nope + (c * 64 - nope) * 2 + (lane & 7) * 16;
+#pragma unroll
+                    for (int i = 0; i < kFours; ++i) {
+                        const uint32_t dst = (r_dst + c * kChunkBytes + i * 512) ^ ((i & 1) * 64);
+                        if (kSrc == kTokens) {
+                            const uint4 x = ld_stream_v4(data[i] + at);
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            if (any_non_finite(x) && clear_non_finite(w)) sh.row_bad[buf][r_row + 4 * i] = 1;
+                            sts_v4(dst, w[0], w[1], w[2], w[3]);
+                        } else {
+                            copy16(dst, data[i] + at, 16);
+                        }
                     }
                 }
             }
+            if (mixed) {
+                const int c = fp8_chunks - 1;
+                uint32_t scale[kEights];
 #pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-                if (j < pure) {
+                for (int i = 0; i < kEights; ++i) scale[i] = sc[(c_row + 8 * i) * 8 + c];
+                if (!need(c / 2)) return false;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)  // 4 rows on, bit 2 of the swizzle turns
-                        put(raw[j][i], b_row + 4 * i, 2 * j + b_chunk,
-                            (b_dst + at + j * 2 * kChunkBytes + i * 512) ^ (i * 64));
-                } else if (j == pure && mixed) {
-                    put(raw[j][0], c_row, fp8_chunks - 1, c_dst + at + (fp8_chunks - 1) * kChunkBytes);
+                for (int i = 0; i < kEights; ++i)  // 8 rows on, the swizzle is the same
+                    put(raw_chunk[i], scale[i], c_row + 8 * i, c_dst + c * kChunkBytes + i * 1024);
+            }
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int j = rope_from - 1 - b;
+                if (j < 0) break;
+                uint32_t scale[kFours];
+#pragma unroll
+                for (int i = 0; i < kFours; ++i) scale[i] = sc[(b_row + 4 * i) * 8 + 2 * j + b_chunk];
+                if (!need(j)) return false;
+#pragma unroll
+                for (int i = 0; i < kFours; ++i)  // 4 rows on, bit 2 of the swizzle turns
+                    put(raw[b % 2][i], scale[i], b_row + 4 * i,
+                        (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
+                if (j >= 2) load_block(tl, raw[b % 2], j - 2);
+                if (b == 0 && (flags & kFirst)) copies_done();  // hands over the unit's queries too
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[j]);
+            }
+            if (rope_from < kBlocks) {
+                copies_done();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    for (int j = rope_from; j < kBlocks; ++j) mbar_arrive(&sh.full[j]);
+            }
+        }
+        // ---- the next tile's loads, in flight during the softmax
+        if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
+        const int32_t next_flags = sh.tile[nslot].flags;
+        const bool next_rows = !(next_flags & (kDone | kEmpty));
+        if (next_rows) start(sh.tile[nslot]);
+
+        if (!(flags & kEmpty)) {
+            // ---- softmax of the tile: this lane's row, NC columns
+            const int buf = step & 1;
+            if (!wait_all(&sh.s_ready, step & 1)) return false;
+            tmem_fence_after();
+            float s[NC];
+            tmem_ld<NC>(lane_base, s);
+            const bool ok = tl.row[srow].data != reinterpret_cast<const uint8_t*>(g_zero_row);
+            if (kSrc == kTokens) {
+                // every worker has handed over its share of the tile: its flags are there
+                if (!wait_all(&sh.full[0], step & 1)) return false;
+                if (rope_from < kBlocks && !wait_all(&sh.full[kBlocks - 1], step & 1)) return false;
+                const int32_t pos = tl.pos + srow;
+                const bool bad = sh.row_bad[buf][srow];
+                if (!__all_sync(0xFFFFFFFFu, ok && !bad && pos >= un.all_lo && pos <= un.all_hi)) {
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) {
+                        const bool see = ok && pos >= un.col_lo[group * NC + k] && pos <= un.col_hi[group * NC + k];
+                        s[k] = see ? (bad ? NAN : s[k]) : -INFINITY;
+                    }
+                }
+            } else if (!__all_sync(0xFFFFFFFFu, ok)) {
+#pragma unroll
+                for (int k = 0; k < NC; ++k) s[k] = ok ? s[k] : -INFINITY;
+            }
+            // The reference of a column only has to lie near its maximum: it is set by
+            // the first tile and raised where a score lies far above it, which the
+            // group's four warps have to agree on.
+            bool raise = flags & kFirst;
+            float* ref = sh.ref + warp * NC;
+            if (!raise) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < NC; k += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(&ref[k]);
+                    top = fmaxf(top, fmaf(s[k], ls.scale_log2, -m.x));
+                    top = fmaxf(top, fmaf(s[k + 1], ls.scale_log2, -m.y));
+                    top = fmaxf(top, fmaf(s[k + 2], ls.scale_log2, -m.z));
+                    top = fmaxf(top, fmaf(s[k + 3], ls.scale_log2, -m.w));
+                }
+                const bool over = __any_sync(0xFFFFFFFFu, top > kLazy);
+                int32_t(&flag)[4] = sh.over[group][exchange & 1];
+                if (lane == 0) {
+                    flag[quad] = over;
+                    mbar_arrive(&sh.group_bar[group]);
+                }
+                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+                ++exchange;
+                raise = flag[0] | flag[1] | flag[2] | flag[3];
+            }
+            if (raise) {
+                float* red = sh.red[exchange & 1][quad] + group * NC;
+#pragma unroll
+                for (int k = 0; k < NC; k += 4) {
+                    const float x0 = warp_max(s[k]), x1 = warp_max(s[k + 1]);
+                    const float x2 = warp_max(s[k + 2]), x3 = warp_max(s[k + 3]);
+                    if (lane == 0) *reinterpret_cast<float4*>(&red[k]) = make_float4(x0, x1, x2, x3);
+                }
+                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
+                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+                if (lane < NC) {
+                    const float(&all)[4][kMaxCols] = sh.red[exchange & 1];
+                    const int c = group * NC + lane;
+                    const float top = ls.scale_log2 * fmaxf(fmaxf(all[0][c], all[1][c]), fmaxf(all[2][c], all[3][c]));
+                    float alpha = 1.0f;
+                    if (top > m_used) {
+                        alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
+                        m_used = top;
+                    }
+                    ref[lane] = m_used == -INFINITY ? kNone : m_used;
+                    aux[lane] = alpha;
+                }
+                ++exchange;
+                __syncwarp();
+                if (!(flags & kFirst)) {
+                    // the previous tile's second product is done: s_ready came after it
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) l[k] *= aux[k];
+                    for (int j = 0; j < kBlocks; ++j) {
+#pragma unroll
+                        for (int k0 = 0; k0 < NC; k0 += 8) {
+                            float o[8];
+                            tmem_ld<8>(lane_base + N + j * N + k0, o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] *= aux[k0 + k];
+                            tmem_st8(lane_base + N + j * N + k0, o);
+                        }
+                    }
+                    tmem_wait_st();
                 }
             }
-            copies_done();  // rope dims, and the queries at the head of a unit
+            // weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by side
+#pragma unroll
+            for (int k = 0; k < NC; k += 8) {
+                const float4 m0 = *reinterpret_cast<const float4*>(&ref[k]);
+                const float4 m1 = *reinterpret_cast<const float4*>(&ref[k + 4]);
+                const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s[k + i] = ex2_approx(fmaf(s[k + i], ls.scale_log2, -m[i]));
+                    l[k + i] += s[k + i];
+                }
+                sts_v4(p_tile + (group * NC + k) / 8 * (kTile * 16) + srow * 16,
+                       pack_bf16x2(s[k], s[k + 1]), pack_bf16x2(s[k + 2], s[k + 3]),
+                       pack_bf16x2(s[k + 4], s[k + 5]), pack_bf16x2(s[k + 6], s[k + 7]));
+            }
             fence_async_smem();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full[buf]);
+            if (lane == 0) mbar_arrive(&sh.p_ready);
             ++step;
         }
-        if (!(flags & kDone)) {
-            // ---- the next tile's loads, in flight during the softmax
-            if (!wait_all(&sh.tile_full[nslot], ((seq + 1) / kTiles) & 1)) return false;
-            next_flags = sh.tile[nslot].flags;
-            loaded = !(next_flags & (kDone | kEmpty));
-            if (loaded) load_tile(sh.tile[nslot]);
-        }
-
-        if (due) {
-            // ---- weights of the tile before
-            const uint32_t st = step - 1 - (rows ? 1 : 0);
-            const int buf = st & 1;
-            const Unit& un = sh.unit[prev_unit];
-            if (!wait_all(&sh.s_ready[buf], (st >> 1) & 1)) return false;
-            tmem_fence_after();
-            if (kSrc == kTokens && !wait_all(&sh.full[buf], (st >> 1) & 1)) return false;  // row_bad
-            // s[4 k + 2 r + i]: row row0 + 8 r, column 8 k + 2 (lane % 4) + i
-            float s[2 * kCols];
-            const auto scores = [&]() {
-                tmem_ld_frag<kPairs>(s_base + buf * N, s);
-                if (kSrc == kTokens) {
-                    const int32_t pos = prev_pos + row0;
-                    const bool bad0 = sh.row_bad[buf][row0], bad1 = sh.row_bad[buf][row0 + 8];
-#pragma unroll
-                    for (int k = 0; k < kPairs; ++k) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = group * NC + 8 * k + 2 * (lane & 3) + i;
-                            const int32_t lo = un.col_lo[c], hi = un.col_hi[c];
-                            const bool see0 = ok0 && pos >= lo && pos <= hi, see1 = ok1 && pos + 8 >= lo && pos + 8 <= hi;
-                            s[4 * k + i] = see0 ? (bad0 ? NAN : s[4 * k + i]) : -INFINITY;
-                            s[4 * k + 2 + i] = see1 ? (bad1 ? NAN : s[4 * k + 2 + i]) : -INFINITY;
+        if (flags & kLast) {
+            // the first product of this unit is done with its queries
+            if (next_rows) load_queries<N, D, kWorkers>(p, sh.unit[sh.tile[nslot].unit], q_tile, tid);
+            // ---- the unit's sums: over the lanes, then over the group's four warps
+            const float mine = column_sums<NC>(l, lane);
+            float(&red)[4][kMaxCols] = sh.red[exchange & 1];
+            if (lane < NC) red[quad][group * NC + lane] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.group_bar[group]);
+            if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
+            ++exchange;
+            if (lane < NC) {
+                const int n = group * NC + lane;
+                const float total = (red[0][n] + red[1][n]) + (red[2][n] + red[3][n]);
+                const int32_t t = un.col_token[n], h = un.col_head[n];
+                float inv = 1.0f;
+                if (t >= 0) {
+                    if (ls.splits > 1) {
+                        if (quad == 0) {
+                            float* ml = ls.part_ml + (((int64_t)t * p.num_heads + h) * ls.splits + un.part) * 2;
+                            ml[0] = m_used;
+                            ml[1] = total;
                         }
-                    }
-                } else if (!__all_sync(0xFFFFFFFFu, ok0 && ok1)) {
-#pragma unroll
-                    for (int k = 0; k < kPairs; ++k) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            s[4 * k + i] = ok0 ? s[4 * k + i] : -INFINITY;
-                            s[4 * k + 2 + i] = ok1 ? s[4 * k + 2 + i] : -INFINITY;
-                        }
+                    } else {
+                        const float m = m_used == -INFINITY ? 0.0f : m_used;
+                        const float den = total + ex2_approx(un.col_sink[n] - m);
+                        inv = total == 0.0f ? 0.0f : 1.0f / den;
+                        if (p.lse && quad == 0)
+                            p.lse[(int64_t)t * p.lse_stride_t + h] =
+                                total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
                     }
                 }
-            };
-            // The reference of a column only has to lie near its maximum: the first
-            // tile sets it, and it is raised where a weight would exceed kMostWeight.
-            // alpha: the factor on what has been summed so far.
-            float alpha[kCols];
-            const auto set_reference = [&]() {
-                float top[kCols];
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    const int k = c / 2, i = c % 2;
-                    top[c] = fmaxf(s[4 * k + i], s[4 * k + 2 + i]);
-#pragma unroll
-                    for (int o = 4; o < kWarp; o *= 2) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], o));
-                }
-                float(&red)[4][kMaxCols / kGroups] = sh.red[group][exchange & 1];
-                if (lane < 4) {
-#pragma unroll
-                    for (int k = 0; k < kPairs; ++k)
-                        *reinterpret_cast<float2*>(&red[quad][8 * k + 2 * lane]) = make_float2(top[2 * k], top[2 * k + 1]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    const int at = 8 * (c / 2) + 2 * (lane & 3) + c % 2;
-                    const float t = ls.scale_log2 * fmaxf(fmaxf(red[0][at], red[1][at]), fmaxf(red[2][at], red[3][at]));
-                    alpha[c] = 1.0f;
-                    if (t > ref[c]) {
-                        alpha[c] = ref[c] == kNone ? 1.0f : ex2_approx(ref[c] - t);  // no sums before
-                        ref[c] = t;
-                    }
-                }
-                return true;
-            };
-            // Weights to the N-major B tile: 8 columns (16 bytes) of a row, rows side by
-            // side.  Returns the largest one.
-            const auto weights = [&]() {
-                float most = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float& a = s[4 * k + 2 * r];
-                        float& b = s[4 * k + 2 * r + 1];
-                        a = ex2_approx(fmaf(a, ls.scale_log2, -ref[2 * k]));
-                        b = ex2_approx(fmaf(b, ls.scale_log2, -ref[2 * k + 1]));
-                        most = fmaxf(most, fmaxf(a, b));
-                        sts_u32(w_dst + buf * kWeightBytes + k * (kTile * 16) + r * 128, pack_bf16x2(a, b));
-                    }
-                }
-                return most;
-            };
-            const auto hand_over = [&]() {
-                fence_async_smem();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready);
-            };
-            const bool first = prev & kFirst;
-            if (first) {
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) {
-                    l[c] = 0.0f;
-                    ref[c] = kNone;
-                }
+                aux[lane] = inv;
             }
-            scores();
-            if (first && !set_reference()) return false;
-            const float most = weights();
-            if (!first && __any_sync(0xFFFFFFFFu, most > kMostWeight) && lane == 0)
-                *const_cast<volatile int32_t*>(&sh.over[buf]) = 1;
-            hand_over();
-            if (!wait_all(&sh.p_ready, round++ & 1)) return false;
-            if (!first && again(sh, st)) {
-                // once more with raised references, after the second products issued so far
-                if (!wait_all(&sh.freed[buf ^ 1], ((st - 1) >> 1) & 1)) return false;
+            __syncwarp();
+            if (!(flags & kEmpty)) {
+                if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
                 tmem_fence_after();
-                scores();
-                if (!set_reference()) return false;
-                float(&aux)[kMaxCols / kGroups] = sh.aux[group][0];
-                if (quad == 0 && lane < 4) {
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) aux[8 * (c / 2) + 2 * lane + c % 2] = alpha[c];
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) l[c] *= alpha[c];
+            }
+            if (ls.splits > 1) {
                 for (int j = 0; j < kBlocks; ++j) {
+                    float o[NC];
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                    if (!(flags & kEmpty)) tmem_ld<NC>(lane_base + N + j * N, o);
+                    const int d = j * 128 + srow;
+#pragma unroll
                     for (int k0 = 0; k0 < NC; k0 += 8) {
-                        float o[8];
-                        tmem_ld<8>(o_base + j * N + k0, o);
+                        int64_t at[8];
+                        bool used[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] *= aux[k0 + k];
-                        tmem_st8(o_base + j * N + k0, o);
+                        for (int k = 0; k < 8; ++k) {
+                            at[k] = un.col_out[group * NC + k0 + k] + d;
+                            used[k] = un.col_token[group * NC + k0 + k] >= 0;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (used[k]) ls.part_o[at[k]] = o[k0 + k];
                     }
                 }
-                tmem_wait_st();
-                weights();
-                hand_over();
-                if (!wait_all(&sh.p_ready, round++ & 1)) return false;
-            }
-            if (tid == 0) sh.over[buf ^ 1] = 0;  // everyone is past the step that used it
+            } else {
+                // 4 x 4 exchanges among four lanes: each then holds four dims of the columns
+                // k + lane % 4, where it stores them
+                uint16_t* dst[NC / 4];
 #pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) l[2 * k + i] += s[4 * k + i] + s[4 * k + 2 + i];
-            }
-            due = false;
-            if (prev & kLast) {
-                // ---- the unit's sums: over a column's 8 lanes, then over the group's warps
-                float(&red)[4][kMaxCols / kGroups] = sh.red[group][exchange & 1];
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-#pragma unroll
-                    for (int o = 4; o < kWarp; o *= 2) l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], o);
-                if (lane < 4) {
-#pragma unroll
-                    for (int k = 0; k < kPairs; ++k)
-                        *reinterpret_cast<float2*>(&red[quad][8 * k + 2 * lane]) = make_float2(l[2 * k], l[2 * k + 1]);
+                for (int k = 0; k < NC / 4; ++k) {
+                    const int n = group * NC + 4 * k + (lane & 3);
+                    dst[k] = un.col_token[n] >= 0 ? p.out + un.col_out[n] + (srow & ~3) : nullptr;
                 }
-                // columns' factors on O^T, worked out by the quad's first warp for all
-                float(&aux)[kMaxCols / kGroups] = sh.aux[group][1];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-                if (quad == 0 && lane < 4) {
+                const bool odd = lane & 1, upper = lane & 2;
+                for (int j = 0; j < kBlocks; ++j) {
+                    float o[NC];
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        const int at = 8 * (c / 2) + 2 * lane + c % 2, n = group * NC + at;
-                        const float total = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
-                        aux[at] = finish_column(p, ls, un, n, ref[c], total);
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                    if (!(flags & kEmpty)) tmem_ld<NC>(lane_base + N + j * N, o);
+#pragma unroll
+                    for (int k = 0; k < NC / 4; ++k) {
+                        const float4 inv = *reinterpret_cast<const float4*>(&aux[4 * k]);
+                        const float a0 = o[4 * k] * inv.x, a1 = o[4 * k + 1] * inv.y;
+                        const float a2 = o[4 * k + 2] * inv.z, a3 = o[4 * k + 3] * inv.w;
+                        const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
+                        const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
+                        // columns 4 k (+ 1 if odd) and 4 k + 2 (+ 1)
+                        const uint32_t w0 = pack_bf16x2(odd ? b0 : a0, odd ? a1 : b0);
+                        const uint32_t w1 = pack_bf16x2(odd ? b1 : a2, odd ? a3 : b1);
+                        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                        if (dst[k] != nullptr)
+                            st_v2(dst[k] + j * 128, make_uint2(upper ? x : w0, upper ? w1 : x));
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.group_bar[group]);
-                if (!wait_all(&sh.group_bar[group], exchange & 1)) return false;
-                ++exchange;
-                if (!wait_all(&sh.freed[buf], (st >> 1) & 1)) return false;
-                tmem_fence_after();
-                write_out<N, D, NC>(p, ls, un, o_base, aux, group, quad * kWarp + lane, lane, true);
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.unit_empty[prev_unit]);
             }
-        }
-        if (flags & kDone) return true;
-        if (flags & kEmpty) {
-            const Unit& un = sh.unit[tl.unit];
-            float(&aux)[kMaxCols / kGroups] = sh.aux[group][1];
-            if (quad == 0)
-                for (int c = lane; c < NC; c += kWarp) finish_column(p, ls, un, group * NC + c, kNone, 0.0f);
-            write_out<N, D, NC>(p, ls, un, o_base, aux, group, quad * kWarp + lane, lane, false);
+            tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[tl.unit]);
-        } else {
-            due = true;
-            prev = flags;
-            prev_unit = tl.unit;
-            prev_pos = tl.pos;
-            ok0 = cur_ok0;
-            ok1 = cur_ok1;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.tile_empty[slot]);
@@ -970,36 +948,39 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 constexpr size_t kAlign = 1024;
 
 size_t smem_bytes(int n, int head_dim) {
-    return kAlign + 2 * ((size_t)head_dim / 64 * kChunkBytes) + (size_t)head_dim / 64 * n * 128 +
-           2 * ((size_t)kTile * n * 2) + sizeof(Shared);
+    return kAlign + (size_t)head_dim / 64 * kChunkBytes + (size_t)head_dim / 64 * n * 128 +
+           (size_t)n / 8 * kTile * 16 + sizeof(Shared);
 }
 
 template <int N, int kSrc, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ LaunchShape ls) {
+    constexpr int kWorkers = Roles<kSrc>::kWorkers, kGroups = Roles<kSrc>::kGroups;
+    constexpr int kMmaWarp = Roles<kSrc>::kMmaWarp, kPlanWarp = Roles<kSrc>::kPlanWarp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((kAlign - (smem_u32(smem_raw) & (kAlign - 1))) & (kAlign - 1));
     uint8_t* k_tile = base;
-    uint8_t* q_tile = k_tile + 2 * (D / 64 * kChunkBytes);
+    uint8_t* q_tile = k_tile + D / 64 * kChunkBytes;
     uint8_t* p_tile = q_tile + D / 64 * (N * 128);
-    Shared& sh = *reinterpret_cast<Shared*>(p_tile + 2 * (kTile * N * 2));
+    Shared& sh = *reinterpret_cast<Shared*>(p_tile + N / 8 * kTile * 16);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kUnits; ++i) mbar_init(&sh.unit_empty[i], kWorkers);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.unit_empty[i], kWorkers);
+        }
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(&sh.tile_full[i], 1);
             mbar_init(&sh.tile_empty[i], kWorkers + 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxBlocks; ++i) {
             mbar_init(&sh.full[i], kWorkers);
             mbar_init(&sh.freed[i], 1);
-            mbar_init(&sh.s_ready[i], 1);
         }
+        mbar_init(&sh.s_ready, 1);
         mbar_init(&sh.p_ready, kWorkers);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < kGroups; ++i) mbar_init(&sh.group_bar[i], 4);
-        sh.over[0] = sh.over[1] = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(&sh.tmem, ls.tmem_cols);
@@ -1016,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kPlanWarp) {
         ok = plan<kSrc>(p, ls, sh);
     } else {
-        ok = issue<N, D>(sh, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
+        ok = issue<N, D>(sh, (D - p.rope_dim) / 128, smem_u32(k_tile), smem_u32(q_tile), smem_u32(p_tile), tmem);
         if (!ok) {  // wait for the MMAs in flight before the operands go
             umma_commit(&sh.drain, elect_one());
             mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);
@@ -1103,7 +1084,7 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     if (splits > tiles) splits = tiles;
     ls.splits = (int32_t)(splits < 1 ? 1 : splits);
     ls.units = base * ls.splits;
-    const uint32_t need = (uint32_t)pl.n * (2 + head_dim / 128);  // two tiles' scores, O^T
+    const uint32_t need = (uint32_t)pl.n * (1 + head_dim / 128);
     ls.tmem_cols = 32;
     while (ls.tmem_cols < need) ls.tmem_cols *= 2;
     return pl;
@@ -1120,13 +1101,15 @@ cudaError_t launch(const AttnParams& p, const LaunchShape& ls, cudaStream_t stre
     const cudaError_t e = set_smem_limit_per_device(attention_kernel<N, kSrc, D>, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = ls.units < sm_count() ? ls.units : sm_count();
-    return launch_pdl(attention_kernel<N, kSrc, D>, dim3((unsigned)grid), dim3(kThreads), smem, stream, p, ls);
+    return launch_pdl(attention_kernel<N, kSrc, D>, dim3((unsigned)grid), dim3(Roles<kSrc>::kThreads), smem, stream, p, ls);
 }
 
 template <int kSrc, int D>
 cudaError_t launch_n(const AttnParams& p, const Plan& pl, cudaStream_t stream) {
-    return pl.n == 16 ? launch<16, kSrc, D>(p, pl.ls, stream)
-                      : pl.n == 32 ? launch<32, kSrc, D>(p, pl.ls, stream) : launch<64, kSrc, D>(p, pl.ls, stream);
+    if constexpr (kSrc != kTokens) {  // several tokens fill more than 16 columns
+        if (pl.n == 16) return launch<16, kSrc, D>(p, pl.ls, stream);
+    }
+    return pl.n == 32 ? launch<32, kSrc, D>(p, pl.ls, stream) : launch<64, kSrc, D>(p, pl.ls, stream);
 }
 
 template <int kSrc>

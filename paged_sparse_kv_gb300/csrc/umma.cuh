@@ -144,35 +144,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The 16-lane shape: for each of K groups of 8 columns, four values per lane: rows
-// lane / 4 (twice) and lane / 4 + 8 of the warp's 16, columns 2 (lane % 4) + {0, 1}.
-template <int K>
-__device__ __forceinline__ void tmem_ld_frag(uint32_t addr, float (&v)[4 * K]) {
-    static_assert(K == 1 || K == 2 || K == 4, "column counts in use");
-    uint32_t r[4 * K];
-    if constexpr (K == 1) {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "r"(addr));
-    } else if constexpr (K == 2) {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7])
-                     : "r"(addr));
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                       "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(addr));
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * K; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 __device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
                  ::"r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
@@ -193,15 +164,18 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return r;
 }
 
+// Largest value over the warp (NaN passed over).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Operand tiles are only written here and read by the tensor cores, so these
 // order themselves among volatile asm (barriers included) and need not hold back
 // other memory accesses.
 __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
-}
-
-__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t a) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a));
 }
 
 }  // namespace psk
