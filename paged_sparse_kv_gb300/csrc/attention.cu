@@ -76,7 +76,8 @@ struct Roles {
 
 // A set of columns; its tiles follow one another in the stream of tiles.
 struct Unit {
-    int32_t part;                  // which part of the split work (row of the workspace)
+    int64_t part_row;              // a unit cut in parts: row of its column 0 among such columns; else -1
+    int32_t part;                  // which part
     int32_t all_lo, all_hi;        // kTokens: positions that every column in use sees
     int32_t pad;
     int64_t col_q[kMaxCols];       // element offset of the column's query
@@ -128,11 +129,13 @@ struct LaunchShape {
     int32_t head_groups;     // ceil(num_heads / heads_per_unit)
     int32_t tokens_per_unit; // kTokens: neighbouring tokens in a unit
     int32_t splits;
-    int64_t units;
+    int64_t units;           // with every part of a cut unit counted
+    int64_t whole;           // units before this one are not cut
+    int64_t part_rows;       // columns of the cut ones
     uint32_t tmem_cols;
     float scale_log2;
-    float* part_o;           // [token][head][split][D]
-    float* part_ml;          // [token][head][split][2]
+    float* part_o;           // [row of a cut unit's column][split][D]
+    float* part_ml;          // [row][split][2]
 };
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
@@ -314,13 +317,13 @@ __device__ __forceinline__ bool unit_slot(Shared& sh, const Stream& st) {
 }
 
 __device__ __forceinline__ void set_column(const AttnParams& p, const LaunchShape& ls, Unit& un, int c,
-                                           int32_t part, int64_t t, int32_t h, bool used, int32_t lo,
-                                           int32_t hi) {
+                                           int32_t part, int64_t part_row, int64_t t, int32_t h, bool used,
+                                           int32_t lo, int32_t hi) {
     un.col_sink[c] = used && p.sink ? p.sink[h] * kLog2e : -INFINITY;
     un.col_token[c] = used ? (int32_t)t : -1;
     un.col_head[c] = h;
     un.col_q[c] = t * p.q_stride_t + h * p.q_stride_h;
-    un.col_out[c] = ls.splits > 1 ? ((t * p.num_heads + h) * ls.splits + part) * p.head_dim
+    un.col_out[c] = part_row >= 0 ? ((part_row + c) * ls.splits + part) * p.head_dim
                                   : t * p.out_stride_t + h * p.out_stride_h;
     un.col_lo[c] = used ? lo : 0;
     un.col_hi[c] = used ? hi : -1;
@@ -331,8 +334,10 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
     const int lane = threadIdx.x % kWarp;
     Stream st;
     for (int64_t u = blockIdx.x; u < ls.units; u += gridDim.x) {
-        const int32_t part = (int32_t)(u % ls.splits);
-        const int64_t v = u / ls.splits;
+        const bool cut = u >= ls.whole;
+        const int32_t parts = cut ? ls.splits : 1, part = cut ? (int32_t)((u - ls.whole) % parts) : 0;
+        const int64_t v = cut ? ls.whole + (u - ls.whole) / parts : u;
+        const int64_t part_row = cut ? (v - ls.whole) * ls.heads_per_unit * ls.tokens_per_unit : -1;
         if (kSrc != kTokens) {
             const int64_t t = v / ls.head_groups;
             const int32_t h0 = (int32_t)(v % ls.head_groups) * ls.heads_per_unit;
@@ -349,13 +354,16 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 if (p.base_off && x.req >= 0) src.base = p.base_off[x.req];
                 n = x.hi < x.lo ? 0 : (x.hi - x.lo) / kTile + 1;
             }
-            share(n, part, ls.splits, first, end);
+            share(n, part, parts, first, end);
             if (!unit_slot(sh, st)) return false;
             Unit& un = sh.unit[st.units & 1];
-            if (lane == 0) un.part = part;
+            if (lane == 0) {
+                un.part = part;
+                un.part_row = part_row;
+            }
 #pragma unroll
-            for (int c = lane; c < kMaxCols; c += kWarp) 
-                set_column(p, ls, un, c, part, t, h0 + c, c < heads, 0, 0);
+            for (int c = lane; c < kMaxCols; c += kWarp)
+                set_column(p, ls, un, c, part, part_row, t, h0 + c, c < heads, 0, 0);
             if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
         } else {
             // a run of neighbouring tokens of one request is a unit
@@ -378,13 +386,15 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                 src.base = p.base_off && src.req >= 0 ? p.base_off[src.req] : 0;
                 const int32_t tiles = src.hi < src.lo ? 0 : (src.hi - src.lo) / kTile + 1;
                 int32_t first, end;
-                share(tiles, part, ls.splits, first, end);
+                share(tiles, part, parts, first, end);
+                const int64_t run_row = cut ? part_row + a * p.num_heads : -1;
                 if (!unit_slot(sh, st)) return false;
                 Unit& un = sh.unit[st.units & 1];
                 const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, lane >= a && lane < b ? x.lo : INT32_MIN);
                 const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, lane >= a && lane < b ? x.hi : INT32_MAX);
                 if (lane == 0) {
                     un.part = part;
+                    un.part_row = run_row;
                     un.all_lo = all_lo;
                     un.all_hi = all_hi;
                 }
@@ -394,7 +404,7 @@ __device__ bool plan(const AttnParams& p, const LaunchShape& ls, Shared& sh) {
                     const int tok = a + c / p.num_heads;
                     const int32_t lo = __shfl_sync(0xFFFFFFFFu, x.lo, tok & 31);
                     const int32_t hi = __shfl_sync(0xFFFFFFFFu, x.hi, tok & 31);
-                    set_column(p, ls, un, c, part, t0 + tok, c % p.num_heads, tok < b, lo, hi);
+                    set_column(p, ls, un, c, part, run_row, t0 + tok, c % p.num_heads, tok < b, lo, hi);
                 }
                 if (!stream_unit<kSrc>(p, sh, st, src, first, end, lane)) return false;
             }
@@ -861,9 +871,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 const int32_t t = un.col_token[n], h = un.col_head[n];
                 float inv = 1.0f;
                 if (t >= 0) {
-                    if (ls.splits > 1) {
+                    if (un.part_row >= 0) {
                         if (quad == 0) {
-                            float* ml = ls.part_ml + (((int64_t)t * p.num_heads + h) * ls.splits + un.part) * 2;
+                            float* ml = ls.part_ml + ((un.part_row + n) * ls.splits + un.part) * 2;
                             ml[0] = m_used;
                             ml[1] = total;
                         }
@@ -883,7 +893,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
                 tmem_fence_after();
             }
-            if (ls.splits > 1) {
+            if (un.part_row >= 0) {
                 for (int j = 0; j < kBlocks; ++j) {
                     float o[NC];
 #pragma unroll
@@ -1013,14 +1023,23 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
 // ---- joining the parts of a split row ----------------------------------------------------
 //
 // out = sum_i 2^(m_i - m) o_i / (sum_i 2^(m_i - m) l_i + 2^(sink' - m)), m = max m_i
-// (log2 units).  One CTA per (token, head); a thread takes four dims, so the
+// (log2 units).  One CTA per column of a cut unit; a thread takes four dims, so the
 // parts are read as whole rows.
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParams p, const LaunchShape ls) {
     extern __shared__ float s_ml[];
-    pdl_wait();
     const int64_t th = blockIdx.x;
-    const int32_t h = (int32_t)(th % p.num_heads);
-    const int64_t t = th / p.num_heads;
+    int32_t h;
+    int64_t t;
+    if (ls.tokens_per_unit > 1) {
+        t = ls.whole * ls.tokens_per_unit + th / p.num_heads;
+        h = (int32_t)(th % p.num_heads);
+    } else {
+        const int64_t v = ls.whole + th / ls.heads_per_unit;
+        t = v / ls.head_groups;
+        h = (int32_t)(v % ls.head_groups) * ls.heads_per_unit + (int32_t)(th % ls.heads_per_unit);
+    }
+    if (t >= p.num_tokens || h >= p.num_heads) return;  // columns not in use
+    pdl_wait();
     const int S = ls.splits;
     for (int i = threadIdx.x; i < 2 * S; i += blockDim.x) s_ml[i] = ls.part_ml[th * 2 * S + i];
     __syncthreads();
@@ -1078,20 +1097,31 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     }
     pl.n = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
     const int64_t base = (num_tokens + ls.tokens_per_unit - 1) / ls.tokens_per_unit * ls.head_groups;
-    // Few units: each is cut along its tiles until they fill the SMs.
-    const int64_t tiles = (max_keys + kTile - 1) / kTile;
-    int64_t splits = base < sm_count() ? sm_count() / base : 1;
+    // The units that do not fill the SMs once more are cut along their tiles until
+    // they do: all of them, where there are fewer than SMs, and the last ones of the
+    // index form, whose units are of one length (634 units of 9 tiles on 152 SMs: 209
+    // us against 228; in the position form 476 units of up to 60 tiles took 857 against
+    // 777, as the parts also went to the SMs with the longest units).
+    const int64_t sms = sm_count(), tiles = (max_keys + kTile - 1) / kTile;
+    ls.whole = base / sms * sms;
+    int64_t rest = base - ls.whole, splits = rest > 0 ? sms / rest : 1;
     if (splits > tiles) splits = tiles;
-    ls.splits = (int32_t)(splits < 1 ? 1 : splits);
-    ls.units = base * ls.splits;
+    if (splits <= 1 || (!indexed && ls.whole > 0)) {
+        splits = 1;
+        rest = 0;
+        ls.whole = base;
+    }
+    ls.splits = (int32_t)splits;
+    ls.units = ls.whole + rest * splits;
+    ls.part_rows = rest * ls.heads_per_unit * ls.tokens_per_unit;
     const uint32_t need = (uint32_t)pl.n * (1 + head_dim / 128);
     ls.tmem_cols = 32;
     while (ls.tmem_cols < need) ls.tmem_cols *= 2;
     return pl;
 }
 
-int64_t part_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int32_t splits) {
-    return splits <= 1 ? 0 : num_tokens * num_heads * splits * (head_dim + 4) * (int64_t)sizeof(float);
+int64_t part_bytes(const LaunchShape& ls, int32_t head_dim) {
+    return (ls.part_rows * ls.splits * (head_dim + 2) * (int64_t)sizeof(float) + 15) / 16 * 16;
 }
 
 template <int N, int kSrc, int D>
@@ -1124,12 +1154,12 @@ cudaError_t run(AttnParams p, int64_t max_keys, bool indexed, cudaStream_t strea
     p.extra.shift = log2_if_pow2(p.extra.block_size);
     pl.ls.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
     pl.ls.part_o = static_cast<float*>(p.workspace);
-    pl.ls.part_ml = pl.ls.part_o + p.num_tokens * p.num_heads * pl.ls.splits * p.head_dim;
+    pl.ls.part_ml = pl.ls.part_o + pl.ls.part_rows * pl.ls.splits * p.head_dim;
     cudaError_t e = pl.src == kIndexed ? launch_d<kIndexed>(p, pl, stream)
                     : pl.src == kOneToken ? launch_d<kOneToken>(p, pl, stream)
                                           : launch_d<kTokens>(p, pl, stream);
     if (e != cudaSuccess || pl.ls.splits == 1) return e;
-    return launch_pdl(attention_join_kernel, dim3((unsigned)(p.num_tokens * p.num_heads)), dim3(128),
+    return launch_pdl(attention_join_kernel, dim3((unsigned)pl.ls.part_rows), dim3(128),
                       (size_t)pl.ls.splits * 2 * sizeof(float), stream, p, pl.ls);
 }
 
@@ -1138,7 +1168,7 @@ cudaError_t run(AttnParams p, int64_t max_keys, bool indexed, cudaStream_t strea
 int64_t attention_workspace_bytes(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t max_keys,
                                   bool indexed, int32_t num_reqs) {
     const Plan pl = make_plan(num_tokens, num_heads, head_dim, max_keys, indexed, num_reqs);
-    return part_bytes(num_tokens, num_heads, head_dim, pl.ls.splits);
+    return part_bytes(pl.ls, head_dim);
 }
 
 cudaError_t launch_attention_indexed(AttnParams p, cudaStream_t stream) {

@@ -149,6 +149,12 @@ def test_sparse_many_tokens(cuda_device):
     _run_sparse(cuda_device, 6, 200, 66, 512, 64, 129, 65)
 
 
+@pytest.mark.parametrize("T,H,D,C", [(160, 9, 128, 700), (60, 130, 512, 600), (153, 64, 256, 2000)])
+def test_sparse_last_units_cut(cuda_device, T, H, D, C):
+    """A few more units than CTAs: the last ones are cut along their columns and joined."""
+    _run_sparse(cuda_device, T + H, T, H, D, 64, C, C // 3)
+
+
 def test_sparse_growing_scores(cuda_device):
     """Scores that grow from the first column to the last, so that every tile
     raises the maximum, by little and by more than any lazy threshold."""
