@@ -664,6 +664,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (kSrc == kTokens) sh.row_bad[buf][own + lane] = 0;
             }
             __syncwarp();
+            uint2 row_scales[kFours];  // one 8-byte read per row instead of a byte per block
+#pragma unroll
+            for (int i = 0; i < kFours; ++i) row_scales[i] = sh.scales[buf][b_row + 4 * i];
             const uint8_t* sc = reinterpret_cast<const uint8_t*>(sh.scales[buf]);
             // ---- dequantisation, from the last dims down
             int block = kBlocks;  // blocks from here on are free
@@ -716,7 +719,8 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (j < 0) break;
                 uint32_t scale[kFours];
 #pragma unroll
-                for (int i = 0; i < kFours; ++i) scale[i] = sc[(b_row + 4 * i) * 8 + 2 * j + b_chunk];
+                for (int i = 0; i < kFours; ++i)
+                    scale[i] = ((j < 2 ? row_scales[i].x : row_scales[i].y) >> (16 * (j & 1) + 8 * b_chunk)) & 0xFFu;
                 if (!need(j)) return false;
 #pragma unroll
                 for (int i = 0; i < kFours; ++i)  // 4 rows on, bit 2 of the swizzle turns
@@ -820,8 +824,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                     // the previous tile's second product is done: s_ready came after it
 #pragma unroll
                     for (int k = 0; k < NC; ++k) l[k] *= aux[k];
+#pragma unroll 1  // rare: short code, few registers
                     for (int j = 0; j < kBlocks; ++j) {
-#pragma unroll
+#pragma unroll 1
                         for (int k0 = 0; k0 < NC; k0 += 8) {
                             float o[8];
                             tmem_ld<8>(lane_base + N + j * N + k0, o);
@@ -858,7 +863,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             // the first product of this unit is done with its queries
             if (next_rows) load_queries<N, D, kWorkers>(p, sh.unit[sh.tile[nslot].unit], q_tile, tid);
             // ---- the unit's sums: over the lanes, then over the group's four warps
-            const float mine = column_sums<NC>(l, lane);
+            const float mine = column_sums(l, lane);
             float(&red)[4][kMaxCols] = sh.red[exchange & 1];
             if (lane < NC) red[quad][group * NC + lane] = mine;
             __syncwarp();

@@ -77,19 +77,16 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const SlotMapParams 
         }
     }
     pdl_launch_dependents();
-    if constexpr (V == 4) {
+    if constexpr (V == 2) {
         if (t0 + V <= p.num_tokens) {  // 16-byte stores: the launcher checked the alignment
             const auto put = [&](int64_t* dst, const int64_t* x) {
-                if (!dst) return;
-                *reinterpret_cast<longlong2*>(dst + t0) = make_longlong2(x[0], x[1]);
-                *reinterpret_cast<longlong2*>(dst + t0 + 2) = make_longlong2(x[2], x[3]);
+                if (dst) *reinterpret_cast<longlong2*>(dst + t0) = make_longlong2(x[0], x[1]);
             };
             put(p.positions, pos);
             put(p.slots, slot);
             put(p.comp_slots, comp);
             if (p.token_to_req)
-                *reinterpret_cast<int4*>(p.token_to_req + t0) =
-                    make_int4(req[0], req[1], req[2], req[3]);
+                *reinterpret_cast<int2*>(p.token_to_req + t0) = make_int2(req[0], req[1]);
             return;
         }
     }
@@ -195,12 +192,12 @@ cudaError_t launch_slot_mappings(SlotMapParams p, cudaStream_t stream) {
                           reinterpret_cast<uintptr_t>(p.token_to_req) |
                           reinterpret_cast<uintptr_t>(p.slots) |
                           reinterpret_cast<uintptr_t>(p.comp_slots);
-    const bool four = all % 16 == 0 && p.num_tokens >= (int64_t)sm_count() * kThreads * 4;
+    const bool two = all % 16 == 0 && p.num_tokens >= (int64_t)sm_count() * kThreads * 2;
     const bool stage = p.num_reqs < kStageReqs;
-    const int V = four ? 4 : 1;
+    const int V = two ? 2 : 1;
     const int64_t ctas = (p.num_tokens + (int64_t)kThreads * V - 1) / ((int64_t)kThreads * V);
     const size_t smem = stage ? (size_t)(p.num_reqs + 1) * 4 : 0;
-    auto* k = four ? (stage ? slot_map_kernel<4, true> : slot_map_kernel<4, false>)
+    auto* k = two ? (stage ? slot_map_kernel<2, true> : slot_map_kernel<2, false>)
                    : (stage ? slot_map_kernel<1, true> : slot_map_kernel<1, false>);
     return launch_pdl(k, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p);
 }
