@@ -928,7 +928,11 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                     const int n = group * NC + 4 * k + (lane & 3);
                     dst[k] = un.col_token[n] >= 0 ? p.out + un.col_out[n] + (srow & ~3) : nullptr;
                 }
-                const bool odd = lane & 1, upper = lane & 2;
+                // first the pairs of columns (with lane ^ 2), then the halves of the pairs
+                const bool upper = lane & 2;
+                const uint32_t low = upper ? 0x1054u : 0x5410u, high = upper ? 0x3276u : 0x7632u;
+                const uint32_t keep = lane & 1 ? high : low, send = lane & 1 ? low : high;
+                const uint32_t dims01 = lane & 1 ? 0x1054u : 0x5410u, dims23 = lane & 1 ? 0x3276u : 0x7632u;
                 for (int j = 0; j < kBlocks; ++j) {
                     float o[NC];
 #pragma unroll
@@ -937,16 +941,14 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 #pragma unroll
                     for (int k = 0; k < NC / 4; ++k) {
                         const float4 inv = *reinterpret_cast<const float4*>(&aux[4 * k]);
-                        const float a0 = o[4 * k] * inv.x, a1 = o[4 * k + 1] * inv.y;
-                        const float a2 = o[4 * k + 2] * inv.z, a3 = o[4 * k + 3] * inv.w;
-                        const float b0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a0 : a1, 1);
-                        const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a2 : a3, 1);
-                        // columns 4 k (+ 1 if odd) and 4 k + 2 (+ 1)
-                        const uint32_t w0 = pack_bf16x2(odd ? b0 : a0, odd ? a1 : b0);
-                        const uint32_t w1 = pack_bf16x2(odd ? b1 : a2, odd ? a3 : b1);
-                        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                        const uint32_t w0 = pack_bf16x2(o[4 * k] * inv.x, o[4 * k + 1] * inv.y);
+                        const uint32_t w1 = pack_bf16x2(o[4 * k + 2] * inv.z, o[4 * k + 3] * inv.w);
+                        const uint32_t x = upper ? w1 : w0;
+                        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, upper ? w0 : w1, 2);
+                        const uint32_t u = __byte_perm(x, y, keep);
+                        const uint32_t v = __shfl_xor_sync(0xFFFFFFFFu, __byte_perm(x, y, send), 1);
                         if (dst[k] != nullptr)
-                            st_v2(dst[k] + j * 128, make_uint2(upper ? x : w0, upper ? w1 : x));
+                            st_v2(dst[k] + j * 128, make_uint2(__byte_perm(u, v, dims01), __byte_perm(u, v, dims23)));
                     }
                 }
             }
