@@ -1095,29 +1095,51 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     ls.tokens_per_unit = 1;
     pl.src = indexed ? kIndexed : kOneToken;
     int cols = ls.heads_per_unit;
-    // Neighbouring tokens share a unit where most requests bring several: a unit
-    // never crosses a request.
-    if (!indexed && num_heads <= kMaxCols / 2 && num_tokens >= 4 * (int64_t)num_reqs) {
-        ls.tokens_per_unit = kMaxCols / num_heads < kWarp ? kMaxCols / num_heads : kWarp;
-        cols = ls.tokens_per_unit * num_heads;
-        pl.src = kTokens;
+    // Neighbouring tokens of a request share a unit, and with it the tiles, where few
+    // heads leave room and requests bring enough tokens that units seldom end at their
+    // boundaries.  16 heads, contexts up to 8192, 8 tokens a request: 224 us against 329
+    // with one token a unit, 4 tokens a request 437 against 383; two tokens a unit (32
+    // heads) with 32 tokens a request 935 against 1120, with 16 1200 against 1124.  Not
+    // where windows are so short that the shared tiles are no fewer (32 heads, a window
+    // of 128, 4096 tokens: 206 us against 167).
+    const auto tiles_of = [](int64_t keys) { return keys / kTile + (keys % kTile != 0); };
+    const int64_t tiles = tiles_of(max_keys);
+    if (!indexed && num_heads <= kMaxCols / 2) {
+        const int32_t n = kMaxCols / num_heads < kWarp ? kMaxCols / num_heads : kWarp;
+        if (num_tokens >= (n < 4 ? 16 : 8) * (int64_t)num_reqs && tiles_of(max_keys + n - 1) < n * tiles) {
+            ls.tokens_per_unit = n;
+            cols = n * num_heads;
+            pl.src = kTokens;
+        }
     }
     pl.n = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
     const int64_t base = (num_tokens + ls.tokens_per_unit - 1) / ls.tokens_per_unit * ls.head_groups;
-    // The units that do not fill the SMs once more are cut along their tiles until
-    // they do: all of them, where there are fewer than SMs, and the last ones of the
-    // index form, whose units are of one length (634 units of 9 tiles on 152 SMs: 209
-    // us against 228; in the position form 476 units of up to 60 tiles took 857 against
-    // 777, as the parts also went to the SMs with the longest units).
-    const int64_t sms = sm_count(), tiles = (max_keys + kTile - 1) / kTile;
-    ls.whole = base / sms * sms;
-    int64_t rest = base - ls.whole, splits = rest > 0 ? sms / rest : 1;
+    // Units are cut along their tiles to fill the SMs evenly.  In the index form all
+    // are of one length: whole rounds of them stay whole, and the rest is cut until it
+    // fills the SMs too (634 units of 9 tiles on 152 SMs: 209 us against 228 uncut).  In
+    // the position form lengths differ from request to request: about four parts per SM
+    // (32 requests of 8 tokens, contexts up to 8192: one per SM 325 us, two 272, four 224,
+    // eight 224), of eight tiles or more; very few units are cut into one part per SM
+    // (two requests of 131072 rows: 107 us, four per SM 135).
+    const int64_t sms = sm_count();
+    int64_t rest = base, splits;
+    if (indexed) {
+        rest = base % sms;
+        splits = rest > 0 ? sms / rest : 1;
+    } else {
+        splits = sms / base;
+        if (base * 8 > sms) {
+            const int64_t most = tiles / 8 > splits ? tiles / 8 : splits;
+            splits = (4 * sms + base - 1) / base;
+            if (splits > most) splits = most;
+        }
+    }
     if (splits > tiles) splits = tiles;
-    if (splits <= 1 || (!indexed && ls.whole > 0)) {
+    if (splits <= 1) {
         splits = 1;
         rest = 0;
-        ls.whole = base;
     }
+    ls.whole = base - rest;
     ls.splits = (int32_t)splits;
     ls.units = ls.whole + rest * splits;
     ls.part_rows = rest * ls.heads_per_unit * ls.tokens_per_unit;

@@ -322,6 +322,45 @@ def test_chunk_decode_batch_of_many_requests(cuda_device):
     _run_chunk(cuda_device, 9, [1] * 40, rng.integers(0, 500, size=40), 8, 512, 64, 64, 0)
 
 
+@pytest.mark.parametrize("q_lens,prefix,H,D,window", [
+    ([64, 9, 0, 40], [3000, 1500, 5, 10], 16, 128, 0), ([50, 21], [2500, 40], 5, 256, 2000),
+    ([40, 40], [1100, 1800], 32, 128, 0), ([1] * 40, list(range(0, 3000, 75)), 70, 128, 0),
+    ([8] * 30, list(range(0, 2400, 80)), 8, 128, 1100)])
+def test_chunk_units_cut(cuda_device, q_lens, prefix, H, D, window):
+    """Units of one and of several tokens, cut along their positions and joined."""
+    _run_chunk(cuda_device, H + D, q_lens, prefix, H, D, 64, 64, window, pad=3, missing=0.05)
+
+
+@pytest.mark.parametrize("what", ["scale 247", "scale 255", "byte", "rope nan", "rope inf"])
+@pytest.mark.parametrize("H", [1, 8, 33])
+def test_chunk_non_finite_rows(cuda_device, what, H):
+    """Every way a record can hold a NaN or an infinity: only tokens that see it notice."""
+    d = cuda_device
+    rng = np.random.default_rng(13)
+    D, bs, bad = 256, 16, 53
+    cache = _cache(rng, 8, bs, D, 64)
+    rec, at = D + 64, bad % bs
+    page = cache[bad // bs]
+    scales = page[bs * rec + at * (D // 64):]
+    if what.startswith("scale"):
+        page[at * rec + 3] = 0xFE          # -448
+        scales[0] = int(what.split()[1])
+    elif what == "byte":
+        page[at * rec + 130] = 0xFF
+    else:
+        page[at * rec + D - 64 + 6:at * rec + D - 64 + 8] = (0xC1, 0x7F) if what == "rope nan" else (0x80, 0xFF)
+    q, q64 = _query(rng, 40, H, D, 1.0, d)
+    args = ([0, 40], [75], np.zeros(40, np.int32), np.arange(8, dtype=np.int32)[None, :])  # positions 35 ... 74
+    with np.errstate(all="ignore"):
+        want = plain.chunk_mla_attention(q64, cache, *args, bs, 64, np.float64(np.float32(D ** -0.5)), window=10)
+    out, lse = ops.chunk_mla_attention(q, torch.from_numpy(cache).to(d), *(_i32(a, d) for a in args), bs, window_size=10)
+    sees = (np.arange(35, 75) >= bad) & (np.arange(35, 75) < bad + 10)
+    dark = torch.from_numpy(~sees).to(d)
+    _close(out[dark], lse[dark], [w[~sees] for w in want], f"H {H} {what}")
+    assert bool((~torch.isfinite(out[~dark].float())).any((1, 2)).all())
+    assert ops.device_wait_timeouts() == 0
+
+
 def test_chunk_more_new_tokens_than_positions(cuda_device):
     """seq_lens below the query length: the first tokens lie before position 0."""
     d = cuda_device
