@@ -18,24 +18,41 @@
 // tile that both products read: with the dims contiguous as the K-major A
 // operand of the first, as the M-major A operand of the second.
 //
-// Roles.  8 worker warps dequantise a tile, take the softmax of S^T and at the
-// end of a unit write O^T; one thread issues the MMAs; one warp plans ahead: it
-// finds the tiles that hold anything visible and puts the addresses of their
-// rows into a ring, across units.  The tile is handed over in blocks of
-// 128 dims: the first product follows the dequantisation block by block, and
-// the next tile is dequantised into the blocks the second product has finished
-// with.  The first loads of a tile are in flight during the softmax of the one
-// before.  Every wait is bounded (2 s of
-// wall time, counted in psk_device_wait_timeouts).
+// Roles.  Worker warps dequantise a tile, take the softmax of S^T and at the end of a
+// unit write O^T; one warp issues the MMAs; one plans ahead: it finds the tiles
+// that hold anything visible and puts the addresses of their rows into a ring,
+// across units.  The tile is handed over in blocks of 128 dims: the first product
+// follows the dequantisation block by block, and the next tile is dequantised into
+// the blocks the second product has finished with.  The first loads of a tile are in
+// flight during the softmax of the one before.  Every wait is bounded (2 s of wall
+// time, counted in psk_device_wait_timeouts).
 //
 // Softmax in one pass: a running reference m per column.  It follows the
 // maximum lazily: the first tile sets it, and later ones raise it only where a
 // weight would exceed 2^16, so that O^T is hardly ever rescaled and the maxima
-// of most tiles are never formed; the reference cancels in out and in lse.  Sums and weights are binary32; the weights are
-// rounded to bf16 for the second product alone (the operands of one MMA share a
-// type, and a row's bf16 values do not fit fp16's range), while l sums them
-// unrounded, so that lse keeps binary32 accuracy and the roundings in out, being
-// unbiased, average out.
+// of most tiles are never formed; the reference cancels in out and in lse.  Sums
+// and weights are binary32; the weights are rounded to bf16 for the second
+// product alone (the operands of one MMA share a type, and a row's bf16 values do
+// not fit fp16's range), while l sums them unrounded, so that lse keeps binary32
+// accuracy and the roundings in out, being unbiased, average out.
+//
+// What bounds it.  The tensor cores read both operands from shared memory: an MMA of
+// 128 rows and 64 columns moves 6 KB and takes the 48 cycles those need at 128 bytes a
+// cycle, half again its arithmetic.  A tile (head_dim 512, 64 columns) is 64 of
+// them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
+// barriers and weights share the pipe.  Measured 8700 cycles a tile in the loop plus
+// 6000 a unit for O^T: 4096 tokens of 128 heads over 640 rows take 1077 us, 508
+// TFLOP/s, against 288 us at the matrix rate and 460 at the shared-memory rate.  The
+// rest is the chain dequantise - scores - softmax - weights, which one 128 KB tile
+// beside 64 KB of queries cannot overlap with itself.
+// Other forms of it, measured on 317 tokens of 128 heads over 1152 rows (205 us)
+// and on the 4096 tokens:
+//  * tiles of 64 rows, two in work: 283 and 1454 us; the first product drops to half
+//    rate and each tile pays the waits of a whole one;
+//  * separate warps for dequantisation and softmax on top of it: 293 and 1510;
+//  * records copied into shared memory in bulk, one copy a row, by a copying warp:
+//    470 and 2364 (a copy of 576 bytes takes some 130 cycles of the copy unit);
+//  * 16 worker warps: 239 against 227 and 1168 against 1154, fewer registers each.
 #include <atomic>
 #include <cmath>
 
@@ -47,8 +64,7 @@ namespace psk {
 namespace {
 
 constexpr int kTile = 128;            // rows of a tile (M of the first product)
-constexpr int kMaxWorkers = 16;
-constexpr int kMaxGroups = kMaxWorkers / 4;
+constexpr int kMaxGroups = 4;
 constexpr int kMaxBlocks = 4;         // 128-dim blocks of a row (head_dim 512)
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
@@ -66,9 +82,12 @@ __device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
+// Units of several tokens test what they dequantise for NaN and mask by column, which
+// twice the warps do faster (1901 tokens of 16 heads over up to 6144 rows: 755 us with
+// 16, 933 with 8).
 template <int kSrc>
 struct Roles {
-    static constexpr int kWorkers = kSrc == kTokens ? 16 : 8;  // worker warps
+    static constexpr int kWorkers = kSrc == kTokens ? 16 : 8;
     static constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 32 rows
     static constexpr int kMmaWarp = kWorkers, kPlanWarp = kWorkers + 1;
     static constexpr int kThreads = (kWorkers + 2) * kWarp;
@@ -1031,7 +1050,8 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
 //
 // out = sum_i 2^(m_i - m) o_i / (sum_i 2^(m_i - m) l_i + 2^(sink' - m)), m = max m_i
 // (log2 units).  One CTA per column of a cut unit; a thread takes four dims, so the
-// parts are read as whole rows.
+// parts are read as whole rows.  Bound by the bytes of the parts; two requests of 64
+// heads in 76 parts each: 20 MB from L2.
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParams p, const LaunchShape ls) {
     extern __shared__ float s_ml[];
     const int64_t th = blockIdx.x;

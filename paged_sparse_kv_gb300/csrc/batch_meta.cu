@@ -16,6 +16,15 @@ constexpr int kThreads = 256;
 // its slot is table[r][pos / bs - base[r]] * bs + pos % bs.  The request is found
 // by binary search; up to kStageReqs boundaries are staged in shared memory by
 // one coalesced read, so that the search costs no chain of L2 reads.
+//
+// Bound by the 28 bytes written per token and, with few tokens, by the launch and a
+// chain of four dependent reads (boundary, length, table, store): 1000003 tokens of
+// 37 requests 9.6 us, 2.9 TB/s of the 6.8 measured; 256 tokens 2.6 us.  Two tokens a
+// thread halve the searches and make every store of a warp 512 contiguous bytes
+// (one takes 11.2 us; four, whose 16-byte stores leave gaps, 11.9), which pays once
+// the SMs are full: 300000 tokens 4.37 us against 4.64 with one, 100000 3.55 against
+// 2.90.  Staging the boundaries: 256 requests 2.76 us against 3.24 from L2, 4000
+// requests of 250 tokens 13.3 against 13.9, 8000 of 125 15.0 against 14.4.
 constexpr int kStageReqs = 4096;
 
 __device__ __forceinline__ int64_t map_slot(const SlotMapTable& m, int32_t r, int64_t entry) {
@@ -108,6 +117,12 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const SlotMapParams 
 // rows.  Every CTA works out the demand before its first row by itself (two reads
 // per earlier row, from L2), so rows are filled in parallel by one launch that
 // keeps no counters; the CTA whose rows hold the last served one writes the head.
+//
+// Bound by the table written and the pages read, and by the chain before them
+// (counts and lengths of all earlier rows, the head, the pages): 2048 rows of 2048
+// columns 11.1 us, 2.4 TB/s of the 6.8 measured; 256 rows of 128 2.6 us.  Filling
+// the tails of the rows before the demand is known took 12.5, one row a CTA 13.0, 512
+// threads a CTA 13.6.
 
 struct Demand {
     int32_t have, more;
@@ -192,7 +207,7 @@ cudaError_t launch_slot_mappings(SlotMapParams p, cudaStream_t stream) {
                           reinterpret_cast<uintptr_t>(p.token_to_req) |
                           reinterpret_cast<uintptr_t>(p.slots) |
                           reinterpret_cast<uintptr_t>(p.comp_slots);
-    const bool two = all % 16 == 0 && p.num_tokens >= (int64_t)sm_count() * kThreads * 2;
+    const bool two = all % 16 == 0 && p.num_tokens >= (int64_t)sm_count() * kThreads * 6;
     const bool stage = p.num_reqs < kStageReqs;
     const int V = two ? 2 : 1;
     const int64_t ctas = (p.num_tokens + (int64_t)kThreads * V - 1) / ((int64_t)kThreads * V);
