@@ -65,12 +65,23 @@ def _need(t: torch.Tensor, dtype: torch.dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _page_size(cache: torch.Tensor) -> int:
+    """Bytes of a page, -1 where a page is not contiguous (from the strides: a view of a page
+    would cost 2 us)."""
+    n, gap = 1, False
+    for size, stride in zip(cache.shape[:0:-1], cache.stride()[:0:-1]):
+        gap |= size != 1 and stride != n
+        n *= size
+    return -1 if gap and n > 0 else n
+
+
 def _pages(cache: torch.Tensor):
     _need(cache, torch.uint8, "cache")
-    if cache.dim() < 2 or cache.shape[0] == 0 or not cache[0].is_contiguous():
+    size = _page_size(cache) if cache.dim() > 1 and cache.shape[0] > 0 else -1
+    if size < 0:
         raise ValueError("cache must be [num_pages >= 1, ...] uint8 with contiguous pages")
     if cache.shape[0] == 1:  # a size-1 dim may carry any stride (0 from broadcasting)
-        return 1, max(cache.stride(0), cache[0].numel())
+        return 1, max(cache.stride(0), size)
     return cache.shape[0], cache.stride(0)
 
 
