@@ -132,8 +132,10 @@ struct Demand {
 __device__ __forceinline__ Demand demand_of(const ExtendParams& p, int32_t r) {
     Demand d;
     const int32_t seq = max(p.seq_lens[r], 0);
-    const int32_t entries = seq / p.compress_ratio;
-    const int32_t need = entries / p.block_size + (entries % p.block_size != 0 ? 1 : 0);
+    int32_t rem;
+    const int32_t entries = div_block32(seq, p.compress_ratio, p.ratio_shift, rem);
+    const int32_t whole = div_block32(entries, p.block_size, p.block_shift, rem);
+    const int32_t need = whole + (rem != 0 ? 1 : 0);
     d.have = p.page_counts ? min(max(p.page_counts[r], 0), p.bt_width) : 0;
     d.wide = need > p.bt_width;
     d.more = d.wide ? 0 : max(need - d.have, 0);
@@ -218,6 +220,8 @@ cudaError_t launch_slot_mappings(SlotMapParams p, cudaStream_t stream) {
 }
 
 cudaError_t launch_extend_block_tables(ExtendParams p, cudaStream_t stream) {
+    p.ratio_shift = log2_if_pow2(p.compress_ratio);
+    p.block_shift = log2_if_pow2(p.block_size);
     const int64_t most = (int64_t)sm_count() * 8;  // eight CTAs of 256 threads fill an SM
     p.rows_per_cta = (int32_t)((p.num_reqs + most - 1) / most);
     const int32_t ctas = (p.num_reqs + p.rows_per_cta - 1) / p.rows_per_cta;

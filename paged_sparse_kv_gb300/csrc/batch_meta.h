@@ -46,7 +46,7 @@ struct ExtendParams {
     int32_t* page_counts_out;
     int32_t* pool_head_out;
     int32_t* err_count;          // nullable
-    int32_t rows_per_cta;        // set by the launcher
+    int32_t rows_per_cta, ratio_shift, block_shift;  // set by the launcher
 };
 
 cudaError_t launch_extend_block_tables(ExtendParams p, cudaStream_t stream);
