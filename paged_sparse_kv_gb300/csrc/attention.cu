@@ -40,9 +40,9 @@
 // 128 rows and 64 columns moves 6 KB and takes the 48 cycles those need at 128 bytes a
 // cycle, half again its arithmetic.  A tile (head_dim 512, 64 columns) is 64 of
 // them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
-// barriers and weights share the pipe.  Measured 8700 cycles a tile in the loop plus
+// barriers and weights share the pipe.  Measured 7700 cycles a tile in the loop plus
 // 6000 a unit for O^T: 4096 tokens of 128 heads over 640 rows take 1077 us, 508
-// TFLOP/s, against 288 us at the matrix rate and 460 at the shared-memory rate.  The
+// TFLOP/s, against 288 us at the matrix rate and 490 at the shared-memory rate.  The
 // rest is the chain dequantise - scores - softmax - weights, which one 128 KB tile
 // beside 64 KB of queries cannot overlap with itself.
 // Other forms of it, measured on 317 tokens of 128 heads over 1152 rows (205 us)
