@@ -3,7 +3,7 @@
 // Each entry point validates its arguments on the host, returns
 // PSK_ERR_INVALID_ARGUMENT before touching the GPU when they are wrong,
 // returns PSK_OK without a launch when there is no work, and otherwise
-// launches exactly one kernel on the caller's stream.  Nothing here
+// launches one kernel (the attention calls one or two) on the caller's stream.  Nothing here
 // allocates, synchronises or keeps state beyond the per-thread error text.
 #include <cmath>
 #include <cstdarg>

@@ -48,7 +48,8 @@ def test_slot_mappings_fuzz(cuda_device, seed):
                  comp=bool(rng.integers(0, 2)), with_base=bool(rng.integers(0, 2)))
 
 
-@pytest.mark.parametrize("R,T", [(1, 1), (5000, 7001), (9, 170003), (4095, 3), (4096, 3)])
+@pytest.mark.parametrize("R,T", [(1, 1), (5000, 7001), (9, 170003), (4095, 3), (4096, 3),
+                                 (9, 250003), (5000, 240001), (3, 233471), (3, 233472)])
 def test_slot_mappings_sizes(cuda_device, R, T):
     """One token; more requests than are staged in shared memory (and the last
     that are); enough tokens for four per thread with a ragged end."""
@@ -59,8 +60,12 @@ def test_slot_mappings_sizes(cuda_device, R, T):
 def test_slot_mappings_partial_outputs_and_bounds(cuda_device):
     """Outputs left out, an output that is not 16-byte aligned (one per thread is
     stored), and entries around the outputs that stay as they were."""
-    d = cuda_device
-    T, R = 200001, 3
+    for T in (200001, 250001):
+        _check_partial(cuda_device, T)
+
+
+def _check_partial(d, T):
+    R = 3
     rng = np.random.default_rng(5)
     q = _ragged(rng, R, T)
     seq = (q + 17).astype(np.int32)
