@@ -68,6 +68,7 @@ constexpr int kMaxGroups = 4;
 constexpr int kMaxBlocks = 4;         // 128-dim blocks of a row (head_dim 512)
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kMaxCols = 64;
+constexpr int kMostParts = 8;         // parts a cluster joins
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 16.0f;        // log2 units the maximum may run ahead of the reference
@@ -141,6 +142,8 @@ struct Shared {
     uint32_t tmem;
     uint2 scales[2][kTile];        // UE8M0 bytes of the rows
     uint8_t row_bad[2][kTile];     // kTokens: the row holds a NaN or an infinity
+    int32_t failed;                // a wait of this CTA expired
+    float2 part_ml[kMaxCols];      // joined in a cluster: the columns' references and sums
 };
 
 struct LaunchShape {
@@ -151,6 +154,7 @@ struct LaunchShape {
     int64_t units;           // with every part of a cut unit counted
     int64_t whole;           // units before this one are not cut
     int64_t part_rows;       // columns of the cut ones
+    int32_t cluster;         // 1: a unit's parts are the CTAs of a cluster, which joins them
     uint32_t tmem_cols;
     float scale_log2;
     float* part_o;           // [row of a cut unit's column][split][D]
@@ -896,7 +900,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 float inv = 1.0f;
                 if (t >= 0) {
                     if (un.part_row >= 0) {
-                        if (quad == 0) {
+                        if (kSrc != kTokens && ls.cluster) {
+                            if (quad == 0) sh.part_ml[n] = make_float2(m_used, total);
+                        } else if (quad == 0) {
                             float* ml = ls.part_ml + ((un.part_row + n) * ls.splits + un.part) * 2;
                             ml[0] = m_used;
                             ml[1] = total;
@@ -917,7 +923,18 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!wait_all(&sh.freed[0], (step - 1) & 1)) return false;  // the last block
                 tmem_fence_after();
             }
-            if (un.part_row >= 0) {
+            if (kSrc != kTokens && ls.cluster) {
+                // in place of the tile, which the products are done with: [column][dim]
+                for (int j = 0; j < kBlocks; ++j) {
+                    float o[NC];
+#pragma unroll
+                    for (int k = 0; k < NC; ++k) o[k] = 0.0f;
+                    if (!(flags & kEmpty)) tmem_ld<NC>(lane_base + N + j * N, o);
+#pragma unroll
+                    for (int k = 0; k < NC; ++k)
+                        sts_f32(k_tile + ((group * NC + k) * D + j * 128 + srow) * 4, o[k]);
+                }
+            } else if (un.part_row >= 0) {
                 for (int j = 0; j < kBlocks; ++j) {
                     float o[NC];
 #pragma unroll
@@ -981,6 +998,73 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
     }
 }
 
+// ---- joining the parts of a unit in a cluster -------------------------------------------
+//
+// The formula of attention_join_kernel, for few parts (kMostParts): their O^T stay in
+// shared memory, and each CTA joins every splits-th column, a thread four dims of it.
+template <int kCols, int D, int kWorking>
+__device__ __forceinline__ void join_in_cluster(const AttnParams& p, const LaunchShape& ls, Shared& sh,
+                                                uint32_t k_tile) {
+    const Unit& un = sh.unit[0];
+    const int S = ls.splits, rank = (int)(blockIdx.x % S);
+    constexpr int kPer = D / 4, kAtOnce = kCols / 16;  // threads of a column; columns a thread has in work
+    const int d = (int)threadIdx.x % kPer * 4, step = kWorking / kPer * S;
+    for (int c0 = rank + (int)threadIdx.x / kPer * S; c0 < ls.heads_per_unit; c0 += kAtOnce * step) {
+        float2 ml[kAtOnce][kMostParts];
+        float ref[kAtOnce], total[kAtOnce];
+        float4 a[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kMostParts; ++i)
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int c = min(c0 + u * step, kCols - 1);  // columns not in use are not stored
+                ml[u][i] = make_float2(-INFINITY, 0.0f);
+                if (i < S) ml[u][i] = ld_cluster_f32x2(smem_u32(&sh.part_ml[c]), i);
+            }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kMostParts; ++i) m = fmaxf(m, ml[u][i].x);
+            ref[u] = m == -INFINITY ? 0.0f : m;
+            total[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kMostParts; ++i) {
+                ml[u][i].x = ex2_approx(ml[u][i].x - ref[u]);
+                total[u] += ml[u][i].x * ml[u][i].y;
+            }
+            a[u] = make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kMostParts; ++i) {
+            if (i >= S) break;
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+                v[u] = ld_cluster_f32x4(k_tile + (min(c0 + u * step, kCols - 1) * D + d) * 4, i);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                a[u].x += ml[u][i].x * v[u].x;
+                a[u].y += ml[u][i].x * v[u].y;
+                a[u].z += ml[u][i].x * v[u].z;
+                a[u].w += ml[u][i].x * v[u].w;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int c = c0 + u * step;
+            if (c >= ls.heads_per_unit || un.col_token[c] < 0) continue;
+            const int64_t t = un.col_token[c], h = un.col_head[c];
+            const float den = total[u] + ex2_approx(un.col_sink[c] - ref[u]);
+            const float inv = total[u] == 0.0f ? 0.0f : 1.0f / den;
+            st_v2(p.out + t * p.out_stride_t + h * p.out_stride_h + d,
+                  make_uint2(pack_bf16x2(a[u].x * inv, a[u].y * inv), pack_bf16x2(a[u].z * inv, a[u].w * inv)));
+            if (p.lse && d == 0)
+                p.lse[t * p.lse_stride_t + h] = total[u] == 0.0f ? -INFINITY : (ref[u] + log2f(total[u])) * kLn2;
+        }
+    }
+}
+
 constexpr size_t kAlign = 1024;
 
 size_t smem_bytes(int n, int head_dim) {
@@ -1017,6 +1101,7 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
         mbar_init(&sh.p_ready, kWorkers);
         mbar_init(&sh.drain, 1);
         for (int i = 0; i < kGroups; ++i) mbar_init(&sh.group_bar[i], 4);
+        sh.failed = 0;
         mbar_fence_init();
     }
     if (warp == kMmaWarp) tmem_alloc(&sh.tmem, ls.tmem_cols);
@@ -1040,6 +1125,14 @@ __global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
         }
     }
     if (!ok && lane == 0) atomicAdd(&g_attn_wait_timeouts, 1u);
+    if (kSrc != kTokens && ls.cluster) {
+        // every CTA comes to both barriers, also one whose waits expired
+        if (!ok) sh.failed = 1;
+        __syncwarp();
+        cluster_sync();
+        if (warp < kWorkers && !sh.failed) join_in_cluster<N, D, kWorkers * kWarp>(p, ls, sh, smem_u32(k_tile));
+        cluster_sync();
+    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -1163,6 +1256,11 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     ls.splits = (int32_t)splits;
     ls.units = ls.whole + rest * splits;
     ls.part_rows = rest * ls.heads_per_unit * ls.tokens_per_unit;
+    // Few parts, one to a CTA, are joined in a cluster: no second launch, no workspace.
+    // Pairs of SMs can always be had; more of them in a cluster only for few units, as
+    // what is left of a GPC's SMs cannot take part.
+    ls.cluster = pl.src != kTokens && ls.whole == 0 && splits > 1 && splits <= kMostParts && ls.units <= sms &&
+                 (splits == 2 || ls.units <= 64);
     const uint32_t need = (uint32_t)pl.n * (1 + head_dim / 128);
     ls.tmem_cols = 32;
     while (ls.tmem_cols < need) ls.tmem_cols *= 2;
@@ -1170,7 +1268,7 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
 }
 
 int64_t part_bytes(const LaunchShape& ls, int32_t head_dim) {
-    return (ls.part_rows * ls.splits * (head_dim + 2) * (int64_t)sizeof(float) + 15) / 16 * 16;
+    return ls.cluster ? 0 : (ls.part_rows * ls.splits * (head_dim + 2) * (int64_t)sizeof(float) + 15) / 16 * 16;
 }
 
 template <int N, int kSrc, int D>
@@ -1180,7 +1278,8 @@ cudaError_t launch(const AttnParams& p, const LaunchShape& ls, cudaStream_t stre
     const cudaError_t e = set_smem_limit_per_device(attention_kernel<N, kSrc, D>, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t grid = ls.units < sm_count() ? ls.units : sm_count();
-    return launch_pdl(attention_kernel<N, kSrc, D>, dim3((unsigned)grid), dim3(Roles<kSrc>::kThreads), smem, stream, p, ls);
+    return launch_pdl_clusters(attention_kernel<N, kSrc, D>, ls.cluster ? ls.splits : 1, dim3((unsigned)grid),
+                               dim3(Roles<kSrc>::kThreads), smem, stream, p, ls);
 }
 
 template <int kSrc, int D>
@@ -1207,7 +1306,7 @@ cudaError_t run(AttnParams p, int64_t max_keys, bool indexed, cudaStream_t strea
     cudaError_t e = pl.src == kIndexed ? launch_d<kIndexed>(p, pl, stream)
                     : pl.src == kOneToken ? launch_d<kOneToken>(p, pl, stream)
                                           : launch_d<kTokens>(p, pl, stream);
-    if (e != cudaSuccess || pl.ls.splits == 1) return e;
+    if (e != cudaSuccess || pl.ls.splits == 1 || pl.ls.cluster) return e;
     return launch_pdl(attention_join_kernel, dim3((unsigned)pl.ls.part_rows), dim3(128),
                       (size_t)pl.ls.splits * 2 * sizeof(float), stream, p, pl.ls);
 }

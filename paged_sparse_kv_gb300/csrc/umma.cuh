@@ -174,6 +174,33 @@ __device__ __forceinline__ float warp_max(float v) {
 // Operand tiles are only written here and read by the tensor cores, so these
 // order themselves among volatile asm (barriers included) and need not hold back
 // other memory accesses.
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Every thread of every CTA of the cluster; orders shared-memory writes before it
+// against reads of them after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// What stands at `addr` (this CTA's) in the shared memory of cluster CTA `rank`; in
+// order with cluster_sync, both being volatile.
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr, int rank) {
+    float2 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+                 "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank));
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, int rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank));
+    return v;
+}
+
 __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
