@@ -1002,6 +1002,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 //
 // The formula of attention_join_kernel, for few parts (kMostParts): their O^T stay in
 // shared memory, and each CTA joins every splits-th column, a thread four dims of it.
+// Bound by the latency of the other CTAs' shared memory, hence several columns at once.
 template <int kCols, int D, int kWorking>
 __device__ __forceinline__ void join_in_cluster(const AttnParams& p, const LaunchShape& ls, Shared& sh,
                                                 uint32_t k_tile) {
@@ -1256,11 +1257,15 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     ls.splits = (int32_t)splits;
     ls.units = ls.whole + rest * splits;
     ls.part_rows = rest * ls.heads_per_unit * ls.tokens_per_unit;
-    // Few parts, one to a CTA, are joined in a cluster: no second launch, no workspace.
-    // Pairs of SMs can always be had; more of them in a cluster only for few units, as
-    // what is left of a GPC's SMs cannot take part.
+    // Few parts, one to a CTA, are joined in a cluster, which saves a launch and the
+    // workspace (4 us of the host's time): pairs of parts (64 tokens of 64 heads 27.7 us
+    // with either join, 76 28.1 against 28.7), and up to eight parts of 16 columns (one
+    // token of 16 heads 10.7 against 10.4).  Five parts of 64 columns take 17.4 against
+    // 13.6, as each CTA then reads 130 KB from the others.  At most 64 SMs in clusters of
+    // more than two: what a GPC has left over cannot take part (30 units in 150 CTAs
+    // 35 us against 17).
     ls.cluster = pl.src != kTokens && ls.whole == 0 && splits > 1 && splits <= kMostParts && ls.units <= sms &&
-                 (splits == 2 || ls.units <= 64);
+                 (splits == 2 || (pl.n == 16 && ls.units <= 64));
     const uint32_t need = (uint32_t)pl.n * (1 + head_dim / 128);
     ls.tmem_cols = 32;
     while (ls.tmem_cols < need) ls.tmem_cols *= 2;
