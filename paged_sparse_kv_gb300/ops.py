@@ -65,24 +65,28 @@ def _need(t: torch.Tensor, dtype: torch.dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _page_size(cache: torch.Tensor) -> int:
+def _page_size(shape, stride) -> int:
     """Bytes of a page, -1 where a page is not contiguous (from the strides: a view of a page
     would cost 2 us)."""
     n, gap = 1, False
-    for size, stride in zip(cache.shape[:0:-1], cache.stride()[:0:-1]):
-        gap |= size != 1 and stride != n
+    for size, step in zip(shape[:0:-1], stride[:0:-1]):
+        gap |= size != 1 and step != n
         n *= size
     return -1 if gap and n > 0 else n
 
 
 def _pages(cache: torch.Tensor):
     _need(cache, torch.uint8, "cache")
-    size = _page_size(cache) if cache.dim() > 1 and cache.shape[0] > 0 else -1
-    if size < 0:
+    shape, stride = cache.shape, cache.stride()
+    if len(shape) == 2 and stride[1] == 1:
+        size = shape[1]
+    else:
+        size = _page_size(shape, stride) if len(shape) > 1 else -1
+    if size < 0 or shape[0] == 0:
         raise ValueError("cache must be [num_pages >= 1, ...] uint8 with contiguous pages")
-    if cache.shape[0] == 1:  # a size-1 dim may carry any stride (0 from broadcasting)
-        return 1, max(cache.stride(0), size)
-    return cache.shape[0], cache.stride(0)
+    if shape[0] == 1:  # a size-1 dim may carry any stride (0 from broadcasting)
+        return 1, max(stride[0], size)
+    return shape[0], stride[0]
 
 
 def _rows(t: torch.Tensor, name: str):
