@@ -41,7 +41,7 @@
 // cycle, half again its arithmetic.  A tile (head_dim 512, 64 columns) is 64 of
 // them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
 // barriers and weights share the pipe.  Measured 7700 cycles a tile in the loop plus
-// 6000 a unit for O^T: 4096 tokens of 128 heads over 640 rows take 1077 us, 508
+// 6000 a unit for O^T: 4096 tokens of 128 heads over 640 rows take 1088 us, 503
 // TFLOP/s, against 288 us at the matrix rate and 490 at the shared-memory rate.  The
 // rest is the chain dequantise - scores - softmax - weights, which one 128 KB tile
 // beside 64 KB of queries cannot overlap with itself.
