@@ -163,6 +163,38 @@ def test_sparse_last_units_cut(cuda_device, T, H, D, C):
     _run_sparse(cuda_device, T + H, T, H, D, 64, C, C // 3)
 
 
+@pytest.mark.parametrize("T,H,D,C,sink", [
+    (64, 64, 512, 640, True), (76, 33, 256, 300, False), (1, 16, 512, 1000, True), (3, 5, 128, 1024, False),
+    (8, 16, 512, 640, True), (30, 128, 512, 300, True), (52, 130, 128, 257, True), (2, 1, 256, 129, True)])
+def test_sparse_joined_in_cluster(cuda_device, T, H, D, C, sink):
+    """Two parts of a unit, or up to eight of 16 columns, joined through shared memory."""
+    _run_sparse(cuda_device, T + H + C, T, H, D, 64, C, C // 5, sink=sink, hole=0.5)
+
+
+def test_sparse_joined_in_cluster_captured(cuda_device):
+    """Captured, replayed, and run beside another call of its kind: the eager call's bits."""
+    d = cuda_device
+    cases = [_decode_case(d, 30, T=64), _decode_case(d, 31, T=1, H=16)]
+    want = [ops.sparse_mla_attention(q, c, i, 64) for q, c, i in cases]
+    torch.cuda.synchronize(d)
+    graphs, outs = [], []
+    for q, c, i in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ops.sparse_mla_attention(q, c, i, 64))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(d), torch.cuda.Stream(d)]
+    for _ in range(3):
+        for s, g, o in zip(streams, graphs, outs):
+            o[0].fill_(-3.0)
+            s.wait_stream(torch.cuda.current_stream(d))
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize(d)
+        for (a, b), (x, y) in zip(want, outs):
+            assert torch.equal(a, x) and torch.equal(b, y)
+
+
 def test_sparse_growing_scores(cuda_device):
     """Scores that grow from the first column to the last, so that every tile
     raises the maximum, by little and by more than any lazy threshold."""
