@@ -83,9 +83,9 @@ __device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
-// Units of several tokens test what they dequantise for NaN and mask by column, which
-// twice the warps do faster (1901 tokens of 16 heads over up to 6144 rows: 755 us with
-// 16, 933 with 8).
+// Units of several tokens look at every score for NaN and mask by column, which twice
+// the warps do faster (1901 tokens of 16 heads over up to 6144 rows: 623 us with 16,
+// 722 with 8).
 template <int kSrc>
 struct Roles {
     static constexpr int kWorkers = kSrc == kTokens ? 16 : 8;
@@ -523,33 +523,29 @@ __device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t (&w)[8
     }
 }
 
-// Whether any of 16 E4M3 bytes of scale byte b may be NaN or overflow bf16: a byte
-// of all ones below its sign, or a scale that takes the largest value, 1.75 * 2^8, past 2^128.
-__device__ __forceinline__ bool may_be_non_finite(uint4 raw, uint32_t b) {
-    const uint32_t ones = ((raw.x & 0x7F7F7F7Fu) + 0x01010101u) | ((raw.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                          ((raw.z & 0x7F7F7F7Fu) + 0x01010101u) | ((raw.w & 0x7F7F7F7Fu) + 0x01010101u);
-    return (ones & 0x80808080u) != 0 || b >= 127 + 128 - 8;
-}
-
-// The same of eight bf16 values: all exponent bits set.
+// Whether any of eight bf16 values is an infinity or a NaN: all exponent bits set.
 __device__ __forceinline__ bool any_non_finite(uint4 v) {
     const uint32_t ones = ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
                           ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
     return (ones & 0x80008000u) != 0;
 }
 
-// Clears the non-finite values of w; true if there were any.
-template <int K>
-__device__ __forceinline__ bool clear_non_finite(uint32_t (&w)[K]) {
+// Whether a row of the tile holds a value that is not finite; if so it is cleared, as
+// a weight of 0 would not keep it from the columns that do not see the row.
+// `flag` is set first, for the warps that look at the row when it is cleared.
+template <int D>
+__device__ __noinline__ bool clear_bad_row(uint32_t k_tile, int row, volatile uint8_t* flag) {
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
-        if (lo) w[i] &= 0xFFFF0000u;
-        if (hi) w[i] &= 0x0000FFFFu;
-        bad |= lo | hi;
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i) bad |= any_non_finite(lds_v4(k_tile + i / 8 * kChunkBytes + row * 128 + i % 8 * 16));
+    if (bad) {
+        *flag = 1;
+        __threadfence_block();
+#pragma unroll 1
+        for (int i = 0; i < D / 8; ++i) sts_v4(k_tile + i / 8 * kChunkBytes + row * 128 + i % 8 * 16, 0, 0, 0, 0);
     }
-    return bad;
+    __threadfence_block();
+    return bad || *flag != 0;
 }
 
 // 16-byte copy global -> shared; `bytes` 0 writes zeros.
@@ -698,10 +694,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 block = j;
                 return step == 0 || wait_all(&sh.freed[j], (step - 1) & 1);
             };
-            const auto put = [&](uint4 x, uint32_t scale, int row, uint32_t dst) {
+            const auto put = [&](uint4 x, uint32_t scale, uint32_t dst) {
                 uint32_t w[8];
                 dequant16(x, scale, w);
-                if (kSrc == kTokens && may_be_non_finite(x, scale) && clear_non_finite(w)) sh.row_bad[buf][row] = 1;
                 sts_v4(dst, w[0], w[1], w[2], w[3]);
                 sts_v4(dst ^ 16, w[4], w[5], w[6], w[7]);
             };
@@ -715,14 +710,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
 #pragma unroll
                     for (int i = 0; i < kFours; ++i) {
                         const uint32_t dst = (r_dst + c * kChunkBytes + i * 512) ^ ((i & 1) * 64);
-                        if (kSrc == kTokens) {
-                            const uint4 x = ld_stream_v4(data[i] + at);
-                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                            if (any_non_finite(x) && clear_non_finite(w)) sh.row_bad[buf][r_row + 4 * i] = 1;
-                            sts_v4(dst, w[0], w[1], w[2], w[3]);
-                        } else {
-                            copy16(dst, data[i] + at, 16);
-                        }
+                        copy16(dst, data[i] + at, 16);
                     }
                 }
             }
@@ -734,7 +722,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!need(c / 2)) return false;
 #pragma unroll
                 for (int i = 0; i < kEights; ++i)  // 8 rows on, the swizzle is the same
-                    put(raw_chunk[i], scale[i], c_row + 8 * i, c_dst + c * kChunkBytes + i * 1024);
+                    put(raw_chunk[i], scale[i], c_dst + c * kChunkBytes + i * 1024);
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
@@ -747,8 +735,7 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                 if (!need(j)) return false;
 #pragma unroll
                 for (int i = 0; i < kFours; ++i)  // 4 rows on, bit 2 of the swizzle turns
-                    put(raw[b % 2][i], scale[i], b_row + 4 * i,
-                        (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
+                    put(raw[b % 2][i], scale[i], (b_dst + j * 2 * kChunkBytes + i * 512) ^ ((i & 1) * 64));
                 if (j >= 2) load_block(tl, raw[b % 2], j - 2);
                 if (b == 0 && (flags & kFirst)) copies_done();  // hands over the unit's queries too
                 fence_async_smem();
@@ -778,11 +765,19 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
             tmem_ld<NC>(lane_base, s);
             const bool ok = tl.row[srow].data != reinterpret_cast<const uint8_t*>(g_zero_row);
             if (kSrc == kTokens) {
-                // every worker has handed over its share of the tile: its flags are there
-                if (!wait_all(&sh.full[0], step & 1)) return false;
-                if (rope_from < kBlocks && !wait_all(&sh.full[kBlocks - 1], step & 1)) return false;
+                // A row with an infinity or a NaN gives none but such scores, whatever the query.
+                float z = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NC; ++k) z = fmaf(s[k], 0.0f, z);
+                bool bad = false;
+                if (__any_sync(0xFFFFFFFFu, z != 0.0f)) {
+                    // every worker has handed over its share of the tile
+                    if (!wait_all(&sh.full[0], step & 1)) return false;
+                    if (rope_from < kBlocks && !wait_all(&sh.full[kBlocks - 1], step & 1)) return false;
+                    if (z != 0.0f) bad = clear_bad_row<D>(k_tile, srow, &sh.row_bad[buf][srow]);
+                    __syncwarp();
+                }
                 const int32_t pos = tl.pos + srow;
-                const bool bad = sh.row_bad[buf][srow];
                 if (!__all_sync(0xFFFFFFFFu, ok && !bad && pos >= un.all_lo && pos <= un.all_hi)) {
 #pragma unroll
                     for (int k = 0; k < NC; ++k) {
