@@ -83,12 +83,9 @@ __device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
-// Units of several tokens look at every score for NaN and mask by column, which twice
-// the warps do faster (1901 tokens of 16 heads over up to 6144 rows: 623 us with 16,
-// 722 with 8).
-template <int kSrc>
+template <int N>
 struct Roles {
-    static constexpr int kWorkers = kSrc == kTokens ? 16 : 8;
+    static constexpr int kWorkers = N == 16 ? 8 : 16;  // a worker has 8 columns at least
     static constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 32 rows
     static constexpr int kMmaWarp = kWorkers, kPlanWarp = kWorkers + 1;
     static constexpr int kThreads = (kWorkers + 2) * kWarp;
@@ -598,7 +595,7 @@ __device__ __forceinline__ float column_sums(float (&v)[K], int lane) {
 template <int N, int kSrc, int D>
 __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uint32_t k_tile,
                      uint32_t q_tile, uint32_t p_tile, uint32_t tmem) {
-    constexpr int kWorkers = Roles<kSrc>::kWorkers, kGroups = Roles<kSrc>::kGroups;
+    constexpr int kWorkers = Roles<N>::kWorkers, kGroups = Roles<N>::kGroups;
     constexpr int NC = N / kGroups;  // columns of a worker warp
     constexpr int kChunks = D / 64, kBlocks = D / 128;
     constexpr int kOwn = kTile / kWorkers;             // rows of a warp
@@ -1069,10 +1066,10 @@ size_t smem_bytes(int n, int head_dim) {
 }
 
 template <int N, int kSrc, int D>
-__global__ void __launch_bounds__(Roles<kSrc>::kThreads, 1)
+__global__ void __launch_bounds__(Roles<N>::kThreads, 1)
     attention_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ LaunchShape ls) {
-    constexpr int kWorkers = Roles<kSrc>::kWorkers, kGroups = Roles<kSrc>::kGroups;
-    constexpr int kMmaWarp = Roles<kSrc>::kMmaWarp, kPlanWarp = Roles<kSrc>::kPlanWarp;
+    constexpr int kWorkers = Roles<N>::kWorkers, kGroups = Roles<N>::kGroups;
+    constexpr int kMmaWarp = Roles<N>::kMmaWarp, kPlanWarp = Roles<N>::kPlanWarp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = smem_raw + ((kAlign - (smem_u32(smem_raw) & (kAlign - 1))) & (kAlign - 1));
     uint8_t* k_tile = base;
@@ -1279,7 +1276,7 @@ cudaError_t launch(const AttnParams& p, const LaunchShape& ls, cudaStream_t stre
     if (e != cudaSuccess) return e;
     const int64_t grid = ls.units < sm_count() ? ls.units : sm_count();
     return launch_pdl_clusters(attention_kernel<N, kSrc, D>, ls.cluster ? ls.splits : 1, dim3((unsigned)grid),
-                               dim3(Roles<kSrc>::kThreads), smem, stream, p, ls);
+                               dim3(Roles<N>::kThreads), smem, stream, p, ls);
 }
 
 template <int kSrc, int D>
