@@ -40,19 +40,17 @@
 // 128 rows and 64 columns moves 6 KB and takes the 48 cycles those need at 128 bytes a
 // cycle, half again its arithmetic.  A tile (head_dim 512, 64 columns) is 64 of
 // them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
-// barriers and weights share the pipe.  Measured 7700 cycles a tile in the loop plus
-// 6000 a unit for O^T: 4096 tokens of 128 heads over 640 rows take 1088 us, 503
-// TFLOP/s, against 288 us at the matrix rate and 490 at the shared-memory rate.  The
-// rest is the chain dequantise - scores - softmax - weights, which one 128 KB tile
-// beside 64 KB of queries cannot overlap with itself.
-// Other forms of it, measured on 317 tokens of 128 heads over 1152 rows (205 us)
-// and on the 4096 tokens:
-//  * tiles of 64 rows, two in work: 283 and 1454 us; the first product drops to half
-//    rate and each tile pays the waits of a whole one;
-//  * separate warps for dequantisation and softmax on top of it: 293 and 1510;
+// barriers and weights share the port, which the counters have busy 64 % of the time.
+// Measured 8400 cycles a tile, its share of writing O^T (6000 a unit) included: 4096
+// tokens of 128 heads over 640 rows take 1008 us, 543 TFLOP/s, against 288 us at the
+// matrix rate and 490 at the port's.  The rest is the chain dequantise - scores - softmax -
+// weights, which one 128 KB tile beside 64 KB of queries cannot overlap with itself.
+// Other forms of it, measured on the 4096 tokens when this one took 1164 us:
+//  * tiles of 64 rows, two in work: 1454 us; the first product drops to half rate and
+//    each tile pays the waits of a whole one;
+//  * separate warps for dequantisation and softmax on top of it: 1510;
 //  * records copied into shared memory in bulk, one copy a row, by a copying warp:
-//    470 and 2364 (a copy of 576 bytes takes some 130 cycles of the copy unit);
-//  * 16 worker warps: 239 against 227 and 1168 against 1154, fewer registers each.
+//    2364 (a copy of 576 bytes takes some 130 cycles of the copy unit).
 #include <atomic>
 #include <cmath>
 
@@ -83,9 +81,13 @@ __device__ const uint4 g_zero_row[64 + 2 * 448 / 16] = {};
 
 enum { kIndexed = 0, kOneToken = 1, kTokens = 2 };
 
+// 16 worker warps (64 heads: 64 tokens 23.8 us against 27.9 with 8; 32 heads: 19.1
+// against 21.4), 8 where 16 would have fewer than 8 columns each.  16 columns as 32
+// with 16 warps: 64 tokens of 16 heads 19.1 us against 18.7, one row of 8192 keys for
+// each 122 against 114.
 template <int N>
 struct Roles {
-    static constexpr int kWorkers = N == 16 ? 8 : 16;  // a worker has 8 columns at least
+    static constexpr int kWorkers = N == 16 ? 8 : 16;
     static constexpr int kGroups = kWorkers / 4;  // warps of a group share their columns, each with 32 rows
     static constexpr int kMmaWarp = kWorkers, kPlanWarp = kWorkers + 1;
     static constexpr int kThreads = (kWorkers + 2) * kWarp;
@@ -1250,12 +1252,12 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     ls.units = ls.whole + rest * splits;
     ls.part_rows = rest * ls.heads_per_unit * ls.tokens_per_unit;
     // Few parts, one to a CTA, are joined in a cluster, which saves a launch and the
-    // workspace (4 us of the host's time): pairs of parts (64 tokens of 64 heads 27.7 us
-    // with either join, 76 28.1 against 28.7), and up to eight parts of 16 columns (one
-    // token of 16 heads 10.7 against 10.4).  Five parts of 64 columns take 17.4 against
-    // 13.6, as each CTA then reads 130 KB from the others.  At most 64 SMs in clusters of
-    // more than two: what a GPC has left over cannot take part (30 units in 150 CTAs
-    // 35 us against 17).
+    // workspace (4 us of the host's time): pairs of parts (64 tokens of 64 heads 23.6 us
+    // against 26.8 with the second kernel, 76 24.0 against 27.9), and up to eight parts of
+    // 16 columns (one token of 16 heads 11.1 against 10.7 of device time).  Five parts of
+    // 64 columns take 17.4 against 13.4, as each CTA then reads 130 KB from the others.  At
+    // most 64 SMs in clusters of more than two: what a GPC has left over cannot take part
+    // (30 units of 16 columns in 150 CTAs 22.0 us against 14.0).
     ls.cluster = pl.src != kTokens && ls.whole == 0 && splits > 1 && splits <= kMostParts && ls.units <= sms &&
                  (splits == 2 || (pl.n == 16 && ls.units <= 64));
     const uint32_t need = (uint32_t)pl.n * (1 + head_dim / 128);
