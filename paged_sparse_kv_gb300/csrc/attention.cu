@@ -627,8 +627,8 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
     float m_used = -INFINITY;  // of column `lane` of the group, for lane < NC
     constexpr int kFours = kOwn / 4, kEights = kOwn / 8;
     uint4 raw[2][kFours];      // blocks rope_from - 1, rope_from - 2, ... of a lane's rows
-    uint4 raw_chunk[kEights];        // the E4M3 chunk of a mixed block
-    uint2 scales = make_uint2(0, 0);  // of row own + lane % 16
+    uint4 raw_chunk[kEights];  // the E4M3 chunk of a mixed block
+    uint2 scales = make_uint2(0, 0);  // of row own + lane % kOwn
 
     const auto load_block = [&](const Tile& t, uint4(&x)[kFours], int j) {
         const uint8_t* data[kFours];
@@ -1205,16 +1205,16 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     int cols = ls.heads_per_unit;
     // Neighbouring tokens of a request share a unit, and with it the tiles, where few
     // heads leave room and requests bring enough tokens that units seldom end at their
-    // boundaries.  16 heads, contexts up to 8192, 8 tokens a request: 224 us against 329
-    // with one token a unit, 4 tokens a request 437 against 383; two tokens a unit (32
-    // heads) with 32 tokens a request 935 against 1120, with 16 1200 against 1124.  Not
-    // where windows are so short that the shared tiles are no fewer (32 heads, a window
-    // of 128, 4096 tokens: 206 us against 167).
+    // boundaries.  64 requests, contexts up to 8192, 16 heads: 4 tokens a request 227 us
+    // against 287 with one token a unit, 3 259 against 233; 32 heads, two tokens a unit:
+    // 6 tokens a request 412 against 518, 4 354 against 325.  Not where windows are so
+    // short that the shared tiles are no fewer (32 heads, a window of 128, 4096 tokens:
+    // 184 us against 153).
     const auto tiles_of = [](int64_t keys) { return keys / kTile + (keys % kTile != 0); };
     const int64_t tiles = tiles_of(max_keys);
     if (!indexed && num_heads <= kMaxCols / 2) {
         const int32_t n = kMaxCols / num_heads < kWarp ? kMaxCols / num_heads : kWarp;
-        if (num_tokens >= (n < 4 ? 16 : 8) * (int64_t)num_reqs && tiles_of(max_keys + n - 1) < n * tiles) {
+        if (num_tokens >= (n < 4 ? 6 : 4) * (int64_t)num_reqs && tiles_of(max_keys + n - 1) < n * tiles) {
             ls.tokens_per_unit = n;
             cols = n * num_heads;
             pl.src = kTokens;
@@ -1224,11 +1224,12 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     const int64_t base = (num_tokens + ls.tokens_per_unit - 1) / ls.tokens_per_unit * ls.head_groups;
     // Units are cut along their tiles to fill the SMs evenly.  In the index form all
     // are of one length: whole rounds of them stay whole, and the rest is cut until it
-    // fills the SMs too (634 units of 9 tiles on 152 SMs: 209 us against 228 uncut).  In
+    // fills the SMs too (634 units of 9 tiles on 152 SMs: 191 us against 205 uncut).  In
     // the position form lengths differ from request to request: about four parts per SM
-    // (32 requests of 8 tokens, contexts up to 8192: one per SM 325 us, two 272, four 224,
-    // eight 224), of eight tiles or more; very few units are cut into one part per SM
-    // (two requests of 131072 rows: 107 us, four per SM 135).
+    // (32 requests of 8 tokens, contexts up to 8192: one per SM 253 us, two 238, four 196,
+    // eight 195; 32 of 32 tokens 1013, 1012, 779, 823), of eight tiles or more; very few
+    // units are cut into one part per SM (two requests of 131072 rows: 100 us, four per
+    // SM 130).
     const int64_t sms = sm_count();
     int64_t rest = base, splits;
     if (indexed) {

@@ -51,8 +51,8 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a, uint64_t 
 }
 
 // Bounded wait for a barrier phase, without the suspend-time hint of mbar_try_wait and
-// with the clock read once in 64 polls: phases are short here (317 tokens of 128
-// heads: 187.0 us against 188.6 with mbar_wait_bounded).
+// with the clock read once in 64 polls: phases are short here (1901 tokens of 16 heads
+// over up to 6144 rows: 618 us against 632 with mbar_wait_bounded).
 __device__ __forceinline__ bool mbar_poll_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
     const uint32_t addr = smem_u32(bar);
     const auto done = [&]() {
