@@ -40,9 +40,9 @@
 // 128 rows and 64 columns moves 6 KB and takes the 48 cycles those need at 128 bytes a
 // cycle, half again its arithmetic.  A tile (head_dim 512, 64 columns) is 64 of
 // them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
-// barriers and weights share the port, which the counters have busy 64 % of the time.
-// Measured 8400 cycles a tile, its share of writing O^T (6000 a unit) included: 4096
-// tokens of 128 heads over 640 rows take 1007 us, 544 TFLOP/s, against 288 us at the
+// barriers and weights share the port, which the counters have busy 68 % of the time.
+// Measured 8100 cycles a tile, its share of writing O^T (6000 a unit) included: 4096
+// tokens of 128 heads over 640 rows take 968 us, 566 TFLOP/s, against 288 us at the
 // matrix rate and 490 at the port's.  The rest is the chain dequantise - scores - softmax -
 // weights, which one 128 KB tile beside 64 KB of queries cannot overlap with itself.
 // Other forms of it, measured on the 4096 tokens when this one took 1164 us:
