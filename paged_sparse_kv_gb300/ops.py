@@ -633,14 +633,15 @@ def _vec(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, size: int, in
 
 
 def _table(t: torch.Tensor, name: str, rows: int, index: int):
-    """Address, row stride and width of an int32 block table with ``rows`` rows at least."""
+    """Address, row stride and width of an int32 block table with ``rows`` rows at least; the
+    library refuses a stride below the width (expanded or overlapping rows)."""
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
     _same(t, index, name)
     stride, (n, width) = _rows(t, name), t.shape
     if n < rows:
         raise ValueError(f"{name} must have at least {rows} rows, got {n}")
-    return t.data_ptr(), max(stride, width), width
+    return t.data_ptr(), stride, width
 
 
 def compute_slot_mappings(query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
@@ -814,7 +815,7 @@ def sparse_mla_attention(q: torch.Tensor, cache: torch.Tensor, indices: torch.Te
     _call(q.device, "sparse_mla_attention", *qa, T, H, *_cache_of(cache, "cache", i), block_size,
           *_cache_of(extra_cache, "extra_cache", i),
           block_size if extra_block_size is None else extra_block_size, D, rope_dim,
-          indices.data_ptr(), max(_rows(indices, "indices"), C), C, C if split is None else split,
+          indices.data_ptr(), _rows(indices, "indices"), C, C if split is None else split,
           D ** -0.5 if softmax_scale is None else softmax_scale,
           _vec(sink, torch.float32, "sink", H, i), *oa)
     return out, lse
