@@ -727,8 +727,9 @@ psk_status compute_slot_mappings(
  *   pool_head_out   int32 [1]: first page of the pool that is still unused.
  *   err_count       nullable int32 [1], incremented for every row that is not
  *                   extended and keeps the pages it holds: one that needs more
- *                   than bt_width pages (it demands none), or one whose pages
- *                   would end past pool_size (it keeps its place in the sums).
+ *                   than bt_width pages (it demands none), or one whose missing
+ *                   pages would end past pool_size (it keeps its place in the
+ *                   sums).  A row that misses none is never counted.
  *   The inputs are not changed apart from block_table, so a repeated call gives
  *   the same result; page_counts_out and pool_head_out must not overlap the
  *   other arrays or each other.  pool_size <= INT32_MAX.  With num_reqs = 0

@@ -54,7 +54,7 @@ def extend_block_tables(seq_lens, pool, table, block_size, counts=None, head=0, 
             got = more
             if more:
                 head_out = start + more
-        if need > width or start + more > len(pool):
+        if need > width or (more > 0 and start + more > len(pool)):
             errors += 1
         for c in range(have, width):
             table[r, c] = pool[start + c - have] if c < have + got else -1

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
     const bool own_head = start <= p.pool_size || blockIdx.x == 0;
     for (int32_t r = r0; r < r1; ++r) {
         const Demand d = demand_of(p, r);
-        const bool served = start + d.more <= p.pool_size;
+        const bool served = d.more == 0 || start + d.more <= p.pool_size;
         const int32_t got = served ? d.more : 0;
         int32_t* row = p.bt + (int64_t)r * p.bt_stride;
         const int32_t count = d.have + got;
