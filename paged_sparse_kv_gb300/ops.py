@@ -703,8 +703,6 @@ def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
         page_counts_out = torch.empty((R,), dtype=i32, device=dev)
     if pool_head_out is None:
         pool_head_out = torch.empty((1,), dtype=i32, device=dev)
-    if R == 0:  # no launch: the head stays where it is
-        pool_head_out.fill_(0) if pool_head is None else pool_head_out.copy_(pool_head)
     _call(dev, "extend_block_tables", _vec(seq_lens, i32, "seq_lens", R, i), R, block_size,
           compress_ratio, _vec(page_counts, i32, "page_counts", R, i),
           _vec(page_pool, i32, "page_pool", 0, i), page_pool.numel(),
@@ -712,6 +710,11 @@ def extend_block_tables(seq_lens: torch.Tensor, page_pool: torch.Tensor,
           _vec(page_counts_out, i32, "page_counts_out", R, i),
           _vec(pool_head_out, i32, "pool_head_out", 1, i),
           _vec(err_count, i32, "err_count", 1, i))
+    if R == 0:  # nothing was launched: the head stays where it is
+        if pool_head is None:
+            pool_head_out[:1].fill_(0)
+        else:
+            torch.clamp(pool_head[:1], min=0, out=pool_head_out[:1])
     return block_table, page_counts_out, pool_head_out
 
 
