@@ -783,9 +783,11 @@ psk_status extend_block_tables(
  *                 16-byte aligned (may be NULL when that is 0).  Scratch for the
  *                 call: its contents need not be kept between calls, and two
  *                 calls that can run at the same time need one each.
- *   A NaN in q or in a visible row, or a score that is NaN or +infinity, makes
- *   that (t, h) NaN; what is not visible to a token has no influence on it,
- *   whatever it holds.
+ *   A NaN in q or in a visible row, or a score that is NaN or +infinity (also
+ *   where s_j * log2(e) leaves the range of binary32), makes that (t, h) NaN; a
+ *   score of -infinity is a weight of 0, and a (t, h) with no other scores has
+ *   out and lse as if it saw nothing.  What is not visible to a token has no
+ *   influence on it, whatever it holds.
  */
 int64_t sparse_mla_attention_workspace_bytes(int64_t num_tokens, int32_t num_heads,
                                              int32_t head_dim, int32_t cols);

@@ -835,7 +835,9 @@ __device__ bool work(const AttnParams& p, const LaunchShape& ls, Shared& sh, uin
                         alpha = m_used == -INFINITY ? 1.0f : ex2_approx(m_used - top);  // no sums before
                         m_used = top;
                     }
-                    ref[lane] = m_used == -INFINITY ? kNone : m_used;
+                    // A score past binary32 makes the column NaN; fma(s, scale, -infinity) of a
+                    // finite s would be -infinity, a weight of 0.
+                    ref[lane] = m_used == -INFINITY ? kNone : m_used == INFINITY ? NAN : m_used;
                     aux[lane] = alpha;
                 }
                 ++exchange;
