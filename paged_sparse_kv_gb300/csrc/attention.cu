@@ -42,7 +42,7 @@
 // them, 3100 cycles; dequantising it writes 128 KB more, 1000 cycles, and the loads,
 // barriers and weights share the port, which the counters have busy 68 % of the time.
 // Measured 8100 cycles a tile, its share of writing O^T (6000 a unit) included: 4096
-// tokens of 128 heads over 640 rows take 968 us, 566 TFLOP/s, against 288 us at the
+// tokens of 128 heads over 640 rows take 964 us, 568 TFLOP/s, against 288 us at the
 // matrix rate and 490 at the port's.  The rest is the chain dequantise - scores - softmax -
 // weights, which one 128 KB tile beside 64 KB of queries cannot overlap with itself.
 // Other forms of it, measured on the 4096 tokens when this one took 1164 us:
@@ -1234,7 +1234,9 @@ Plan make_plan(int64_t num_tokens, int32_t num_heads, int32_t head_dim, int64_t 
     // (32 requests of 8 tokens, contexts up to 8192: one per SM 253 us, two 238, four 196,
     // eight 195; 32 of 32 tokens 1013, 1012, 779, 823), of eight tiles or more; very few
     // units are cut into one part per SM (two requests of 131072 rows: 100 us, four per
-    // SM 130).
+    // SM 130).  The tiles are those the table has room for, the lengths being on the device:
+    // parts behind a short context's tiles are empty, write zeros and are joined all the same
+    // (figures of wide tables at chunk_mla_attention in psk.h).
     const int64_t sms = sm_count();
     int64_t rest = base, splits;
     if (indexed) {

@@ -17,13 +17,14 @@ constexpr int kThreads = 256;
 // by binary search; up to kStageReqs boundaries are staged in shared memory by
 // one coalesced read, so that the search costs no chain of L2 reads.
 //
-// Bound by the 28 bytes written per token and, with few tokens, by the launch and a
-// chain of four dependent reads (boundary, length, table, store): 1000003 tokens of
-// 37 requests 9.6 us, 2.9 TB/s of the 6.8 measured; 256 tokens 2.6 us.  Two tokens a
-// thread halve the searches and make every store of a warp 512 contiguous bytes
-// (one takes 11.2 us; four, whose 16-byte stores leave gaps, 11.9), which pays once
-// the SMs are full: 300000 tokens 4.37 us against 4.64 with one, 100000 3.55 against
-// 2.90.  Staging the boundaries: 256 requests 2.76 us against 3.24 from L2, 4000
+// With few tokens the time is the launch and a chain of four dependent reads (boundary,
+// length, table, store): 256 tokens 2.7 us.  With many it is 2.3 times that of the 28 bytes
+// written per token (1000003 tokens of 37 requests 9.6 us, 2.9 TB/s of the 6.8 measured),
+// with 55 % of the issue slots in use.  No unit is full; the chain of a search and three
+// reads, in 2.6 waves of CTAs, is the likely rest.  Two tokens a thread halve the searches
+// and make every store of a warp 512 contiguous bytes (one takes 11.2 us; four, whose
+// 16-byte stores leave gaps, 11.9), which pays once the SMs are full: 300000 tokens 4.37 us
+// against 4.64 with one, 100000 3.55 against 2.90.  Staging the boundaries: 256 requests 2.76 us against 3.24 from L2, 4000
 // requests of 250 tokens 13.3 against 13.9, 8000 of 125 15.0 against 14.4.
 constexpr int kStageReqs = 4096;
 
@@ -120,9 +121,9 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const SlotMapParams 
 //
 // Bound by the table written and the pages read, and by the chain before them
 // (counts and lengths of all earlier rows, the head, the pages): 2048 rows of 2048
-// columns 11.1 us, 2.4 TB/s of the 6.8 measured; 256 rows of 128 2.6 us.  Filling
-// the tails of the rows before the demand is known took 12.5, one row a CTA 13.0, 512
-// threads a CTA 13.6.
+// columns 8.7 us, 3.0 TB/s of the 6.8 measured; 256 rows of 128 2.4 us.  Measured before
+// powers of two were divided by shifts, when this form took 11.1: the tails of the rows
+// filled before the demand is known 12.5, one row a CTA 13.0, 512 threads a CTA 13.6.
 
 struct Demand {
     int32_t have, more;

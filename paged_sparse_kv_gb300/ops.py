@@ -801,7 +801,8 @@ def sparse_mla_attention(q: torch.Tensor, cache: torch.Tensor, indices: torch.Te
                          sink: Optional[torch.Tensor] = None, rope_dim: int = 64,
                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None):
-    """Attention of ``q`` [T, H, D] over the fp8_ds_mla rows ``indices`` [T, C] names: slots of
+    """Attention of ``q`` [T, H, D] over the fp8_ds_mla rows ``indices`` [T, C] names (records with
+    UE8M0 scales; binary32 ones, is_ue8m0=False at the insert, would be misread): slots of
     ``cache`` in columns [0, split), of ``extra_cache`` in the others (``split`` defaults to all
     columns).  Returns (out [T, H, D] bf16, lse [T, H] binary32); scale defaults to D^-1/2.
     ``workspace`` (uint8) is scratch; two calls that can run at once need one each."""
@@ -836,7 +837,9 @@ def chunk_mla_attention(q: torch.Tensor, cache: torch.Tensor, query_start_loc: t
                         workspace: Optional[torch.Tensor] = None):
     """Causal attention of a chunk of new tokens ``q`` [T, H, D] over their requests' positions
     through ``block_table`` (whole context, or the last ``window_size`` positions); rows of the
-    new tokens must be in the cache.  Returns (out [T, H, D] bf16, lse [T, H] binary32)."""
+    new tokens must be in the cache (records with UE8M0 scales).  Returns (out [T, H, D] bf16,
+    lse [T, H] binary32).  Whole contexts: time and scratch grow with the table's width; where a
+    bound on ``seq_lens`` is known, pass ``block_table[:, :ceil(bound / block_size)]``."""
     i, i32 = _index(q), torch.int32
     qa = _heads(q, "q", i)
     T, H, D = q.shape

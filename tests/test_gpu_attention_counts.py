@@ -113,3 +113,23 @@ def test_chunk_wide_tables(cuda_device, q_lens, seq, H, D, window):
     _chunk(cuda_device, q_lens, seq, H, D, window, 131072 // BS, len(seq) + H)
 
 
+
+
+def test_chunk_narrowed_table(cuda_device):
+    """The first columns of a wide table: the plan, the scratch and the bits of a tight one."""
+    d, R, H, W = cuda_device, 64, 64, 16
+    cache = torch.from_numpy(_unit_rows(4096, 512)).to(d)
+    wide = torch.randint(0, 4096 // BS, (R, 2048), dtype=torch.int32, device=d)
+    q = torch.randn((R, H, 512), device=d).to(torch.bfloat16)
+    cu, seq, t2r = (torch.arange(R + 1, dtype=torch.int32, device=d), torch.arange(1, R + 1, dtype=torch.int32, device=d) * 16,
+                    torch.arange(R, dtype=torch.int32, device=d))
+    need = [ops.chunk_mla_attention_workspace_bytes(d, R, R, H, 512, w, BS) for w in (W, 2048)]
+    assert need[0] < need[1]
+    ws = torch.empty((max(need[0], 16),), dtype=torch.uint8, device=d)
+    a = ops.chunk_mla_attention(q, cache, cu, seq, t2r, wide[:, :W], BS, workspace=ws)
+    b = ops.chunk_mla_attention(q, cache, cu, seq, t2r, wide[:, :W].contiguous(), BS)
+    c = ops.chunk_mla_attention(q, cache, cu, seq, t2r, wide, BS)
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, y)
+        # other parts: the same weights, rounded to bf16 against other references
+        assert torch.allclose(x.float(), z.float(), rtol=2**-6, atol=2**-8)
