@@ -85,6 +85,20 @@ typedef enum psk_record {
     PSK_REC_FP8_INDEXER = 2
 } psk_record;
 
+/* Element types of apply_rotary_embedding's tensors. */
+typedef enum psk_dtype {
+    PSK_DTYPE_BF16 = 0,
+    PSK_DTYPE_FP16 = 1,
+    PSK_DTYPE_FP32 = 2
+} psk_dtype;
+
+/* Frequencies of build_rope_cos_sin_cache. */
+typedef enum psk_rope_scaling {
+    PSK_ROPE_UNSCALED = 0,
+    PSK_ROPE_LINEAR = 1,
+    PSK_ROPE_YARN = 2
+} psk_rope_scaling;
+
 /* Message describing the calling thread's most recent error ("" if none). */
 const char* psk_last_error(void);
 
@@ -842,6 +856,73 @@ psk_status chunk_mla_attention(
     float softmax_scale, const float* sink, void* out, int64_t out_stride_t,
     int64_t out_stride_h, float* lse, int64_t lse_stride_t, void* workspace,
     int64_t workspace_bytes, psk_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions                                                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * build_rope_cos_sin_cache -- the table of cosines and sines that
+ * apply_rotary_embedding, indexer_k_norm_rope_store and compress_kv_cache_insert
+ * read (GPT-J layout of [OPS] _apply_gptj_rope_tail_rows: cosines, then sines).
+ *
+ *   cos_sin_cache  binary32 [num_pos, rope_dim], row stride cs_stride (written):
+ *                  with n = rope_dim / 2, i < n and pos = first_pos + row,
+ *                    row[i] = m cos(pos f_i),  row[n + i] = m sin(pos f_i).
+ *                  Angles are reduced exactly; a value is off by at most m 2^-22.
+ *   first_pos, num_pos  0 <= first_pos, first_pos + num_pos <= 2^31.
+ *   rope_dim       even, in [2, 512].
+ *   theta          base > 1: f_i = theta^(-2i / rope_dim) where unscaled.
+ *   scaling        PSK_ROPE_LINEAR: f_i / factor.  PSK_ROPE_YARN (the by-parts rule of
+ *                  the YaRN method): f_i (1 - g_i) + f_i / factor g_i with g_i =
+ *                  clamp((i - lo) / (hi - lo), 0, 1), lo = max(floor(d(beta_fast)), 0),
+ *                  hi = min(ceil(d(beta_slow)), rope_dim - 1) (hi - lo at least 0.001),
+ *                  d(b) = rope_dim ln(original_max_pos / (2 pi b)) / (2 ln theta): pairs
+ *                  that make more than beta_fast turns over the original length keep
+ *                  their frequency, those that make fewer than beta_slow are stretched.
+ *   factor         >= 1 (not used unscaled); original_max_pos >= 1 and
+ *                  beta_fast >= beta_slow > 0 (used by PSK_ROPE_YARN alone).
+ *   attention_factor  m, finite and > 0.
+ */
+psk_status build_rope_cos_sin_cache(
+    float* cos_sin_cache, int64_t cs_stride, int64_t first_pos, int64_t num_pos,
+    int32_t rope_dim, double theta, psk_rope_scaling scaling, double factor,
+    int64_t original_max_pos, double beta_fast, double beta_slow, double attention_factor,
+    psk_stream_t stream);
+
+/*
+ * apply_rotary_embedding -- rotates rope_dim dims of every head of queries and,
+ * in the same launch, of keys: what the inserts and the attention calls expect to
+ * have been done ([OPS] _apply_gptj_rope_tail_rows on the last dims), and, with
+ * inverse = 1, what is undone on the attention's output, whose rows are rotated
+ * keys.  The inverse is also the gradient of the forward rotation.
+ *
+ *   q              [num_tokens, num_heads, head_dim] of `dtype`; (t, h) at q +
+ *                  t*q_stride_t + h*q_stride_h (elements).  k: the same with
+ *                  num_k_heads heads, or NULL.
+ *   q_out, k_out   as q and k.  q_out == q (with equal strides) rotates in place
+ *                  and touches nothing else; otherwise the dims outside
+ *                  [rope_offset, rope_offset + rope_dim) are copied.  Rows of an
+ *                  output must not overlap one another, nor, out of place, any input.
+ *   dtype          products and sums are binary32, rounded once to it.
+ *   interleaved    1: pairs (2i, 2i + 1) of the rotated dims; 0: (i, i + rope_dim/2).
+ *                  Pair i: (a, b) -> (a c_i - b s_i, b c_i + a s_i); inverse: s_i -> -s_i.
+ *   positions      int64 [num_tokens]; row pos of cos_sin_cache [max_pos, rope_dim]
+ *                  (row stride cs_stride) holds c, then s.  A negative position marks a
+ *                  padding token and leaves its rows unrotated (copied out of place);
+ *                  so does a position >= max_pos, which is counted in err_count
+ *                  (nullable device int32, once per token).
+ *   Addresses and strides need the element's own alignment; 16-byte accesses are
+ *   used where all of them, rope_offset, rope_dim and head_dim allow it.
+ */
+psk_status apply_rotary_embedding(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t num_heads,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h, int32_t num_k_heads,
+    int64_t num_tokens, psk_dtype dtype, int32_t head_dim, int32_t rope_offset,
+    int32_t rope_dim, int32_t interleaved, int32_t inverse, const int64_t* positions,
+    const float* cos_sin_cache, int64_t cs_stride, int64_t max_pos, void* q_out,
+    int64_t q_out_stride_t, int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t,
+    int64_t k_out_stride_h, int32_t* err_count, psk_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,12 @@ PSK_ERR_CUDA = 3
 PSK_REC_FP8_DS_MLA = 0
 PSK_REC_MXFP4 = 1
 PSK_REC_FP8_INDEXER = 2
+PSK_DTYPE_BF16 = 0
+PSK_DTYPE_FP16 = 1
+PSK_DTYPE_FP32 = 2
+PSK_ROPE_UNSCALED = 0
+PSK_ROPE_LINEAR = 1
+PSK_ROPE_YARN = 2
 
 STATUS_NAMES = {0: "PSK_OK", 1: "PSK_ERR_INVALID_ARGUMENT", 2: "PSK_ERR_UNSUPPORTED",
                 3: "PSK_ERR_CUDA"}
@@ -28,6 +34,7 @@ STATUS_NAMES = {0: "PSK_OK", 1: "PSK_ERR_INVALID_ARGUMENT", 2: "PSK_ERR_UNSUPPOR
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F64 = ctypes.c_double
 
 SIGNATURES = {
     "psk_last_error": (ctypes.c_char_p, []),
@@ -97,6 +104,11 @@ SIGNATURES = {
                _P, _P, _P]),
     "extend_block_tables": (
         _I32, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _I64, _I32, _P, _P, _P, _P]),
+    "build_rope_cos_sin_cache": (
+        _I32, [_P, _I64, _I64, _I64, _I32, _F64, _I32, _F64, _I64, _F64, _F64, _F64, _P]),
+    "apply_rotary_embedding": (
+        _I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32,
+               _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]),
     "indexer_k_norm_rope_store": (
         _I32, [_P, _I64, _P, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I32, _I32, _P, _I64,
                _I64, _I32, _P, _P]),

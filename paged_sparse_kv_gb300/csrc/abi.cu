@@ -20,6 +20,7 @@
 #include "launch.h"
 #include "psk.h"
 #include "psk_common.cuh"
+#include "rotary.h"
 
 namespace {
 
@@ -107,6 +108,22 @@ psk_status check_attention(const psk::AttnParams& p, bool work, int64_t workspac
     return PSK_OK;
 }
 
+// The strides of one of apply_rotary_embedding's tensors, in elements of `size` bytes.
+psk_status check_rotary(const void* in, int64_t it, int64_t ih, const void* out, int64_t ot, int64_t oh,
+                        int32_t heads, int64_t num_tokens, int32_t head_dim, int32_t size, const char* name) {
+    CHECK(heads >= 1, "the number of heads of %s must be >= 1", name);
+    CHECK(in != nullptr && out != nullptr, "%s and its output must be non-null", name);
+    CHECK(aligned(in, size) && aligned(out, size), "%s and its output must be aligned to their elements", name);
+    CHECK(it >= 0 && ih >= 0 && ot >= 0 && oh >= 0, "strides of %s must not be negative", name);
+    const int64_t most = INT64_MAX / 8;
+    CHECK(it <= most && ih <= most && ot <= most && oh <= most, "strides of %s overflow", name);
+    CHECK((num_tokens <= 1 || ot >= head_dim) && (heads <= 1 || oh >= head_dim),
+          "output strides of %s must be at least head_dim", name);
+    CHECK(in != out || ((num_tokens <= 1 || it == ot) && (heads <= 1 || ih == oh)),
+          "%s in place needs equal strides", name);
+    return PSK_OK;
+}
+
 // The largest number of positions a token of a call can see.
 int64_t chunk_max_keys(int32_t bt_width, int32_t block_size, int32_t window) {
     const int64_t all = (int64_t)bt_width * block_size;
@@ -119,7 +136,7 @@ extern "C" {
 
 const char* psk_last_error(void) { return g_last_error.c_str(); }
 
-int32_t psk_abi_version(void) { return 6; }
+int32_t psk_abi_version(void) { return 7; }
 
 psk_status psk_device_wait_timeouts(uint32_t* count) {
     CHECK(count != nullptr, "count must be non-null");
@@ -1103,6 +1120,116 @@ psk_status chunk_mla_attention(
           "int32 arrays must be 4-byte aligned");
     return cuda_status(psk::launch_attention_chunk(p, reinterpret_cast<cudaStream_t>(stream)),
                        "chunk_mla_attention launch");
+}
+
+psk_status build_rope_cos_sin_cache(float* cos_sin_cache, int64_t cs_stride, int64_t first_pos,
+                                    int64_t num_pos, int32_t rope_dim, double theta,
+                                    psk_rope_scaling scaling, double factor,
+                                    int64_t original_max_pos, double beta_fast, double beta_slow,
+                                    double attention_factor, psk_stream_t stream) {
+    CHECK(num_pos >= 0 && first_pos >= 0 && first_pos <= (1ll << 31) && num_pos <= (1ll << 31) - first_pos,
+          "need 0 <= first_pos and first_pos + num_pos <= 2^31");
+    CHECK(rope_dim >= 2 && rope_dim % 2 == 0 && rope_dim <= 2 * psk::kMaxTablePairs,
+          "rope_dim must be even and in [2, %d] (got %d)", 2 * psk::kMaxTablePairs, rope_dim);
+    CHECK(std::isfinite(theta) && theta > 1.0, "theta must be finite and > 1");
+    CHECK(scaling == PSK_ROPE_UNSCALED || scaling == PSK_ROPE_LINEAR || scaling == PSK_ROPE_YARN,
+          "unknown scaling %d", (int)scaling);
+    CHECK(scaling == PSK_ROPE_UNSCALED || (std::isfinite(factor) && factor >= 1.0),
+          "factor must be finite and >= 1");
+    CHECK(scaling != PSK_ROPE_YARN ||
+              (original_max_pos >= 1 && beta_slow > 0.0 && beta_fast >= beta_slow && std::isfinite(beta_fast)),
+          "need original_max_pos >= 1 and beta_fast >= beta_slow > 0");
+    const float m = (float)attention_factor;
+    CHECK(std::isfinite(m) && m > 0.0f, "attention_factor must be finite and > 0");
+    CHECK(cs_stride >= rope_dim, "cs_stride must be >= rope_dim");
+    CHECK(cs_stride <= (INT64_MAX >> 34), "cs_stride overflows");
+    if (num_pos == 0) return ok();
+    CHECK(cos_sin_cache != nullptr && aligned(cos_sin_cache, 4), "cos_sin_cache must be non-null and 4-byte aligned");
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    psk::RopeTableParams p{};
+    p.out = cos_sin_cache;
+    p.stride = cs_stride;
+    p.first_pos = first_pos;
+    p.num_pos = num_pos;
+    p.pairs = rope_dim / 2;
+    p.factor = m;
+    const auto pair_of = [&](double turns) {
+        return rope_dim * std::log((double)original_max_pos / (kTwoPi * turns)) / (2.0 * std::log(theta));
+    };
+    double lo = 0.0, span = 1.0;
+    if (scaling == PSK_ROPE_YARN) {
+        lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        span = std::fmax(std::fmin(std::ceil(pair_of(beta_slow)), rope_dim - 1.0) - lo, 0.001);
+    }
+    for (int32_t i = 0; i < p.pairs; ++i) {
+        const double f = std::pow(theta, -2.0 * i / rope_dim);
+        const double g = scaling == PSK_ROPE_YARN ? std::fmin(std::fmax((i - lo) / span, 0.0), 1.0)
+                                                  : scaling == PSK_ROPE_LINEAR ? 1.0 : 0.0;
+        const double turns = (scaling == PSK_ROPE_UNSCALED ? f : f * (1.0 - g) + f / factor * g) / kTwoPi;
+        p.turn[i] = (uint64_t)std::ldexp(turns, 64);
+    }
+    return cuda_status(psk::launch_rope_table(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "build_rope_cos_sin_cache launch");
+}
+
+psk_status apply_rotary_embedding(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int32_t num_heads, const void* k,
+    int64_t k_stride_t, int64_t k_stride_h, int32_t num_k_heads, int64_t num_tokens,
+    psk_dtype dtype, int32_t head_dim, int32_t rope_offset, int32_t rope_dim,
+    int32_t interleaved, int32_t inverse, const int64_t* positions, const float* cos_sin_cache,
+    int64_t cs_stride, int64_t max_pos, void* q_out, int64_t q_out_stride_t,
+    int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t, int64_t k_out_stride_h,
+    int32_t* err_count, psk_stream_t stream) {
+    CHECK(num_tokens >= 0 && num_tokens <= (int64_t)INT32_MAX, "num_tokens must be in [0, INT32_MAX]");
+    CHECK(dtype == PSK_DTYPE_BF16 || dtype == PSK_DTYPE_FP16 || dtype == PSK_DTYPE_FP32, "unknown dtype %d",
+          (int)dtype);
+    CHECK(head_dim >= 2 && head_dim <= (1 << 16), "head_dim must be in [2, 65536] (got %d)", head_dim);
+    CHECK(rope_dim >= 2 && rope_dim % 2 == 0, "rope_dim must be even and >= 2 (got %d)", rope_dim);
+    CHECK(rope_offset >= 0 && rope_offset <= head_dim - rope_dim, "need 0 <= rope_offset <= head_dim - rope_dim");
+    CHECK(interleaved == 0 || interleaved == 1, "interleaved must be 0 or 1");
+    CHECK(inverse == 0 || inverse == 1, "inverse must be 0 or 1");
+    CHECK(max_pos >= 0 && cs_stride >= rope_dim, "need max_pos >= 0 and cs_stride >= rope_dim");
+    CHECK(num_heads >= 1 && (k == nullptr || num_k_heads >= 1), "numbers of heads must be >= 1");
+    CHECK((int64_t)num_heads + (k == nullptr ? 0 : num_k_heads) <= (int64_t)INT32_MAX, "too many heads");
+    if (num_tokens == 0) return ok();
+    const int32_t size = dtype == PSK_DTYPE_FP32 ? 4 : 2;
+    psk_status st = check_rotary(q, q_stride_t, q_stride_h, q_out, q_out_stride_t, q_out_stride_h, num_heads,
+                                 num_tokens, head_dim, size, "q");
+    if (st != PSK_OK) return st;
+    if (k != nullptr) {
+        st = check_rotary(k, k_stride_t, k_stride_h, k_out, k_out_stride_t, k_out_stride_h, num_k_heads,
+                          num_tokens, head_dim, size, "k");
+        if (st != PSK_OK) return st;
+    }
+    CHECK(positions != nullptr && aligned(positions, 8), "positions must be non-null and 8-byte aligned");
+    CHECK((max_pos == 0 || cos_sin_cache != nullptr) && aligned(cos_sin_cache, 4),
+          "cos_sin_cache must be non-null and 4-byte aligned");
+    CHECK(aligned(err_count, 4), "err_count must be 4-byte aligned");
+    psk::RotaryParams p{};
+    p.q = {static_cast<const uint8_t*>(q), static_cast<uint8_t*>(q_out), q_stride_t * size, q_stride_h * size,
+           q_out_stride_t * size, q_out_stride_h * size};
+    p.heads = p.all_heads = num_heads;
+    p.copy_q = q != q_out;
+    if (k != nullptr) {
+        p.k = {static_cast<const uint8_t*>(k), static_cast<uint8_t*>(k_out), k_stride_t * size,
+               k_stride_h * size, k_out_stride_t * size, k_out_stride_h * size};
+        p.all_heads += num_k_heads;
+        p.copy_k = k != k_out;
+    }
+    p.num_tokens = num_tokens;
+    p.dtype = dtype;
+    p.head_dim = head_dim;
+    p.offset = rope_offset;
+    p.rope_dim = rope_dim;
+    p.half = !interleaved;
+    p.inverse = inverse;
+    p.positions = positions;
+    p.cos_sin = cos_sin_cache;
+    p.cs_stride = cs_stride;
+    p.max_pos = max_pos;
+    p.err = err_count;
+    return cuda_status(psk::launch_rotary(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "apply_rotary_embedding launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,236 @@
+// rotary.cu -- rotary positions: the table of cosines and sines, and the
+// rotation of a part of each head.
+#include "psk.h"
+#include "psk_common.cuh"
+#include "rotary.h"
+
+namespace psk {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---- the table ---------------------------------------------------------------------
+//
+// Row p holds cos and sin of (first + p) f_i.  The angle is kept as a fraction of a turn
+// in 64 bits, turn_i = f_i / (2 pi) 2^64: a product modulo 2^64 drops whole turns exactly,
+// so a far position costs no accuracy and no binary64 arithmetic (of which this part does
+// little).  An eighth of a turn to either side of the nearest quarter is left for the
+// series of sine and cosine.
+
+// sin and cos of a fraction of a turn: quarters off, then Taylor's series on
+// [-pi/4, pi/4], whose first dropped terms (x^11/11!, x^12/12!) are below 2^-28.
+__device__ __forceinline__ void sincos_turn(uint64_t u, float& s, float& c) {
+    const uint32_t quarter = (uint32_t)((u + (1ull << 61)) >> 62);
+    constexpr float kRadians = (float)(6.283185307179586 / 18446744073709551616.0);  // 2 pi / 2^64
+    const float x = __ll2float_rn((long long)(u - ((uint64_t)quarter << 62))) * kRadians;
+    const float y = x * x;
+    float a = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
+    a = fmaf(a, y, 8.3333333e-3f);
+    a = fmaf(a, y, -0.16666667f);
+    const float sn = fmaf(a * y, x, x);
+    float b = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);
+    b = fmaf(b, y, -1.3888889e-3f);
+    b = fmaf(b, y, 4.1666667e-2f);
+    b = fmaf(b, y, -0.5f);
+    const float cs = fmaf(b, y, 1.0f);
+    s = quarter & 1 ? cs : sn;
+    c = quarter & 1 ? sn : cs;
+    if (quarter & 2) s = -s;
+    if ((quarter + 1) & 2) c = -c;
+}
+
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
+    pdl_wait();
+    const int64_t n = p.num_pos * p.pairs;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = i / p.pairs;
+        const int32_t pair = (int32_t)(i - row * p.pairs);
+        float s, c;
+        sincos_turn((uint64_t)(p.first_pos + row) * p.turn[pair], s, c);
+        float* out = p.out + row * p.stride + pair;
+        out[0] = c * p.factor;
+        out[p.pairs] = s * p.factor;
+    }
+    pdl_launch_dependents();
+}
+
+// ---- the rotation -------------------------------------------------------------------
+//
+// (a, b) -> (a c - b s, b c + a s) for the pairs (2i, 2i + 1) or (i, i + rope_dim / 2) of
+// the rotated dims; products and sums in binary32, one rounding to the tensor's type.
+// A unit is what one thread takes of a row at a time: 16 bytes that hold whole pairs, or
+// two times 16 bytes of the half layout, or 16 bytes to copy; single pairs and elements
+// where sizes, strides or addresses allow no 16-byte accesses.  A thread keeps its unit
+// for all the heads it visits, so a token's cosines and sines are read once per CTA.
+
+template <int kType> struct Elem;
+template <> struct Elem<PSK_DTYPE_BF16> {
+    using Raw = uint16_t;
+    static __device__ __forceinline__ float get(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+    static __device__ __forceinline__ uint16_t put(float x) { return (uint16_t)pack_bf16x2(x, 0.0f); }
+};
+template <> struct Elem<PSK_DTYPE_FP16> {
+    using Raw = uint16_t;
+    static __device__ __forceinline__ float get(uint16_t x) {
+        float f;
+        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(x));
+        return f;
+    }
+    static __device__ __forceinline__ uint16_t put(float x) {
+        uint16_t r;
+        asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(x));
+        return r;
+    }
+};
+template <> struct Elem<PSK_DTYPE_FP32> {
+    using Raw = float;
+    static __device__ __forceinline__ float get(float x) { return x; }
+    static __device__ __forceinline__ float put(float x) { return x; }
+};
+
+// Elements a thread moves at once.
+template <int kType, bool kWide>
+constexpr int per_access() { return kWide ? 16 / (int)sizeof(typename Elem<kType>::Raw) : 1; }
+
+template <typename Raw, int V>
+struct alignas(sizeof(Raw) * V) Pack {
+    Raw v[V];
+};
+
+// (a, b) of packs that hold pairs side by side, or of one pack with interleaved pairs.
+template <int kType, int V>
+__device__ __forceinline__ void turn(typename Elem<kType>::Raw& a, typename Elem<kType>::Raw& b, float c, float s) {
+    using E = Elem<kType>;
+    const float x = E::get(a), y = E::get(b);
+    a = E::put(fmaf(x, c, -(y * s)));
+    b = E::put(fmaf(y, c, x * s));
+}
+
+struct RotaryShape {
+    int32_t units, rope_units;  // of a row; those that rotate come first
+    int32_t rows_at_once;       // rows a CTA works on at a time
+    int32_t tokens;             // tokens of a CTA (where all rows of several fit at once)
+};
+
+template <int kType, bool kHalf, bool kWide>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, const RotaryShape sh) {
+    using Raw = typename Elem<kType>::Raw;
+    constexpr int V = per_access<kType, kWide>();
+    // pairs of a unit; interleaved single elements make no pair, so two are taken
+    constexpr int kPairs = kHalf ? V : V > 1 ? V / 2 : 1;
+    using P = Pack<Raw, V>;
+    pdl_wait();
+    const int slot = (int)threadIdx.x / min(sh.units, kThreads);
+    const int unit0 = (int)threadIdx.x % min(sh.units, kThreads);
+    int row0 = slot + (int)blockIdx.y * sh.rows_at_once, row_step = sh.rows_at_once * (int)gridDim.y;
+    int64_t t = (int64_t)blockIdx.x * sh.tokens;
+    bool in = slot < sh.rows_at_once;
+    if (sh.tokens > 1) {
+        t += slot / p.all_heads;
+        row0 = slot % p.all_heads;
+        row_step = p.all_heads;
+        in = slot < sh.tokens * p.all_heads;
+    }
+    if (!in || t >= p.num_tokens) return;
+    const int64_t pos = p.positions[t];
+    const bool known = pos >= 0 && pos < p.max_pos;  // else the rows stay as they are
+    if (p.err && pos >= p.max_pos && unit0 == 0 && row0 == 0) atomicAdd(p.err, 1);
+    const int n = p.rope_dim / 2;
+    for (int unit = unit0; unit < sh.units; unit += kThreads) {
+        const bool rotates = unit < sh.rope_units;
+        // first element of the unit, and of its second pack
+        int at, second = 0;
+        float c[kPairs], s[kPairs];
+        if (rotates) {
+            const int pair = unit * kPairs;
+            at = p.offset + (kHalf ? pair : 2 * pair);
+            second = kHalf ? n : 1;
+            if (known) {
+                const float* cs = p.cos_sin + pos * p.cs_stride + pair;
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    c[i] = cs[i];
+                    s[i] = p.inverse ? -cs[n + i] : cs[n + i];
+                }
+            }
+        } else {
+            at = (unit - sh.rope_units) * V;
+            if (at >= p.offset) at += p.rope_dim;
+        }
+        for (int row = row0; row < p.all_heads; row += row_step) {
+            const bool is_k = row >= p.heads;
+            const RotaryTensor& x = is_k ? p.k : p.q;
+            const int h = is_k ? row - p.heads : row;
+            const bool copy = is_k ? p.copy_k : p.copy_q;
+            const uint8_t* src = x.in + t * x.in_stride_t + h * x.in_stride_h + (int64_t)at * sizeof(Raw);
+            uint8_t* dst = x.out + t * x.out_stride_t + h * x.out_stride_h + (int64_t)at * sizeof(Raw);
+            if (!copy && (!rotates || !known)) continue;
+            P a = *reinterpret_cast<const P*>(src);
+            if (!rotates) {
+                *reinterpret_cast<P*>(dst) = a;
+            } else if constexpr (kHalf || V == 1) {
+                P b = *reinterpret_cast<const P*>(src + second * sizeof(Raw));
+                if (known) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) turn<kType, V>(a.v[i], b.v[i], c[i], s[i]);
+                }
+                *reinterpret_cast<P*>(dst) = a;
+                *reinterpret_cast<P*>(dst + second * sizeof(Raw)) = b;
+            } else {
+                if (known) {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) turn<kType, V>(a.v[2 * i], a.v[2 * i + 1], c[i], s[i]);
+                }
+                *reinterpret_cast<P*>(dst) = a;
+            }
+        }
+    }
+    pdl_launch_dependents();
+}
+
+template <int kType, bool kHalf, bool kWide>
+cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
+    constexpr int V = per_access<kType, kWide>();
+    RotaryShape sh{};
+    sh.rope_units = kHalf ? p.rope_dim / 2 / V : V > 1 ? p.rope_dim / V : p.rope_dim / 2;
+    sh.units = sh.rope_units + (p.copy_q || p.copy_k ? (p.head_dim - p.rope_dim) / V : 0);
+    sh.rows_at_once = sh.units >= kThreads ? 1 : kThreads / sh.units;
+    sh.tokens = p.all_heads < sh.rows_at_once ? sh.rows_at_once / p.all_heads : 1;
+    if (sh.tokens > p.num_tokens) sh.tokens = (int32_t)p.num_tokens;
+    if (sh.tokens == 1 && sh.rows_at_once > p.all_heads) sh.rows_at_once = p.all_heads;
+    const int64_t x = (p.num_tokens + sh.tokens - 1) / sh.tokens;
+    // few tokens: their rows are spread over CTAs until there are two per SM
+    int64_t y = (2 * (int64_t)sm_count() + x - 1) / x;
+    const int64_t most = sh.tokens > 1 ? 1 : (p.all_heads + sh.rows_at_once - 1) / sh.rows_at_once;
+    if (y > most) y = most;
+    return launch_pdl(rotary_kernel<kType, kHalf, kWide>, dim3((unsigned)x, (unsigned)y), dim3(kThreads), 0, stream, p, sh);
+}
+
+template <int kType>
+cudaError_t launch_type(const RotaryParams& p, cudaStream_t stream) {
+    constexpr int kSize = sizeof(typename Elem<kType>::Raw), V = 16 / kSize;
+    const auto even = [](const RotaryTensor& x) {
+        return ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out) | (uintptr_t)x.in_stride_t |
+                 (uintptr_t)x.in_stride_h | (uintptr_t)x.out_stride_t | (uintptr_t)x.out_stride_h) & 15) == 0;
+    };
+    const bool wide = even(p.q) && (p.all_heads == p.heads || even(p.k)) && p.offset % V == 0 &&
+                      p.rope_dim % (p.half ? 2 * V : V) == 0 && p.head_dim % V == 0;
+    if (p.half) return wide ? launch<kType, true, true>(p, stream) : launch<kType, true, false>(p, stream);
+    return wide ? launch<kType, false, true>(p, stream) : launch<kType, false, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream) {
+    const int64_t n = p.num_pos * p.pairs, most = (int64_t)sm_count() * 8;
+    const int64_t ctas = (n + kThreads - 1) / kThreads;
+    return launch_pdl(rope_table_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, stream, p);
+}
+
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream) {
+    return p.dtype == PSK_DTYPE_BF16   ? launch_type<PSK_DTYPE_BF16>(p, stream)
+           : p.dtype == PSK_DTYPE_FP16 ? launch_type<PSK_DTYPE_FP16>(p, stream)
+                                       : launch_type<PSK_DTYPE_FP32>(p, stream);
+}
+
+}  // namespace psk

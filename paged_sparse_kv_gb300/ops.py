@@ -858,3 +858,98 @@ def chunk_mla_attention(q: torch.Tensor, cache: torch.Tensor, query_start_loc: t
           D ** -0.5 if softmax_scale is None else softmax_scale,
           _vec(sink, torch.float32, "sink", H, i), *oa)
     return out, lse
+
+
+# ---- rotary positions ------------------------------------------------------------------------
+
+_ROPE_SCALING = {"none": _abi.PSK_ROPE_UNSCALED, "linear": _abi.PSK_ROPE_LINEAR, "yarn": _abi.PSK_ROPE_YARN}
+_ROTARY_DTYPES = {torch.bfloat16: _abi.PSK_DTYPE_BF16, torch.float16: _abi.PSK_DTYPE_FP16,
+                  torch.float32: _abi.PSK_DTYPE_FP32}
+
+
+def build_rope_cos_sin_cache(num_positions: int, rope_dim: int, *, theta: float = 10000.0,
+                             scaling: str = "none", factor: float = 1.0,
+                             original_positions: int = 0, beta_fast: float = 32.0,
+                             beta_slow: float = 1.0, attention_factor: float = 1.0,
+                             first_position: int = 0, device=None,
+                             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Table [num_positions, rope_dim] binary32 of the cosines, then sines, of positions from
+    ``first_position`` on; ``scaling`` "none", "linear" (by ``factor``) or "yarn" (by parts, from
+    ``original_positions``); every value times ``attention_factor``."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    if out is None:
+        if num_positions < 0 or rope_dim < 0:
+            raise ValueError("num_positions and rope_dim must be >= 0")
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError("libpsk operates on CUDA tensors only (no CPU fallback)")
+        out = torch.empty((num_positions, rope_dim), dtype=torch.float32, device=dev)
+    else:
+        _index(out)
+        _need(out, torch.float32, "out")
+        if out.shape != (num_positions, rope_dim):
+            raise ValueError(f"out must be [{num_positions}, {rope_dim}]")
+    _call(out.device, "build_rope_cos_sin_cache", out.data_ptr(), _rows(out, "out"), first_position,
+          num_positions, rope_dim, theta, _ROPE_SCALING[scaling], factor, original_positions,
+          beta_fast, beta_slow, attention_factor)
+    return out
+
+
+def _rotated(t: torch.Tensor, name: str, T: int, D: int, dtype: torch.dtype, index: int):
+    """Address and strides of a [T, H, D] (or, one head, [T, D]) tensor with unit inner stride (a
+    size-1 dim may carry any stride), and its heads."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _same(t, index, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) not in (2, 3) or shape[0] != T or shape[-1] != D or (stride[-1] != 1 and D > 1):
+        raise ValueError(f"{name} must be [{T}, heads, {D}] or [{T}, {D}] with unit inner stride")
+    H, sh = (shape[1], stride[1]) if len(shape) == 3 else (1, D)
+    if H == 1:
+        sh = D
+    return (t.data_ptr(), stride[0] if T > 1 else H * D, sh), H
+
+
+def apply_rotary_embedding(positions: torch.Tensor, q: torch.Tensor, cos_sin_cache: torch.Tensor,
+                           k: Optional[torch.Tensor] = None, *, rope_offset: Optional[int] = None,
+                           interleaved: bool = True, inverse: bool = False,
+                           q_out: Optional[torch.Tensor] = None,
+                           k_out: Optional[torch.Tensor] = None,
+                           err_count: Optional[torch.Tensor] = None):
+    """Rotate ``rope_dim = cos_sin_cache.shape[1]`` dims from ``rope_offset`` on (default: the last
+    ones) of every head of ``q`` [T, H, D] and ``k`` [T, Hk, D] or [T, D] (bf16, fp16 or binary32) by
+    ``positions`` [T] int64 (negative: a padding token, not rotated).  Returns (q_out, k_out);
+    ``q_out=q`` rotates in place.  ``inverse`` turns back, and is the gradient of the forward
+    rotation."""
+    i = _index(q)
+    if q.dtype not in _ROTARY_DTYPES:
+        raise TypeError(f"q must be one of {[str(d) for d in _ROTARY_DTYPES]}, got {q.dtype}")
+    T, D = q.shape[0], q.shape[-1]
+    _need(cos_sin_cache, torch.float32, "cos_sin_cache")
+    _same(cos_sin_cache, i, "cos_sin_cache")
+    if positions.numel() != T:
+        raise ValueError(f"positions must have {T} entries, got {positions.numel()}")
+    qa, H = _rotated(q, "q", T, D, q.dtype, i)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out {tuple(q_out.shape)} does not match q {tuple(q.shape)}")
+    qo, _ = _rotated(q_out, "q_out", T, D, q.dtype, i)
+    ka, ko, Hk = (None, 0, 0), (None, 0, 0), 0
+    if k is not None:
+        ka, Hk = _rotated(k, "k", T, D, q.dtype, i)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k_out.shape != k.shape:
+            raise ValueError(f"k_out {tuple(k_out.shape)} does not match k {tuple(k.shape)}")
+        ko, _ = _rotated(k_out, "k_out", T, D, q.dtype, i)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    stride, (rows, rope) = _rows(cos_sin_cache, "cos_sin_cache"), cos_sin_cache.shape
+    _call(q.device, "apply_rotary_embedding", *qa, H, *ka, Hk, T, _ROTARY_DTYPES[q.dtype], D,
+          D - rope if rope_offset is None else rope_offset, rope, int(bool(interleaved)),
+          int(bool(inverse)), _vec(positions, torch.int64, "positions", T, i),
+          cos_sin_cache.data_ptr(), stride, rows, *qo, *ko,
+          _vec(err_count, torch.int32, "err_count", 1, i))
+    return q_out, k_out
