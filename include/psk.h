@@ -924,6 +924,74 @@ psk_status apply_rotary_embedding(
     int64_t q_out_stride_t, int64_t q_out_stride_h, void* k_out, int64_t k_out_stride_t,
     int64_t k_out_stride_h, int32_t* err_count, psk_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Eviction from a cache                                                      */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * select_cache_evictions -- which rows of each request stay in a bounded cache,
+ * by their accumulated attention weight, and what moves where (the pages have no
+ * counterpart: their caches only grow).
+ *
+ *   For request r with n = seq_lens[r] cached rows, m = min(n, max(keep_lens[r], 0))
+ *   of them stay: the protected ones first, then those of the greatest weight;
+ *   among equals (and among protected ones, where m is too small for all) the
+ *   lower row.  A row is protected when its position is < num_first, or > newest -
+ *   num_recent with newest the greatest position of the request (num_recent > 0).
+ *   Weights compare as numbers; NaN is below all.
+ *   Rows below m that stay do not move.  The others that stay fill the rows below m
+ *   that go: with both in ascending order the i-th moves into the i-th.
+ *
+ *   weights        binary32 [num_reqs, width], row stride w_stride: row j of the cache.
+ *   seq_lens       int32 [num_reqs].  A request with seq_lens[r] > width has rows
+ *                  without a weight: it is left as it is (no moves, its length
+ *                  handed on) and counted in err_count (nullable device int32).
+ *   row_positions  nullable int32 [num_reqs, width], row stride pos_stride: position of
+ *                  row j, which after an eviction is no longer j.  NULL: j.
+ *   weights_out, positions_out  nullable, as weights and row_positions, strides
+ *                  wo_stride and po_stride: entries [0, m) of the rows that are there
+ *                  afterwards; the others are left as they were.  Each may be the
+ *                  input itself (with its stride): then moved entries alone are
+ *                  written.  They must not overlap the inputs otherwise.
+ *   moves          int32 pairs [num_reqs, >= width / 2, 2] (from, to), row stride
+ *                  moves_stride (elements, even; 8-byte aligned): entries [0,
+ *                  num_moves[r]) are written.  from >= m > to, so moves may be made in
+ *                  any order.
+ *   num_moves, seq_lens_out  int32 [num_reqs].  seq_lens_out may be seq_lens.
+ *   The pages past ceil(m / block_size) of a request hold nothing any more.
+ *   0 <= width <= 2^30; num_reqs <= 2^27.
+ */
+psk_status select_cache_evictions(
+    const float* weights, int64_t w_stride, const int32_t* seq_lens, const int32_t* keep_lens,
+    int32_t num_reqs, int32_t width, const int32_t* row_positions, int64_t pos_stride,
+    int32_t num_first, int32_t num_recent, float* weights_out, int64_t wo_stride,
+    int32_t* positions_out, int64_t po_stride, int32_t* moves, int64_t moves_stride,
+    int32_t* num_moves, int32_t* seq_lens_out, int32_t* err_count, psk_stream_t stream);
+
+/*
+ * move_cache_rows -- carries out the moves of select_cache_evictions in one paged
+ * cache: record `to` of the request becomes a copy of record `from`, bytes and
+ * scales.  A request's caches that share its rows (main and indexer records, one
+ * per layer) take one call each with the same moves where the selection is common.
+ *
+ *   cache          uint8 [num_pages, page_stride] pages of any record kind
+ *                  (head_dim, rope_dim and is_ue8m0 as in dequantize_and_gather_k_cache).
+ *   block_table    int32 [num_reqs, >= bt_width] with base_offsets as in
+ *                  compute_global_topk_indices_and_lens.
+ *   moves          int32 pairs [num_reqs, max_moves, 2], row stride moves_stride
+ *                  (elements, even; 8-byte aligned); num_moves int32 [num_reqs], of
+ *                  which at most max_moves are taken.
+ *   A move with a row without a page is not made and is counted in err_count
+ *   (nullable device int32).  No row may be `to` of two moves, or `from` of one and
+ *   `to` of another; pages that requests share must hold no row that is a `to`.
+ */
+psk_status move_cache_rows(
+    uint8_t* cache, int64_t num_pages, int64_t page_stride, int32_t block_size,
+    psk_record record, int32_t head_dim, int32_t rope_dim, int32_t is_ue8m0,
+    const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t num_reqs, const int32_t* moves, int64_t moves_stride,
+    int32_t max_moves, const int32_t* num_moves, int32_t* err_count, psk_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

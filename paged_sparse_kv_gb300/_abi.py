@@ -109,6 +109,12 @@ SIGNATURES = {
     "apply_rotary_embedding": (
         _I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32,
                _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]),
+    "select_cache_evictions": (
+        _I32, [_P, _I64, _P, _P, _I32, _I32, _P, _I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P,
+               _P, _P, _P]),
+    "move_cache_rows": (
+        _I32, [_P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I32, _P, _I32, _P, _I64, _I32,
+               _P, _P, _P]),
     "indexer_k_norm_rope_store": (
         _I32, [_P, _I64, _P, _P, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I32, _I32, _P, _I64,
                _I64, _I32, _P, _P]),

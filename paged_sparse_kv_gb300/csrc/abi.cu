@@ -14,6 +14,7 @@
 #include "attention.h"
 #include "batch_meta.h"
 #include "compressor.h"
+#include "evict.h"
 #include "gather.h"
 #include "index_build.h"
 #include "insert.h"
@@ -1230,6 +1231,96 @@ psk_status apply_rotary_embedding(
     p.err = err_count;
     return cuda_status(psk::launch_rotary(p, reinterpret_cast<cudaStream_t>(stream)),
                        "apply_rotary_embedding launch");
+}
+
+psk_status select_cache_evictions(
+    const float* weights, int64_t w_stride, const int32_t* seq_lens, const int32_t* keep_lens,
+    int32_t num_reqs, int32_t width, const int32_t* row_positions, int64_t pos_stride,
+    int32_t num_first, int32_t num_recent, float* weights_out, int64_t wo_stride,
+    int32_t* positions_out, int64_t po_stride, int32_t* moves, int64_t moves_stride,
+    int32_t* num_moves, int32_t* seq_lens_out, int32_t* err_count, psk_stream_t stream) {
+    CHECK(num_reqs >= 0 && num_reqs <= (1 << 27), "num_reqs must be in [0, 2^27]");
+    CHECK(width >= 0 && width <= (1 << 30), "width must be in [0, 2^30]");
+    CHECK(num_first >= 0 && num_recent >= 0, "num_first and num_recent must be >= 0");
+    CHECK(w_stride >= width && (row_positions == nullptr || pos_stride >= width),
+          "strides of the inputs must be >= width");
+    CHECK((weights_out == nullptr || wo_stride >= width) && (positions_out == nullptr || po_stride >= width),
+          "strides of the outputs must be >= width");
+    CHECK(moves_stride >= width / 2 * 2 && moves_stride % 2 == 0,
+          "moves_stride must be even and hold width / 2 pairs");
+    if (num_reqs == 0) return ok();
+    CHECK(seq_lens && keep_lens && num_moves && seq_lens_out,
+          "seq_lens, keep_lens, num_moves and seq_lens_out must be non-null");
+    CHECK(width == 0 || weights != nullptr, "weights must be non-null");
+    CHECK(width < 2 || moves != nullptr, "moves must be non-null");
+    CHECK(aligned(moves, 8), "moves must be 8-byte aligned");
+    CHECK(aligned(weights, 4) && aligned(seq_lens, 4) && aligned(keep_lens, 4) && aligned(row_positions, 4) &&
+              aligned(weights_out, 4) && aligned(positions_out, 4) && aligned(num_moves, 4) &&
+              aligned(seq_lens_out, 4) && aligned(err_count, 4),
+          "arrays must be 4-byte aligned");
+    CHECK(weights_out != weights || weights == nullptr || wo_stride == w_stride,
+          "weights in place need equal strides");
+    CHECK(positions_out != row_positions || row_positions == nullptr || po_stride == pos_stride,
+          "positions in place need equal strides");
+    CHECK(num_moves != seq_lens_out && num_moves != seq_lens && num_moves != keep_lens && seq_lens_out != keep_lens,
+          "num_moves and seq_lens_out must not overlap the inputs or each other");
+    psk::SelectParams p{weights, w_stride, seq_lens, keep_lens, num_reqs, width, row_positions, pos_stride,
+                        num_first, num_recent, weights_out, wo_stride, positions_out, po_stride,
+                        reinterpret_cast<int2*>(moves), moves_stride / 2, num_moves, seq_lens_out, err_count};
+    return cuda_status(psk::launch_select_evictions(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "select_cache_evictions launch");
+}
+
+psk_status move_cache_rows(
+    uint8_t* cache, int64_t num_pages, int64_t page_stride, int32_t block_size,
+    psk_record record, int32_t head_dim, int32_t rope_dim, int32_t is_ue8m0,
+    const int32_t* block_table, int64_t bt_stride, int32_t bt_width,
+    const int32_t* base_offsets, int32_t num_reqs, const int32_t* moves, int64_t moves_stride,
+    int32_t max_moves, const int32_t* num_moves, int32_t* err_count, psk_stream_t stream) {
+    CHECK(num_reqs >= 0 && max_moves >= 0, "num_reqs and max_moves must be >= 0");
+    CHECK(record == PSK_REC_FP8_DS_MLA || record == PSK_REC_MXFP4 || record == PSK_REC_FP8_INDEXER,
+          "unknown record kind %d", (int)record);
+    CHECK(is_ue8m0 == 0 || is_ue8m0 == 1, "is_ue8m0 must be 0 or 1");
+    psk::MoveParams p{};
+    if (record == PSK_REC_FP8_DS_MLA) {
+        CHECK(fp8_head_dim_ok(head_dim), "head_dim must be one of 64, 128, 256, 512, 1024 (got %d)", head_dim);
+        CHECK(rope_dim >= 0 && rope_dim < head_dim && rope_dim % 64 == 0,
+              "rope_dim must be a multiple of 64 in [0, head_dim) (got %d)", rope_dim);
+        p.data_bytes = head_dim + rope_dim;
+        p.scale_bytes = head_dim / 64 * (is_ue8m0 ? 1 : 4);
+    } else {
+        CHECK(mxfp4_head_dim_ok(head_dim), "head_dim must be one of 32, 64, 128, 256, 512, 1024 (got %d)", head_dim);
+        CHECK(rope_dim == 0, "rope_dim must be 0 for this record (got %d)", rope_dim);
+        p.data_bytes = record == PSK_REC_MXFP4 ? head_dim / 2 : head_dim;
+        p.scale_bytes = record == PSK_REC_MXFP4 ? head_dim / 32 : 4;
+    }
+    psk_status st = check_cache(cache, num_pages, page_stride, block_size, p.data_bytes + p.scale_bytes);
+    if (st != PSK_OK) return st;
+    CHECK(bt_width >= 0 && bt_stride >= bt_width, "need 0 <= bt_width <= bt_stride");
+    CHECK(moves_stride >= 2 * (int64_t)max_moves && moves_stride % 2 == 0,
+          "moves_stride must be even and hold max_moves pairs");
+    if (num_reqs == 0 || max_moves == 0) return ok();
+    CHECK(moves && num_moves, "moves and num_moves must be non-null");
+    CHECK(bt_width == 0 || block_table, "block_table must be non-null");
+    CHECK(aligned(moves, 8), "moves must be 8-byte aligned");
+    CHECK(aligned(num_moves, 4) && aligned(block_table, 4) && aligned(base_offsets, 4) && aligned(err_count, 4),
+          "int32 arrays must be 4-byte aligned");
+    p.cache = cache;
+    p.num_pages = num_pages;
+    p.page_stride = page_stride;
+    p.block_size = block_size;
+    p.bt = block_table;
+    p.bt_stride = bt_stride;
+    p.bt_width = bt_width;
+    p.base = base_offsets;
+    p.num_reqs = num_reqs;
+    p.moves = reinterpret_cast<const int2*>(moves);
+    p.moves_stride = moves_stride / 2;
+    p.max_moves = max_moves;
+    p.num_moves = num_moves;
+    p.err = err_count;
+    return cuda_status(psk::launch_move_rows(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "move_cache_rows launch");
 }
 
 }  // extern "C"

@@ -953,3 +953,91 @@ def apply_rotary_embedding(positions: torch.Tensor, q: torch.Tensor, cos_sin_cac
           cos_sin_cache.data_ptr(), stride, rows, *qo, *ko,
           _vec(err_count, torch.int32, "err_count", 1, i))
     return q_out, k_out
+
+
+# ---- eviction from a cache -------------------------------------------------------------------
+
+def _per_row(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, R: int, width: int, index: int):
+    """Address and row stride of a [>= R, >= width] matrix of values per cached row."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _same(t, index, name)
+    stride = _rows(t, name)
+    if t.shape[0] < R or t.shape[1] < width:
+        raise ValueError(f"{name} must be at least [{R}, {width}], got {tuple(t.shape)}")
+    return t.data_ptr(), stride
+
+
+def _move_list(t: torch.Tensor, R: int, count: int, index: int):
+    """Address and row stride of the moves [>= R, >= count, 2] int32."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"moves must be {torch.int32}, got {t.dtype}")
+    _same(t, index, "moves")
+    if t.dim() != 3 or t.shape[2] != 2 or t.shape[0] < R or t.shape[1] < count:
+        raise ValueError(f"moves must be at least [{R}, {count}, 2], got {tuple(t.shape)}")
+    st = t.stride()
+    if t.numel() > 0 and (st[2] != 1 or (t.shape[1] > 1 and st[1] != 2)):
+        raise ValueError("moves must hold its pairs side by side")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else 2 * t.shape[1])
+
+
+def select_cache_evictions(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor, *,
+                           row_positions: Optional[torch.Tensor] = None, num_first: int = 0,
+                           num_recent: int = 0, weights_out: Optional[torch.Tensor] = None,
+                           positions_out: Optional[torch.Tensor] = None,
+                           moves: Optional[torch.Tensor] = None,
+                           num_moves: Optional[torch.Tensor] = None,
+                           seq_lens_out: Optional[torch.Tensor] = None,
+                           err_count: Optional[torch.Tensor] = None):
+    """Choose the ``keep_lens`` [R] rows of the greatest ``weights`` [R, W] of each request (with the
+    first ``num_first`` positions and the ``num_recent`` newest ones protected) and the moves that
+    bring them below the new length.  ``weights`` and ``row_positions`` are updated in place unless
+    ``weights_out`` / ``positions_out`` are given.  Returns (moves [R, W // 2, 2] of which
+    ``num_moves`` are set, num_moves [R], seq_lens [R], weights, row_positions)."""
+    i, i32 = _index(weights), torch.int32
+    dev, R = weights.device, seq_lens.numel()
+    width = weights.shape[1] if weights.dim() == 2 else 0
+    w = _per_row(weights, torch.float32, "weights", R, width, i)
+    p = _per_row(row_positions, i32, "row_positions", R, width, i)
+    if weights_out is None:
+        weights_out, wo = weights, w
+    else:
+        wo = _per_row(weights_out, torch.float32, "weights_out", R, width, i)
+    if positions_out is None:
+        positions_out, po = row_positions, p
+    else:
+        po = _per_row(positions_out, i32, "positions_out", R, width, i)
+    for t, a in ((weights_out, wo), (positions_out, po)):
+        if t is not None and R > 1 and a[1] < width:
+            raise ValueError("rows of weights and row_positions must not overlap")
+    if moves is None:
+        moves = torch.empty((R, width // 2, 2), dtype=i32, device=dev)
+    if num_moves is None:
+        num_moves = torch.empty((R,), dtype=i32, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty((R,), dtype=i32, device=dev)
+    _call(dev, "select_cache_evictions", *w, _vec(seq_lens, i32, "seq_lens", R, i),
+          _vec(keep_lens, i32, "keep_lens", R, i), R, width, *p, num_first, num_recent, *wo, *po,
+          *_move_list(moves, R, width // 2, i), _vec(num_moves, i32, "num_moves", R, i),
+          _vec(seq_lens_out, i32, "seq_lens_out", R, i), _vec(err_count, i32, "err_count", 1, i))
+    return moves, num_moves, seq_lens_out, weights_out, positions_out
+
+
+def move_cache_rows(cache: torch.Tensor, block_table: torch.Tensor, moves: torch.Tensor,
+                    num_moves: torch.Tensor, block_size: int, head_dim: int, *,
+                    record: int = PSK_REC_FP8_DS_MLA, rope_dim: int = 64, is_ue8m0: bool = True,
+                    base_offsets: Optional[torch.Tensor] = None,
+                    err_count: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Carry out the ``moves`` [R, M, 2] (from, to; ``num_moves`` [R] of them) of
+    select_cache_evictions in ``cache``, through ``block_table``."""
+    i, i32 = _index(cache), torch.int32
+    R = num_moves.numel()
+    count = moves.shape[1] if moves.dim() == 3 else 0
+    _call(cache.device, "move_cache_rows", cache.data_ptr(), *_pages(cache), block_size, record, head_dim,
+          rope_dim if record == PSK_REC_FP8_DS_MLA else 0, int(bool(is_ue8m0)),
+          *_table(block_table, "block_table", R, i), _vec(base_offsets, i32, "base_offsets", R, i), R,
+          *_move_list(moves, R, count, i), count, _vec(num_moves, i32, "num_moves", R, i),
+          _vec(err_count, i32, "err_count", 1, i))
+    return cache
