@@ -929,6 +929,51 @@ psk_status apply_rotary_embedding(
 /* ------------------------------------------------------------------------ */
 
 /*
+ * accumulate_attention_weights -- the attention each cached row got from a chunk of
+ * new tokens, added to what it got before: what select_cache_evictions ranks rows by
+ * (the pages have no counterpart).  It takes the chunk as chunk_mla_attention did, and
+ * the lse of that call.
+ *
+ *   For row j of request r, 0 <= j < min(seq_lens[r], width):
+ *     out[r][j] = decay * weights[r][j] + sum over the tokens t of r that see row j and
+ *                 all heads h of exp(softmax_scale * q[t][h].k_j - L[t][h]),
+ *     L[t][h] = log(exp(lse[t][h]) + exp(sink[h]))  (sink null: L = lse).
+ *   Token t of request r, query_start_loc[r] <= t < query_start_loc[r+1] (and t <
+ *   num_tokens), sees the rows chunk_mla_attention lets it see: those in
+ *   [max(replay_start[r], pos - window + 1, 0), pos] that have a page; none where
+ *   is_valid_token[t] is 0.  A row nobody sees has the sum 0.  Other entries of out
+ *   are left as they were.
+ *   Products are exact in bf16 operands, sums are binary32; a row's sum is formed in
+ *   an order that depends on the sizes and the device alone.
+ *
+ *   q, softmax_scale, cache, head_dim, rope_dim, sink, the metadata and the block
+ *   table as in chunk_mla_attention, but q_stride_t and q_stride_h must be at least
+ *   head_dim where there is more than one token or head.
+ *   lse            binary32; (t, h) at lse + t*lse_stride_t + h; -infinity (with no
+ *                  sink) marks a (t, h) that saw nothing and gives no weight.
+ *   weights        binary32 [num_reqs, width], row stride w_stride.  decay finite and
+ *                  >= 0; where it is 0 weights is not read and may be NULL.
+ *   out            as weights, row stride out_stride; may be weights itself (with its
+ *                  stride) and must not overlap it otherwise.
+ *   workspace      at least accumulate_attention_weights_workspace_bytes() bytes (they
+ *                  depend on the current device), 16-byte aligned; scratch as in
+ *                  sparse_mla_attention.
+ *   A NaN or infinity reaches only the rows of the (t, h, j) it belongs to.
+ */
+int64_t accumulate_attention_weights_workspace_bytes(void);
+
+psk_status accumulate_attention_weights(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const float* lse, int64_t lse_stride_t, const uint8_t* cache,
+    int64_t num_pages, int64_t page_stride, int32_t block_size, int32_t head_dim,
+    int32_t rope_dim, const int32_t* query_start_loc, const int32_t* seq_lens,
+    const int32_t* replay_start, int32_t num_reqs, const int32_t* block_table,
+    int64_t bt_stride, int32_t bt_width, const int32_t* base_offsets, int32_t window,
+    const uint8_t* is_valid_token, float softmax_scale, const float* sink,
+    const float* weights, int64_t w_stride, int32_t width, float decay, float* out,
+    int64_t out_stride, void* workspace, int64_t workspace_bytes, psk_stream_t stream);
+
+/*
  * select_cache_evictions -- which rows of each request stay in a bounded cache,
  * by their accumulated attention weight, and what moves where (the pages have no
  * counterpart: their caches only grow).

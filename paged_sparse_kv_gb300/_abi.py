@@ -109,6 +109,11 @@ SIGNATURES = {
     "apply_rotary_embedding": (
         _I32, [_P, _I64, _I64, _I32, _P, _I64, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32,
                _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]),
+    "accumulate_attention_weights_workspace_bytes": (_I64, []),
+    "accumulate_attention_weights": (
+        _I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _I32,
+               _P, _I64, _I32, _P, _I32, _P, ctypes.c_float, _P, _P, _I64, _I32, ctypes.c_float, _P,
+               _I64, _P, _I64, _P]),
     "select_cache_evictions": (
         _I32, [_P, _I64, _P, _P, _I32, _I32, _P, _I64, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P,
                _P, _P, _P]),

@@ -12,6 +12,7 @@
 #include <string>
 
 #include "attention.h"
+#include "attn_weights.h"
 #include "batch_meta.h"
 #include "compressor.h"
 #include "evict.h"
@@ -1231,6 +1232,91 @@ psk_status apply_rotary_embedding(
     p.err = err_count;
     return cuda_status(psk::launch_rotary(p, reinterpret_cast<cudaStream_t>(stream)),
                        "apply_rotary_embedding launch");
+}
+
+int64_t accumulate_attention_weights_workspace_bytes(void) {
+    return psk::attn_weights_workspace_bytes();
+}
+
+psk_status accumulate_attention_weights(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, int64_t num_tokens,
+    int32_t num_heads, const float* lse, int64_t lse_stride_t, const uint8_t* cache,
+    int64_t num_pages, int64_t page_stride, int32_t block_size, int32_t head_dim,
+    int32_t rope_dim, const int32_t* query_start_loc, const int32_t* seq_lens,
+    const int32_t* replay_start, int32_t num_reqs, const int32_t* block_table,
+    int64_t bt_stride, int32_t bt_width, const int32_t* base_offsets, int32_t window,
+    const uint8_t* is_valid_token, float softmax_scale, const float* sink,
+    const float* weights, int64_t w_stride, int32_t width, float decay, float* out,
+    int64_t out_stride, void* workspace, int64_t workspace_bytes, psk_stream_t stream) {
+    CHECK(num_tokens >= 0 && num_tokens <= (int64_t)INT32_MAX, "num_tokens must be in [0, INT32_MAX]");
+    CHECK(num_reqs >= 0 && num_reqs <= (1 << 27), "num_reqs must be in [0, 2^27]");
+    CHECK(num_heads >= 1 && num_heads <= (1 << 20), "num_heads must be in [1, 2^20]");
+    CHECK(window >= 0, "window must be >= 0");
+    CHECK(attn_head_dim_ok(head_dim), "head_dim must be one of 128, 256, 512 (got %d)", head_dim);
+    CHECK(rope_dim >= 0 && rope_dim < head_dim && rope_dim % 64 == 0,
+          "rope_dim must be a multiple of 64 in [0, head_dim) (got %d)", rope_dim);
+    psk_status st = check_cache(cache, num_pages, page_stride, block_size,
+                                fp8_record_bytes(head_dim, rope_dim, 1));
+    if (st != PSK_OK) return st;
+    CHECK(bt_width >= 0 && bt_stride >= bt_width, "need 0 <= bt_width <= bt_stride");
+    CHECK(std::isnormal(softmax_scale) && softmax_scale > 0.0f && softmax_scale <= 1e38f,
+          "softmax_scale must be a normal number in (0, 1e38]");
+    CHECK(std::isfinite(decay) && decay >= 0.0f, "decay must be finite and >= 0");
+    CHECK(width >= 0 && width <= (1 << 30), "width must be in [0, 2^30]");
+    CHECK(out_stride >= width && (decay == 0.0f || w_stride >= width), "strides of weights and out must be >= width");
+    CHECK(q_stride_t % 8 == 0 && q_stride_h % 8 == 0 && (num_tokens <= 1 || q_stride_t >= head_dim) &&
+              (num_heads <= 1 || q_stride_h >= head_dim),
+          "query strides must be multiples of 8 elements and at least head_dim");
+    CHECK(q_stride_t <= (1ll << 38) && q_stride_h <= (1ll << 38), "query strides must be at most 2^38");
+    CHECK(num_tokens <= 1 || lse_stride_t >= num_heads, "lse_stride_t must be >= num_heads");
+    if (num_reqs == 0 || width == 0) return ok();
+    CHECK(seq_lens && query_start_loc, "query_start_loc and seq_lens must be non-null");
+    CHECK(num_tokens == 0 || (q != nullptr && lse != nullptr), "q and lse must be non-null");
+    CHECK(aligned(q, 16), "q must be 16-byte aligned");
+    CHECK(out != nullptr && (decay == 0.0f || weights != nullptr), "weights and out must be non-null");
+    CHECK(out != weights || out_stride == w_stride, "weights in place need equal strides");
+    CHECK(bt_width == 0 || block_table, "block_table must be non-null");
+    CHECK(aligned(query_start_loc, 4) && aligned(seq_lens, 4) && aligned(replay_start, 4) &&
+              aligned(block_table, 4) && aligned(base_offsets, 4) && aligned(lse, 4) && aligned(sink, 4) &&
+              aligned(weights, 4) && aligned(out, 4),
+          "int32 and binary32 arrays must be 4-byte aligned");
+    const int64_t need = psk::attn_weights_workspace_bytes();
+    CHECK(workspace_bytes >= need, "workspace must hold %lld bytes (got %lld)", (long long)need,
+          (long long)workspace_bytes);
+    CHECK(need == 0 || (workspace != nullptr && aligned(workspace, 16)),
+          "workspace must be non-null and 16-byte aligned");
+    psk::WeightParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride_t = q_stride_t;
+    p.q_stride_h = q_stride_h;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.head_dim = head_dim;
+    p.rope_dim = rope_dim;
+    p.lse = lse;
+    p.lse_stride_t = lse_stride_t;
+    p.sink = sink;
+    p.scale = softmax_scale;
+    p.cache = {cache, num_pages, page_stride, block_size, -1};
+    p.qsl = query_start_loc;
+    p.seq_lens = seq_lens;
+    p.replay = replay_start;
+    p.valid = is_valid_token;
+    p.num_reqs = num_reqs;
+    p.bt = block_table;
+    p.bt_stride = bt_stride;
+    p.bt_width = bt_width;
+    p.base_off = base_offsets;
+    p.window = window;
+    p.weights = weights;
+    p.w_stride = w_stride;
+    p.width = width;
+    p.decay = decay;
+    p.out = out;
+    p.out_stride = out_stride;
+    p.workspace = workspace;
+    return cuda_status(psk::launch_attn_weights(p, reinterpret_cast<cudaStream_t>(stream)),
+                       "accumulate_attention_weights launch");
 }
 
 psk_status select_cache_evictions(

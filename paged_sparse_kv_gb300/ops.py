@@ -983,6 +983,63 @@ def _move_list(t: torch.Tensor, R: int, count: int, index: int):
     return t.data_ptr(), (st[0] if t.shape[0] > 1 else 2 * t.shape[1])
 
 
+def accumulate_attention_weights_workspace_bytes(device: torch.device) -> int:
+    """Bytes of ``workspace`` an accumulate_attention_weights call needs on ``device``."""
+    index = torch.device(device).index
+    return _on(_current_device() if index is None else index,
+               _abi.lib().accumulate_attention_weights_workspace_bytes)
+
+
+def accumulate_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor,
+                                 query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                                 block_table: torch.Tensor, block_size: int, weights: torch.Tensor, *,
+                                 decay: float = 1.0, window_size: int = 0,
+                                 replay_start: Optional[torch.Tensor] = None,
+                                 base_offsets: Optional[torch.Tensor] = None,
+                                 is_valid_token: Optional[torch.Tensor] = None,
+                                 softmax_scale: Optional[float] = None,
+                                 sink: Optional[torch.Tensor] = None, rope_dim: int = 64,
+                                 out: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``decay * weights`` [R, W] plus the attention each cached row got from the new tokens ``q``
+    [T, H, D], summed over tokens and heads: a chunk as chunk_mla_attention took it, with the
+    ``lse`` [T, H] it returned.  In place unless ``out`` is given; entries past ``seq_lens`` are left
+    as they were.  ``workspace`` (uint8) is scratch; two calls that can run at once need one each."""
+    i, i32 = _index(q), torch.int32
+    qa = _heads(q, "q", i)
+    T, H, D = q.shape
+    if lse.dtype != torch.float32:
+        raise TypeError(f"lse must be {torch.float32}, got {lse.dtype}")
+    _same(lse, i, "lse")
+    if lse.shape != (T, H) or (H > 1 and lse.stride(1) != 1):
+        raise ValueError(f"lse must be [{T}, {H}] with unit inner stride")
+    R = seq_lens.numel()
+    width = weights.shape[1] if weights.dim() == 2 else 0
+    w = _per_row(weights, torch.float32, "weights", R, width, i)
+    if out is None:
+        out, o = weights, w
+    else:
+        o = _per_row(out, torch.float32, "out", R, width, i)
+    if R > 1 and o[1] < width:
+        raise ValueError("rows of weights must not overlap")
+    valid = None if is_valid_token is None else is_valid_token.to(torch.uint8)
+    if workspace is None:
+        need = _on(i, _abi.lib().accumulate_attention_weights_workspace_bytes)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    else:
+        _vec(workspace, torch.uint8, "workspace", 0, i)
+    _call(q.device, "accumulate_attention_weights", *qa, T, H, lse.data_ptr(),
+          lse.stride(0) if T > 1 else H, *_cache_of(cache, "cache", i), block_size, D, rope_dim,
+          _vec(query_start_loc, i32, "query_start_loc", R + 1, i), _vec(seq_lens, i32, "seq_lens", R, i),
+          _vec(replay_start, i32, "replay_start", R, i), R, *_table(block_table, "block_table", R, i),
+          _vec(base_offsets, i32, "base_offsets", R, i), window_size,
+          _vec(valid, torch.uint8, "is_valid_token", T, i),
+          D ** -0.5 if softmax_scale is None else softmax_scale,
+          _vec(sink, torch.float32, "sink", H, i), *w, width, decay, *o, workspace.data_ptr(),
+          workspace.numel())
+    return out
+
+
 def select_cache_evictions(weights: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor, *,
                            row_positions: Optional[torch.Tensor] = None, num_first: int = 0,
                            num_recent: int = 0, weights_out: Optional[torch.Tensor] = None,
