@@ -142,7 +142,7 @@ int32_t psk_abi_version(void) { return 7; }
 
 psk_status psk_device_wait_timeouts(uint32_t* count) {
     CHECK(count != nullptr, "count must be non-null");
-    uint32_t gather = 0, index = 0, compress = 0, attention = 0;
+    uint32_t gather = 0, index = 0, compress = 0, attention = 0, weights = 0;
     psk_status st = cuda_status(psk::read_wait_timeouts(&gather), "reading the wait-timeout counter");
     if (st != PSK_OK) return st;
     st = cuda_status(psk::read_index_wait_timeouts(&index), "reading the wait-timeout counter");
@@ -152,7 +152,9 @@ psk_status psk_device_wait_timeouts(uint32_t* count) {
     st = cuda_status(psk::read_attention_wait_timeouts(&attention),
                      "reading the wait-timeout counter");
     if (st != PSK_OK) return st;
-    *count = gather + index + compress + attention;
+    st = cuda_status(psk::read_attn_weights_wait_timeouts(&weights), "reading the wait-timeout counter");
+    if (st != PSK_OK) return st;
+    *count = gather + index + compress + attention + weights;
     return PSK_OK;
 }
 

@@ -1,11 +1,37 @@
 // attn_weights.cu -- attention weights summed per cached row over new tokens and
-// heads: what eviction ranks rows by.
+// heads, on the 5th-generation tensor cores: what eviction ranks rows by.
 //
 //   sum_j = sum over tokens t that see row j, heads h, of exp(s_thj - L_th)
 //   s = scale q.k_j,  L = log(exp(lse) + exp(sink)),  out_j = decay w_j + sum_j
 //
-// A CTA takes 32 rows of a request, dequantised to binary32 in shared memory.  A warp
-// takes a (token, head) at a time: 16 dims of the query a lane, one row after another.
+// Layout.  A tile is 128 rows of a request, a column a (token, head) of it, and a
+// column tile up to 128 columns: whole tokens of few heads, or a part of many heads.
+//   S^T [128 rows x N columns] = K [128 x D] Q^T         (D/16 MMAs of M = 128)
+// The logarithms are known, so a score becomes a weight by one fused multiply-add and
+// one exp2, and a row's sum is a sum along a lane of tensor memory: nothing passes
+// between threads until the tile ends.  K is dequantised into tensor memory (D/2 columns,
+// two bf16 each) and is the MMAs' A operand from there, so that shared memory carries
+// only the queries (a K tile there would be read again by every column tile: 128 bytes
+// a cycle, all there is), and stays while the column tiles of its rows go by.  Scores
+// have the other columns, two column tiles.
+//
+// Work.  Tiles and their column tiles stand in one sequence over all requests (a tile
+// counts kTileCost column tiles besides, its dequantisation), which is cut into one
+// equal range per CTA whatever the lengths are.  A tile cut between CTAs has its partial
+// sums written to the workspace; a second kernel adds them up in order.
+//
+// Roles.  Eight worker warps bring records into shared memory by asynchronous copies
+// (32 rows and half the dims each, a copy of the next tile issued as soon as a block of 64
+// dims is read), dequantise them and write them to tensor memory; one warp fetches
+// queries by TMA into a ring of 64-dim stages and prepares the columns' logarithms and
+// bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
+// the column tile does not change (a decode batch: one column tile per request).
+// Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
+#include <cuda.h>
+
+#include <atomic>
+#include <cmath>
+
 #include "attn_weights.h"
 #include "psk_common.cuh"
 #include "umma.cuh"
@@ -13,108 +39,906 @@
 namespace psk {
 namespace {
 
-constexpr int kRows = 32, kThreads = 256;
+constexpr int kTile = 128;          // rows of a tile
+constexpr int kCols = 128;          // columns of a column tile, at most
+constexpr int kWorkers = 8, kSummers = 8;
+constexpr int kQueryWarp = kWorkers + kSummers, kMmaWarp = kQueryWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * kWarp;
+constexpr int kTileCost = 1;
+constexpr int kMostStages = 24;
+constexpr int kColSlots = 3;
+constexpr int kStaged = 64;         // requests whose metadata stand in shared memory
+constexpr int kMostBlocks = 8;      // 64-dim blocks of a row (head_dim 512)
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-__global__ void __launch_bounds__(kThreads) attn_weights_kernel(const WeightParams p, const int32_t tiles) {
-    extern __shared__ float s_k[];  // [row][dim]
-    __shared__ float s_sum[kThreads / kWarp][kRows];
-    __shared__ const uint8_t* s_data[kRows];
-    __shared__ const uint8_t* s_scale[kRows];
-    pdl_wait();
+__device__ unsigned int g_weights_wait_timeouts = 0;
+
+// A request's share of the call.
+struct Request {
+    int32_t tokens;   // new tokens, and the first of them
+    int32_t token0;
+    int32_t row0;     // row of its first new token (negative: before row 0)
+    int32_t end;      // rows that have a weight
+    int32_t replay;
+    int32_t base;
+};
+
+// The parts of a cut tile: which tile a CTA starts in the middle of, and what it does there.
+enum { kNone = 0, kMiddle = 1, kEnds = 2, kEmptyRange = 3 };
+struct Record {
+    int32_t kind, request, tile, pad;
+};
+
+struct Columns {
+    float log[kCols];                 // log2 units
+    int32_t lo[kCols], hi[kCols];     // rows a column sees
+    int32_t all_lo, all_hi;           // rows that every column in use sees
+    int32_t all_used, pad;
+};
+
+struct LaunchShape {
+    int32_t heads, tokens;        // of a column tile
+    int32_t head_groups;
+    int32_t stages, stage_bytes;
+    int32_t keep_queries;         // the ring holds a whole column tile
+    int32_t stride[2];            // bytes of a staged row, by half
+    float scale_log2;
+    float* parts;                 // [CTA][2][kTile]
+    Record* records;              // [CTA]
+};
+
+struct Shared {
+    Columns columns[kColSlots];
+    Request request[kStaged];
+    float half_sum[4][2][kWarp];  // second half of a quad's columns: sum and compensation
+    uint64_t k_full[kMostBlocks], k_free[kMostBlocks];
+    uint64_t q_full[kMostStages], q_free[kMostStages];
+    uint64_t col_full[kColSlots], col_free[kColSlots];
+    uint64_t s_full[2], s_free[2];
+    uint64_t half_full[4], half_free[4];
+    uint64_t drain;
+    int64_t scan[kThreads / kWarp];
+    int64_t first_at;             // where the CTA's range starts: prefix of that request
+    int32_t first_request;
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_poll_bounded(bar, parity, kWaitLimitNs);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// ---- the sequence of tiles --------------------------------------------------------------
+
+__device__ __forceinline__ Request load_request(const WeightParams& p, int32_t r) {
+    Request x;
+    const int32_t rows = p.seq_lens[r];
+    const int64_t q0 = p.qsl[r], q1 = p.qsl[r + 1];
+    const int64_t first = q0 > 0 ? q0 : 0, last = q1 < p.num_tokens ? q1 : p.num_tokens;
+    x.tokens = last > first ? (int32_t)(last - first) : 0;
+    x.token0 = (int32_t)first;
+    const int64_t row0 = (int64_t)rows - (q1 - q0) + (first - q0);
+    x.row0 = (int32_t)(row0 < -(1 << 30) ? -(1 << 30) : row0 > INT32_MAX ? INT32_MAX : row0);
+    x.end = rows < 0 ? 0 : rows < p.width ? rows : p.width;
+    x.replay = p.replay ? p.replay[r] : 0;
+    x.base = p.base_off ? p.base_off[r] : 0;
+    return x;
+}
+
+// Column tiles of tile `k`: those of the token groups [first, first + groups).
+__device__ __forceinline__ void column_tiles(const WeightParams& p, const LaunchShape& ls, const Request& q, int32_t k,
+                                             int32_t& first, int32_t& groups) {
+    // tokens i with row0 + i >= 128 k, and (window) row0 + i - window + 1 <= 128 k + 127
+    const int64_t a = (int64_t)k * kTile - q.row0;
+    const int32_t i0 = a <= 0 ? 0 : a >= q.tokens ? q.tokens : (int32_t)a;
+    int32_t i1 = q.tokens;
+    if (p.window > 0) {
+        const int64_t b = (int64_t)k * kTile + kTile - 1 + p.window - q.row0;
+        if (b < i1) i1 = b > i0 ? (int32_t)b : i0;
+    }
+    first = i0 / ls.tokens;
+    groups = i1 > i0 ? (i1 + ls.tokens - 1) / ls.tokens - first : 0;
+}
+
+// The first `count` tiles of a request that cost the same, and that cost.  The others are
+// few (rows of the new tokens, and of their windows) and are counted one by one.
+__device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchShape& ls, const Request& q, int32_t tiles,
+                                           int32_t& count, int64_t& cost) {
+    int64_t n;
+    if (p.window > 0) {  // tiles before every window
+        n = ((int64_t)q.row0 - p.window + 1) / kTile;
+        cost = kTileCost;
+    } else {             // tiles all tokens see
+        const int64_t x = (int64_t)q.row0 + min(ls.tokens, q.tokens) - 1;
+        n = x < 0 ? 0 : x / kTile + 1;
+        cost = kTileCost + (int64_t)((q.tokens + ls.tokens - 1) / ls.tokens) * ls.head_groups;
+    }
+    count = n < 0 || q.tokens == 0 ? 0 : n > tiles ? tiles : (int32_t)n;
+    if (q.tokens == 0) {
+        count = tiles;
+        cost = kTileCost;
+    }
+}
+
+__device__ __forceinline__ int32_t tiles_of(const Request& q) { return q.end / kTile + (q.end % kTile != 0); }
+
+__device__ int64_t request_cost(const WeightParams& p, const LaunchShape& ls, const Request& q) {
+    const int32_t tiles = tiles_of(q);
+    int32_t even;
+    int64_t cost;
+    even_tiles(p, ls, q, tiles, even, cost);
+    int64_t sum = cost * even;
+    for (int32_t k = even; k < tiles; ++k) {
+        int32_t first, groups;
+        column_tiles(p, ls, q, k, first, groups);
+        sum += kTileCost + (int64_t)groups * ls.head_groups;
+    }
+    return sum;
+}
+
+// A CTA's walk over its range of the sequence.  All roles walk it by themselves.
+struct Walk {
+    int64_t from, to;        // the range
+    int64_t at;              // place of the current tile in the sequence
+    int32_t r, k;            // request and tile; r == num_reqs: past the end
+    int32_t first, total;    // its token groups start at `first`; its column tiles
+    int32_t c0, c1;          // those of them in the range
+    Request q;
+
+    __device__ __forceinline__ bool done() const { return r < 0; }
+    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == total; }
+
+    __device__ __forceinline__ void request(const WeightParams& p, const Shared& sh) {
+        const int32_t i = r - sh.first_request;
+        q = i < kStaged ? sh.request[i] : load_request(p, r);
+    }
+    // Moves on to the next tile of which something lies in the range, the current one included.
+    __device__ void settle(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
+        for (;;) {
+            while (k >= tiles_of(q)) {
+                if (++r >= p.num_reqs || at >= to) {
+                    r = -1;
+                    return;
+                }
+                k = 0;
+                request(p, sh);
+            }
+            if (at >= to) {
+                r = -1;
+                return;
+            }
+            int32_t groups;
+            column_tiles(p, ls, q, k, first, groups);
+            total = groups * ls.head_groups;
+            const int64_t a = from - at - kTileCost, b = to - at - kTileCost;
+            c0 = a > 0 ? (int32_t)(a < total ? a : total) : 0;
+            c1 = b > 0 ? (int32_t)(b < total ? b : total) : 0;
+            if (total == 0 ? at >= from : c0 < c1) return;
+            at += kTileCost + total;
+            ++k;
+        }
+    }
+    __device__ void start(const WeightParams& p, const LaunchShape& ls, const Shared& sh, int64_t from_, int64_t to_) {
+        from = from_;
+        to = to_;
+        r = sh.first_request;
+        at = sh.first_at;
+        k = 0;
+        if (from >= to) {
+            r = -1;
+            return;
+        }
+        request(p, sh);
+        int32_t even;
+        int64_t cost;
+        even_tiles(p, ls, q, tiles_of(q), even, cost);
+        const int64_t skip = (from - at) / cost;
+        k = skip < even ? (int32_t)skip : even;
+        at += cost * k;
+        settle(p, ls, sh);
+    }
+    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
+        at += kTileCost + total;
+        ++k;
+        settle(p, ls, sh);
+    }
+    // The same for roles that have nothing to do on tiles without columns.
+    __device__ __forceinline__ void start_columns(const WeightParams& p, const LaunchShape& ls, const Shared& sh, int64_t a, int64_t b) {
+        start(p, ls, sh, a, b);
+        while (!done() && total == 0) next(p, ls, sh);
+    }
+    __device__ __forceinline__ void next_columns(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
+        do next(p, ls, sh);
+        while (!done() && total == 0);
+    }
+    // Whether the first column tile of `x` is the last one of this tile.
+    __device__ __forceinline__ bool same_columns(const LaunchShape& ls, const Walk& x) const {
+        return ls.keep_queries && !x.done() && x.r == r && x.total > 0 &&
+               first * ls.head_groups + c1 - 1 == x.first * ls.head_groups + x.c0;
+    }
+};
+
+// Sum over the CTA, the same in all threads.
+__device__ int64_t block_sum(Shared& sh, int64_t v) {
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();
+    if (lane == 0) sh.scan[warp] = v;
+    __syncthreads();
+    int64_t sum = 0;
+    for (int i = 0; i < kThreads / kWarp; ++i) sum += sh.scan[i];
+    return sum;
+}
+
+// The CTA's range of the sequence, and the request it starts in (sh.first_*).
+__device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t& from, int64_t& to) {
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
-    const int32_t r = (int32_t)(blockIdx.x / tiles), first = (int32_t)(blockIdx.x % tiles) * kRows;
-    const int32_t rows = p.seq_lens[r], end = min(rows, p.width);
-    if (first >= end) return;
-    const int D = p.head_dim, nope = D - p.rope_dim;
-    if (tid < kRows) {
-        const int32_t j = first + tid;
-        s_data[tid] = nullptr;
-        if (j < end) {
-            int32_t off;
-            const int64_t logical =
-                (int64_t)div_block32(j, p.cache.block_size, p.cache.shift, off) - (p.base_off ? p.base_off[r] : 0);
-            if (logical >= 0 && logical < p.bt_width) {
-                const int32_t page = p.bt[(int64_t)r * p.bt_stride + logical];
-                if (page >= 0 && page < p.cache.num_pages) {
-                    const uint8_t* pg = p.cache.base + (int64_t)page * p.cache.page_stride;
-                    s_data[tid] = pg + (int64_t)off * (D + p.rope_dim);
-                    s_scale[tid] = pg + (int64_t)p.cache.block_size * (D + p.rope_dim) + (int64_t)off * (D / 64);
+    int64_t mine = 0, cost = 0;
+    for (int32_t r = tid; r < p.num_reqs; r += kThreads) {
+        cost = request_cost(p, ls, load_request(p, r));
+        mine += cost;
+    }
+    const int64_t all = block_sum(sh, mine);
+    const int64_t b = blockIdx.x, n = gridDim.x;
+    from = all / n * b + all % n * b / n;
+    to = all / n * (b + 1) + all % n * (b + 1) / n;
+    if (tid == 0) {
+        sh.first_request = 0;
+        sh.first_at = 0;
+    }
+    int64_t before = 0;
+    for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
+        const int32_t r = r0 + tid;
+        if (p.num_reqs > kThreads) cost = r < p.num_reqs ? request_cost(p, ls, load_request(p, r)) : 0;
+        int64_t sum = cost;
+        for (int o = 1; o < kWarp; o *= 2) {
+            const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        __syncthreads();
+        if (lane == kWarp - 1) sh.scan[warp] = sum;
+        __syncthreads();
+        int64_t at = before + sum - cost;
+        for (int i = 0; i < warp; ++i) at += sh.scan[i];
+        if (at <= from && from < at + cost) {
+            sh.first_request = r;
+            sh.first_at = at;
+        }
+        for (int i = 0; i < kThreads / kWarp; ++i) before += sh.scan[i];
+        if (before > from) break;
+    }
+    __syncthreads();
+    const int32_t r = sh.first_request + tid;
+    if (tid < kStaged && r < p.num_reqs) sh.request[tid] = load_request(p, r);
+    __syncthreads();
+}
+
+// Address of row j's data and scales; null without a page.
+__device__ __forceinline__ int32_t page_of(const WeightParams& p, int32_t r, const Request& q, int32_t j) {
+    if (j >= q.end) return -1;
+    int32_t off;
+    const int64_t logical = (int64_t)div_block32(j, p.cache.block_size, p.cache.shift, off) - q.base;
+    if (logical < 0 || logical >= p.bt_width) return -1;
+    const int32_t page = p.bt[(int64_t)r * p.bt_stride + logical];
+    return page < p.cache.num_pages ? page : -1;
+}
+
+// ---- workers: records to tensor memory -----------------------------------------------------
+
+// 16-byte copy global -> shared; `bytes` 0 writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 16 E4M3 bytes of UE8M0 scale byte b as eight bf16 pairs, by the rule of the gather.
+__device__ __forceinline__ void dequant16(uint4 raw, uint32_t b, uint32_t* w) {
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    const uint64_t s2 = splat_f32x2(ue8m0_scale(b));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[2 * i] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] & 0xFFFFu), s2);
+        w[2 * i + 1] = scale_f16x2_to_bf16x2(cvt_e4m3x2_to_f16x2(in[i] >> 16), s2);
+    }
+}
+
+// Lane i's row of tensor memory: 32 columns from `addr` on.
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+          "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+          "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+          "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
+        : "memory");
+}
+
+// A worker warp has the rows 32 * quad ... of each tile and the dims of one half.  Records
+// stand in its part of shared memory with a row stride that is an odd number of 16 bytes,
+// so that lanes reading 16 bytes of their own rows hit different banks.
+template <int D>
+__device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t staging, uint32_t tmem_k,
+                     int64_t from, int64_t to) {
+    constexpr int kBlocks = D / 128;  // 64-dim blocks of a half
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, quad = warp % 4, half = warp / 4;
+    const int nope = D - p.rope_dim;
+    const int d0 = half * (D / 2);
+    const auto byte_of = [&](int d) { return d <= nope ? d : nope + 2 * (d - nope); };
+    const int stride = ls.stride[half], byte0 = byte_of(d0);
+    const uint32_t mine = staging + (half ? 4 * kWarp * ls.stride[0] : 0) + quad * kWarp * stride;
+    const int64_t token_stride = D + p.rope_dim;
+
+    // A tile's row of this lane: page, address
+    const auto lookup = [&](const Walk& x) {
+        return x.done() ? -1 : page_of(p, x.r, x.q, x.k * kTile + quad * kWarp + lane);
+    };
+    const auto row_of = [&](const Walk& x, int32_t page, const uint8_t*& scales) -> const uint8_t* {
+        scales = nullptr;
+        if (page < 0) return nullptr;
+        int32_t off;
+        div_block32(x.k * kTile + quad * kWarp + lane, p.cache.block_size, p.cache.shift, off);
+        const uint8_t* pg = p.cache.base + (int64_t)page * p.cache.page_stride;
+        scales = pg + p.cache.block_size * token_stride + (int64_t)off * (D / 64);
+        return pg + off * token_stride;
+    };
+    const auto load_scales = [&](const uint8_t* at) {
+        uint2 s = make_uint2(0, 0);
+        if (at == nullptr) return s;
+        if (D == 512) {
+            s = ld_nc_v2(at);
+        } else if (D == 256) {
+            s.x = ld_nc_u32(at);
+        } else {
+            s.x = ld_nc_u8(at) | (ld_nc_u8(at + 1) << 8);
+        }
+        return s;
+    };
+    // Copies block b of the rows whose addresses the lanes hold.
+    const auto fetch = [&](const uint8_t* row, int b) {
+        const int d = d0 + b * 64, at = byte_of(d);
+        const uint64_t addr = reinterpret_cast<uint64_t>(row);
+        const int per = d >= nope ? 8 : 4;  // 16-byte pieces of a row
+        const int first = lane / per, piece = lane % per;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int src = first + i * (kWarp / per);
+            if (i >= per) break;
+            const uint64_t a = __shfl_sync(0xFFFFFFFFu, addr, src);
+            const uint8_t* from_row = a ? reinterpret_cast<const uint8_t*>(a) + at + piece * 16 : p.cache.base;
+            copy16(mine + src * stride + (at - byte0) + piece * 16, from_row, a ? 16 : 0);
+        }
+    };
+
+    Walk cur, nxt;
+    cur.start_columns(p, ls, sh, from, to);
+    if (cur.done()) return true;
+    const uint8_t *scales_at, *row = row_of(cur, lookup(cur), scales_at);
+    for (int b = 0; b < kBlocks; ++b) {
+        fetch(row, b);
+        copies_commit();
+    }
+    uint2 scales = load_scales(scales_at);
+    nxt = cur;
+    nxt.next_columns(p, ls, sh);
+    int32_t next_page = lookup(nxt);
+    for (uint32_t step = 0;; ++step) {
+        const bool more = !nxt.done();
+        const uint8_t *next_scales_at, *next_row = row_of(nxt, next_page, next_scales_at);
+        const uint2 next_scales = load_scales(next_scales_at);
+        if (more) {
+            nxt.next_columns(p, ls, sh);
+            next_page = lookup(nxt);
+        }
+        for (int b = 0; b < kBlocks; ++b) {
+            const int d = d0 + b * 64, block = d / 64;
+            const uint32_t at = mine + lane * stride + byte_of(d) - byte0;
+            copies_wait<kBlocks - 1>();
+            __syncwarp();
+            uint32_t w[32];
+            if (d < nope) {
+                const uint32_t sc = ((block < 4 ? scales.x : scales.y) >> (8 * (block & 3))) & 0xFFu;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dequant16(lds_v4(at + i * 16), sc, w + 8 * i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = lds_v4(at + i * 16);
+                    w[4 * i] = v.x;
+                    w[4 * i + 1] = v.y;
+                    w[4 * i + 2] = v.z;
+                    w[4 * i + 3] = v.w;
                 }
             }
+            __syncwarp();  // the block has been read: the next tile's copy may land there
+            if (more) fetch(next_row, b);
+            copies_commit();
+            if (step > 0 && !wait_all(&sh.k_free[block], (step - 1) & 1)) return false;
+            tmem_fence_after();
+            tmem_st32(tmem_k + ((uint32_t)(quad * kWarp) << 16) + block * 32, w);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.k_full[block]);
+        }
+        if (!more) return true;
+        scales = next_scales;
+    }
+}
+
+// The order in which blocks are multiplied: the halves' blocks in turn, as they come.
+template <int D>
+__device__ __forceinline__ constexpr int block_at(int i) { return (i & 1) * (D / 128) + i / 2; }
+
+// ---- queries and columns ---------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map, int32_t d, int32_t h, int32_t t, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
+}
+
+template <int D>
+__device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring,
+                              int64_t from, int64_t to) {
+    constexpr int kBlocks = D / 64;
+    const int lane = threadIdx.x % kWarp;
+    const uint32_t bytes = (uint32_t)(ls.heads * ls.tokens * 128);
+    uint32_t stage = 0, round = 0, seq = 0;
+    bool ok = true;
+    Walk cur, nxt;
+    cur.start_columns(p, ls, sh, from, to);
+    bool loaded = false;
+    while (ok && !cur.done()) {
+        nxt = cur;
+        nxt.next_columns(p, ls, sh);
+        for (int32_t c = cur.c0 + (loaded ? 1 : 0); ok && c < cur.c1; ++c) {
+            const int32_t i0 = (cur.first + c / ls.head_groups) * ls.tokens, h0 = c % ls.head_groups * ls.heads;
+            // the columns' logarithms, in flight while the stages are fetched
+            float lse[kCols / kWarp], sink[kCols / kWarp];
+            bool used[kCols / kWarp];
+            int32_t pos[kCols / kWarp];
+#pragma unroll
+            for (int k = 0; k < kCols / kWarp; ++k) {
+                const int col = lane + k * kWarp, i = i0 + col / ls.heads, h = h0 + col % ls.heads;
+                used[k] = col < ls.heads * ls.tokens && i < cur.q.tokens && h < p.num_heads;
+                pos[k] = (int32_t)((uint32_t)cur.q.row0 + (uint32_t)i);
+                lse[k] = 0.0f;
+                sink[k] = -INFINITY;
+                if (used[k]) {
+                    const int64_t t = (int64_t)cur.q.token0 + i;
+                    lse[k] = p.lse[t * p.lse_stride_t + h];
+                    if (p.sink) sink[k] = p.sink[h];
+                    if (p.valid) used[k] = p.valid[t] != 0;
+                }
+            }
+            for (int b = 0; b < kBlocks; ++b) {
+                if (round > 0 && !wait_all(&sh.q_free[stage], (round - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
+                    tma_queries(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h0, cur.q.token0 + i0,
+                                &sh.q_full[stage]);
+                }
+                __syncwarp();
+                if (++stage == (uint32_t)ls.stages) {
+                    stage = 0;
+                    ++round;
+                }
+            }
+            const uint32_t slot = seq % kColSlots;
+            if (!ok || (seq >= kColSlots && !wait_all(&sh.col_free[slot], (seq / kColSlots - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            Columns& co = sh.columns[slot];
+            int32_t all_lo = INT32_MIN, all_hi = INT32_MAX;
+            bool all_used = true;
+            const int32_t n = min(ls.tokens, cur.q.tokens - i0) * ls.heads, padded = (n + 15) / 16 * 16;
+#pragma unroll
+            for (int k = 0; k < kCols / kWarp; ++k) {
+                const int col = lane + k * kWarp;
+                const float a = lse[k] * kLog2e, b = sink[k] * kLog2e, top = fmaxf(a, b);
+                float x = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
+                if (x == -INFINITY) used[k] = false;  // a token that saw nothing
+                int32_t lo = p.window > 0 && pos[k] >= p.window ? pos[k] - p.window + 1 : 0, hi = pos[k];
+                lo = max(lo, cur.q.replay);
+                if (!used[k]) {
+                    x = 0.0f;
+                    lo = INT32_MAX;
+                    hi = -1;
+                } else {
+                    all_lo = max(all_lo, lo);
+                    all_hi = min(all_hi, hi);
+                }
+                all_used &= used[k] || col >= padded;
+                co.log[col] = x;
+                co.lo[col] = lo;
+                co.hi[col] = hi;
+            }
+            all_lo = __reduce_max_sync(0xFFFFFFFFu, all_lo);
+            all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
+            all_used = __all_sync(0xFFFFFFFFu, all_used);
+            if (lane == 0) {
+                co.all_lo = all_lo;
+                co.all_hi = all_hi;
+                co.all_used = all_used;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.col_full[slot]);
+            ++seq;
+        }
+        loaded = cur.same_columns(ls, nxt);
+        cur = nxt;
+    }
+    if (!ok) {  // copies in flight land before the CTA ends
+        for (int i = 0; i < ls.stages; ++i) {
+            stage = (stage + ls.stages - 1) % ls.stages;
+            if (stage == (uint32_t)ls.stages - 1) {
+                if (round == 0) break;
+                --round;
+            }
+            mbar_poll_bounded(&sh.q_full[stage], round & 1, kWaitLimitNs / 8);
         }
     }
-    __syncthreads();
-    for (int i = tid; i < kRows * D; i += kThreads) {
-        const int row = i / D, d = i % D;
-        float x = 0.0f;
-        if (s_data[row] != nullptr) {
-            if (d < nope) {
-                const float v = f16_lo(cvt_e4m3x2_to_f16x2(s_data[row][d]));
-                x = bf16_lo(pack_bf16x2(v * ue8m0_scale(s_scale[row][d / 64]), 0.0f));
+    return ok;
+}
+
+// ---- the MMA warp ------------------------------------------------------------------------------
+
+// A from tensor memory; issued by the lane whose `lead` is 1.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate,
+                                             uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+
+// Columns of a column tile, padded to what an MMA takes.
+__device__ __forceinline__ int32_t width_of(const LaunchShape& ls, const Walk& x, int32_t c) {
+    const int32_t i0 = (x.first + c / ls.head_groups) * ls.tokens;
+    return (min(ls.tokens, x.q.tokens - i0) * ls.heads + 15) / 16 * 16;
+}
+
+template <int D>
+__device__ bool issue(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s,
+                      int64_t from, int64_t to) {
+    constexpr int kBlocks = D / 64;
+    const uint32_t lead = elect_one();
+    const uint64_t q_desc = umma_desc(ring, 16, 1024, kSwizzle128);
+    uint32_t stage = 0, round = 0, step = 0, tile = 0;
+    Walk cur, nxt;
+    cur.start_columns(p, ls, sh, from, to);
+    for (; !cur.done(); ++tile) {
+        nxt = cur;
+        nxt.next_columns(p, ls, sh);
+        for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
+            const bool last = c == cur.c1 - 1, keep = last && cur.same_columns(ls, nxt);
+            const uint32_t idesc = umma_idesc(kTile, width_of(ls, cur, c), false), d = tmem_s + (step & 1) * kCols;
+            if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
+            uint32_t st = stage, rd = round;
+            for (int b = 0; b < kBlocks; ++b) {
+                const int block = block_at<D>(b);
+                if (c == cur.c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
+                if (!wait_all(&sh.q_full[st], rd & 1)) return false;
+                tmem_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_bf16_ts(d, tmem_k + block * 32 + k * 8, q_desc + ((st * ls.stage_bytes + k * 32) >> 4), idesc,
+                                 b > 0 || k > 0, lead);
+                if (last) umma_commit(&sh.k_free[block], lead);
+                if (!keep) umma_commit(&sh.q_free[st], lead);
+                if (++st == (uint32_t)ls.stages) {
+                    st = 0;
+                    ++rd;
+                }
+            }
+            umma_commit(&sh.s_full[step & 1], lead);
+            if (!keep) {
+                stage = st;
+                round = rd;
+            }
+        }
+        cur = nxt;
+    }
+    return true;
+}
+
+// ---- scores to sums --------------------------------------------------------------------------
+
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;  // compensated by Kahan's rule
+    __device__ __forceinline__ void add(float x) {
+        const float y = x - lo, z = hi + y;
+        lo = isfinite(z) ? (z - hi) - y : 0.0f;
+        hi = z;
+    }
+};
+
+__device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s, int64_t from, int64_t to) {
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kWorkers, quad = warp % 4, half = warp / 4;
+    const uint32_t lane_base = tmem_s + ((uint32_t)(quad * kWarp) << 16);
+    uint32_t step = 0, seq = 0, tile = 0;
+    bool loaded = false;
+    Walk cur, nxt;
+    cur.start(p, ls, sh, from, to);
+    if (half == 0 && quad == 0 && lane == 0) {
+        Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
+        if (!cur.done() && cur.c0 > 0) rec = {cur.c1 == cur.total ? kEnds : kMiddle, cur.r, cur.k, 0};
+        ls.records[blockIdx.x] = rec;
+    }
+    while (!cur.done()) {
+        nxt = cur;
+        nxt.next(p, ls, sh);
+        const int32_t j = cur.k * kTile + quad * kWarp + lane;
+        const bool ok = page_of(p, cur.r, cur.q, j) >= 0, in = j < cur.q.end;
+        const int64_t out_at = (int64_t)cur.r * p.out_stride + j;
+        float old = 0.0f;
+        if (p.decay != 0.0f && in && half == 0 && cur.whole()) old = p.weights[(int64_t)cur.r * p.w_stride + j];
+        Sum sum;
+        for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
+            const int32_t n = width_of(ls, cur, c);
+            if (loaded) {
+                --seq;  // the columns are those of the step before
+                loaded = false;
+            } else if (!wait_all(&sh.col_full[seq % kColSlots], (seq / kColSlots) & 1)) {
+                return false;
+            }
+            const Columns& co = sh.columns[seq % kColSlots];
+            if (!wait_all(&sh.s_full[step & 1], (step / 2) & 1)) return false;
+            tmem_fence_after();
+            const bool all = __all_sync(0xFFFFFFFFu, ok && co.all_used && j >= co.all_lo && j <= co.all_hi);
+            const uint32_t s_at = lane_base + (step & 1) * kCols;
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int32_t n0 = half * 16; n0 < n; n0 += 32) {
+                float s[16];
+                tmem_ld<16>(s_at + n0, s);
+                if (all) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
+                        part[0] += ex2_approx(fmaf(s[k], ls.scale_log2, -x.x));
+                        part[1] += ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y));
+                        part[2] += ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z));
+                        part[3] += ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const bool sees = ok && j >= co.lo[n0 + k] && j <= co.hi[n0 + k];
+                        part[k % 4] += sees ? ex2_approx(fmaf(s[k], ls.scale_log2, -co.log[n0 + k])) : 0.0f;
+                    }
+                }
+            }
+            sum.add((part[0] + part[1]) + (part[2] + part[3]));
+            tmem_fence_before();
+            __syncwarp();
+            const bool keep = c == cur.c1 - 1 && cur.same_columns(ls, nxt);
+            if (lane == 0) {
+                mbar_arrive(&sh.s_free[step & 1]);
+                if (!keep) mbar_arrive(&sh.col_free[seq % kColSlots]);
+            }
+            loaded = keep;
+            ++seq;
+        }
+        // the halves of the columns
+        if (half == 1) {
+            if (tile > 0 && !wait_all(&sh.half_free[quad], (tile - 1) & 1)) return false;
+            sh.half_sum[quad][0][lane] = sum.hi;
+            sh.half_sum[quad][1][lane] = sum.lo;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.half_full[quad]);
+        } else {
+            if (!wait_all(&sh.half_full[quad], tile & 1)) return false;
+            sum.add(sh.half_sum[quad][0][lane]);
+            sum.add(-sh.half_sum[quad][1][lane]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.half_free[quad]);
+            const float total = sum.hi - sum.lo;
+            if (cur.whole()) {
+                if (in) p.out[out_at] = p.decay == 0.0f ? total : fmaf(p.decay, old, total);
             } else {
-                x = bf16_lo(*reinterpret_cast<const uint16_t*>(s_data[row] + nope + 2 * (d - nope)));
+                ls.parts[((int64_t)blockIdx.x * 2 + (cur.c0 > 0 ? 0 : 1)) * kTile + quad * kWarp + lane] = total;
             }
         }
-        s_k[i] = x;
+        cur = nxt;
+        ++tile;
     }
-    __syncthreads();
-    const bool there = s_data[lane] != nullptr;
-    const int64_t q0 = p.qsl[r], q1 = min((int64_t)p.qsl[r + 1], p.num_tokens);
-    const int64_t at0 = (int64_t)rows - ((int64_t)p.qsl[r + 1] - q0);  // row of token q0
-    const float c = p.scale * kLog2e;
-    const int32_t j = first + lane;
-    float sum = 0.0f, low = 0.0f;  // Kahan's compensation in `low`
-    for (int64_t t = max(q0, (int64_t)0) ; t < q1; ++t) {
-        const int64_t pos = at0 + (t - q0);
-        if (pos < first || (p.valid && !p.valid[t])) continue;
-        int64_t from = p.window > 0 ? pos - p.window + 1 : 0;
-        if (p.replay) from = max(from, (int64_t)p.replay[r]);
-        if (from >= first + kRows) continue;
-        const bool sees = there && j <= pos && j >= from;
-        for (int h = warp; h < p.num_heads; h += kThreads / kWarp) {
-            const float a = p.lse[t * p.lse_stride_t + h] * kLog2e, b = p.sink ? p.sink[h] * kLog2e : -INFINITY;
-            const float top = fmaxf(a, b);
-            if (top == -INFINITY && !(a != a) && !(b != b)) continue;  // a token that saw nothing
-            const float L = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
-            const uint16_t* q = p.q + t * p.q_stride_t + h * p.q_stride_h;
-            float mine = 0.0f;
-            for (int row = 0; row < kRows; ++row) {
-                float s = 0.0f;
-                for (int d = lane; d < D; d += kWarp) s = fmaf(bf16_lo(q[d]), s_k[row * D + d], s);
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-                if (row == lane) mine = s;
-            }
-            const float w = sees ? exp2f(fmaf(mine, c, -L)) : 0.0f;
-            const float y = w - low, z = sum + y;
-            low = isfinite(z) ? (z - sum) - y : 0.0f;
-            sum = z;
+    return true;
+}
+
+constexpr size_t kAlign = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ LaunchShape ls,
+                        const __grid_constant__ CUtensorMap map) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_raw + ((kAlign - (smem_u32(smem_raw) & (kAlign - 1))) & (kAlign - 1));
+    uint8_t* staging = ring + ls.stages * ls.stage_bytes;
+    Shared& sh = *reinterpret_cast<Shared*>(staging + 4 * kWarp * (ls.stride[0] + ls.stride[1]));
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMostBlocks; ++i) {
+            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_free[i], 1);
         }
+        for (int i = 0; i < kMostStages; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_free[i], 1);
+        }
+        for (int i = 0; i < kColSlots; ++i) {
+            mbar_init(&sh.col_full[i], 1);
+            mbar_init(&sh.col_free[i], kSummers);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_free[i], kSummers);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.half_full[i], 1);
+            mbar_init(&sh.half_free[i], 1);
+        }
+        mbar_init(&sh.drain, 1);
+        mbar_fence_init();
     }
-    s_sum[warp][lane] = sum;
+    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
+    tmem_fence_before();
     __syncthreads();
-    if (warp == 0 && j < end) {
-        float all = 0.0f;
-        for (int i = 0; i < kThreads / kWarp; ++i) all += s_sum[i][lane];
-        float* out = p.out + (int64_t)r * p.out_stride + j;
-        *out = p.decay == 0.0f ? all : fmaf(p.decay, p.weights[(int64_t)r * p.w_stride + j], all);
-    }
+    tmem_fence_after();
+    const uint32_t tmem_s = sh.tmem, tmem_k = tmem_s + 2 * kCols;
+    pdl_wait();
     pdl_launch_dependents();
+    int64_t from, to;
+    find_range(p, ls, sh, from, to);
+
+    bool ok = true;
+    if (warp < kWorkers) {
+        ok = work<D>(p, ls, sh, smem_u32(staging), tmem_k, from, to);
+        if (!ok) copies_wait<0>();
+    } else if (warp < kQueryWarp) {
+        ok = summarise(p, ls, sh, tmem_s, from, to);
+    } else if (warp == kQueryWarp) {
+        ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring), from, to);
+    } else {
+        ok = issue<D>(p, ls, sh, smem_u32(ring), tmem_k, tmem_s, from, to);
+        if (!ok) {  // wait for the MMAs in flight before the operands go
+            umma_commit(&sh.drain, elect_one());
+            mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);
+        }
+    }
+    if (!ok && lane == 0) atomicAdd(&g_weights_wait_timeouts, 1u);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(sh.tmem, 512);
+}
+
+// ---- joining the parts of cut tiles ------------------------------------------------------------
+//
+// The CTA a tile ends in adds up its parts, from its own back to the one it starts in.
+__global__ void __launch_bounds__(kTile) join_kernel(const WeightParams p, const LaunchShape ls) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const Record rec = ls.records[blockIdx.x];
+    if (rec.kind != kEnds) return;
+    const int i = threadIdx.x;
+    double sum = ls.parts[(int64_t)blockIdx.x * 2 * kTile + i];
+    for (int c = (int)blockIdx.x - 1; c >= 0; --c) {
+        const int kind = ls.records[c].kind;
+        if (kind == kEmptyRange) continue;
+        if (kind == kMiddle) {
+            sum += ls.parts[(int64_t)c * 2 * kTile + i];
+        } else {
+            sum += ls.parts[((int64_t)c * 2 + 1) * kTile + i];
+            break;
+        }
+    }
+    const int32_t rows = p.seq_lens[rec.request], j = rec.tile * kTile + i;
+    if (j >= rows || j >= p.width) return;
+    float* out = p.out + (int64_t)rec.request * p.out_stride + j;
+    const float total = (float)sum;
+    *out = p.decay == 0.0f ? total : fmaf(p.decay, p.weights[(int64_t)rec.request * p.w_stride + j], total);
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cached.store(fn, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(fn);
+}
+
+// Queries as [token][head][dim], read in boxes of 64 dims of a column tile.
+bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_heads, (cuuint64_t)p.num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.q_stride_h * 2, (cuuint64_t)p.q_stride_t * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)ls.heads, (cuuint32_t)ls.tokens}, ones[3] = {1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMostShared = 227 * 1024;
+
+LaunchShape make_shape(const WeightParams& p) {
+    LaunchShape ls{};
+    ls.head_groups = (p.num_heads + kCols - 1) / kCols;
+    ls.heads = (p.num_heads + ls.head_groups - 1) / ls.head_groups;
+    ls.tokens = ls.head_groups > 1 ? 1 : kCols / ls.heads;
+    if (ls.tokens > p.num_tokens) ls.tokens = p.num_tokens > 0 ? (int32_t)p.num_tokens : 1;
+    const int nope = p.head_dim - p.rope_dim, mid = p.head_dim / 2;
+    const int first = mid <= nope ? mid : nope + 2 * (mid - nope);
+    ls.stride[0] = first + 16;
+    ls.stride[1] = p.head_dim + p.rope_dim - first + 16;
+    ls.stage_bytes = (ls.heads * ls.tokens + 15) / 16 * 16 * 128;
+    const int room = kMostShared - (int)kAlign - 4 * kWarp * (ls.stride[0] + ls.stride[1]) - (int)sizeof(Shared);
+    ls.stages = room / ls.stage_bytes;
+    if (ls.stages > kMostStages) ls.stages = kMostStages;
+    const int most = 3 * p.head_dim / 64;
+    if (ls.stages > most) ls.stages = most;
+    ls.keep_queries = ls.stages >= p.head_dim / 64;
+    return ls;
+}
+
+template <int D>
+cudaError_t launch(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, int ctas, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel<D>, kMostShared, done);
+    if (e != cudaSuccess) return e;
+    const size_t smem = kAlign + (size_t)ls.stages * ls.stage_bytes + 4 * kWarp * (size_t)(ls.stride[0] + ls.stride[1]) + sizeof(Shared);
+    return launch_pdl(attn_weights_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, ls, map);
 }
 
 }  // namespace
 
-int64_t attn_weights_workspace_bytes() { return 0; }
+int64_t attn_weights_workspace_bytes() {
+    return (int64_t)sm_count() * (2 * kTile * (int64_t)sizeof(float) + (int64_t)sizeof(Record));
+}
 
 cudaError_t launch_attn_weights(WeightParams p, cudaStream_t stream) {
     p.cache.shift = log2_if_pow2(p.cache.block_size);
-    const int32_t tiles = p.width / kRows + (p.width % kRows != 0);
-    const int smem = kRows * p.head_dim * (int)sizeof(float);
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel, kRows * 512 * (int)sizeof(float), done);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(attn_weights_kernel, dim3((unsigned)((int64_t)tiles * p.num_reqs)), dim3(kThreads), smem, stream, p,
-                      tiles);
+    LaunchShape ls = make_shape(p);
+    const int ctas = sm_count();
+    ls.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
+    ls.parts = static_cast<float*>(p.workspace);
+    ls.records = reinterpret_cast<Record*>(ls.parts + (int64_t)ctas * 2 * kTile);
+    CUtensorMap map{};
+    if (p.num_tokens > 0 && !query_map(p, ls, map)) return cudaErrorNotSupported;
+    cudaError_t e = p.head_dim == 512   ? launch<512>(p, ls, map, ctas, stream)
+                    : p.head_dim == 256 ? launch<256>(p, ls, map, ctas, stream)
+                                        : launch<128>(p, ls, map, ctas, stream);
+    // a request of one column tile at most is never cut
+    const int64_t most = (p.num_tokens + ls.tokens - 1) / ls.tokens * ls.head_groups;
+    if (e != cudaSuccess || most <= 1) return e;
+    return launch_pdl(join_kernel, dim3((unsigned)ctas), dim3(kTile), 0, stream, p, ls);
+}
+
+cudaError_t read_attn_weights_wait_timeouts(uint32_t* count) {
+    return cudaMemcpyFromSymbol(count, g_weights_wait_timeouts, sizeof(uint32_t));
 }
 
 }  // namespace psk

@@ -40,4 +40,7 @@ int64_t attn_weights_workspace_bytes();
 
 cudaError_t launch_attn_weights(WeightParams p, cudaStream_t stream);
 
+// Count of expired bounded waits in the kernel.
+cudaError_t read_attn_weights_wait_timeouts(uint32_t* count);
+
 }  // namespace psk
