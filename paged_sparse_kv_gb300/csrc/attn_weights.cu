@@ -23,7 +23,7 @@
 // Roles.  Eight worker warps bring records into shared memory by asynchronous copies
 // (32 rows and half the dims each, a copy of the next tile issued as soon as a block of 64
 // dims is read), dequantise them and write them to tensor memory; one warp fetches
-// queries by TMA into a ring of 64-dim stages and prepares the columns' logarithms and
+// queries by TMA into a ring of 64-dim stages, four prepare the columns' logarithms and
 // bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
 // the column tile does not change (a decode batch: one column tile per request).
 // Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
@@ -41,8 +41,8 @@ namespace {
 
 constexpr int kTile = 128;          // rows of a tile
 constexpr int kCols = 128;          // columns of a column tile, at most
-constexpr int kWorkers = 8, kSummers = 8;
-constexpr int kQueryWarp = kWorkers + kSummers, kMmaWarp = kQueryWarp + 1;
+constexpr int kWorkers = 8, kSummers = 8, kColumnWarps = kCols / kWarp;
+constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps, kMmaWarp = kQueryWarp + 1;
 constexpr int kThreads = (kMmaWarp + 1) * kWarp;
 constexpr int kTileCost = 1;
 constexpr int kMostStages = 24;
@@ -73,8 +73,8 @@ struct Record {
 struct Columns {
     float log[kCols];                 // log2 units
     int32_t lo[kCols], hi[kCols];     // rows a column sees
-    int32_t all_lo, all_hi;           // rows that every column in use sees
-    int32_t all_used, pad;
+    // by column warp: rows that every column in use sees, and whether all are in use
+    int4 all_lo, all_hi, all_used;
 };
 
 struct LaunchShape {
@@ -184,33 +184,41 @@ struct Walk {
     int32_t r, k;            // request and tile; r == num_reqs: past the end
     int32_t first, total;    // its token groups start at `first`; its column tiles
     int32_t c0, c1;          // those of them in the range
+    int32_t tiles, even;     // of the request; how many in front are alike
     Request q;
 
     __device__ __forceinline__ bool done() const { return r < 0; }
     __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == total; }
 
-    __device__ __forceinline__ void request(const WeightParams& p, const Shared& sh) {
+    // Takes up request r; returns what one of its even tiles costs.
+    __device__ __forceinline__ int64_t request(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
         const int32_t i = r - sh.first_request;
         q = i < kStaged ? sh.request[i] : load_request(p, r);
+        tiles = tiles_of(q);
+        int64_t cost;
+        even_tiles(p, ls, q, tiles, even, cost);
+        return cost;
     }
     // Moves on to the next tile of which something lies in the range, the current one included.
     __device__ void settle(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
         for (;;) {
-            while (k >= tiles_of(q)) {
+            while (k >= tiles) {
                 if (++r >= p.num_reqs || at >= to) {
                     r = -1;
                     return;
                 }
                 k = 0;
-                request(p, sh);
+                request(p, ls, sh);
             }
             if (at >= to) {
                 r = -1;
                 return;
             }
-            int32_t groups;
-            column_tiles(p, ls, q, k, first, groups);
-            total = groups * ls.head_groups;
+            if (k >= even || k == 0) {  // before `even` tiles are alike
+                int32_t groups;
+                column_tiles(p, ls, q, k, first, groups);
+                total = groups * ls.head_groups;
+            }
             const int64_t a = from - at - kTileCost, b = to - at - kTileCost;
             c0 = a > 0 ? (int32_t)(a < total ? a : total) : 0;
             c1 = b > 0 ? (int32_t)(b < total ? b : total) : 0;
@@ -229,13 +237,14 @@ struct Walk {
             r = -1;
             return;
         }
-        request(p, sh);
-        int32_t even;
-        int64_t cost;
-        even_tiles(p, ls, q, tiles_of(q), even, cost);
-        const int64_t skip = (from - at) / cost;
+        const int64_t cost = request(p, ls, sh), skip = (from - at) / cost;
         k = skip < even ? (int32_t)skip : even;
         at += cost * k;
+        if (k > 0 && k < even) {
+            int32_t groups;
+            column_tiles(p, ls, q, k, first, groups);
+            total = groups * ls.head_groups;
+        }
         settle(p, ls, sh);
     }
     __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
@@ -481,97 +490,40 @@ __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
+// One thread fetches the queries.
 template <int D>
 __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring,
                               int64_t from, int64_t to) {
     constexpr int kBlocks = D / 64;
-    const int lane = threadIdx.x % kWarp;
     const uint32_t bytes = (uint32_t)(ls.heads * ls.tokens * 128);
-    uint32_t stage = 0, round = 0, seq = 0;
-    bool ok = true;
+    uint32_t stage = 0, round = 0;
+    bool ok = true, loaded = false;
     Walk cur, nxt;
     cur.start_columns(p, ls, sh, from, to);
-    bool loaded = false;
     while (ok && !cur.done()) {
         nxt = cur;
         nxt.next_columns(p, ls, sh);
-        for (int32_t c = cur.c0 + (loaded ? 1 : 0); ok && c < cur.c1; ++c) {
-            const int32_t i0 = (cur.first + c / ls.head_groups) * ls.tokens, h0 = c % ls.head_groups * ls.heads;
-            // the columns' logarithms, in flight while the stages are fetched
-            float lse[kCols / kWarp], sink[kCols / kWarp];
-            bool used[kCols / kWarp];
-            int32_t pos[kCols / kWarp];
-#pragma unroll
-            for (int k = 0; k < kCols / kWarp; ++k) {
-                const int col = lane + k * kWarp, i = i0 + col / ls.heads, h = h0 + col % ls.heads;
-                used[k] = col < ls.heads * ls.tokens && i < cur.q.tokens && h < p.num_heads;
-                pos[k] = (int32_t)((uint32_t)cur.q.row0 + (uint32_t)i);
-                lse[k] = 0.0f;
-                sink[k] = -INFINITY;
-                if (used[k]) {
-                    const int64_t t = (int64_t)cur.q.token0 + i;
-                    lse[k] = p.lse[t * p.lse_stride_t + h];
-                    if (p.sink) sink[k] = p.sink[h];
-                    if (p.valid) used[k] = p.valid[t] != 0;
-                }
-            }
+        int32_t c = cur.c0 + (loaded ? 1 : 0);
+        int32_t group = c / ls.head_groups, part = c - group * ls.head_groups;
+        for (; ok && c < cur.c1; ++c) {
+            const int32_t t = cur.q.token0 + (cur.first + group) * ls.tokens, h = part * ls.heads;
+#pragma unroll 1
             for (int b = 0; b < kBlocks; ++b) {
-                if (round > 0 && !wait_all(&sh.q_free[stage], (round - 1) & 1)) {
+                if (round > 0 && !mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
-                    tma_queries(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h0, cur.q.token0 + i0,
-                                &sh.q_full[stage]);
-                }
-                __syncwarp();
+                mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
+                tma_queries(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h, t, &sh.q_full[stage]);
                 if (++stage == (uint32_t)ls.stages) {
                     stage = 0;
                     ++round;
                 }
             }
-            const uint32_t slot = seq % kColSlots;
-            if (!ok || (seq >= kColSlots && !wait_all(&sh.col_free[slot], (seq / kColSlots - 1) & 1))) {
-                ok = false;
-                break;
+            if (++part == ls.head_groups) {
+                part = 0;
+                ++group;
             }
-            Columns& co = sh.columns[slot];
-            int32_t all_lo = INT32_MIN, all_hi = INT32_MAX;
-            bool all_used = true;
-            const int32_t n = min(ls.tokens, cur.q.tokens - i0) * ls.heads, padded = (n + 15) / 16 * 16;
-#pragma unroll
-            for (int k = 0; k < kCols / kWarp; ++k) {
-                const int col = lane + k * kWarp;
-                const float a = lse[k] * kLog2e, b = sink[k] * kLog2e, top = fmaxf(a, b);
-                float x = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
-                if (x == -INFINITY) used[k] = false;  // a token that saw nothing
-                int32_t lo = p.window > 0 && pos[k] >= p.window ? pos[k] - p.window + 1 : 0, hi = pos[k];
-                lo = max(lo, cur.q.replay);
-                if (!used[k]) {
-                    x = 0.0f;
-                    lo = INT32_MAX;
-                    hi = -1;
-                } else {
-                    all_lo = max(all_lo, lo);
-                    all_hi = min(all_hi, hi);
-                }
-                all_used &= used[k] || col >= padded;
-                co.log[col] = x;
-                co.lo[col] = lo;
-                co.hi[col] = hi;
-            }
-            all_lo = __reduce_max_sync(0xFFFFFFFFu, all_lo);
-            all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
-            all_used = __all_sync(0xFFFFFFFFu, all_used);
-            if (lane == 0) {
-                co.all_lo = all_lo;
-                co.all_hi = all_hi;
-                co.all_used = all_used;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.col_full[slot]);
-            ++seq;
         }
         loaded = cur.same_columns(ls, nxt);
         cur = nxt;
@@ -589,6 +541,90 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
     return ok;
 }
 
+// The logarithms and bounds of the columns, one a thread.  The next column tile's lse is in
+// flight while this one's is worked on.
+__device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t from, int64_t to) {
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kColumnWarp, col = warp * kWarp + lane;
+    const int32_t token = col / ls.heads, head = col - token * ls.heads;
+    struct Column {
+        bool used;
+        int32_t pos, rows_from;
+        float lse, sink;
+    };
+    Walk cur{};
+    int32_t c = 0, group = 0, part = 0;
+    bool end = false;
+    // the column of the next column tile, which the walk stands at
+    const auto load = [&]() {
+        Column x{false, 0, cur.q.replay, 0.0f, -INFINITY};
+        const int32_t i = (cur.first + group) * ls.tokens + token, h = part * ls.heads + head;
+        if (token < ls.tokens && i < cur.q.tokens && h < p.num_heads) {
+            const int64_t t = (int64_t)cur.q.token0 + i;
+            x.used = p.valid == nullptr || p.valid[t] != 0;
+            x.pos = cur.q.row0 + i;
+            x.lse = p.lse[t * p.lse_stride_t + h];
+            if (p.sink) x.sink = p.sink[h];
+        }
+        return x;
+    };
+    const auto at = [&]() {
+        group = c / ls.head_groups;
+        part = c - group * ls.head_groups;
+    };
+    const auto advance = [&]() {
+        if (++c < cur.c1) {
+            if (++part == ls.head_groups) {
+                part = 0;
+                ++group;
+            }
+            return;
+        }
+        for (;;) {
+            const int32_t r = cur.r, last = cur.first * ls.head_groups + cur.c1 - 1;
+            cur.next_columns(p, ls, sh);
+            if (cur.done()) {
+                end = true;
+                return;
+            }
+            // as Walk::same_columns
+            c = cur.c0 + (ls.keep_queries && cur.r == r && last == cur.first * ls.head_groups + cur.c0 ? 1 : 0);
+            if (c < cur.c1) break;
+        }
+        at();
+    };
+    cur.start_columns(p, ls, sh, from, to);
+    if (cur.done()) return true;
+    c = cur.c0;
+    at();
+    Column next = load();
+    for (uint32_t seq = 0; !end; ++seq) {
+        const Column x = next;
+        advance();
+        if (!end) next = load();
+        const float a = x.lse * kLog2e, b = x.sink * kLog2e, top = fmaxf(a, b);
+        const float log = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
+        const bool used = x.used && log != -INFINITY;  // else a token that saw nothing
+        const int32_t lo = max(p.window > 0 && x.pos >= p.window ? x.pos - p.window + 1 : 0, x.rows_from);
+        const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, used ? lo : INT32_MIN);
+        const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, used ? x.pos : INT32_MAX);
+        const uint32_t in_use = __ballot_sync(0xFFFFFFFFu, used);
+        const uint32_t slot = seq % kColSlots;
+        if (seq >= kColSlots && !wait_all(&sh.col_free[slot], (seq / kColSlots - 1) & 1)) return false;
+        Columns& co = sh.columns[slot];
+        co.log[col] = used ? log : 0.0f;
+        co.lo[col] = used ? lo : INT32_MAX;
+        co.hi[col] = used ? x.pos : -1;
+        if (lane == 0) {
+            (&co.all_lo.x)[warp] = all_lo;
+            (&co.all_hi.x)[warp] = all_hi;
+            (&co.all_used.x)[warp] = (int32_t)in_use;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.col_full[slot]);
+    }
+    return true;
+}
+
 // ---- the MMA warp ------------------------------------------------------------------------------
 
 // A from tensor memory; issued by the lane whose `lead` is 1.
@@ -603,9 +639,9 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
-// Columns of a column tile, padded to what an MMA takes.
-__device__ __forceinline__ int32_t width_of(const LaunchShape& ls, const Walk& x, int32_t c) {
-    const int32_t i0 = (x.first + c / ls.head_groups) * ls.tokens;
+// Columns of a column tile of a token group, padded to what an MMA takes.
+__device__ __forceinline__ int32_t width_of(const LaunchShape& ls, const Walk& x, int32_t group) {
+    const int32_t i0 = (x.first + group) * ls.tokens;
     return (min(ls.tokens, x.q.tokens - i0) * ls.heads + 15) / 16 * 16;
 }
 
@@ -621,11 +657,13 @@ __device__ bool issue(const WeightParams& p, const LaunchShape& ls, Shared& sh, 
     for (; !cur.done(); ++tile) {
         nxt = cur;
         nxt.next_columns(p, ls, sh);
+        int32_t group = cur.c0 / ls.head_groups, part = cur.c0 - group * ls.head_groups;
         for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
             const bool last = c == cur.c1 - 1, keep = last && cur.same_columns(ls, nxt);
-            const uint32_t idesc = umma_idesc(kTile, width_of(ls, cur, c), false), d = tmem_s + (step & 1) * kCols;
+            const uint32_t idesc = umma_idesc(kTile, width_of(ls, cur, group), false), d = tmem_s + (step & 1) * kCols;
             if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
             uint32_t st = stage, rd = round;
+#pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int block = block_at<D>(b);
                 if (c == cur.c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
@@ -646,6 +684,10 @@ __device__ bool issue(const WeightParams& p, const LaunchShape& ls, Shared& sh, 
             if (!keep) {
                 stage = st;
                 round = rd;
+            }
+            if (++part == ls.head_groups) {
+                part = 0;
+                ++group;
             }
         }
         cur = nxt;
@@ -685,8 +727,9 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
         float old = 0.0f;
         if (p.decay != 0.0f && in && half == 0 && cur.whole()) old = p.weights[(int64_t)cur.r * p.w_stride + j];
         Sum sum;
+        int32_t group = cur.c0 / ls.head_groups, part_of = cur.c0 - group * ls.head_groups;
         for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
-            const int32_t n = width_of(ls, cur, c);
+            const int32_t n = width_of(ls, cur, group);
             if (loaded) {
                 --seq;  // the columns are those of the step before
                 loaded = false;
@@ -694,28 +737,46 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
                 return false;
             }
             const Columns& co = sh.columns[seq % kColSlots];
+            const int4 lo4 = co.all_lo, hi4 = co.all_hi, used4 = co.all_used;
+            const bool rows = __all_sync(0xFFFFFFFFu, ok && j >= max(max(lo4.x, lo4.y), max(lo4.z, lo4.w)) &&
+                                                          j <= min(min(hi4.x, hi4.y), min(hi4.z, hi4.w)));
             if (!wait_all(&sh.s_full[step & 1], (step / 2) & 1)) return false;
             tmem_fence_after();
-            const bool all = __all_sync(0xFFFFFFFFu, ok && co.all_used && j >= co.all_lo && j <= co.all_hi);
             const uint32_t s_at = lane_base + (step & 1) * kCols;
             float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int32_t n0 = half * 16; n0 < n; n0 += 32) {
-                float s[16];
-                tmem_ld<16>(s_at + n0, s);
-                if (all) {
+#pragma unroll 1
+            for (int32_t n0 = half * 32; n0 < n; n0 += 64) {
+                float s[32];
+                tmem_ld<32>(s_at + n0, s);
+                const int32_t used = n0 == 0 ? used4.x : n0 == 32 ? used4.y : n0 == 64 ? used4.z : used4.w;
+                if (rows && used == -1) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
+                    for (int k = 0; k < 32; k += 4) {
                         const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
                         part[0] += ex2_approx(fmaf(s[k], ls.scale_log2, -x.x));
                         part[1] += ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y));
                         part[2] += ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z));
                         part[3] += ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w));
                     }
+                } else if (rows) {  // the columns in use see all rows
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
+                        part[0] += used >> k & 1 ? ex2_approx(fmaf(s[k], ls.scale_log2, -x.x)) : 0.0f;
+                        part[1] += used >> (k + 1) & 1 ? ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y)) : 0.0f;
+                        part[2] += used >> (k + 2) & 1 ? ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z)) : 0.0f;
+                        part[3] += used >> (k + 3) & 1 ? ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w)) : 0.0f;
+                    }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const bool sees = ok && j >= co.lo[n0 + k] && j <= co.hi[n0 + k];
-                        part[k % 4] += sees ? ex2_approx(fmaf(s[k], ls.scale_log2, -co.log[n0 + k])) : 0.0f;
+                    for (int k = 0; k < 32; k += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
+                        const int4 lo = *reinterpret_cast<const int4*>(&co.lo[n0 + k]);
+                        const int4 hi = *reinterpret_cast<const int4*>(&co.hi[n0 + k]);
+                        part[0] += ok && j >= lo.x && j <= hi.x ? ex2_approx(fmaf(s[k], ls.scale_log2, -x.x)) : 0.0f;
+                        part[1] += ok && j >= lo.y && j <= hi.y ? ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y)) : 0.0f;
+                        part[2] += ok && j >= lo.z && j <= hi.z ? ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z)) : 0.0f;
+                        part[3] += ok && j >= lo.w && j <= hi.w ? ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w)) : 0.0f;
                     }
                 }
             }
@@ -729,6 +790,10 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             }
             loaded = keep;
             ++seq;
+            if (++part_of == ls.head_groups) {
+                part_of = 0;
+                ++group;
+            }
         }
         // the halves of the columns
         if (half == 1) {
@@ -778,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.q_free[i], 1);
         }
         for (int i = 0; i < kColSlots; ++i) {
-            mbar_init(&sh.col_full[i], 1);
+            mbar_init(&sh.col_full[i], kColumnWarps);
             mbar_init(&sh.col_free[i], kSummers);
         }
         for (int i = 0; i < 2; ++i) {
@@ -806,10 +871,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kWorkers) {
         ok = work<D>(p, ls, sh, smem_u32(staging), tmem_k, from, to);
         if (!ok) copies_wait<0>();
-    } else if (warp < kQueryWarp) {
+    } else if (warp < kColumnWarp) {
         ok = summarise(p, ls, sh, tmem_s, from, to);
+    } else if (warp < kQueryWarp) {
+        ok = columns(p, ls, sh, from, to);
     } else if (warp == kQueryWarp) {
-        ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring), from, to);
+        if (lane == 0) ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring), from, to);
+        __syncwarp();
     } else {
         ok = issue<D>(p, ls, sh, smem_u32(ring), tmem_k, tmem_s, from, to);
         if (!ok) {  // wait for the MMAs in flight before the operands go
