@@ -20,11 +20,12 @@
 // equal range per CTA whatever the lengths are.  A tile cut between CTAs has its partial
 // sums written to the workspace; a second kernel adds them up in order.
 //
-// Roles.  Eight worker warps bring records into shared memory by asynchronous copies
-// (32 rows and half the dims each, a copy of the next tile issued as soon as a block of 64
-// dims is read), dequantise them and write them to tensor memory; one warp fetches
-// queries by TMA into a ring of 64-dim stages, four prepare the columns' logarithms and
-// bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
+// Roles.  One warp plans: it walks the CTA's range and puts tiles with the addresses of
+// their rows into a ring.  Eight worker warps bring records into shared memory by
+// asynchronous copies (32 rows and half the dims each, a copy of the next tile issued as
+// soon as a block of 64 dims is read), dequantise them and write them to tensor memory; one
+// thread fetches queries by TMA into a ring of 64-dim stages, four warps prepare the
+// columns' logarithms and bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
 // the column tile does not change (a decode batch: one column tile per request).
 // Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
 #include <cuda.h>
@@ -42,17 +43,21 @@ namespace {
 constexpr int kTile = 128;          // rows of a tile
 constexpr int kCols = 128;          // columns of a column tile, at most
 constexpr int kWorkers = 8, kSummers = 8, kColumnWarps = kCols / kWarp;
-constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps, kMmaWarp = kQueryWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * kWarp;
+constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps, kMmaWarp = kQueryWarp + 1,
+              kPlanWarp = kMmaWarp + 1;
+constexpr int kThreads = (kPlanWarp + 1) * kWarp;
 constexpr int kTileCost = 1;
 constexpr int kMostStages = 24;
 constexpr int kColSlots = 3;
-constexpr int kStaged = 64;         // requests whose metadata stand in shared memory
+constexpr int kTiles = 4;           // tiles the planning warp may be ahead
 constexpr int kMostBlocks = 8;      // 64-dim blocks of a row (head_dim 512)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ unsigned int g_weights_wait_timeouts = 0;
+
+// What a row without a page is read from: the longest record, all zero.
+__device__ const uint4 g_zero_row[(512 + 448) / 16] = {};
 
 // A request's share of the call.
 struct Request {
@@ -77,6 +82,23 @@ struct Columns {
     int4 all_lo, all_hi, all_used;
 };
 
+struct Row {
+    const uint8_t* data;
+    const uint8_t* scales;
+};
+
+// A step of the walk with columns, as the planning warp publishes it.
+struct Tile {
+    int32_t request, tile;    // request -1: the end
+    int32_t first_row, end;   // its first row; the rows of the request that have a weight
+    int32_t first, total;     // first token group and number of its column tiles
+    int32_t c0, c1;           // those of them that are this CTA's
+    int32_t tokens, token0, row0, replay;  // of the request
+    int32_t kept, keeps;      // the first column tile is at hand; the last one is the next tile's first
+    uint32_t there[4];        // rows with a page
+    Row row[kTile];
+};
+
 struct LaunchShape {
     int32_t heads, tokens;        // of a column tile
     int32_t head_groups;
@@ -89,9 +111,10 @@ struct LaunchShape {
 };
 
 struct Shared {
+    Tile tile[kTiles];
     Columns columns[kColSlots];
-    Request request[kStaged];
     float half_sum[4][2][kWarp];  // second half of a quad's columns: sum and compensation
+    uint64_t tile_full[kTiles], tile_free[kTiles];
     uint64_t k_full[kMostBlocks], k_free[kMostBlocks];
     uint64_t q_full[kMostStages], q_free[kMostStages];
     uint64_t col_full[kColSlots], col_free[kColSlots];
@@ -163,21 +186,38 @@ __device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchSh
 
 __device__ __forceinline__ int32_t tiles_of(const Request& q) { return q.end / kTile + (q.end % kTile != 0); }
 
-__device__ int64_t request_cost(const WeightParams& p, const LaunchShape& ls, const Request& q) {
-    const int32_t tiles = tiles_of(q);
-    int32_t even;
-    int64_t cost;
-    even_tiles(p, ls, q, tiles, even, cost);
-    int64_t sum = cost * even;
-    for (int32_t k = even; k < tiles; ++k) {
-        int32_t first, groups;
-        column_tiles(p, ls, q, k, first, groups);
-        sum += kTileCost + (int64_t)groups * ls.head_groups;
+// Cost of the tiles of 32 requests, one a lane.
+__device__ __forceinline__ int64_t request_costs(const WeightParams& p, const LaunchShape& ls, int32_t r) {
+    const int lane = threadIdx.x % kWarp;
+    Request q{};
+    int32_t tiles = 0, even = 0;
+    int64_t cost = 0, sum = 0;
+    if (r < p.num_reqs) {
+        q = load_request(p, r);
+        tiles = tiles_of(q);
+        even_tiles(p, ls, q, tiles, even, cost);
+        sum = cost * even;
+    }
+    // the uneven tiles of a request, 32 at a time
+    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, even < tiles); rest; rest &= rest - 1) {
+        const int src = __ffs(rest) - 1;
+        Request x{};
+        x.tokens = __shfl_sync(0xFFFFFFFFu, q.tokens, src);
+        x.row0 = __shfl_sync(0xFFFFFFFFu, q.row0, src);
+        const int32_t a = __shfl_sync(0xFFFFFFFFu, even, src), b = __shfl_sync(0xFFFFFFFFu, tiles, src);
+        int64_t mine = 0;
+        for (int32_t k = a + lane; k < b; k += kWarp) {
+            int32_t first, groups;
+            column_tiles(p, ls, x, k, first, groups);
+            mine += kTileCost + (int64_t)groups * ls.head_groups;
+        }
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+        if (lane == src) sum += mine;
     }
     return sum;
 }
 
-// A CTA's walk over its range of the sequence.  All roles walk it by themselves.
+// A CTA's walk over its range of the sequence.
 struct Walk {
     int64_t from, to;        // the range
     int64_t at;              // place of the current tile in the sequence
@@ -188,19 +228,17 @@ struct Walk {
     Request q;
 
     __device__ __forceinline__ bool done() const { return r < 0; }
-    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == total; }
 
     // Takes up request r; returns what one of its even tiles costs.
-    __device__ __forceinline__ int64_t request(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
-        const int32_t i = r - sh.first_request;
-        q = i < kStaged ? sh.request[i] : load_request(p, r);
+    __device__ __forceinline__ int64_t request(const WeightParams& p, const LaunchShape& ls) {
+        q = load_request(p, r);
         tiles = tiles_of(q);
         int64_t cost;
         even_tiles(p, ls, q, tiles, even, cost);
         return cost;
     }
     // Moves on to the next tile of which something lies in the range, the current one included.
-    __device__ void settle(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
+    __device__ void settle(const WeightParams& p, const LaunchShape& ls) {
         for (;;) {
             while (k >= tiles) {
                 if (++r >= p.num_reqs || at >= to) {
@@ -208,7 +246,7 @@ struct Walk {
                     return;
                 }
                 k = 0;
-                request(p, ls, sh);
+                request(p, ls);
             }
             if (at >= to) {
                 r = -1;
@@ -237,7 +275,7 @@ struct Walk {
             r = -1;
             return;
         }
-        const int64_t cost = request(p, ls, sh), skip = (from - at) / cost;
+        const int64_t cost = request(p, ls), skip = (from - at) / cost;
         k = skip < even ? (int32_t)skip : even;
         at += cost * k;
         if (k > 0 && k < even) {
@@ -245,21 +283,12 @@ struct Walk {
             column_tiles(p, ls, q, k, first, groups);
             total = groups * ls.head_groups;
         }
-        settle(p, ls, sh);
+        settle(p, ls);
     }
-    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
+    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
         at += kTileCost + total;
         ++k;
-        settle(p, ls, sh);
-    }
-    // The same for roles that have nothing to do on tiles without columns.
-    __device__ __forceinline__ void start_columns(const WeightParams& p, const LaunchShape& ls, const Shared& sh, int64_t a, int64_t b) {
-        start(p, ls, sh, a, b);
-        while (!done() && total == 0) next(p, ls, sh);
-    }
-    __device__ __forceinline__ void next_columns(const WeightParams& p, const LaunchShape& ls, const Shared& sh) {
-        do next(p, ls, sh);
-        while (!done() && total == 0);
+        settle(p, ls);
     }
     // Whether the first column tile of `x` is the last one of this tile.
     __device__ __forceinline__ bool same_columns(const LaunchShape& ls, const Walk& x) const {
@@ -284,8 +313,9 @@ __device__ int64_t block_sum(Shared& sh, int64_t v) {
 __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t& from, int64_t& to) {
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
     int64_t mine = 0, cost = 0;
-    for (int32_t r = tid; r < p.num_reqs; r += kThreads) {
-        cost = request_cost(p, ls, load_request(p, r));
+    for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
+        if (r0 + warp * kWarp >= p.num_reqs) break;
+        cost = request_costs(p, ls, r0 + tid);
         mine += cost;
     }
     const int64_t all = block_sum(sh, mine);
@@ -298,8 +328,7 @@ __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared&
     }
     int64_t before = 0;
     for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
-        const int32_t r = r0 + tid;
-        if (p.num_reqs > kThreads) cost = r < p.num_reqs ? request_cost(p, ls, load_request(p, r)) : 0;
+        if (p.num_reqs > kThreads) cost = r0 + warp * kWarp < p.num_reqs ? request_costs(p, ls, r0 + tid) : 0;
         int64_t sum = cost;
         for (int o = 1; o < kWarp; o *= 2) {
             const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -309,21 +338,20 @@ __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared&
         if (lane == kWarp - 1) sh.scan[warp] = sum;
         __syncthreads();
         int64_t at = before + sum - cost;
-        for (int i = 0; i < warp; ++i) at += sh.scan[i];
+        for (int i = 0; i < kThreads / kWarp; ++i) {
+            if (i < warp) at += sh.scan[i];
+            before += sh.scan[i];
+        }
         if (at <= from && from < at + cost) {
-            sh.first_request = r;
+            sh.first_request = r0 + tid;
             sh.first_at = at;
         }
-        for (int i = 0; i < kThreads / kWarp; ++i) before += sh.scan[i];
         if (before > from) break;
     }
     __syncthreads();
-    const int32_t r = sh.first_request + tid;
-    if (tid < kStaged && r < p.num_reqs) sh.request[tid] = load_request(p, r);
-    __syncthreads();
 }
 
-// Address of row j's data and scales; null without a page.
+// The page that holds row j; negative without one.
 __device__ __forceinline__ int32_t page_of(const WeightParams& p, int32_t r, const Request& q, int32_t j) {
     if (j >= q.end) return -1;
     int32_t off;
@@ -332,6 +360,108 @@ __device__ __forceinline__ int32_t page_of(const WeightParams& p, int32_t r, con
     const int32_t page = p.bt[(int64_t)r * p.bt_stride + logical];
     return page < p.cache.num_pages ? page : -1;
 }
+
+// ---- the planning warp ------------------------------------------------------------------------
+
+__device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t from, int64_t to) {
+    constexpr int kPer = kTile / kWarp;
+    const int lane = threadIdx.x % kWarp;
+    const int64_t token_stride = p.head_dim + p.rope_dim;
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+    Walk cur, nxt;
+    int32_t page[kPer], ahead[kPer];
+    const auto lookup = [&](const Walk& x, int32_t(&to)[kPer]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) to[i] = x.done() ? -1 : page_of(p, x.r, x.q, x.k * kTile + i * kWarp + lane);
+    };
+    // Tiles no token sees rows of are dealt with here.
+    const auto skip_empty = [&](Walk& x) {
+        for (; !x.done() && x.total == 0; x.next(p, ls)) {
+            if (p.decay == 1.0f && p.out == p.weights) continue;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int32_t j = x.k * kTile + i * kWarp + lane;
+                if (j >= x.q.end) continue;
+                const float old = p.decay == 0.0f ? 0.0f : p.decay * p.weights[(int64_t)x.r * p.w_stride + j];
+                p.out[(int64_t)x.r * p.out_stride + j] = old;
+            }
+        }
+    };
+    cur.start(p, ls, sh, from, to);
+    skip_empty(cur);
+    if (lane == 0) {
+        Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
+        if (!cur.done() && cur.c0 > 0) rec = {cur.c1 == cur.total ? kEnds : kMiddle, cur.r, cur.k, 0};
+        ls.records[blockIdx.x] = rec;
+    }
+    lookup(cur, page);
+    bool kept = false;
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t slot = n % kTiles;
+        Tile& t = sh.tile[slot];
+        if (n >= kTiles && !wait_all(&sh.tile_free[slot], (n / kTiles - 1) & 1)) return false;
+        if (cur.done()) {
+            if (lane == 0) {
+                t.request = -1;
+                mbar_arrive(&sh.tile_full[slot]);
+            }
+            return true;
+        }
+        nxt = cur;
+        nxt.next(p, ls);
+        skip_empty(nxt);
+        lookup(nxt, ahead);
+        const bool keeps = cur.same_columns(ls, nxt);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            Row row{zero, zero};
+            if (page[i] >= 0) {
+                int32_t off;
+                div_block32(cur.k * kTile + i * kWarp + lane, p.cache.block_size, p.cache.shift, off);
+                const uint8_t* pg = p.cache.base + (int64_t)page[i] * p.cache.page_stride;
+                row.data = pg + off * token_stride;
+                row.scales = pg + p.cache.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
+            }
+            t.row[i * kWarp + lane] = row;
+            const uint32_t there = __ballot_sync(0xFFFFFFFFu, page[i] >= 0);
+            if (lane == 0) t.there[i] = there;
+            page[i] = ahead[i];
+        }
+        if (lane == 0) {
+            t.request = cur.r;
+            t.tile = cur.k;
+            t.first_row = cur.k * kTile;
+            t.end = cur.q.end;
+            t.first = cur.first;
+            t.total = cur.total;
+            t.c0 = cur.c0;
+            t.c1 = cur.c1;
+            t.tokens = cur.q.tokens;
+            t.token0 = cur.q.token0;
+            t.row0 = cur.q.row0;
+            t.replay = cur.q.replay;
+            t.kept = kept;
+            t.keeps = keeps;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.tile_full[slot]);
+        kept = keeps;
+        cur = nxt;
+    }
+}
+
+// Place of a role in the ring of tiles.
+struct Tiles {
+    uint32_t n = 0;
+    __device__ __forceinline__ bool wait(Shared& sh) const { return wait_all(&sh.tile_full[n % kTiles], (n / kTiles) & 1); }
+    __device__ __forceinline__ const Tile& at(const Shared& sh) const { return sh.tile[n % kTiles]; }
+    // The tile has been read (by this warp).
+    __device__ __forceinline__ void next(Shared& sh) {
+        __syncwarp();
+        if (threadIdx.x % kWarp == 0) mbar_arrive(&sh.tile_free[n % kTiles]);
+        ++n;
+    }
+};
 
 // ---- workers: records to tensor memory -----------------------------------------------------
 
@@ -370,8 +500,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
 // stand in its part of shared memory with a row stride that is an odd number of 16 bytes,
 // so that lanes reading 16 bytes of their own rows hit different banks.
 template <int D>
-__device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t staging, uint32_t tmem_k,
-                     int64_t from, int64_t to) {
+__device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t staging, uint32_t tmem_k) {
     constexpr int kBlocks = D / 128;  // 64-dim blocks of a half
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, quad = warp % 4, half = warp / 4;
     const int nope = D - p.rope_dim;
@@ -379,24 +508,10 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
     const auto byte_of = [&](int d) { return d <= nope ? d : nope + 2 * (d - nope); };
     const int stride = ls.stride[half], byte0 = byte_of(d0);
     const uint32_t mine = staging + (half ? 4 * kWarp * ls.stride[0] : 0) + quad * kWarp * stride;
-    const int64_t token_stride = D + p.rope_dim;
+    const uint32_t own = mine + lane * stride;
 
-    // A tile's row of this lane: page, address
-    const auto lookup = [&](const Walk& x) {
-        return x.done() ? -1 : page_of(p, x.r, x.q, x.k * kTile + quad * kWarp + lane);
-    };
-    const auto row_of = [&](const Walk& x, int32_t page, const uint8_t*& scales) -> const uint8_t* {
-        scales = nullptr;
-        if (page < 0) return nullptr;
-        int32_t off;
-        div_block32(x.k * kTile + quad * kWarp + lane, p.cache.block_size, p.cache.shift, off);
-        const uint8_t* pg = p.cache.base + (int64_t)page * p.cache.page_stride;
-        scales = pg + p.cache.block_size * token_stride + (int64_t)off * (D / 64);
-        return pg + off * token_stride;
-    };
     const auto load_scales = [&](const uint8_t* at) {
         uint2 s = make_uint2(0, 0);
-        if (at == nullptr) return s;
         if (D == 512) {
             s = ld_nc_v2(at);
         } else if (D == 256) {
@@ -406,45 +521,40 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
         }
         return s;
     };
-    // Copies block b of the rows whose addresses the lanes hold.
-    const auto fetch = [&](const uint8_t* row, int b) {
+    // Copies block b of a tile's rows: 4 or 8 lanes a row.
+    const auto fetch = [&](const Tile& t, int b) {
         const int d = d0 + b * 64, at = byte_of(d);
-        const uint64_t addr = reinterpret_cast<uint64_t>(row);
-        const int per = d >= nope ? 8 : 4;  // 16-byte pieces of a row
-        const int first = lane / per, piece = lane % per;
+        const Row* row = t.row + quad * kWarp;
+        if (d >= nope) {
+            const int first = lane / 8, piece = lane % 8 * 16;
+            const uint32_t dst = mine + first * stride + (at - byte0) + piece;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int src = first + i * (kWarp / per);
-            if (i >= per) break;
-            const uint64_t a = __shfl_sync(0xFFFFFFFFu, addr, src);
-            const uint8_t* from_row = a ? reinterpret_cast<const uint8_t*>(a) + at + piece * 16 : p.cache.base;
-            copy16(mine + src * stride + (at - byte0) + piece * 16, from_row, a ? 16 : 0);
+            for (int i = 0; i < 8; ++i) copy16(dst + i * 4 * stride, row[first + i * 4].data + at + piece, 16);
+        } else {
+            const int first = lane / 4, piece = lane % 4 * 16;
+            const uint32_t dst = mine + first * stride + (at - byte0) + piece;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy16(dst + i * 8 * stride, row[first + i * 8].data + at + piece, 16);
         }
     };
-
-    Walk cur, nxt;
-    cur.start_columns(p, ls, sh, from, to);
-    if (cur.done()) return true;
-    const uint8_t *scales_at, *row = row_of(cur, lookup(cur), scales_at);
+    Tiles tiles;
+    if (!tiles.wait(sh)) return false;
+    if (tiles.at(sh).request < 0) return true;
     for (int b = 0; b < kBlocks; ++b) {
-        fetch(row, b);
+        fetch(tiles.at(sh), b);
         copies_commit();
     }
-    uint2 scales = load_scales(scales_at);
-    nxt = cur;
-    nxt.next_columns(p, ls, sh);
-    int32_t next_page = lookup(nxt);
+    uint2 scales = load_scales(tiles.at(sh).row[quad * kWarp + lane].scales);
+    tiles.next(sh);
     for (uint32_t step = 0;; ++step) {
-        const bool more = !nxt.done();
-        const uint8_t *next_scales_at, *next_row = row_of(nxt, next_page, next_scales_at);
-        const uint2 next_scales = load_scales(next_scales_at);
-        if (more) {
-            nxt.next_columns(p, ls, sh);
-            next_page = lookup(nxt);
-        }
+        if (!tiles.wait(sh)) return false;
+        const bool more = tiles.at(sh).request >= 0;
+        uint2 next_scales = make_uint2(0, 0);
+        if (more) next_scales = load_scales(tiles.at(sh).row[quad * kWarp + lane].scales);
+#pragma unroll 1
         for (int b = 0; b < kBlocks; ++b) {
-            const int d = d0 + b * 64, block = d / 64;
-            const uint32_t at = mine + lane * stride + byte_of(d) - byte0;
+            const int d = d0 + b * 64, block = half * kBlocks + b;
+            const uint32_t at = own + byte_of(d) - byte0;
             copies_wait<kBlocks - 1>();
             __syncwarp();
             uint32_t w[32];
@@ -463,7 +573,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
                 }
             }
             __syncwarp();  // the block has been read: the next tile's copy may land there
-            if (more) fetch(next_row, b);
+            if (more) fetch(tiles.at(sh), b);
             copies_commit();
             if (step > 0 && !wait_all(&sh.k_free[block], (step - 1) & 1)) return false;
             tmem_fence_after();
@@ -474,6 +584,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             if (lane == 0) mbar_arrive(&sh.k_full[block]);
         }
         if (!more) return true;
+        tiles.next(sh);
         scales = next_scales;
     }
 }
@@ -492,21 +603,25 @@ __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map
 
 // One thread fetches the queries.
 template <int D>
-__device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring,
-                              int64_t from, int64_t to) {
+__device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring) {
     constexpr int kBlocks = D / 64;
     const uint32_t bytes = (uint32_t)(ls.heads * ls.tokens * 128);
     uint32_t stage = 0, round = 0;
-    bool ok = true, loaded = false;
-    Walk cur, nxt;
-    cur.start_columns(p, ls, sh, from, to);
-    while (ok && !cur.done()) {
-        nxt = cur;
-        nxt.next_columns(p, ls, sh);
-        int32_t c = cur.c0 + (loaded ? 1 : 0);
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        const uint32_t slot = n % kTiles;
+        if (!mbar_poll_bounded(&sh.tile_full[slot], (n / kTiles) & 1, kWaitLimitNs)) {
+            ok = false;
+            break;
+        }
+        const Tile& tile = sh.tile[slot];
+        if (tile.request < 0) return true;
+        const int32_t c1 = tile.c1, token0 = tile.token0 + tile.first * ls.tokens;
+        int32_t c = tile.c0 + tile.kept;
+        mbar_arrive(&sh.tile_free[slot]);
         int32_t group = c / ls.head_groups, part = c - group * ls.head_groups;
-        for (; ok && c < cur.c1; ++c) {
-            const int32_t t = cur.q.token0 + (cur.first + group) * ls.tokens, h = part * ls.heads;
+        for (; ok && c < c1; ++c) {
+            const int32_t t = token0 + group * ls.tokens, h = part * ls.heads;
 #pragma unroll 1
             for (int b = 0; b < kBlocks; ++b) {
                 if (round > 0 && !mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs)) {
@@ -525,25 +640,22 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
                 ++group;
             }
         }
-        loaded = cur.same_columns(ls, nxt);
-        cur = nxt;
     }
-    if (!ok) {  // copies in flight land before the CTA ends
-        for (int i = 0; i < ls.stages; ++i) {
-            stage = (stage + ls.stages - 1) % ls.stages;
-            if (stage == (uint32_t)ls.stages - 1) {
-                if (round == 0) break;
-                --round;
-            }
-            mbar_poll_bounded(&sh.q_full[stage], round & 1, kWaitLimitNs / 8);
+    // a wait expired: copies in flight land before the CTA ends
+    for (int i = 0; i < ls.stages; ++i) {
+        stage = (stage + ls.stages - 1) % ls.stages;
+        if (stage == (uint32_t)ls.stages - 1) {
+            if (round == 0) break;
+            --round;
         }
+        mbar_poll_bounded(&sh.q_full[stage], round & 1, kWaitLimitNs / 8);
     }
-    return ok;
+    return false;
 }
 
 // The logarithms and bounds of the columns, one a thread.  The next column tile's lse is in
 // flight while this one's is worked on.
-__device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t from, int64_t to) {
+__device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh) {
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kColumnWarp, col = warp * kWarp + lane;
     const int32_t token = col / ls.heads, head = col - token * ls.heads;
     struct Column {
@@ -551,56 +663,59 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
         int32_t pos, rows_from;
         float lse, sink;
     };
-    Walk cur{};
-    int32_t c = 0, group = 0, part = 0;
+    Tiles tiles;
+    int32_t c = 0, c1 = 0, group = 0, part = 0, tokens = 0, token0 = 0, row0 = 0, replay = 0;
     bool end = false;
-    // the column of the next column tile, which the walk stands at
+    // this thread's column of the column tile at hand
     const auto load = [&]() {
-        Column x{false, 0, cur.q.replay, 0.0f, -INFINITY};
-        const int32_t i = (cur.first + group) * ls.tokens + token, h = part * ls.heads + head;
-        if (token < ls.tokens && i < cur.q.tokens && h < p.num_heads) {
-            const int64_t t = (int64_t)cur.q.token0 + i;
+        Column x{false, 0, replay, 0.0f, -INFINITY};
+        const int32_t i = group * ls.tokens + token, h = part * ls.heads + head;
+        if (token < ls.tokens && i < tokens && h < p.num_heads) {
+            const int64_t t = (int64_t)token0 + i;
             x.used = p.valid == nullptr || p.valid[t] != 0;
-            x.pos = cur.q.row0 + i;
+            x.pos = row0 + i;
             x.lse = p.lse[t * p.lse_stride_t + h];
             if (p.sink) x.sink = p.sink[h];
         }
         return x;
     };
-    const auto at = [&]() {
-        group = c / ls.head_groups;
-        part = c - group * ls.head_groups;
+    // moves on to the first column tile of a later tile
+    const auto next_tile = [&]() {
+        for (;;) {
+            if (!tiles.wait(sh)) return false;
+            const Tile& t = tiles.at(sh);
+            if (t.request < 0) {
+                end = true;
+                return true;
+            }
+            c = t.c0 + t.kept;
+            c1 = t.c1;
+            tokens = t.tokens;
+            token0 = t.token0;
+            row0 = t.row0;
+            replay = t.replay;
+            group = c / ls.head_groups;
+            part = c - group * ls.head_groups;
+            group += t.first;
+            tiles.next(sh);
+            if (c < c1) return true;
+        }
     };
-    const auto advance = [&]() {
-        if (++c < cur.c1) {
+    if (!next_tile()) return false;
+    Column next{};
+    if (!end) next = load();
+    for (uint32_t seq = 0; !end; ++seq) {
+        const Column x = next;
+        // the next column is read ahead where that waits for no other role, which may be
+        // waiting for this one
+        const bool ahead = ++c < c1;
+        if (ahead) {
             if (++part == ls.head_groups) {
                 part = 0;
                 ++group;
             }
-            return;
+            next = load();
         }
-        for (;;) {
-            const int32_t r = cur.r, last = cur.first * ls.head_groups + cur.c1 - 1;
-            cur.next_columns(p, ls, sh);
-            if (cur.done()) {
-                end = true;
-                return;
-            }
-            // as Walk::same_columns
-            c = cur.c0 + (ls.keep_queries && cur.r == r && last == cur.first * ls.head_groups + cur.c0 ? 1 : 0);
-            if (c < cur.c1) break;
-        }
-        at();
-    };
-    cur.start_columns(p, ls, sh, from, to);
-    if (cur.done()) return true;
-    c = cur.c0;
-    at();
-    Column next = load();
-    for (uint32_t seq = 0; !end; ++seq) {
-        const Column x = next;
-        advance();
-        if (!end) next = load();
         const float a = x.lse * kLog2e, b = x.sink * kLog2e, top = fmaxf(a, b);
         const float log = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
         const bool used = x.used && log != -INFINITY;  // else a token that saw nothing
@@ -621,58 +736,68 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.col_full[slot]);
+        if (!ahead) {
+            if (!next_tile()) return false;
+            if (!end) next = load();
+        }
     }
     return true;
 }
 
 // ---- the MMA warp ------------------------------------------------------------------------------
 
-// A from tensor memory; issued by the lane whose `lead` is 1.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate,
-                                             uint32_t lead) {
+// Four steps of 16 dims, A from tensor memory; issued by the lane whose `lead` is 1.
+__device__ __forceinline__ void umma_bf16_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate,
+                                              uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p, q, one;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
         "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        "setp.eq.u32 one, 0, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+        "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
+        "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
         : "memory");
 }
 
-// Columns of a column tile of a token group, padded to what an MMA takes.
-__device__ __forceinline__ int32_t width_of(const LaunchShape& ls, const Walk& x, int32_t group) {
-    const int32_t i0 = (x.first + group) * ls.tokens;
-    return (min(ls.tokens, x.q.tokens - i0) * ls.heads + 15) / 16 * 16;
+// Columns of a column tile of token group `group`, padded to what an MMA takes.
+__device__ __forceinline__ int32_t width_of(const LaunchShape& ls, int32_t tokens, int32_t group) {
+    return (min(ls.tokens, tokens - group * ls.tokens) * ls.heads + 15) / 16 * 16;
 }
 
 template <int D>
-__device__ bool issue(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s,
-                      int64_t from, int64_t to) {
+__device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s) {
     constexpr int kBlocks = D / 64;
     const uint32_t lead = elect_one();
     const uint64_t q_desc = umma_desc(ring, 16, 1024, kSwizzle128);
+    const uint32_t stage_step = (uint32_t)ls.stage_bytes >> 4;
     uint32_t stage = 0, round = 0, step = 0, tile = 0;
-    Walk cur, nxt;
-    cur.start_columns(p, ls, sh, from, to);
-    for (; !cur.done(); ++tile) {
-        nxt = cur;
-        nxt.next_columns(p, ls, sh);
-        int32_t group = cur.c0 / ls.head_groups, part = cur.c0 - group * ls.head_groups;
-        for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
-            const bool last = c == cur.c1 - 1, keep = last && cur.same_columns(ls, nxt);
-            const uint32_t idesc = umma_idesc(kTile, width_of(ls, cur, group), false), d = tmem_s + (step & 1) * kCols;
+    Tiles tiles;
+    for (;;) {
+        if (!tiles.wait(sh)) return false;
+        const Tile& t = tiles.at(sh);
+        if (t.request < 0) return true;
+        const int32_t c0 = t.c0, c1 = t.c1, first = t.first, tokens = t.tokens;
+        const bool keeps = t.keeps;
+        tiles.next(sh);
+        int32_t group = c0 / ls.head_groups, part = c0 - group * ls.head_groups;
+        for (int32_t c = c0; c < c1; ++c, ++step) {
+            const bool last = c == c1 - 1, keep = last && keeps;
+            const uint32_t idesc = umma_idesc(kTile, width_of(ls, tokens, first + group), false), d = tmem_s + (step & 1) * kCols;
             if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
             uint32_t st = stage, rd = round;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const int block = block_at<D>(b);
-                if (c == cur.c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
+                if (c == c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
                 if (!wait_all(&sh.q_full[st], rd & 1)) return false;
                 tmem_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_bf16_ts(d, tmem_k + block * 32 + k * 8, q_desc + ((st * ls.stage_bytes + k * 32) >> 4), idesc,
-                                 b > 0 || k > 0, lead);
+                umma_bf16_ts4(d, tmem_k + block * 32, q_desc + st * stage_step, idesc, b > 0, lead);
                 if (last) umma_commit(&sh.k_free[block], lead);
                 if (!keep) umma_commit(&sh.q_free[st], lead);
                 if (++st == (uint32_t)ls.stages) {
@@ -690,9 +815,8 @@ __device__ bool issue(const WeightParams& p, const LaunchShape& ls, Shared& sh, 
                 ++group;
             }
         }
-        cur = nxt;
+        ++tile;
     }
-    return true;
 }
 
 // ---- scores to sums --------------------------------------------------------------------------
@@ -706,30 +830,29 @@ struct Sum {
     }
 };
 
-__device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s, int64_t from, int64_t to) {
+__device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s) {
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kWorkers, quad = warp % 4, half = warp / 4;
     const uint32_t lane_base = tmem_s + ((uint32_t)(quad * kWarp) << 16);
     uint32_t step = 0, seq = 0, tile = 0;
     bool loaded = false;
-    Walk cur, nxt;
-    cur.start(p, ls, sh, from, to);
-    if (half == 0 && quad == 0 && lane == 0) {
-        Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
-        if (!cur.done() && cur.c0 > 0) rec = {cur.c1 == cur.total ? kEnds : kMiddle, cur.r, cur.k, 0};
-        ls.records[blockIdx.x] = rec;
-    }
-    while (!cur.done()) {
-        nxt = cur;
-        nxt.next(p, ls, sh);
-        const int32_t j = cur.k * kTile + quad * kWarp + lane;
-        const bool ok = page_of(p, cur.r, cur.q, j) >= 0, in = j < cur.q.end;
-        const int64_t out_at = (int64_t)cur.r * p.out_stride + j;
+    Tiles tiles;
+    for (;; ++tile) {
+        if (!tiles.wait(sh)) return false;
+        const Tile& t = tiles.at(sh);
+        const int32_t request = t.request;
+        if (request < 0) return true;
+        const int32_t c0 = t.c0, c1 = t.c1, first = t.first, tokens = t.tokens;
+        const bool ok = t.there[quad] >> lane & 1, whole = c0 == 0 && c1 == t.total, keeps = t.keeps;
+        const int32_t j = t.first_row + quad * kWarp + lane;
+        const bool in = j < t.end;
+        tiles.next(sh);
+        const int64_t out_at = (int64_t)request * p.out_stride + j;
         float old = 0.0f;
-        if (p.decay != 0.0f && in && half == 0 && cur.whole()) old = p.weights[(int64_t)cur.r * p.w_stride + j];
+        if (p.decay != 0.0f && in && half == 0 && whole) old = p.weights[(int64_t)request * p.w_stride + j];
         Sum sum;
-        int32_t group = cur.c0 / ls.head_groups, part_of = cur.c0 - group * ls.head_groups;
-        for (int32_t c = cur.c0; c < cur.c1; ++c, ++step) {
-            const int32_t n = width_of(ls, cur, group);
+        int32_t group = c0 / ls.head_groups, part_of = c0 - group * ls.head_groups;
+        for (int32_t c = c0; c < c1; ++c, ++step) {
+            const int32_t n = width_of(ls, tokens, first + group);
             if (loaded) {
                 --seq;  // the columns are those of the step before
                 loaded = false;
@@ -783,7 +906,7 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             sum.add((part[0] + part[1]) + (part[2] + part[3]));
             tmem_fence_before();
             __syncwarp();
-            const bool keep = c == cur.c1 - 1 && cur.same_columns(ls, nxt);
+            const bool keep = c == c1 - 1 && keeps;
             if (lane == 0) {
                 mbar_arrive(&sh.s_free[step & 1]);
                 if (!keep) mbar_arrive(&sh.col_free[seq % kColSlots]);
@@ -809,16 +932,13 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.half_free[quad]);
             const float total = sum.hi - sum.lo;
-            if (cur.whole()) {
+            if (whole) {
                 if (in) p.out[out_at] = p.decay == 0.0f ? total : fmaf(p.decay, old, total);
             } else {
-                ls.parts[((int64_t)blockIdx.x * 2 + (cur.c0 > 0 ? 0 : 1)) * kTile + quad * kWarp + lane] = total;
+                ls.parts[((int64_t)blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * kTile + quad * kWarp + lane] = total;
             }
         }
-        cur = nxt;
-        ++tile;
     }
-    return true;
 }
 
 constexpr size_t kAlign = 1024;
@@ -834,6 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(&sh.tile_full[i], 1);
+            mbar_init(&sh.tile_free[i], kPlanWarp);  // every other warp
+        }
         for (int i = 0; i < kMostBlocks; ++i) {
             mbar_init(&sh.k_full[i], 4);
             mbar_init(&sh.k_free[i], 1);
@@ -869,17 +993,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool ok = true;
     if (warp < kWorkers) {
-        ok = work<D>(p, ls, sh, smem_u32(staging), tmem_k, from, to);
+        ok = work<D>(p, ls, sh, smem_u32(staging), tmem_k);
         if (!ok) copies_wait<0>();
     } else if (warp < kColumnWarp) {
-        ok = summarise(p, ls, sh, tmem_s, from, to);
+        ok = summarise(p, ls, sh, tmem_s);
     } else if (warp < kQueryWarp) {
-        ok = columns(p, ls, sh, from, to);
+        ok = columns(p, ls, sh);
     } else if (warp == kQueryWarp) {
-        if (lane == 0) ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring), from, to);
+        if (lane == 0) ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring));
         __syncwarp();
+    } else if (warp == kPlanWarp) {
+        ok = plan(p, ls, sh, from, to);
     } else {
-        ok = issue<D>(p, ls, sh, smem_u32(ring), tmem_k, tmem_s, from, to);
+        ok = issue<D>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
         if (!ok) {  // wait for the MMAs in flight before the operands go
             umma_commit(&sh.drain, elect_one());
             mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);

@@ -161,6 +161,12 @@ def test_rows_of_several_ctas(cuda_device, q_lens, prefix, H, D, window):
     _run(cuda_device, H + D, q_lens, prefix, H, D, window=window, pad=3, missing=0.05)
 
 
+@pytest.mark.parametrize("q_lens,prefix,H", [([1], [130000], 16), ([1, 1, 2], [60000, 3, 70000], 40), ([3], [110000], 129)])
+def test_many_tiles_of_few_columns(cuda_device, q_lens, prefix, H):
+    """CTAs with many tiles that share one column tile, or few."""
+    _run(cuda_device, H, q_lens, prefix, H, 128)
+
+
 def test_fewer_rows_than_new_tokens(cuda_device):
     """seq_lens below the query length: the first tokens lie before row 0."""
     _run(cuda_device, 1, [9, 20], [-4, -20], 6, 128, 0, bs=16)
