@@ -39,17 +39,42 @@ __device__ __forceinline__ void sincos_turn(uint64_t u, float& s, float& c) {
     if ((quarter + 1) & 2) c = -c;
 }
 
-__global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
+// A thread keeps V neighbouring pairs and walks over rows, so that an angle is one 64-bit
+// addition from the last; with V = 4 a warp stores whole lines of 128 bytes.
+template <int V>
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeTableParams p, const int32_t rows_per_cta) {
+    const int32_t groups = p.pairs / V, at_once = max(kThreads / groups, 1);
+    const int32_t group = (int32_t)threadIdx.x % groups, row0 = (int32_t)threadIdx.x / groups;
     pdl_wait();
-    const int64_t n = p.num_pos * p.pairs;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = i / p.pairs;
-        const int32_t pair = (int32_t)(i - row * p.pairs);
-        float s, c;
-        sincos_turn((uint64_t)(p.first_pos + row) * p.turn[pair], s, c);
-        float* out = p.out + row * p.stride + pair;
-        out[0] = c * p.factor;
-        out[p.pairs] = s * p.factor;
+    const int64_t first = (int64_t)blockIdx.x * rows_per_cta, end = min(first + rows_per_cta, p.num_pos);
+    if (row0 < at_once) {
+        uint64_t at[V], step[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t turn = p.turn[group * V + i];
+            at[i] = (uint64_t)(p.first_pos + first + row0) * turn;
+            step[i] = (uint64_t)at_once * turn;
+        }
+        float* out = p.out + (first + row0) * p.stride + group * V;
+#pragma unroll 2
+        for (int64_t row = first + row0; row < end; row += at_once) {
+            float s[V], c[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sincos_turn(at[i], s[i], c[i]);
+                s[i] *= p.factor;
+                c[i] *= p.factor;
+                at[i] += step[i];
+            }
+            if constexpr (V == 4) {
+                *reinterpret_cast<float4*>(out) = make_float4(c[0], c[1], c[2], c[3]);
+                *reinterpret_cast<float4*>(out + p.pairs) = make_float4(s[0], s[1], s[2], s[3]);
+            } else {
+                out[0] = c[0];
+                out[p.pairs] = s[0];
+            }
+            out += at_once * p.stride;
+        }
     }
     pdl_launch_dependents();
 }
@@ -222,9 +247,13 @@ cudaError_t launch_type(const RotaryParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream) {
-    const int64_t n = p.num_pos * p.pairs, most = (int64_t)sm_count() * 8;
-    const int64_t ctas = (n + kThreads - 1) / kThreads;
-    return launch_pdl(rope_table_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, stream, p);
+    const bool wide = p.pairs % 4 == 0 && p.stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+    const int32_t groups = p.pairs / (wide ? 4 : 1), at_once = groups < kThreads ? kThreads / groups : 1;
+    // eight CTAs an SM, each with whole turns of its threads
+    const int64_t turns = (p.num_pos + at_once - 1) / at_once, most = (int64_t)sm_count() * 8;
+    const int64_t rows = (turns + most - 1) / most * at_once, ctas = (p.num_pos + rows - 1) / rows;
+    return launch_pdl(wide ? rope_table_kernel<4> : rope_table_kernel<1>, dim3((unsigned)ctas), dim3(kThreads), 0, stream, p,
+                      (int32_t)rows);
 }
 
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream) {
