@@ -40,7 +40,7 @@
 namespace psk {
 namespace {
 
-constexpr int kTile = 128;          // rows of a tile
+constexpr int kTile = 128;          // rows of a CTA's part of a tile
 constexpr int kCols = 128;          // columns of a column tile, at most
 constexpr int kWorkers = 8, kSummers = 8, kColumnWarps = kCols / kWarp;
 constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps, kMmaWarp = kQueryWarp + 1,
@@ -100,8 +100,13 @@ struct Tile {
 };
 
 struct LaunchShape {
+    int32_t ranks;                // CTAs that share a tile, 1 or 2
+    int32_t row_shift;            // log2 of a tile's rows
     int32_t heads, tokens;        // of a column tile
     int32_t head_groups;
+    int32_t box_heads, box_tokens;  // of what a CTA fetches of it
+    int32_t box_cols;             // columns of that, padded
+    int32_t by_heads;             // two CTAs: they fetch the halves of the heads, else of the tokens
     int32_t stages, stage_bytes;
     int32_t keep_queries;         // the ring holds a whole column tile
     int32_t stride[2];            // bytes of a staged row, by half
@@ -152,12 +157,13 @@ __device__ __forceinline__ Request load_request(const WeightParams& p, int32_t r
 // Column tiles of tile `k`: those of the token groups [first, first + groups).
 __device__ __forceinline__ void column_tiles(const WeightParams& p, const LaunchShape& ls, const Request& q, int32_t k,
                                              int32_t& first, int32_t& groups) {
-    // tokens i with row0 + i >= 128 k, and (window) row0 + i - window + 1 <= 128 k + 127
-    const int64_t a = (int64_t)k * kTile - q.row0;
+    // tokens i that see a row of the tile: row0 + i at or behind its first row, and (window)
+    // row0 + i - window + 1 at or before its last
+    const int64_t row = (int64_t)k << ls.row_shift, a = row - q.row0;
     const int32_t i0 = a <= 0 ? 0 : a >= q.tokens ? q.tokens : (int32_t)a;
     int32_t i1 = q.tokens;
     if (p.window > 0) {
-        const int64_t b = (int64_t)k * kTile + kTile - 1 + p.window - q.row0;
+        const int64_t b = row + (1 << ls.row_shift) - 1 + p.window - q.row0;
         if (b < i1) i1 = b > i0 ? (int32_t)b : i0;
     }
     first = i0 / ls.tokens;
@@ -170,11 +176,11 @@ __device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchSh
                                            int32_t& count, int64_t& cost) {
     int64_t n;
     if (p.window > 0) {  // tiles before every window
-        n = ((int64_t)q.row0 - p.window + 1) / kTile;
+        n = ((int64_t)q.row0 - p.window + 1) >> ls.row_shift;
         cost = kTileCost;
     } else {             // tiles all tokens see
         const int64_t x = (int64_t)q.row0 + min(ls.tokens, q.tokens) - 1;
-        n = x < 0 ? 0 : x / kTile + 1;
+        n = (x >> ls.row_shift) + 1;
         cost = kTileCost + (int64_t)((q.tokens + ls.tokens - 1) / ls.tokens) * ls.head_groups;
     }
     count = n < 0 || q.tokens == 0 ? 0 : n > tiles ? tiles : (int32_t)n;
@@ -184,7 +190,9 @@ __device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchSh
     }
 }
 
-__device__ __forceinline__ int32_t tiles_of(const Request& q) { return q.end / kTile + (q.end % kTile != 0); }
+__device__ __forceinline__ int32_t tiles_of(const LaunchShape& ls, const Request& q) {
+    return (int32_t)(((int64_t)q.end + (1 << ls.row_shift) - 1) >> ls.row_shift);
+}
 
 // Cost of the tiles of 32 requests, one a lane.
 __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const LaunchShape& ls, int32_t r) {
@@ -194,7 +202,7 @@ __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const La
     int64_t cost = 0, sum = 0;
     if (r < p.num_reqs) {
         q = load_request(p, r);
-        tiles = tiles_of(q);
+        tiles = tiles_of(ls, q);
         even_tiles(p, ls, q, tiles, even, cost);
         sum = cost * even;
     }
@@ -232,7 +240,7 @@ struct Walk {
     // Takes up request r; returns what one of its even tiles costs.
     __device__ __forceinline__ int64_t request(const WeightParams& p, const LaunchShape& ls) {
         q = load_request(p, r);
-        tiles = tiles_of(q);
+        tiles = tiles_of(ls, q);
         int64_t cost;
         even_tiles(p, ls, q, tiles, even, cost);
         return cost;
@@ -319,7 +327,7 @@ __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared&
         mine += cost;
     }
     const int64_t all = block_sum(sh, mine);
-    const int64_t b = blockIdx.x, n = gridDim.x;
+    const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
     from = all / n * b + all % n * b / n;
     to = all / n * (b + 1) + all % n * (b + 1) / n;
     if (tid == 0) {
@@ -370,9 +378,12 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
     const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
     Walk cur, nxt;
     int32_t page[kPer], ahead[kPer];
+    // row i * 32 + lane of this CTA's part of the tile
+    const int32_t mine = (int32_t)(blockIdx.x % ls.ranks) * kTile + lane;
+    const auto row_at = [&](const Walk& x, int i) { return (int32_t)min(((int64_t)x.k << ls.row_shift) + mine + i * kWarp, (int64_t)INT32_MAX); };
     const auto lookup = [&](const Walk& x, int32_t(&to)[kPer]) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) to[i] = x.done() ? -1 : page_of(p, x.r, x.q, x.k * kTile + i * kWarp + lane);
+        for (int i = 0; i < kPer; ++i) to[i] = x.done() ? -1 : page_of(p, x.r, x.q, row_at(x, i));
     };
     // Tiles no token sees rows of are dealt with here.
     const auto skip_empty = [&](Walk& x) {
@@ -380,7 +391,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
             if (p.decay == 1.0f && p.out == p.weights) continue;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int32_t j = x.k * kTile + i * kWarp + lane;
+                const int32_t j = row_at(x, i);
                 if (j >= x.q.end) continue;
                 const float old = p.decay == 0.0f ? 0.0f : p.decay * p.weights[(int64_t)x.r * p.w_stride + j];
                 p.out[(int64_t)x.r * p.out_stride + j] = old;
@@ -417,7 +428,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
             Row row{zero, zero};
             if (page[i] >= 0) {
                 int32_t off;
-                div_block32(cur.k * kTile + i * kWarp + lane, p.cache.block_size, p.cache.shift, off);
+                div_block32(row_at(cur, i), p.cache.block_size, p.cache.shift, off);
                 const uint8_t* pg = p.cache.base + (int64_t)page[i] * p.cache.page_stride;
                 row.data = pg + off * token_stride;
                 row.scales = pg + p.cache.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
@@ -430,7 +441,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
         if (lane == 0) {
             t.request = cur.r;
             t.tile = cur.k;
-            t.first_row = cur.k * kTile;
+            t.first_row = row_at(cur, 0);  // lane 0's
             t.end = cur.q.end;
             t.first = cur.first;
             t.total = cur.total;
@@ -496,10 +507,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
         : "memory");
 }
 
+// Arrives on a barrier of the CTA that issues the MMAs.  What it hands over stands in tensor
+// memory, ordered by the tcgen05 fences, so that no cluster-wide release is needed (it
+// would cost a step of the sums some 1000 cycles).
+template <bool kPair>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    if constexpr (kPair)
+        asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+ "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+    else
+        mbar_arrive(bar);
+}
+
 // A worker warp has the rows 32 * quad ... of each tile and the dims of one half.  Records
 // stand in its part of shared memory with a row stride that is an odd number of 16 bytes,
 // so that lanes reading 16 bytes of their own rows hit different banks.
-template <int D>
+template <int D, bool kPair>
 __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t staging, uint32_t tmem_k) {
     constexpr int kBlocks = D / 128;  // 64-dim blocks of a half
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, quad = warp % 4, half = warp / 4;
@@ -581,7 +604,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.k_full[block]);
+            if (lane == 0) arrive_leader<kPair>(&sh.k_full[block]);
         }
         if (!more) return true;
         tiles.next(sh);
@@ -595,17 +618,28 @@ __device__ __forceinline__ constexpr int block_at(int i) { return (i & 1) * (D /
 
 // ---- queries and columns ---------------------------------------------------------------------
 
+// kPair: the bytes are counted by the first CTA's barrier.
+template <bool kPair>
 __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map, int32_t d, int32_t h, int32_t t, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %5, 0;\n\t"
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [a];\n\t}"
+            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
 // One thread fetches the queries.
-template <int D>
+template <int D, bool kPair>
 __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring) {
     constexpr int kBlocks = D / 64;
-    const uint32_t bytes = (uint32_t)(ls.heads * ls.tokens * 128);
+    const uint32_t bytes = (uint32_t)(ls.box_heads * ls.box_tokens * 128) * (kPair ? 2 : 1);
+    const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
+    const int32_t from_t = ls.by_heads ? 0 : rank * ls.box_tokens, from_h = ls.by_heads ? rank * ls.box_heads : 0;
     uint32_t stage = 0, round = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -621,15 +655,15 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
         mbar_arrive(&sh.tile_free[slot]);
         int32_t group = c / ls.head_groups, part = c - group * ls.head_groups;
         for (; ok && c < c1; ++c) {
-            const int32_t t = token0 + group * ls.tokens, h = part * ls.heads;
+            const int32_t t = token0 + group * ls.tokens + from_t, h = part * ls.heads + from_h;
 #pragma unroll 1
             for (int b = 0; b < kBlocks; ++b) {
                 if (round > 0 && !mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
-                tma_queries(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h, t, &sh.q_full[stage]);
+                if (rank == 0) mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
+                tma_queries<kPair>(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h, t, &sh.q_full[stage]);
                 if (++stage == (uint32_t)ls.stages) {
                     stage = 0;
                     ++round;
@@ -641,8 +675,9 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
             }
         }
     }
-    // a wait expired: copies in flight land before the CTA ends
-    for (int i = 0; i < ls.stages; ++i) {
+    // a wait expired: copies in flight land before the CTA ends (the first CTA of a pair waits for
+    // both, and they end together)
+    for (int i = 0; i < ls.stages && rank == 0; ++i) {
         stage = (stage + ls.stages - 1) % ls.stages;
         if (stage == (uint32_t)ls.stages - 1) {
             if (round == 0) break;
@@ -657,7 +692,10 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
 // flight while this one's is worked on.
 __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh) {
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kColumnWarp, col = warp * kWarp + lane;
-    const int32_t token = col / ls.heads, head = col - token * ls.heads;
+    const int32_t rank = col / ls.box_cols, at = col - rank * ls.box_cols;
+    const int32_t token = at / ls.box_heads + (ls.by_heads ? 0 : rank * ls.box_tokens);
+    const int32_t head = at % ls.box_heads + (ls.by_heads ? rank * ls.box_heads : 0);
+    const bool in_box = at < ls.box_heads * ls.box_tokens && rank < ls.ranks;
     struct Column {
         bool used;
         int32_t pos, rows_from;
@@ -670,7 +708,7 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
     const auto load = [&]() {
         Column x{false, 0, replay, 0.0f, -INFINITY};
         const int32_t i = group * ls.tokens + token, h = part * ls.heads + head;
-        if (token < ls.tokens && i < tokens && h < p.num_heads) {
+        if (in_box && i < tokens && h < p.num_heads) {
             const int64_t t = (int64_t)token0 + i;
             x.used = p.valid == nullptr || p.valid[t] != 0;
             x.pos = row0 + i;
@@ -747,30 +785,53 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
 // ---- the MMA warp ------------------------------------------------------------------------------
 
 // Four steps of 16 dims, A from tensor memory; issued by the lane whose `lead` is 1.
+template <bool kPair>
 __device__ __forceinline__ void umma_bf16_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate,
                                               uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred p, q, one;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "setp.ne.u32 q, %5, 0;\n\t"
-        "setp.eq.u32 one, 0, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
-        "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t"
-        "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, one;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
-        : "memory");
+#define PSK_TS4(GROUP)                                                                  \
+    asm volatile(                                                                       \
+        "{\n\t.reg .pred p, q, one;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"               \
+        "setp.ne.u32 p, %4, 0;\n\t"                                                     \
+        "setp.ne.u32 q, %5, 0;\n\t"                                                     \
+        "setp.eq.u32 one, 0, 0;\n\t"                                                    \
+        "@q tcgen05.mma." GROUP ".kind::f16 [%0], [%1], %2, %3, p;\n\t"                 \
+        "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t"                                    \
+        "@q tcgen05.mma." GROUP ".kind::f16 [%0], [a], b, %3, one;\n\t"                 \
+        "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\t"                                   \
+        "@q tcgen05.mma." GROUP ".kind::f16 [%0], [a], b, %3, one;\n\t"                 \
+        "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\t"                                   \
+        "@q tcgen05.mma." GROUP ".kind::f16 [%0], [a], b, %3, one;\n\t}"                \
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead) \
+        : "memory")
+    if constexpr (kPair) {
+        PSK_TS4("cta_group::2");
+    } else {
+        PSK_TS4("cta_group::1");
+    }
+#undef PSK_TS4
+}
+
+// The barrier (in both CTAs of a pair) completes one arrival when all MMAs issued by this
+// thread (the lead lane) are done.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.u32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}"
+            ::"r"(smem_u32(bar)), "r"(lead), "h"((uint16_t)3) : "memory");
+    else
+        umma_commit(bar, lead);
 }
 
 // Columns of a column tile of token group `group`, padded to what an MMA takes.
+template <bool kPair>
 __device__ __forceinline__ int32_t width_of(const LaunchShape& ls, int32_t tokens, int32_t group) {
-    return (min(ls.tokens, tokens - group * ls.tokens) * ls.heads + 15) / 16 * 16;
+    return kPair ? 2 * ls.box_cols : (min(ls.tokens, tokens - group * ls.tokens) * ls.heads + 15) / 16 * 16;
 }
 
-template <int D>
+template <int D, bool kPair>
 __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s) {
     constexpr int kBlocks = D / 64;
     const uint32_t lead = elect_one();
@@ -785,10 +846,11 @@ __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t
         const int32_t c0 = t.c0, c1 = t.c1, first = t.first, tokens = t.tokens;
         const bool keeps = t.keeps;
         tiles.next(sh);
+        if (kPair && (blockIdx.x & 1)) continue;  // the first CTA of a pair issues
         int32_t group = c0 / ls.head_groups, part = c0 - group * ls.head_groups;
         for (int32_t c = c0; c < c1; ++c, ++step) {
             const bool last = c == c1 - 1, keep = last && keeps;
-            const uint32_t idesc = umma_idesc(kTile, width_of(ls, tokens, first + group), false), d = tmem_s + (step & 1) * kCols;
+            const uint32_t idesc = umma_idesc(kTile * (kPair ? 2 : 1), width_of<kPair>(ls, tokens, first + group), false), d = tmem_s + (step & 1) * kCols;
             if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
             uint32_t st = stage, rd = round;
 #pragma unroll
@@ -797,15 +859,15 @@ __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t
                 if (c == c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
                 if (!wait_all(&sh.q_full[st], rd & 1)) return false;
                 tmem_fence_after();
-                umma_bf16_ts4(d, tmem_k + block * 32, q_desc + st * stage_step, idesc, b > 0, lead);
-                if (last) umma_commit(&sh.k_free[block], lead);
-                if (!keep) umma_commit(&sh.q_free[st], lead);
+                umma_bf16_ts4<kPair>(d, tmem_k + block * 32, q_desc + st * stage_step, idesc, b > 0, lead);
+                if (last) commit<kPair>(&sh.k_free[block], lead);
+                if (!keep) commit<kPair>(&sh.q_free[st], lead);
                 if (++st == (uint32_t)ls.stages) {
                     st = 0;
                     ++rd;
                 }
             }
-            umma_commit(&sh.s_full[step & 1], lead);
+            commit<kPair>(&sh.s_full[step & 1], lead);
             if (!keep) {
                 stage = st;
                 round = rd;
@@ -830,6 +892,7 @@ struct Sum {
     }
 };
 
+template <bool kPair>
 __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s) {
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kWorkers, quad = warp % 4, half = warp / 4;
     const uint32_t lane_base = tmem_s + ((uint32_t)(quad * kWarp) << 16);
@@ -852,7 +915,7 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
         Sum sum;
         int32_t group = c0 / ls.head_groups, part_of = c0 - group * ls.head_groups;
         for (int32_t c = c0; c < c1; ++c, ++step) {
-            const int32_t n = width_of(ls, tokens, first + group);
+            const int32_t n = width_of<kPair>(ls, tokens, first + group);
             if (loaded) {
                 --seq;  // the columns are those of the step before
                 loaded = false;
@@ -908,7 +971,7 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             __syncwarp();
             const bool keep = c == c1 - 1 && keeps;
             if (lane == 0) {
-                mbar_arrive(&sh.s_free[step & 1]);
+                arrive_leader<kPair>(&sh.s_free[step & 1]);
                 if (!keep) mbar_arrive(&sh.col_free[seq % kColSlots]);
             }
             loaded = keep;
@@ -943,7 +1006,25 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
 
 constexpr size_t kAlign = 1024;
 
-template <int D>
+template <bool kPair>
+__device__ __forceinline__ void alloc_tmem(uint32_t* dst) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        tmem_alloc(dst, 512);
+    }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void free_tmem(uint32_t addr) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr));
+    else
+        tmem_dealloc(addr, 512);
+}
+
+template <int D, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ LaunchShape ls,
                         const __grid_constant__ CUtensorMap map) {
@@ -959,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.tile_free[i], kPlanWarp);  // every other warp
         }
         for (int i = 0; i < kMostBlocks; ++i) {
-            mbar_init(&sh.k_full[i], 4);
+            mbar_init(&sh.k_full[i], kPair ? 8 : 4);
             mbar_init(&sh.k_free[i], 1);
         }
         for (int i = 0; i < kMostStages; ++i) {
@@ -972,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], kSummers);
+            mbar_init(&sh.s_free[i], kPair ? 2 * kSummers : kSummers);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.half_full[i], 1);
@@ -981,7 +1062,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.drain, 1);
         mbar_fence_init();
     }
-    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
+    __syncwarp();
+    if (kPair) cluster_sync();  // the other CTA's barriers are there too
+    if (warp == kMmaWarp) alloc_tmem<kPair>(&sh.tmem);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -993,29 +1076,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     bool ok = true;
     if (warp < kWorkers) {
-        ok = work<D>(p, ls, sh, smem_u32(staging), tmem_k);
+        ok = work<D, kPair>(p, ls, sh, smem_u32(staging), tmem_k);
         if (!ok) copies_wait<0>();
     } else if (warp < kColumnWarp) {
-        ok = summarise(p, ls, sh, tmem_s);
+        ok = summarise<kPair>(p, ls, sh, tmem_s);
     } else if (warp < kQueryWarp) {
         ok = columns(p, ls, sh);
     } else if (warp == kQueryWarp) {
-        if (lane == 0) ok = fetch_queries<D>(p, ls, map, sh, smem_u32(ring));
+        if (lane == 0) ok = fetch_queries<D, kPair>(p, ls, map, sh, smem_u32(ring));
         __syncwarp();
     } else if (warp == kPlanWarp) {
         ok = plan(p, ls, sh, from, to);
     } else {
-        ok = issue<D>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
-        if (!ok) {  // wait for the MMAs in flight before the operands go
-            umma_commit(&sh.drain, elect_one());
+        ok = issue<D, kPair>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
+        if (!ok && (!kPair || (blockIdx.x & 1) == 0)) {  // wait for the MMAs in flight before the operands go
+            commit<kPair>(&sh.drain, elect_one());
             mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);
         }
     }
+    __syncwarp();
     if (!ok && lane == 0) atomicAdd(&g_weights_wait_timeouts, 1u);
     tmem_fence_before();
-    __syncthreads();
+    if (kPair) cluster_sync(); else __syncthreads();
     tmem_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(sh.tmem, 512);
+    if (warp == kMmaWarp) free_tmem<kPair>(sh.tmem);
+    if (kPair) cluster_sync();
 }
 
 // ---- joining the parts of cut tiles ------------------------------------------------------------
@@ -1028,7 +1113,7 @@ __global__ void __launch_bounds__(kTile) join_kernel(const WeightParams p, const
     if (rec.kind != kEnds) return;
     const int i = threadIdx.x;
     double sum = ls.parts[(int64_t)blockIdx.x * 2 * kTile + i];
-    for (int c = (int)blockIdx.x - 1; c >= 0; --c) {
+    for (int c = (int)blockIdx.x - ls.ranks; c >= 0; c -= ls.ranks) {
         const int kind = ls.records[c].kind;
         if (kind == kEmptyRange) continue;
         if (kind == kMiddle) {
@@ -1038,7 +1123,8 @@ __global__ void __launch_bounds__(kTile) join_kernel(const WeightParams p, const
             break;
         }
     }
-    const int32_t rows = p.seq_lens[rec.request], j = rec.tile * kTile + i;
+    const int32_t rows = p.seq_lens[rec.request];
+    const int64_t j = ((int64_t)rec.tile << ls.row_shift) + blockIdx.x % ls.ranks * kTile + i;
     if (j >= rows || j >= p.width) return;
     float* out = p.out + (int64_t)rec.request * p.out_stride + j;
     const float total = (float)sum;
@@ -1070,7 +1156,7 @@ bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
     if (encode == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_heads, (cuuint64_t)p.num_tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)p.q_stride_h * 2, (cuuint64_t)p.q_stride_t * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)ls.heads, (cuuint32_t)ls.tokens}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)ls.box_heads, (cuuint32_t)ls.box_tokens}, ones[3] = {1, 1, 1};
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1078,17 +1164,51 @@ bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
 
 constexpr int kMostShared = 227 * 1024;
 
+// Two CTAs share a tile of 256 rows, and the queries of each column tile, where requests
+// bring many columns: half the bytes of queries per row, and a ring twice as deep.
+constexpr int64_t kPairColumns = 512;
+
 LaunchShape make_shape(const WeightParams& p) {
     LaunchShape ls{};
-    ls.head_groups = (p.num_heads + kCols - 1) / kCols;
-    ls.heads = (p.num_heads + ls.head_groups - 1) / ls.head_groups;
-    ls.tokens = ls.head_groups > 1 ? 1 : kCols / ls.heads;
-    if (ls.tokens > p.num_tokens) ls.tokens = p.num_tokens > 0 ? (int32_t)p.num_tokens : 1;
+    const int H = p.num_heads;
+    const int64_t T = p.num_tokens > 0 ? p.num_tokens : 1;
+    ls.ranks = T * H >= kPairColumns * p.num_reqs && sm_count() % 2 == 0 ? 2 : 1;
+    ls.row_shift = ls.ranks == 2 ? 8 : 7;
+    if (ls.ranks == 1) {
+        ls.head_groups = (H + kCols - 1) / kCols;
+        ls.heads = (H + ls.head_groups - 1) / ls.head_groups;
+        ls.tokens = ls.head_groups > 1 ? 1 : kCols / ls.heads;
+        if (ls.tokens > T) ls.tokens = (int32_t)T;
+        ls.box_heads = ls.heads;
+        ls.box_tokens = ls.tokens;
+        ls.box_cols = kCols;
+    } else {
+        // the cut of heads and tokens that leaves the fewest columns unused
+        double best = 0.0;
+        const int half = kCols / 2;
+        for (int groups = 1; groups <= (H + half - 1) / half + 3 && groups <= H; ++groups)
+            for (int by_heads = 0; by_heads < 2; ++by_heads) {
+                const int heads = (H + groups - 1) / groups, box = by_heads ? (heads + 1) / 2 : heads;
+                if (box > half) continue;
+                int tokens = half / box;
+                if (tokens > T) tokens = (int)T;
+                const double used = (double)H / groups * tokens * (by_heads ? 1 : 2);
+                if (used <= best) continue;
+                best = used;
+                ls.by_heads = by_heads;
+                ls.heads = by_heads ? 2 * box : heads;
+                ls.head_groups = (H + ls.heads - 1) / ls.heads;
+                ls.tokens = by_heads ? tokens : 2 * tokens;
+                ls.box_heads = box;
+                ls.box_tokens = tokens;
+            }
+        ls.box_cols = (ls.box_heads * ls.box_tokens + 15) / 16 * 16;
+    }
     const int nope = p.head_dim - p.rope_dim, mid = p.head_dim / 2;
     const int first = mid <= nope ? mid : nope + 2 * (mid - nope);
     ls.stride[0] = first + 16;
     ls.stride[1] = p.head_dim + p.rope_dim - first + 16;
-    ls.stage_bytes = (ls.heads * ls.tokens + 15) / 16 * 16 * 128;
+    ls.stage_bytes = (ls.box_heads * ls.box_tokens + 15) / 16 * 16 * 128;
     const int room = kMostShared - (int)kAlign - 4 * kWarp * (ls.stride[0] + ls.stride[1]) - (int)sizeof(Shared);
     ls.stages = room / ls.stage_bytes;
     if (ls.stages > kMostStages) ls.stages = kMostStages;
@@ -1098,13 +1218,18 @@ LaunchShape make_shape(const WeightParams& p) {
     return ls;
 }
 
-template <int D>
+template <int D, bool kPair>
 cudaError_t launch(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, int ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel<D>, kMostShared, done);
+    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel<D, kPair>, kMostShared, done);
     if (e != cudaSuccess) return e;
     const size_t smem = kAlign + (size_t)ls.stages * ls.stage_bytes + 4 * kWarp * (size_t)(ls.stride[0] + ls.stride[1]) + sizeof(Shared);
-    return launch_pdl(attn_weights_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, ls, map);
+    return launch_pdl_clusters(attn_weights_kernel<D, kPair>, ls.ranks, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, ls, map);
+}
+
+template <int D>
+cudaError_t launch_ranks(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, int ctas, cudaStream_t stream) {
+    return ls.ranks == 2 ? launch<D, true>(p, ls, map, ctas, stream) : launch<D, false>(p, ls, map, ctas, stream);
 }
 
 }  // namespace
@@ -1122,9 +1247,9 @@ cudaError_t launch_attn_weights(WeightParams p, cudaStream_t stream) {
     ls.records = reinterpret_cast<Record*>(ls.parts + (int64_t)ctas * 2 * kTile);
     CUtensorMap map{};
     if (p.num_tokens > 0 && !query_map(p, ls, map)) return cudaErrorNotSupported;
-    cudaError_t e = p.head_dim == 512   ? launch<512>(p, ls, map, ctas, stream)
-                    : p.head_dim == 256 ? launch<256>(p, ls, map, ctas, stream)
-                                        : launch<128>(p, ls, map, ctas, stream);
+    const cudaError_t e = p.head_dim == 512   ? launch_ranks<512>(p, ls, map, ctas, stream)
+                          : p.head_dim == 256 ? launch_ranks<256>(p, ls, map, ctas, stream)
+                                              : launch_ranks<128>(p, ls, map, ctas, stream);
     // a request of one column tile at most is never cut
     const int64_t most = (p.num_tokens + ls.tokens - 1) / ls.tokens * ls.head_groups;
     if (e != cudaSuccess || most <= 1) return e;
