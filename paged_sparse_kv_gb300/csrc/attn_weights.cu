@@ -24,7 +24,7 @@
 // their rows into a ring.  Eight worker warps bring records into shared memory by
 // asynchronous copies (32 rows and half the dims each, a copy of the next tile issued as
 // soon as a block of 64 dims is read), dequantise them and write them to tensor memory; one
-// thread fetches queries by TMA into a ring of 64-dim stages, four warps prepare the
+// warp fetches queries by TMA into a ring of 128-dim stages, four prepare the
 // columns' logarithms and bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
 // the column tile does not change (a decode batch: one column tile per request).
 // Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
@@ -47,7 +47,7 @@ constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kCol
               kPlanWarp = kMmaWarp + 1;
 constexpr int kThreads = (kPlanWarp + 1) * kWarp;
 constexpr int kTileCost = 1;
-constexpr int kMostStages = 24;
+constexpr int kMostStages = 12;
 constexpr int kColSlots = 3;
 constexpr int kTiles = 4;           // tiles the planning warp may be ahead
 constexpr int kMostBlocks = 8;      // 64-dim blocks of a row (head_dim 512)
@@ -107,7 +107,7 @@ struct LaunchShape {
     int32_t box_heads, box_tokens;  // of what a CTA fetches of it
     int32_t box_cols;             // columns of that, padded
     int32_t by_heads;             // two CTAs: they fetch the halves of the heads, else of the tokens
-    int32_t stages, stage_bytes;
+    int32_t stages, stage_bytes;  // stages of two boxes of 64 dims
     int32_t keep_queries;         // the ring holds a whole column tile
     int32_t stride[2];            // bytes of a staged row, by half
     float scale_log2;
@@ -560,6 +560,12 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             for (int i = 0; i < 4; ++i) copy16(dst + i * 8 * stride, row[first + i * 8].data + at + piece, 16);
         }
     };
+    const auto hand_over = [&](int block) {
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader<kPair>(&sh.k_full[block]);
+    };
     Tiles tiles;
     if (!tiles.wait(sh)) return false;
     if (tiles.at(sh).request < 0) return true;
@@ -582,9 +588,15 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             __syncwarp();
             uint32_t w[32];
             if (d < nope) {
+                uint4 raw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) raw[i] = lds_v4(at + i * 16);
+                __syncwarp();  // the block has been read: the next tile's copy may land there
+                if (more) fetch(tiles.at(sh), b);
+                copies_commit();
                 const uint32_t sc = ((block < 4 ? scales.x : scales.y) >> (8 * (block & 3))) & 0xFFu;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dequant16(lds_v4(at + i * 16), sc, w + 8 * i);
+                for (int i = 0; i < 4; ++i) dequant16(raw[i], sc, w + 8 * i);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -594,27 +606,26 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
                     w[4 * i + 2] = v.z;
                     w[4 * i + 3] = v.w;
                 }
+                __syncwarp();
+                if (more) fetch(tiles.at(sh), b);
+                copies_commit();
             }
-            __syncwarp();  // the block has been read: the next tile's copy may land there
-            if (more) fetch(tiles.at(sh), b);
-            copies_commit();
+            // the block before has had this one's time to be written
+            if (b > 0) hand_over(block - 1);
             if (step > 0 && !wait_all(&sh.k_free[block], (step - 1) & 1)) return false;
             tmem_fence_after();
             tmem_st32(tmem_k + ((uint32_t)(quad * kWarp) << 16) + block * 32, w);
-            tmem_wait_st();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_leader<kPair>(&sh.k_full[block]);
         }
+        hand_over(half * kBlocks + kBlocks - 1);
         if (!more) return true;
         tiles.next(sh);
         scales = next_scales;
     }
 }
 
-// The order in which blocks are multiplied: the halves' blocks in turn, as they come.
+// A stage of queries holds the dims of block `i` of each half, as the workers bring them.
 template <int D>
-__device__ __forceinline__ constexpr int block_at(int i) { return (i & 1) * (D / 128) + i / 2; }
+__device__ __forceinline__ constexpr int block_at(int i, int half) { return half * (D / 128) + i; }
 
 // ---- queries and columns ---------------------------------------------------------------------
 
@@ -633,39 +644,46 @@ __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map
             ::"r"(dst), "l"(reinterpret_cast<uint64_t>(&map)), "r"(d), "r"(h), "r"(t), "r"(smem_u32(bar)) : "memory");
 }
 
-// One thread fetches the queries.
+// Four lanes fetch the queries: a box each, of two stages.
+constexpr int kQueryLanes = 4;
+
 template <int D, bool kPair>
 __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring) {
-    constexpr int kBlocks = D / 64;
-    const uint32_t bytes = (uint32_t)(ls.box_heads * ls.box_tokens * 128) * (kPair ? 2 : 1);
+    constexpr int kStages = D / 128, kAtOnce = kStages > 1 ? 2 : 1;  // of a column tile; at a time
+    constexpr uint32_t kLanes = (1u << (2 * kAtOnce)) - 1;
+    const int lane = threadIdx.x % kWarp, half = lane & 1;
+    if (lane >= 2 * kAtOnce) return true;
+    const uint32_t bytes = (uint32_t)(ls.box_heads * ls.box_tokens * 128) * (kPair ? 4 : 2);
     const int rank = kPair ? (int)(blockIdx.x & 1) : 0;
     const int32_t from_t = ls.by_heads ? 0 : rank * ls.box_tokens, from_h = ls.by_heads ? rank * ls.box_heads : 0;
-    uint32_t stage = 0, round = 0;
+    uint32_t stage = lane / 2, round = 0, issued = lane / 2;  // this lane's next stage of all
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kTiles;
-        if (!mbar_poll_bounded(&sh.tile_full[slot], (n / kTiles) & 1, kWaitLimitNs)) {
-            ok = false;
-            break;
-        }
+        ok = __all_sync(kLanes, mbar_poll_bounded(&sh.tile_full[slot], (n / kTiles) & 1, kWaitLimitNs));
+        if (!ok) break;
         const Tile& tile = sh.tile[slot];
-        if (tile.request < 0) return true;
+        const bool end = tile.request < 0;
         const int32_t c1 = tile.c1, token0 = tile.token0 + tile.first * ls.tokens;
         int32_t c = tile.c0 + tile.kept;
-        mbar_arrive(&sh.tile_free[slot]);
+        __syncwarp(kLanes);
+        if (end) return true;
+        if (lane == 0) mbar_arrive(&sh.tile_free[slot]);
         int32_t group = c / ls.head_groups, part = c - group * ls.head_groups;
         for (; ok && c < c1; ++c) {
             const int32_t t = token0 + group * ls.tokens + from_t, h = part * ls.heads + from_h;
-#pragma unroll 1
-            for (int b = 0; b < kBlocks; ++b) {
-                if (round > 0 && !mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs)) {
-                    ok = false;
-                    break;
-                }
-                if (rank == 0) mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
-                tma_queries<kPair>(ring + stage * ls.stage_bytes, map, block_at<D>(b) * 64, h, t, &sh.q_full[stage]);
-                if (++stage == (uint32_t)ls.stages) {
-                    stage = 0;
+#pragma unroll
+            for (int i = 0; i < kStages; i += kAtOnce) {
+                const bool free = round == 0 || mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs);
+                ok = __all_sync(kLanes, free);
+                if (!ok) break;
+                if (half == 0 && rank == 0) mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
+                tma_queries<kPair>(ring + stage * ls.stage_bytes + half * (ls.stage_bytes / 2), map,
+                                   block_at<D>(i + lane / 2, half) * 64, h, t, &sh.q_full[stage]);
+                issued += kAtOnce;
+                stage += kAtOnce;
+                if (stage >= (uint32_t)ls.stages) {
+                    stage -= ls.stages;
                     ++round;
                 }
             }
@@ -677,13 +695,10 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
     }
     // a wait expired: copies in flight land before the CTA ends (the first CTA of a pair waits for
     // both, and they end together)
-    for (int i = 0; i < ls.stages && rank == 0; ++i) {
-        stage = (stage + ls.stages - 1) % ls.stages;
-        if (stage == (uint32_t)ls.stages - 1) {
-            if (round == 0) break;
-            --round;
-        }
-        mbar_poll_bounded(&sh.q_full[stage], round & 1, kWaitLimitNs / 8);
+    for (int i = 0; i < ls.stages && rank == 0; i += kAtOnce) {
+        if (issued < (uint32_t)(i + kAtOnce)) break;
+        const uint32_t x = issued - kAtOnce - i;
+        mbar_poll_bounded(&sh.q_full[x % ls.stages], (x / ls.stages) & 1, kWaitLimitNs / 8);
     }
     return false;
 }
@@ -833,7 +848,7 @@ __device__ __forceinline__ int32_t width_of(const LaunchShape& ls, int32_t token
 
 template <int D, bool kPair>
 __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s) {
-    constexpr int kBlocks = D / 64;
+    constexpr int kStages = D / 128;
     const uint32_t lead = elect_one();
     const uint64_t q_desc = umma_desc(ring, 16, 1024, kSwizzle128);
     const uint32_t stage_step = (uint32_t)ls.stage_bytes >> 4;
@@ -854,13 +869,17 @@ __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t
             if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
             uint32_t st = stage, rd = round;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const int block = block_at<D>(b);
-                if (c == c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
+            for (int i = 0; i < kStages; ++i) {
                 if (!wait_all(&sh.q_full[st], rd & 1)) return false;
-                tmem_fence_after();
-                umma_bf16_ts4<kPair>(d, tmem_k + block * 32, q_desc + st * stage_step, idesc, b > 0, lead);
-                if (last) commit<kPair>(&sh.k_free[block], lead);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int block = block_at<D>(i, half);
+                    if (c == c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
+                    tmem_fence_after();
+                    umma_bf16_ts4<kPair>(d, tmem_k + block * 32, q_desc + st * stage_step + half * (stage_step / 2), idesc,
+                                         i > 0 || half > 0, lead);
+                    if (last) commit<kPair>(&sh.k_free[block], lead);
+                }
                 if (!keep) commit<kPair>(&sh.q_free[st], lead);
                 if (++st == (uint32_t)ls.stages) {
                     st = 0;
@@ -1083,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kQueryWarp) {
         ok = columns(p, ls, sh);
     } else if (warp == kQueryWarp) {
-        if (lane == 0) ok = fetch_queries<D, kPair>(p, ls, map, sh, smem_u32(ring));
+        ok = fetch_queries<D, kPair>(p, ls, map, sh, smem_u32(ring));
         __syncwarp();
     } else if (warp == kPlanWarp) {
         ok = plan(p, ls, sh, from, to);
@@ -1208,13 +1227,13 @@ LaunchShape make_shape(const WeightParams& p) {
     const int first = mid <= nope ? mid : nope + 2 * (mid - nope);
     ls.stride[0] = first + 16;
     ls.stride[1] = p.head_dim + p.rope_dim - first + 16;
-    ls.stage_bytes = (ls.box_heads * ls.box_tokens + 15) / 16 * 16 * 128;
+    ls.stage_bytes = (ls.box_heads * ls.box_tokens + 15) / 16 * 16 * 128 * 2;
     const int room = kMostShared - (int)kAlign - 4 * kWarp * (ls.stride[0] + ls.stride[1]) - (int)sizeof(Shared);
     ls.stages = room / ls.stage_bytes;
     if (ls.stages > kMostStages) ls.stages = kMostStages;
-    const int most = 3 * p.head_dim / 64;
+    const int most = p.head_dim == 128 ? 4 : 3 * p.head_dim / 128;
     if (ls.stages > most) ls.stages = most;
-    ls.keep_queries = ls.stages >= p.head_dim / 64;
+    ls.keep_queries = ls.stages >= p.head_dim / 128;
     return ls;
 }
 
