@@ -21,11 +21,11 @@
 // sums written to the workspace; a second kernel adds them up in order.
 //
 // Roles.  One warp plans: it walks the CTA's range and puts tiles with the addresses of
-// their rows into a ring.  Eight worker warps bring records into shared memory by
-// asynchronous copies (32 rows and half the dims each, a copy of the next tile issued as
+// their rows into a ring.  Worker warps bring records into shared memory by
+// asynchronous copies (32 rows and a part of the dims each, a copy of the next tile issued as
 // soon as a block of 64 dims is read), dequantise them and write them to tensor memory; one
 // warp fetches queries by TMA into a ring of 128-dim stages, four prepare the
-// columns' logarithms and bounds; one issues the MMAs; eight turn scores into sums.  Queries stay in the ring while
+// columns' logarithms and bounds; one issues the MMAs; others turn scores into sums.  Queries stay in the ring while
 // the column tile does not change (a decode batch: one column tile per request).
 // Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
 #include <cuda.h>
@@ -42,15 +42,24 @@ namespace {
 
 constexpr int kTile = 128;          // rows of a CTA's part of a tile
 constexpr int kCols = 128;          // columns of a column tile, at most
-constexpr int kWorkers = 8, kSummers = 8, kColumnWarps = kCols / kWarp;
-constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps, kMmaWarp = kQueryWarp + 1,
-              kPlanWarp = kMmaWarp + 1;
-constexpr int kThreads = (kPlanWarp + 1) * kWarp;
+// Warps by role.  A CTA of its own has few columns per row and many tiles: 16 warps
+// dequantise and 4 sum up; a pair has many columns: 8 and 8.
+template <int kHeadDim, bool kTwo>
+struct Roles {
+    static constexpr int D = kHeadDim;
+    static constexpr bool kPair = kTwo;
+    static constexpr int kWorkers = kPair || D == 128 ? 8 : 16, kParts = kWorkers / 4;  // each has D / kParts dims
+    static constexpr int kSummers = kPair ? 8 : 4, kShares = kSummers / 4;              // of the columns
+    static constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kCols / kWarp;
+    static constexpr int kMmaWarp = kQueryWarp + 1, kPlanWarp = kMmaWarp + 1;
+    static constexpr int kThreads = (kPlanWarp + 1) * kWarp;
+};
+constexpr int kMostParts = 4, kMostWarps = 32;
 constexpr int kTileCost = 1;
 constexpr int kMostStages = 12;
 constexpr int kColSlots = 3;
 constexpr int kTiles = 4;           // tiles the planning warp may be ahead
-constexpr int kMostBlocks = 8;      // 64-dim blocks of a row (head_dim 512)
+constexpr int kMostBlocks = 4;      // 64-dim blocks of a part
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -99,17 +108,36 @@ struct Tile {
     Row row[kTile];
 };
 
+// Division of n in [0, 2^31) by a divisor fixed for the call: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1 the quotient is (hi(n m) + n) >> s.
+struct Divisor {
+    uint32_t mul, shift;
+};
+
+__device__ __forceinline__ int32_t divide(int32_t n, Divisor d) {
+    return (int32_t)(((uint64_t)__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
+}
+
+Divisor divisor(int32_t d) {
+    Divisor x{0, 0};
+    while ((1ll << x.shift) < d) ++x.shift;
+    x.mul = (uint32_t)((((1ull << x.shift) - (uint64_t)d) << 32) / (uint64_t)d + 1);
+    return x;
+}
+
 struct LaunchShape {
     int32_t ranks;                // CTAs that share a tile, 1 or 2
     int32_t row_shift;            // log2 of a tile's rows
     int32_t heads, tokens;        // of a column tile
     int32_t head_groups;
+    Divisor by_tokens, by_groups; // of those two
     int32_t box_heads, box_tokens;  // of what a CTA fetches of it
     int32_t box_cols;             // columns of that, padded
     int32_t by_heads;             // two CTAs: they fetch the halves of the heads, else of the tokens
+    int32_t staging_bytes;
     int32_t stages, stage_bytes;  // stages of two boxes of 64 dims
     int32_t keep_queries;         // the ring holds a whole column tile
-    int32_t stride[2];            // bytes of a staged row, by half
+    int32_t stride[kMostParts];   // bytes of a staged row, by part of the dims
     float scale_log2;
     float* parts;                 // [CTA][2][kTile]
     Record* records;              // [CTA]
@@ -120,13 +148,13 @@ struct Shared {
     Columns columns[kColSlots];
     float half_sum[4][2][kWarp];  // second half of a quad's columns: sum and compensation
     uint64_t tile_full[kTiles], tile_free[kTiles];
-    uint64_t k_full[kMostBlocks], k_free[kMostBlocks];
+    uint64_t k_full[kMostBlocks], k_free[kMostBlocks];  // by number of the block in its part
     uint64_t q_full[kMostStages], q_free[kMostStages];
     uint64_t col_full[kColSlots], col_free[kColSlots];
     uint64_t s_full[2], s_free[2];
     uint64_t half_full[4], half_free[4];
     uint64_t drain;
-    int64_t scan[kThreads / kWarp];
+    int64_t scan[kMostWarps];
     int64_t first_at;             // where the CTA's range starts: prefix of that request
     int32_t first_request;
     uint32_t tmem;
@@ -166,8 +194,8 @@ __device__ __forceinline__ void column_tiles(const WeightParams& p, const Launch
         const int64_t b = row + (1 << ls.row_shift) - 1 + p.window - q.row0;
         if (b < i1) i1 = b > i0 ? (int32_t)b : i0;
     }
-    first = i0 / ls.tokens;
-    groups = i1 > i0 ? (i1 + ls.tokens - 1) / ls.tokens - first : 0;
+    first = divide(i0, ls.by_tokens);
+    groups = i1 > i0 ? divide(i1 - 1, ls.by_tokens) + 1 - first : 0;
 }
 
 // The first `count` tiles of a request that cost the same, and that cost.  The others are
@@ -181,7 +209,7 @@ __device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchSh
     } else {             // tiles all tokens see
         const int64_t x = (int64_t)q.row0 + min(ls.tokens, q.tokens) - 1;
         n = (x >> ls.row_shift) + 1;
-        cost = kTileCost + (int64_t)((q.tokens + ls.tokens - 1) / ls.tokens) * ls.head_groups;
+        cost = kTileCost + (int64_t)(q.tokens > 0 ? divide(q.tokens - 1, ls.by_tokens) + 1 : 0) * ls.head_groups;
     }
     count = n < 0 || q.tokens == 0 ? 0 : n > tiles ? tiles : (int32_t)n;
     if (q.tokens == 0) {
@@ -225,46 +253,52 @@ __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const La
     return sum;
 }
 
-// A CTA's walk over its range of the sequence.
+// A walk over the tiles of a range of the sequence.
 struct Walk {
     int64_t from, to;        // the range
     int64_t at;              // place of the current tile in the sequence
-    int32_t r, k;            // request and tile; r == num_reqs: past the end
+    int32_t r, k, tiles;     // request and tile; r < 0: past the end; tiles of the request
     int32_t first, total;    // its token groups start at `first`; its column tiles
     int32_t c0, c1;          // those of them in the range
-    int32_t tiles, even;     // of the request; how many in front are alike
     Request q;
 
     __device__ __forceinline__ bool done() const { return r < 0; }
 
-    // Takes up request r; returns what one of its even tiles costs.
-    __device__ __forceinline__ int64_t request(const WeightParams& p, const LaunchShape& ls) {
-        q = load_request(p, r);
-        tiles = tiles_of(ls, q);
-        int64_t cost;
-        even_tiles(p, ls, q, tiles, even, cost);
-        return cost;
-    }
-    // Moves on to the next tile of which something lies in the range, the current one included.
-    __device__ void settle(const WeightParams& p, const LaunchShape& ls) {
+    // Moves to the next tile of which something lies in the range; from a `tiles` of -1 to the
+    // first, which lies in request r at place `at` or behind it.
+    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
+        if (tiles >= 0) {
+            at += kTileCost + total;
+            ++k;
+        }
         for (;;) {
-            while (k >= tiles) {
-                if (++r >= p.num_reqs || at >= to) {
-                    r = -1;
-                    return;
-                }
-                k = 0;
-                request(p, ls);
-            }
             if (at >= to) {
                 r = -1;
                 return;
             }
-            if (k >= even || k == 0) {  // before `even` tiles are alike
-                int32_t groups;
-                column_tiles(p, ls, q, k, first, groups);
-                total = groups * ls.head_groups;
+            if (k >= tiles) {
+                if (tiles >= 0 && ++r >= p.num_reqs) {
+                    r = -1;
+                    return;
+                }
+                const bool first_of_all = tiles < 0;
+                q = load_request(p, r);
+                tiles = tiles_of(ls, q);
+                k = 0;
+                if (first_of_all) {
+                    int32_t even;
+                    int64_t cost;
+                    even_tiles(p, ls, q, tiles, even, cost);
+                    const int64_t ahead = from - at;
+                    const int64_t skip = (ahead | cost) >> 32 == 0 ? (int64_t)((uint32_t)ahead / (uint32_t)cost) : ahead / cost;
+                    k = skip < even ? (int32_t)skip : even;
+                    at += cost * k;
+                }
+                continue;
             }
+            int32_t groups;
+            column_tiles(p, ls, q, k, first, groups);
+            total = groups * ls.head_groups;
             const int64_t a = from - at - kTileCost, b = to - at - kTileCost;
             c0 = a > 0 ? (int32_t)(a < total ? a : total) : 0;
             c1 = b > 0 ? (int32_t)(b < total ? b : total) : 0;
@@ -273,88 +307,57 @@ struct Walk {
             ++k;
         }
     }
-    __device__ void start(const WeightParams& p, const LaunchShape& ls, const Shared& sh, int64_t from_, int64_t to_) {
-        from = from_;
-        to = to_;
-        r = sh.first_request;
-        at = sh.first_at;
-        k = 0;
-        if (from >= to) {
-            r = -1;
-            return;
-        }
-        const int64_t cost = request(p, ls), skip = (from - at) / cost;
-        k = skip < even ? (int32_t)skip : even;
-        at += cost * k;
-        if (k > 0 && k < even) {
-            int32_t groups;
-            column_tiles(p, ls, q, k, first, groups);
-            total = groups * ls.head_groups;
-        }
-        settle(p, ls);
-    }
-    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
-        at += kTileCost + total;
-        ++k;
-        settle(p, ls);
-    }
-    // Whether the first column tile of `x` is the last one of this tile.
-    __device__ __forceinline__ bool same_columns(const LaunchShape& ls, const Walk& x) const {
-        return ls.keep_queries && !x.done() && x.r == r && x.total > 0 &&
-               first * ls.head_groups + c1 - 1 == x.first * ls.head_groups + x.c0;
-    }
 };
 
-// Sum over the CTA, the same in all threads.
-__device__ int64_t block_sum(Shared& sh, int64_t v) {
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if (lane == 0) sh.scan[warp] = v;
-    __syncthreads();
-    int64_t sum = 0;
-    for (int i = 0; i < kThreads / kWarp; ++i) sum += sh.scan[i];
-    return sum;
-}
-
 // The CTA's range of the sequence, and the request it starts in (sh.first_*).
+template <int kThreads>
 __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t& from, int64_t& to) {
+    constexpr int kWarps = kThreads / kWarp;
     const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
-    int64_t mine = 0, cost = 0;
-    for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
-        if (r0 + warp * kWarp >= p.num_reqs) break;
-        cost = request_costs(p, ls, r0 + tid);
-        mine += cost;
-    }
-    const int64_t all = block_sum(sh, mine);
-    const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
-    from = all / n * b + all % n * b / n;
-    to = all / n * (b + 1) + all % n * (b + 1) / n;
     if (tid == 0) {
         sh.first_request = 0;
         sh.first_at = 0;
     }
-    int64_t before = 0;
-    for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
-        if (p.num_reqs > kThreads) cost = r0 + warp * kWarp < p.num_reqs ? request_costs(p, ls, r0 + tid) : 0;
-        int64_t sum = cost;
-        for (int o = 1; o < kWarp; o *= 2) {
-            const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += x;
+    from = to = 0;
+    int64_t cost = 0;
+    // once for the sum of all costs, once for the places (one code: it is in the cache then)
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t before = 0;
+#pragma unroll 1
+        for (int32_t r0 = 0; r0 < p.num_reqs; r0 += kThreads) {
+            if (pass == 0 || p.num_reqs > kThreads)
+                cost = r0 + warp * kWarp < p.num_reqs ? request_costs(p, ls, r0 + tid) : 0;
+            int64_t sum = cost;
+#pragma unroll
+            for (int o = 1; o < kWarp; o *= 2) {
+                const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            __syncthreads();
+            if (lane == kWarp - 1) sh.scan[warp] = sum;
+            __syncthreads();
+            int64_t below = lane < warp ? sh.scan[lane] : 0, all = lane < kWarps ? sh.scan[lane] : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
+                all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            }
+            const int64_t at = before + below + sum - cost;
+            if (pass == 1 && at <= from && from < at + cost) {
+                sh.first_request = r0 + tid;
+                sh.first_at = at;
+            }
+            before += all;
         }
-        __syncthreads();
-        if (lane == kWarp - 1) sh.scan[warp] = sum;
-        __syncthreads();
-        int64_t at = before + sum - cost;
-        for (int i = 0; i < kThreads / kWarp; ++i) {
-            if (i < warp) at += sh.scan[i];
-            before += sh.scan[i];
+        if (pass == 0) {
+            const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
+            const auto share = [&](int64_t i) {
+                return before >> 40 == 0 ? before * i / n : before / n * i + before % n * i / n;
+            };
+            from = share(b);
+            to = share(b + 1);
         }
-        if (at <= from && from < at + cost) {
-            sh.first_request = r0 + tid;
-            sh.first_at = at;
-        }
-        if (before > from) break;
     }
     __syncthreads();
 }
@@ -376,88 +379,95 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
     const int lane = threadIdx.x % kWarp;
     const int64_t token_stride = p.head_dim + p.rope_dim;
     const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
-    Walk cur, nxt;
-    int32_t page[kPer], ahead[kPer];
     // row i * 32 + lane of this CTA's part of the tile
     const int32_t mine = (int32_t)(blockIdx.x % ls.ranks) * kTile + lane;
     const auto row_at = [&](const Walk& x, int i) { return (int32_t)min(((int64_t)x.k << ls.row_shift) + mine + i * kWarp, (int64_t)INT32_MAX); };
-    const auto lookup = [&](const Walk& x, int32_t(&to)[kPer]) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) to[i] = x.done() ? -1 : page_of(p, x.r, x.q, row_at(x, i));
-    };
-    // Tiles no token sees rows of are dealt with here.
-    const auto skip_empty = [&](Walk& x) {
-        for (; !x.done() && x.total == 0; x.next(p, ls)) {
+    Walk w{}, x{};  // where the walk stands, and the tile before, which is to be published
+    w.from = from;
+    w.to = to;
+    w.at = sh.first_at;
+    w.r = sh.first_request;
+    w.tiles = -1;
+    x.r = -1;
+    int32_t page[kPer];  // of x
+    bool kept = false, started = false;
+    for (uint32_t n = 0;;) {
+        // on to the next tile with columns; those no token sees rows of are dealt with here
+        for (;;) {
+            w.next(p, ls);
+            if (!started) {
+                started = true;
+                if (lane == 0) {
+                    Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
+                    if (!w.done() && w.c0 > 0) rec = {w.c1 == w.total ? kEnds : kMiddle, w.r, w.k, 0};
+                    ls.records[blockIdx.x] = rec;
+                }
+            }
+            if (w.done() || w.total > 0) break;
             if (p.decay == 1.0f && p.out == p.weights) continue;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < kPer; ++i) {
-                const int32_t j = row_at(x, i);
-                if (j >= x.q.end) continue;
-                const float old = p.decay == 0.0f ? 0.0f : p.decay * p.weights[(int64_t)x.r * p.w_stride + j];
-                p.out[(int64_t)x.r * p.out_stride + j] = old;
+                const int32_t j = row_at(w, i);
+                if (j >= w.q.end) continue;
+                const float old = p.decay == 0.0f ? 0.0f : p.decay * p.weights[(int64_t)w.r * p.w_stride + j];
+                p.out[(int64_t)w.r * p.out_stride + j] = old;
             }
         }
-    };
-    cur.start(p, ls, sh, from, to);
-    skip_empty(cur);
-    if (lane == 0) {
-        Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
-        if (!cur.done() && cur.c0 > 0) rec = {cur.c1 == cur.total ? kEnds : kMiddle, cur.r, cur.k, 0};
-        ls.records[blockIdx.x] = rec;
-    }
-    lookup(cur, page);
-    bool kept = false;
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t slot = n % kTiles;
-        Tile& t = sh.tile[slot];
-        if (n >= kTiles && !wait_all(&sh.tile_free[slot], (n / kTiles - 1) & 1)) return false;
-        if (cur.done()) {
+        if (!x.done()) {
+            const uint32_t slot = n % kTiles;
+            if (n >= kTiles && !wait_all(&sh.tile_free[slot], (n / kTiles - 1) & 1)) return false;
+            Tile& t = sh.tile[slot];
+            // the first column tile of the walk's tile is the last of this one
+            const bool keeps = ls.keep_queries && w.r == x.r &&
+                               x.first * ls.head_groups + x.c1 - 1 == w.first * ls.head_groups + w.c0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                Row row{zero, zero};
+                if (page[i] >= 0) {
+                    int32_t off;
+                    div_block32(row_at(x, i), p.cache.block_size, p.cache.shift, off);
+                    const uint8_t* pg = p.cache.base + (int64_t)page[i] * p.cache.page_stride;
+                    row.data = pg + off * token_stride;
+                    row.scales = pg + p.cache.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
+                }
+                t.row[i * kWarp + lane] = row;
+                const uint32_t there = __ballot_sync(0xFFFFFFFFu, page[i] >= 0);
+                if (lane == 0) t.there[i] = there;
+            }
             if (lane == 0) {
-                t.request = -1;
+                t.request = x.r;
+                t.tile = x.k;
+                t.first_row = row_at(x, 0);  // lane 0's
+                t.end = x.q.end;
+                t.first = x.first;
+                t.total = x.total;
+                t.c0 = x.c0;
+                t.c1 = x.c1;
+                t.tokens = x.q.tokens;
+                t.token0 = x.q.token0;
+                t.row0 = x.q.row0;
+                t.replay = x.q.replay;
+                t.kept = kept;
+                t.keeps = keeps;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.tile_full[slot]);
+            kept = keeps;
+            ++n;
+        }
+        if (w.done()) {
+            const uint32_t slot = n % kTiles;
+            if (n >= kTiles && !wait_all(&sh.tile_free[slot], (n / kTiles - 1) & 1)) return false;
+            if (lane == 0) {
+                sh.tile[slot].request = -1;
                 mbar_arrive(&sh.tile_full[slot]);
             }
             return true;
         }
-        nxt = cur;
-        nxt.next(p, ls);
-        skip_empty(nxt);
-        lookup(nxt, ahead);
-        const bool keeps = cur.same_columns(ls, nxt);
+        x = w;
+        // in flight until these rows are published
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            Row row{zero, zero};
-            if (page[i] >= 0) {
-                int32_t off;
-                div_block32(row_at(cur, i), p.cache.block_size, p.cache.shift, off);
-                const uint8_t* pg = p.cache.base + (int64_t)page[i] * p.cache.page_stride;
-                row.data = pg + off * token_stride;
-                row.scales = pg + p.cache.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
-            }
-            t.row[i * kWarp + lane] = row;
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, page[i] >= 0);
-            if (lane == 0) t.there[i] = there;
-            page[i] = ahead[i];
-        }
-        if (lane == 0) {
-            t.request = cur.r;
-            t.tile = cur.k;
-            t.first_row = row_at(cur, 0);  // lane 0's
-            t.end = cur.q.end;
-            t.first = cur.first;
-            t.total = cur.total;
-            t.c0 = cur.c0;
-            t.c1 = cur.c1;
-            t.tokens = cur.q.tokens;
-            t.token0 = cur.q.token0;
-            t.row0 = cur.q.row0;
-            t.replay = cur.q.replay;
-            t.kept = kept;
-            t.keeps = keeps;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.tile_full[slot]);
-        kept = keeps;
-        cur = nxt;
+        for (int i = 0; i < kPer; ++i) page[i] = page_of(p, x.r, x.q, row_at(x, i));
     }
 }
 
@@ -519,18 +529,20 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         mbar_arrive(bar);
 }
 
-// A worker warp has the rows 32 * quad ... of each tile and the dims of one half.  Records
+// A worker warp has the rows 32 * quad ... of each tile and the dims of one part.  Records
 // stand in its part of shared memory with a row stride that is an odd number of 16 bytes,
 // so that lanes reading 16 bytes of their own rows hit different banks.
-template <int D, bool kPair>
+template <class R>
 __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t staging, uint32_t tmem_k) {
-    constexpr int kBlocks = D / 128;  // 64-dim blocks of a half
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, quad = warp % 4, half = warp / 4;
+    constexpr int D = R::D, kBlocks = D / 64 / R::kParts;  // 64-dim blocks of a part
+    constexpr bool kPair = R::kPair;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp, quad = warp % 4, part = warp / 4;
     const int nope = D - p.rope_dim;
-    const int d0 = half * (D / 2);
+    const int d0 = part * (D / R::kParts);
     const auto byte_of = [&](int d) { return d <= nope ? d : nope + 2 * (d - nope); };
-    const int stride = ls.stride[half], byte0 = byte_of(d0);
-    const uint32_t mine = staging + (half ? 4 * kWarp * ls.stride[0] : 0) + quad * kWarp * stride;
+    const int stride = ls.stride[part], byte0 = byte_of(d0);
+    uint32_t mine = staging + quad * kWarp * stride;
+    for (int i = 0; i < part; ++i) mine += 4 * kWarp * ls.stride[i];
     const uint32_t own = mine + lane * stride;
 
     const auto load_scales = [&](const uint8_t* at) {
@@ -560,11 +572,11 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             for (int i = 0; i < 4; ++i) copy16(dst + i * 8 * stride, row[first + i * 8].data + at + piece, 16);
         }
     };
-    const auto hand_over = [&](int block) {
+    const auto hand_over = [&](int b) {
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader<kPair>(&sh.k_full[block]);
+        if (lane == 0) arrive_leader<kPair>(&sh.k_full[b]);
     };
     Tiles tiles;
     if (!tiles.wait(sh)) return false;
@@ -582,7 +594,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
         if (more) next_scales = load_scales(tiles.at(sh).row[quad * kWarp + lane].scales);
 #pragma unroll 1
         for (int b = 0; b < kBlocks; ++b) {
-            const int d = d0 + b * 64, block = half * kBlocks + b;
+            const int d = d0 + b * 64, block = part * kBlocks + b;
             const uint32_t at = own + byte_of(d) - byte0;
             copies_wait<kBlocks - 1>();
             __syncwarp();
@@ -611,21 +623,24 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
                 copies_commit();
             }
             // the block before has had this one's time to be written
-            if (b > 0) hand_over(block - 1);
-            if (step > 0 && !wait_all(&sh.k_free[block], (step - 1) & 1)) return false;
+            if (b > 0) hand_over(b - 1);
+            if (step > 0 && !wait_all(&sh.k_free[b], (step - 1) & 1)) return false;
             tmem_fence_after();
             tmem_st32(tmem_k + ((uint32_t)(quad * kWarp) << 16) + block * 32, w);
         }
-        hand_over(half * kBlocks + kBlocks - 1);
+        hand_over(kBlocks - 1);
         if (!more) return true;
         tiles.next(sh);
         scales = next_scales;
     }
 }
 
-// A stage of queries holds the dims of block `i` of each half, as the workers bring them.
-template <int D>
-__device__ __forceinline__ constexpr int block_at(int i, int half) { return half * (D / 128) + i; }
+// The block of 64 dims in half `half` of stage `i`: the parts' blocks in turn, as they come.
+template <class R>
+__device__ __forceinline__ constexpr int block_at(int i, int half) {
+    const int n = 2 * i + half;
+    return n % R::kParts * (R::D / 64 / R::kParts) + n / R::kParts;
+}
 
 // ---- queries and columns ---------------------------------------------------------------------
 
@@ -645,11 +660,10 @@ __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap& map
 }
 
 // Four lanes fetch the queries: a box each, of two stages.
-constexpr int kQueryLanes = 4;
-
-template <int D, bool kPair>
+template <class R>
 __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, Shared& sh, uint32_t ring) {
-    constexpr int kStages = D / 128, kAtOnce = kStages > 1 ? 2 : 1;  // of a column tile; at a time
+    constexpr bool kPair = R::kPair;
+    constexpr int kStages = R::D / 128, kAtOnce = kStages > 1 ? 2 : 1;  // of a column tile; at a time
     constexpr uint32_t kLanes = (1u << (2 * kAtOnce)) - 1;
     const int lane = threadIdx.x % kWarp, half = lane & 1;
     if (lane >= 2 * kAtOnce) return true;
@@ -669,17 +683,17 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
         __syncwarp(kLanes);
         if (end) return true;
         if (lane == 0) mbar_arrive(&sh.tile_free[slot]);
-        int32_t group = c / ls.head_groups, part = c - group * ls.head_groups;
+        int32_t group = divide(c, ls.by_groups), part = c - group * ls.head_groups;
         for (; ok && c < c1; ++c) {
             const int32_t t = token0 + group * ls.tokens + from_t, h = part * ls.heads + from_h;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < kStages; i += kAtOnce) {
                 const bool free = round == 0 || mbar_poll_bounded(&sh.q_free[stage], (round - 1) & 1, kWaitLimitNs);
                 ok = __all_sync(kLanes, free);
                 if (!ok) break;
                 if (half == 0 && rank == 0) mbar_arrive_expect_tx(&sh.q_full[stage], bytes);
                 tma_queries<kPair>(ring + stage * ls.stage_bytes + half * (ls.stage_bytes / 2), map,
-                                   block_at<D>(i + lane / 2, half) * 64, h, t, &sh.q_full[stage]);
+                                   block_at<R>(i + lane / 2, half) * 64, h, t, &sh.q_full[stage]);
                 issued += kAtOnce;
                 stage += kAtOnce;
                 if (stage >= (uint32_t)ls.stages) {
@@ -705,8 +719,9 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
 
 // The logarithms and bounds of the columns, one a thread.  The next column tile's lse is in
 // flight while this one's is worked on.
+template <class R>
 __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh) {
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kColumnWarp, col = warp * kWarp + lane;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - R::kColumnWarp, col = warp * kWarp + lane;
     const int32_t rank = col / ls.box_cols, at = col - rank * ls.box_cols;
     const int32_t token = at / ls.box_heads + (ls.by_heads ? 0 : rank * ls.box_tokens);
     const int32_t head = at % ls.box_heads + (ls.by_heads ? rank * ls.box_heads : 0);
@@ -747,7 +762,7 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
             token0 = t.token0;
             row0 = t.row0;
             replay = t.replay;
-            group = c / ls.head_groups;
+            group = divide(c, ls.by_groups);
             part = c - group * ls.head_groups;
             group += t.first;
             tiles.next(sh);
@@ -846,9 +861,10 @@ __device__ __forceinline__ int32_t width_of(const LaunchShape& ls, int32_t token
     return kPair ? 2 * ls.box_cols : (min(ls.tokens, tokens - group * ls.tokens) * ls.heads + 15) / 16 * 16;
 }
 
-template <int D, bool kPair>
+template <class R>
 __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t tmem_k, uint32_t tmem_s) {
-    constexpr int kStages = D / 128;
+    constexpr bool kPair = R::kPair;
+    constexpr int kStages = R::D / 128;
     const uint32_t lead = elect_one();
     const uint64_t q_desc = umma_desc(ring, 16, 1024, kSwizzle128);
     const uint32_t stage_step = (uint32_t)ls.stage_bytes >> 4;
@@ -862,24 +878,25 @@ __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t
         const bool keeps = t.keeps;
         tiles.next(sh);
         if (kPair && (blockIdx.x & 1)) continue;  // the first CTA of a pair issues
-        int32_t group = c0 / ls.head_groups, part = c0 - group * ls.head_groups;
+        int32_t group = divide(c0, ls.by_groups), part = c0 - group * ls.head_groups;
         for (int32_t c = c0; c < c1; ++c, ++step) {
             const bool last = c == c1 - 1, keep = last && keeps;
             const uint32_t idesc = umma_idesc(kTile * (kPair ? 2 : 1), width_of<kPair>(ls, tokens, first + group), false), d = tmem_s + (step & 1) * kCols;
             if (step >= 2 && !wait_all(&sh.s_free[step & 1], (step / 2 - 1) & 1)) return false;
             uint32_t st = stage, rd = round;
-#pragma unroll
+            // not unrolled: in a batch of single tokens each warp passes its code once a tile,
+            // and what is long has left the instruction cache by then
+#pragma unroll 1
             for (int i = 0; i < kStages; ++i) {
+                const int b = 2 * i / R::kParts;  // which blocks of the parts
+                if (c == c0 && 2 * i % R::kParts == 0 && !wait_all(&sh.k_full[b], tile & 1)) return false;
                 if (!wait_all(&sh.q_full[st], rd & 1)) return false;
+                tmem_fence_after();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int block = block_at<D>(i, half);
-                    if (c == c0 && !wait_all(&sh.k_full[block], tile & 1)) return false;
-                    tmem_fence_after();
-                    umma_bf16_ts4<kPair>(d, tmem_k + block * 32, q_desc + st * stage_step + half * (stage_step / 2), idesc,
-                                         i > 0 || half > 0, lead);
-                    if (last) commit<kPair>(&sh.k_free[block], lead);
-                }
+                for (int half = 0; half < 2; ++half)
+                    umma_bf16_ts4<kPair>(d, tmem_k + block_at<R>(i, half) * 32, q_desc + st * stage_step + half * (stage_step / 2),
+                                         idesc, i > 0 || half > 0, lead);
+                if (last && (2 * i + 2) % R::kParts == 0) commit<kPair>(&sh.k_free[b], lead);
                 if (!keep) commit<kPair>(&sh.q_free[st], lead);
                 if (++st == (uint32_t)ls.stages) {
                     st = 0;
@@ -911,9 +928,10 @@ struct Sum {
     }
 };
 
-template <bool kPair>
+template <class R>
 __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s) {
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - kWorkers, quad = warp % 4, half = warp / 4;
+    constexpr bool kPair = R::kPair;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - R::kWorkers, quad = warp % 4, half = warp / 4;
     const uint32_t lane_base = tmem_s + ((uint32_t)(quad * kWarp) << 16);
     uint32_t step = 0, seq = 0, tile = 0;
     bool loaded = false;
@@ -932,7 +950,7 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
         float old = 0.0f;
         if (p.decay != 0.0f && in && half == 0 && whole) old = p.weights[(int64_t)request * p.w_stride + j];
         Sum sum;
-        int32_t group = c0 / ls.head_groups, part_of = c0 - group * ls.head_groups;
+        int32_t group = divide(c0, ls.by_groups), part_of = c0 - group * ls.head_groups;
         for (int32_t c = c0; c < c1; ++c, ++step) {
             const int32_t n = width_of<kPair>(ls, tokens, first + group);
             if (loaded) {
@@ -950,31 +968,23 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             const uint32_t s_at = lane_base + (step & 1) * kCols;
             float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-            for (int32_t n0 = half * 32; n0 < n; n0 += 64) {
-                float s[32];
-                tmem_ld<32>(s_at + n0, s);
-                const int32_t used = n0 == 0 ? used4.x : n0 == 32 ? used4.y : n0 == 64 ? used4.z : used4.w;
-                if (rows && used == -1) {
+            for (int32_t n0 = half * 16; n0 < n; n0 += 16 * R::kShares) {
+                float s[16];
+                tmem_ld<16>(s_at + n0, s);
+                const int32_t word = n0 < 32 ? used4.x : n0 < 64 ? used4.y : n0 < 96 ? used4.z : used4.w;
+                const uint32_t used = ((uint32_t)word >> (n0 & 16)) & 0xFFFFu;
+                if (rows && used == 0xFFFFu) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
+                    for (int k = 0; k < 16; k += 4) {
                         const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
                         part[0] += ex2_approx(fmaf(s[k], ls.scale_log2, -x.x));
                         part[1] += ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y));
                         part[2] += ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z));
                         part[3] += ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w));
                     }
-                } else if (rows) {  // the columns in use see all rows
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
-                        part[0] += used >> k & 1 ? ex2_approx(fmaf(s[k], ls.scale_log2, -x.x)) : 0.0f;
-                        part[1] += used >> (k + 1) & 1 ? ex2_approx(fmaf(s[k + 1], ls.scale_log2, -x.y)) : 0.0f;
-                        part[2] += used >> (k + 2) & 1 ? ex2_approx(fmaf(s[k + 2], ls.scale_log2, -x.z)) : 0.0f;
-                        part[3] += used >> (k + 3) & 1 ? ex2_approx(fmaf(s[k + 3], ls.scale_log2, -x.w)) : 0.0f;
-                    }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
+                    for (int k = 0; k < 16; k += 4) {
                         const float4 x = *reinterpret_cast<const float4*>(&co.log[n0 + k]);
                         const int4 lo = *reinterpret_cast<const int4*>(&co.lo[n0 + k]);
                         const int4 hi = *reinterpret_cast<const int4*>(&co.hi[n0 + k]);
@@ -1008,11 +1018,13 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.half_full[quad]);
         } else {
-            if (!wait_all(&sh.half_full[quad], tile & 1)) return false;
-            sum.add(sh.half_sum[quad][0][lane]);
-            sum.add(-sh.half_sum[quad][1][lane]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.half_free[quad]);
+            if constexpr (R::kShares == 2) {
+                if (!wait_all(&sh.half_full[quad], tile & 1)) return false;
+                sum.add(sh.half_sum[quad][0][lane]);
+                sum.add(-sh.half_sum[quad][1][lane]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.half_free[quad]);
+            }
             const float total = sum.hi - sum.lo;
             if (whole) {
                 if (in) p.out[out_at] = p.decay == 0.0f ? total : fmaf(p.decay, old, total);
@@ -1043,14 +1055,17 @@ __device__ __forceinline__ void free_tmem(uint32_t addr) {
         tmem_dealloc(addr, 512);
 }
 
-template <int D, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1)
+template <class R>
+__global__ void __launch_bounds__(R::kThreads, 1)
     attn_weights_kernel(const __grid_constant__ WeightParams p, const __grid_constant__ LaunchShape ls,
                         const __grid_constant__ CUtensorMap map) {
+    constexpr bool kPair = R::kPair;
+    constexpr int kWorkers = R::kWorkers, kColumnWarp = R::kColumnWarp, kQueryWarp = R::kQueryWarp, kPlanWarp = R::kPlanWarp;
+    constexpr int kMmaWarp = R::kMmaWarp;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((kAlign - (smem_u32(smem_raw) & (kAlign - 1))) & (kAlign - 1));
     uint8_t* staging = ring + ls.stages * ls.stage_bytes;
-    Shared& sh = *reinterpret_cast<Shared*>(staging + 4 * kWarp * (ls.stride[0] + ls.stride[1]));
+    Shared& sh = *reinterpret_cast<Shared*>(staging + ls.staging_bytes);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 
     if (threadIdx.x == 0) {
@@ -1059,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.tile_free[i], kPlanWarp);  // every other warp
         }
         for (int i = 0; i < kMostBlocks; ++i) {
-            mbar_init(&sh.k_full[i], kPair ? 8 : 4);
+            mbar_init(&sh.k_full[i], (kPair ? 2 : 1) * kWorkers);
             mbar_init(&sh.k_free[i], 1);
         }
         for (int i = 0; i < kMostStages; ++i) {
@@ -1067,12 +1082,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.q_free[i], 1);
         }
         for (int i = 0; i < kColSlots; ++i) {
-            mbar_init(&sh.col_full[i], kColumnWarps);
-            mbar_init(&sh.col_free[i], kSummers);
+            mbar_init(&sh.col_full[i], kCols / kWarp);
+            mbar_init(&sh.col_free[i], R::kSummers);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], kPair ? 2 * kSummers : kSummers);
+            mbar_init(&sh.s_free[i], kPair ? 2 * R::kSummers : R::kSummers);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.half_full[i], 1);
@@ -1091,23 +1106,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     int64_t from, to;
-    find_range(p, ls, sh, from, to);
+    find_range<R::kThreads>(p, ls, sh, from, to);
 
     bool ok = true;
     if (warp < kWorkers) {
-        ok = work<D, kPair>(p, ls, sh, smem_u32(staging), tmem_k);
+        ok = work<R>(p, ls, sh, smem_u32(staging), tmem_k);
         if (!ok) copies_wait<0>();
     } else if (warp < kColumnWarp) {
-        ok = summarise<kPair>(p, ls, sh, tmem_s);
+        ok = summarise<R>(p, ls, sh, tmem_s);
     } else if (warp < kQueryWarp) {
-        ok = columns(p, ls, sh);
+        ok = columns<R>(p, ls, sh);
     } else if (warp == kQueryWarp) {
-        ok = fetch_queries<D, kPair>(p, ls, map, sh, smem_u32(ring));
+        ok = fetch_queries<R>(p, ls, map, sh, smem_u32(ring));
         __syncwarp();
     } else if (warp == kPlanWarp) {
         ok = plan(p, ls, sh, from, to);
     } else {
-        ok = issue<D, kPair>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
+        ok = issue<R>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
         if (!ok && (!kPair || (blockIdx.x & 1) == 0)) {  // wait for the MMAs in flight before the operands go
             commit<kPair>(&sh.drain, elect_one());
             mbar_poll_bounded(&sh.drain, 0, kWaitLimitNs);
@@ -1223,12 +1238,16 @@ LaunchShape make_shape(const WeightParams& p) {
             }
         ls.box_cols = (ls.box_heads * ls.box_tokens + 15) / 16 * 16;
     }
-    const int nope = p.head_dim - p.rope_dim, mid = p.head_dim / 2;
-    const int first = mid <= nope ? mid : nope + 2 * (mid - nope);
-    ls.stride[0] = first + 16;
-    ls.stride[1] = p.head_dim + p.rope_dim - first + 16;
+    ls.by_tokens = divisor(ls.tokens);
+    ls.by_groups = divisor(ls.head_groups);
+    const int nope = p.head_dim - p.rope_dim, parts = ls.ranks == 2 || p.head_dim == 128 ? 2 : 4;
+    const auto byte_of = [&](int d) { return d <= nope ? d : nope + 2 * (d - nope); };
+    for (int i = 0; i < parts; ++i) {
+        ls.stride[i] = byte_of((i + 1) * p.head_dim / parts) - byte_of(i * p.head_dim / parts) + 16;
+        ls.staging_bytes += 4 * kWarp * ls.stride[i];
+    }
     ls.stage_bytes = (ls.box_heads * ls.box_tokens + 15) / 16 * 16 * 128 * 2;
-    const int room = kMostShared - (int)kAlign - 4 * kWarp * (ls.stride[0] + ls.stride[1]) - (int)sizeof(Shared);
+    const int room = kMostShared - (int)kAlign - ls.staging_bytes - (int)sizeof(Shared);
     ls.stages = room / ls.stage_bytes;
     if (ls.stages > kMostStages) ls.stages = kMostStages;
     const int most = p.head_dim == 128 ? 4 : 3 * p.head_dim / 128;
@@ -1237,18 +1256,18 @@ LaunchShape make_shape(const WeightParams& p) {
     return ls;
 }
 
-template <int D, bool kPair>
+template <class R>
 cudaError_t launch(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, int ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel<D, kPair>, kMostShared, done);
+    const cudaError_t e = set_smem_limit_per_device(attn_weights_kernel<R>, kMostShared, done);
     if (e != cudaSuccess) return e;
-    const size_t smem = kAlign + (size_t)ls.stages * ls.stage_bytes + 4 * kWarp * (size_t)(ls.stride[0] + ls.stride[1]) + sizeof(Shared);
-    return launch_pdl_clusters(attn_weights_kernel<D, kPair>, ls.ranks, dim3((unsigned)ctas), dim3(kThreads), smem, stream, p, ls, map);
+    const size_t smem = kAlign + (size_t)ls.stages * ls.stage_bytes + ls.staging_bytes + sizeof(Shared);
+    return launch_pdl_clusters(attn_weights_kernel<R>, ls.ranks, dim3((unsigned)ctas), dim3(R::kThreads), smem, stream, p, ls, map);
 }
 
 template <int D>
 cudaError_t launch_ranks(const WeightParams& p, const LaunchShape& ls, const CUtensorMap& map, int ctas, cudaStream_t stream) {
-    return ls.ranks == 2 ? launch<D, true>(p, ls, map, ctas, stream) : launch<D, false>(p, ls, map, ctas, stream);
+    return ls.ranks == 2 ? launch<Roles<D, true>>(p, ls, map, ctas, stream) : launch<Roles<D, false>>(p, ls, map, ctas, stream);
 }
 
 }  // namespace
