@@ -309,7 +309,56 @@ struct Walk {
     }
 };
 
-// The CTA's range of the sequence, and the request it starts in (sh.first_*).
+// Share i of n of a sequence.
+__device__ __forceinline__ int64_t share(int64_t all, int64_t i, int64_t n) {
+    return all >> 40 == 0 ? all * i / n : all / n * i + all % n * i / n;
+}
+
+// The CTA's range of the sequence and the request it starts in, by one warp.  The costs of up
+// to four requests a lane stay in registers.
+constexpr int kFewRequests = 4 * kWarp;
+
+__device__ __forceinline__ void find_range_of_few(const WeightParams& p, const LaunchShape& ls, Walk& w) {
+    const int lane = threadIdx.x % kWarp;
+    int64_t cost[4], at[4], all = 0;  // request i * 32 + lane
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        int64_t c = 0;
+        if (i * kWarp < p.num_reqs) c = request_costs(p, ls, i * kWarp + lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k == i) cost[k] = c;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int64_t sum = cost[i];
+        if (i * kWarp < p.num_reqs) {
+#pragma unroll
+            for (int o = 1; o < kWarp; o *= 2) {
+                const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += x;
+            }
+        }
+        at[i] = all + sum - cost[i];
+        all = __shfl_sync(0xFFFFFFFFu, all + sum, kWarp - 1);
+    }
+    const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
+    w.from = share(all, b, n);
+    w.to = share(all, b + 1, n);
+    w.r = 0;
+    w.at = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, at[i] <= w.from && w.from < at[i] + cost[i]);
+        if (here) {
+            const int src = __ffs(here) - 1;
+            w.r = i * kWarp + src;
+            w.at = __shfl_sync(0xFFFFFFFFu, at[i], src);
+        }
+    }
+}
+
+// The same by the whole CTA, for the planning warp (sh.first_*).
 template <int kThreads>
 __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t& from, int64_t& to) {
     constexpr int kWarps = kThreads / kWarp;
@@ -352,29 +401,26 @@ __device__ void find_range(const WeightParams& p, const LaunchShape& ls, Shared&
         }
         if (pass == 0) {
             const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
-            const auto share = [&](int64_t i) {
-                return before >> 40 == 0 ? before * i / n : before / n * i + before % n * i / n;
-            };
-            from = share(b);
-            to = share(b + 1);
+            from = share(before, b, n);
+            to = share(before, b + 1, n);
         }
     }
     __syncthreads();
 }
 
-// The page that holds row j; negative without one.
+// What the block table has for row j, -1 where nothing is looked up.  Not looked at here, so
+// that the load stays in flight.
 __device__ __forceinline__ int32_t page_of(const WeightParams& p, int32_t r, const Request& q, int32_t j) {
     if (j >= q.end) return -1;
     int32_t off;
     const int64_t logical = (int64_t)div_block32(j, p.cache.block_size, p.cache.shift, off) - q.base;
     if (logical < 0 || logical >= p.bt_width) return -1;
-    const int32_t page = p.bt[(int64_t)r * p.bt_stride + logical];
-    return page < p.cache.num_pages ? page : -1;
+    return p.bt[(int64_t)r * p.bt_stride + logical];
 }
 
 // ---- the planning warp ------------------------------------------------------------------------
 
-__device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, int64_t from, int64_t to) {
+__device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, Walk w) {
     constexpr int kPer = kTile / kWarp;
     const int lane = threadIdx.x % kWarp;
     const int64_t token_stride = p.head_dim + p.rope_dim;
@@ -382,11 +428,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
     // row i * 32 + lane of this CTA's part of the tile
     const int32_t mine = (int32_t)(blockIdx.x % ls.ranks) * kTile + lane;
     const auto row_at = [&](const Walk& x, int i) { return (int32_t)min(((int64_t)x.k << ls.row_shift) + mine + i * kWarp, (int64_t)INT32_MAX); };
-    Walk w{}, x{};  // where the walk stands, and the tile before, which is to be published
-    w.from = from;
-    w.to = to;
-    w.at = sh.first_at;
-    w.r = sh.first_request;
+    Walk x;  // the tile before the walk's, which is to be published
     w.tiles = -1;
     x.r = -1;
     int32_t page[kPer];  // of x
@@ -398,7 +440,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
             if (!started) {
                 started = true;
                 if (lane == 0) {
-                    Record rec{from >= to ? kEmptyRange : kNone, 0, 0, 0};
+                    Record rec{w.from >= w.to ? kEmptyRange : kNone, 0, 0, 0};
                     if (!w.done() && w.c0 > 0) rec = {w.c1 == w.total ? kEnds : kMiddle, w.r, w.k, 0};
                     ls.records[blockIdx.x] = rec;
                 }
@@ -423,7 +465,8 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 Row row{zero, zero};
-                if (page[i] >= 0) {
+                const bool there = page[i] >= 0 && page[i] < p.cache.num_pages;
+                if (there) {
                     int32_t off;
                     div_block32(row_at(x, i), p.cache.block_size, p.cache.shift, off);
                     const uint8_t* pg = p.cache.base + (int64_t)page[i] * p.cache.page_stride;
@@ -431,8 +474,8 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, i
                     row.scales = pg + p.cache.block_size * token_stride + (int64_t)off * (p.head_dim / 64);
                 }
                 t.row[i * kWarp + lane] = row;
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, page[i] >= 0);
-                if (lane == 0) t.there[i] = there;
+                const uint32_t rows = __ballot_sync(0xFFFFFFFFu, there);
+                if (lane == 0) t.there[i] = rows;
             }
             if (lane == 0) {
                 t.request = x.r;
@@ -1105,8 +1148,14 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     const uint32_t tmem_s = sh.tmem, tmem_k = tmem_s + 2 * kCols;
     pdl_wait();
     pdl_launch_dependents();
-    int64_t from, to;
-    find_range<R::kThreads>(p, ls, sh, from, to);
+    Walk walk{};
+    if (p.num_reqs > kFewRequests) {
+        find_range<R::kThreads>(p, ls, sh, walk.from, walk.to);
+        walk.r = sh.first_request;
+        walk.at = sh.first_at;
+    } else if (warp == kPlanWarp) {
+        find_range_of_few(p, ls, walk);
+    }
 
     bool ok = true;
     if (warp < kWorkers) {
@@ -1120,7 +1169,7 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         ok = fetch_queries<R>(p, ls, map, sh, smem_u32(ring));
         __syncwarp();
     } else if (warp == kPlanWarp) {
-        ok = plan(p, ls, sh, from, to);
+        ok = plan(p, ls, sh, walk);
     } else {
         ok = issue<R>(ls, sh, smem_u32(ring), tmem_k, tmem_s);
         if (!ok && (!kPair || (blockIdx.x & 1) == 0)) {  // wait for the MMAs in flight before the operands go
