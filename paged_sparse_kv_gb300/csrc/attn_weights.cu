@@ -1249,19 +1249,20 @@ constexpr int kMostShared = 227 * 1024;
 
 // Two CTAs share a tile of 256 rows, and the queries of each column tile, where requests
 // bring many columns: half the bytes of queries per row, and a ring twice as deep.
-constexpr int64_t kPairColumns = 512;
+constexpr int64_t kPairColumns = 128;
 
 LaunchShape make_shape(const WeightParams& p) {
     LaunchShape ls{};
     const int H = p.num_heads;
     const int64_t T = p.num_tokens > 0 ? p.num_tokens : 1;
+    const int64_t each = (T + p.num_reqs - 1) / p.num_reqs;  // tokens of a request, on average
     ls.ranks = T * H >= kPairColumns * p.num_reqs && sm_count() % 2 == 0 ? 2 : 1;
     ls.row_shift = ls.ranks == 2 ? 8 : 7;
     if (ls.ranks == 1) {
         ls.head_groups = (H + kCols - 1) / kCols;
         ls.heads = (H + ls.head_groups - 1) / ls.head_groups;
         ls.tokens = ls.head_groups > 1 ? 1 : kCols / ls.heads;
-        if (ls.tokens > T) ls.tokens = (int32_t)T;
+        if (ls.tokens > each) ls.tokens = (int32_t)each;
         ls.box_heads = ls.heads;
         ls.box_tokens = ls.tokens;
         ls.box_cols = kCols;
@@ -1274,8 +1275,10 @@ LaunchShape make_shape(const WeightParams& p) {
                 const int heads = (H + groups - 1) / groups, box = by_heads ? (heads + 1) / 2 : heads;
                 if (box > half) continue;
                 int tokens = half / box;
-                if (tokens > T) tokens = (int)T;
-                const double used = (double)H / groups * tokens * (by_heads ? 1 : 2);
+                const int64_t most = by_heads ? each : (each + 1) / 2;
+                if (tokens > most) tokens = (int)most;
+                const int64_t filled = by_heads ? tokens : 2 * tokens < each ? 2 * tokens : each;
+                const double used = (double)H / groups * (double)filled;
                 if (used <= best) continue;
                 best = used;
                 ls.by_heads = by_heads;
