@@ -26,7 +26,7 @@ constexpr int kMostCtas = 8;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 
 struct SelectShared {
-    uint32_t bins[3][kBins];
+    alignas(8) uint32_t bins[3][kBins];
     uint32_t warp[kWarps];
     uint32_t ties[kWarps], holes[kWarps], movers[kWarps];  // of the rows of a warp
     uint32_t total[3];   // of this CTA: ties, holes, movers
@@ -63,6 +63,26 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* at, int rank)
     return v;
 }
 
+__device__ __forceinline__ uint2 ld_cluster_u32x2(const uint32_t* at, int rank) {
+    uint2 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+                 "ld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+                 : "=r"(v.x), "=r"(v.y) : "r"(smem_u32(at)), "r"(rank) : "memory");
+    return v;
+}
+
+// What stands at `at` in each CTA; all reads are in flight at once (one after the other took
+// a microsecond each).
+template <typename F>
+__device__ __forceinline__ void for_ctas(const uint32_t* at, int ctas, F use) {
+    uint32_t v[kMostCtas];
+#pragma unroll
+    for (int c = 0; c < kMostCtas; ++c) v[c] = c < ctas ? ld_cluster_u32(at, c) : 0;
+#pragma unroll
+    for (int c = 0; c < kMostCtas; ++c)
+        if (c < ctas) use(c, v[c]);
+}
+
 __device__ __forceinline__ void sync_all(int ctas) {
     if (ctas > 1) cluster_sync(); else __syncthreads();
 }
@@ -94,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
     int64_t newest = (int64_t)n - 1;
     if (select && pos && p.num_recent > 0) {  // the same in all CTAs of the request
         int32_t top = INT32_MIN;
+#pragma unroll 8
         for (int32_t j = first + lane; j < end; j += kWarp) top = max(top, pos[j]);
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         if (lane == 0) sh.warp[warp] = (uint32_t)top;
@@ -103,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
             if (lane == 0) sh.newest = top;
         }
         sync_all(ctas);
-        top = INT32_MIN;
-        for (int c = 0; c < ctas; ++c)
-            top = max(top, ctas > 1 ? (int32_t)ld_cluster_u32(reinterpret_cast<const uint32_t*>(&sh.newest), c) : sh.newest);
+        top = sh.newest;
+        if (ctas > 1)
+            for_ctas(reinterpret_cast<const uint32_t*>(&sh.newest), ctas, [&](int, uint32_t v) { top = max(top, (int32_t)v); });
         newest = top;
     }
     const int64_t recent = p.num_recent > 0 ? newest - p.num_recent : INT64_MAX;
@@ -117,6 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
 
     uint32_t threshold = 0, left = (uint32_t)m;  // keys equal to the threshold of which `left` stay
     if (select) {
+        if (kCached) {
+#pragma unroll 8
+            for (int32_t j = first + lane; j < end; j += kWarp) cached[j - first] = key_of(j);
+        }
         __syncthreads();
         // ---- radix selection
         for (int digit = 0; digit < 3; ++digit) {
@@ -127,8 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
                 uint32_t key = 0;
                 bool in = j < end;
                 if (in) {
-                    key = digit == 0 ? key_of(j) : key_at(j);
-                    if (kCached && digit == 0) cached[j - first] = key;
+                    key = key_at(j);
                     in = digit == 0 || (digit == 1 ? key >> 21 == threshold >> 21 : key >> 10 == threshold >> 10);
                 }
                 const uint32_t bin = in ? (key >> shift) & (bins - 1) : ~0u;
@@ -142,14 +166,23 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
             }
             sync_all(ctas);
             // thread i has the bins 2i and 2i + 1 counted from the top
-            uint32_t x[2];
+            uint32_t x[2] = {0, 0};
+            const int lower = (int)bins - 2 - 2 * tid;
+            if (lower >= 0) {
+                const uint32_t* at = &sh.bins[digit][lower];
+                if (ctas == 1) {
+                    x[0] = at[1];
+                    x[1] = at[0];
+                } else {
+                    uint2 v[kMostCtas];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int b = (int)bins - 1 - (2 * tid + k);
-                x[k] = 0;
-                if (b >= 0)
-                    for (int c = 0; c < ctas; ++c)
-                        x[k] += ctas > 1 ? ld_cluster_u32(&sh.bins[digit][b], c) : sh.bins[digit][b];
+                    for (int c = 0; c < kMostCtas; ++c) v[c] = c < ctas ? ld_cluster_u32x2(at, c) : make_uint2(0, 0);
+#pragma unroll
+                    for (int c = 0; c < kMostCtas; ++c) {
+                        x[0] += v[c].y;
+                        x[1] += v[c].x;
+                    }
+                }
             }
             uint32_t sum = x[0] + x[1];
             const uint32_t mine = sum;
@@ -183,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
         uint32_t all, tied = below_warp(sh.ties, all);
         if (tid == 0) sh.total[0] = all;
         sync_all(ctas);
-        for (int c = 0; c < rank; ++c) tied += ld_cluster_u32(&sh.total[0], c);
+        if (ctas > 1)
+            for_ctas(&sh.total[0], ctas, [&](int c, uint32_t v) { tied += c < rank ? v : 0; });
 
         // ---- holes and movers: counts first, then their places
         uint32_t seen = tied, holes = 0, movers = 0;
@@ -214,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
             sh.total[2] = all_movers;
         }
         sync_all(ctas);
-        uint32_t moves = ctas > 1 ? 0 : all_holes;
-        for (int c = 0; c < ctas && ctas > 1; ++c) {
-            const uint32_t h = ld_cluster_u32(&sh.total[1], c);
-            moves += h;
-            if (c < rank) {
-                hole += h;
-                mover += ld_cluster_u32(&sh.total[2], c);
-            }
+        uint32_t moves = all_holes;
+        if (ctas > 1) {
+            moves = 0;
+            for_ctas(&sh.total[1], ctas, [&](int c, uint32_t v) {
+                moves += v;
+                hole += c < rank ? v : 0;
+            });
+            for_ctas(&sh.total[2], ctas, [&](int c, uint32_t v) { mover += c < rank ? v : 0; });
         }
         int2* list = p.moves + (int64_t)r * p.moves_stride;
         const bool copy_w = p.weights_out && p.weights_out != p.weights;
@@ -243,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
             }
         }
         sync_all(ctas);  // the list is whole, and every weight has been read
+#pragma unroll 2
         for (uint32_t i = rank * kThreads + tid; i < moves; i += ctas * kThreads) {
             const int2 move = list[i];
             if (p.weights_out) p.weights_out[(int64_t)r * p.wo_stride + move.y] = w[move.x];
@@ -346,9 +381,10 @@ constexpr int kMostKeys = 48 * 1024;  // of a CTA's rows in shared memory
 }  // namespace
 
 cudaError_t launch_select_evictions(const SelectParams& p, cudaStream_t stream) {
-    // 4096 rows or more a CTA
+    // 4096 rows or more a CTA, and clusters that run at the same time (a CTA fills an SM, and what a
+    // GPC has left over cannot take part: 16 clusters of eight took two rounds)
     int ctas = 1;
-    while (ctas < kMostCtas && (int64_t)ctas * 4096 < p.width) ctas *= 2;
+    while (ctas < kMostCtas && (int64_t)ctas * 4096 < p.width && 3 * ctas * (int64_t)p.num_reqs <= sm_count()) ctas *= 2;
     const int32_t groups = (p.width + kWarp - 1) / kWarp, warps = ctas * kWarps;
     const int64_t keys = (int64_t)((groups + warps - 1) / warps) * kThreads;
     const bool cached = keys <= kMostKeys;
