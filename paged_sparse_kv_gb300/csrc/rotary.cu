@@ -22,7 +22,9 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ void sincos_turn(uint64_t u, float& s, float& c) {
     const uint32_t quarter = (uint32_t)((u + (1ull << 61)) >> 62);
     constexpr float kRadians = (float)(6.283185307179586 / 18446744073709551616.0);  // 2 pi / 2^64
-    const float x = __ll2float_rn((long long)(u - ((uint64_t)quarter << 62))) * kRadians;
+    const uint64_t rest = u - ((uint64_t)quarter << 62);
+    // in two halves: a conversion of 64 bits runs at the rate of binary64
+    const float x = fmaf(__int2float_rn((int32_t)(rest >> 32)), 4294967296.0f, __uint2float_rn((uint32_t)rest)) * kRadians;
     const float y = x * x;
     float a = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
     a = fmaf(a, y, 8.3333333e-3f);
