@@ -1238,7 +1238,10 @@ bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.num_heads, (cuuint64_t)p.num_tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)p.q_stride_h * 2, (cuuint64_t)p.q_stride_t * 2};
+    // a dim of size 1 may carry any stride
+    const cuuint64_t row = (cuuint64_t)p.head_dim * 2;
+    const cuuint64_t strides[2] = {p.num_heads > 1 ? (cuuint64_t)p.q_stride_h * 2 : row,
+                                   p.num_tokens > 1 ? (cuuint64_t)p.q_stride_t * 2 : row * (cuuint64_t)p.num_heads};
     const cuuint32_t box[3] = {64, (cuuint32_t)ls.box_heads, (cuuint32_t)ls.box_tokens}, ones[3] = {1, 1, 1};
     return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.q), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -925,29 +925,32 @@ def apply_rotary_embedding(positions: torch.Tensor, q: torch.Tensor, cos_sin_cac
     i = _index(q)
     if q.dtype not in _ROTARY_DTYPES:
         raise TypeError(f"q must be one of {[str(d) for d in _ROTARY_DTYPES]}, got {q.dtype}")
-    T, D = q.shape[0], q.shape[-1]
+    dtype, dev, shape = q.dtype, q.device, q.shape
+    T, D = shape[0], shape[-1]
     _need(cos_sin_cache, torch.float32, "cos_sin_cache")
     _same(cos_sin_cache, i, "cos_sin_cache")
-    if positions.numel() != T:
-        raise ValueError(f"positions must have {T} entries, got {positions.numel()}")
-    qa, H = _rotated(q, "q", T, D, q.dtype, i)
+    qa, H = _rotated(q, "q", T, D, dtype, i)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"q_out {tuple(q_out.shape)} does not match q {tuple(q.shape)}")
-    qo, _ = _rotated(q_out, "q_out", T, D, q.dtype, i)
+        q_out = torch.empty(shape, dtype=dtype, device=dev)
+        qo = (q_out.data_ptr(), H * D, D)
+    elif q_out.shape != shape:
+        raise ValueError(f"q_out {tuple(q_out.shape)} does not match q {tuple(shape)}")
+    else:
+        qo, _ = _rotated(q_out, "q_out", T, D, dtype, i)
     ka, ko, Hk = (None, 0, 0), (None, 0, 0), 0
     if k is not None:
-        ka, Hk = _rotated(k, "k", T, D, q.dtype, i)
+        ka, Hk = _rotated(k, "k", T, D, dtype, i)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+            ko = (k_out.data_ptr(), Hk * D, D)
         elif k_out.shape != k.shape:
             raise ValueError(f"k_out {tuple(k_out.shape)} does not match k {tuple(k.shape)}")
-        ko, _ = _rotated(k_out, "k_out", T, D, q.dtype, i)
+        else:
+            ko, _ = _rotated(k_out, "k_out", T, D, dtype, i)
     elif k_out is not None:
         raise ValueError("k_out without k")
     stride, (rows, rope) = _rows(cos_sin_cache, "cos_sin_cache"), cos_sin_cache.shape
-    _call(q.device, "apply_rotary_embedding", *qa, H, *ka, Hk, T, _ROTARY_DTYPES[q.dtype], D,
+    _call(dev, "apply_rotary_embedding", *qa, H, *ka, Hk, T, _ROTARY_DTYPES[dtype], D,
           D - rope if rope_offset is None else rope_offset, rope, int(bool(interleaved)),
           int(bool(inverse)), _vec(positions, torch.int64, "positions", T, i),
           cos_sin_cache.data_ptr(), stride, rows, *qo, *ko,
@@ -963,10 +966,16 @@ def _per_row(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, R: int, w
         return None, 0
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _same(t, index, name)
-    stride = _rows(t, name)
-    if t.shape[0] < R or t.shape[1] < width:
-        raise ValueError(f"{name} must be at least [{R}, {width}], got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < R or shape[1] < width:
+        raise ValueError(f"{name} must be at least [{R}, {width}], got {tuple(shape)}")
+    stride, inner = t.stride()
+    if inner != 1 and shape[1] > 1 and shape[0] > 0:
+        raise ValueError(f"{name} must have unit inner stride")
+    if shape[0] <= 1 or shape[1] == 0:  # a size-1 dim may carry any stride (0 from broadcasting)
+        stride = max(stride, shape[1])
     return t.data_ptr(), stride
 
 
@@ -988,6 +997,9 @@ def accumulate_attention_weights_workspace_bytes(device: torch.device) -> int:
     index = torch.device(device).index
     return _on(_current_device() if index is None else index,
                _abi.lib().accumulate_attention_weights_workspace_bytes)
+
+
+_weights_workspace: dict = {}
 
 
 def accumulate_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor,
@@ -1024,7 +1036,9 @@ def accumulate_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torc
         raise ValueError("rows of weights must not overlap")
     valid = None if is_valid_token is None else is_valid_token.to(torch.uint8)
     if workspace is None:
-        need = _on(i, _abi.lib().accumulate_attention_weights_workspace_bytes)
+        need = _weights_workspace.get(i)  # a property of the device
+        if need is None:
+            need = _weights_workspace[i] = accumulate_attention_weights_workspace_bytes(q.device)
         workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
     else:
         _vec(workspace, torch.uint8, "workspace", 0, i)

@@ -343,3 +343,23 @@ def test_refusals(cuda_device):
             continue
         with pytest.raises(kind, match=text):
             call(**kw)
+
+
+def test_strides_of_single_tokens_and_heads(cuda_device):
+    """A size-1 dim may carry any stride, 0 from broadcasting among them."""
+    d, rng = cuda_device, np.random.default_rng(19)
+    cache = torch.from_numpy(_cache(rng, 4, 64, 128, 64)).to(d)
+    meta = (_i32([0, 1], d), _i32([200], d), _i32(np.arange(4)[None, :], d), 64)
+    for H in (1, 5):
+        q, _ = _query(rng, 1, H, 128, 1.0, d, "thd")
+        want = ops.accumulate_attention_weights(q, torch.full((1, H), 5.0, device=d), cache, *meta, torch.zeros(1, 200, device=d))
+        for view in (q.as_strided((1, H, 128), (0, 128, 1)), q.as_strided((1, H, 128), (8, 128 if H > 1 else 0, 1))):
+            got = ops.accumulate_attention_weights(view, torch.full((1, H), 5.0, device=d), cache, *meta, torch.zeros(1, 200, device=d))
+            assert torch.equal(got, want)
+
+
+def test_more_requests_than_a_warp_plans(cuda_device):
+    """The range of a CTA found by one warp (up to 128 requests) and by all of them."""
+    rng = np.random.default_rng(20)
+    for R in (32, 33, 128, 129, 1000):
+        _run(cuda_device, R, rng.integers(0, 4, size=R) + (np.arange(R) == 0), rng.integers(0, 150, size=R), 6, 128, bs=16)
