@@ -24,10 +24,34 @@
 // their rows into a ring.  Worker warps bring records into shared memory by
 // asynchronous copies (32 rows and a part of the dims each, a copy of the next tile issued as
 // soon as a block of 64 dims is read), dequantise them and write them to tensor memory; one
-// warp fetches queries by TMA into a ring of 128-dim stages, four prepare the
-// columns' logarithms and bounds; one issues the MMAs; others turn scores into sums.  Queries stay in the ring while
-// the column tile does not change (a decode batch: one column tile per request).
-// Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
+// warp fetches queries by TMA into a ring of 128-dim stages, four prepare the columns'
+// logarithms and bounds; one issues the MMAs; others turn scores into sums.  Queries stay in
+// the ring while the column tile does not change (a decode batch: one column tile per
+// request).  Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
+//
+// Pairs.  Where requests bring many columns, two CTAs share a tile of 256 rows (MMAs of M =
+// 256, issued by the first): each has 128 of the rows in its own tensor memory and fetches half
+// of each column tile's queries, which halves the bytes of queries per row and lets the
+// ring hold two column tiles.
+//
+// What bounds it.  4096 tokens of 128 heads (1.1 TFLOP): 859 us, 1285 TFLOP/s; the tensor pipe is
+// 71 % in use at the 1.6 GHz that the power limit leaves (cuBLAS: 1734 TFLOP/s sustained).  The
+// rest is queries: 4.3 GB of them pass through L2 and 4.0 GB come from memory, at 4.7 TB/s, as
+// CTAs are at different columns at a time.  41 tokens of 40 heads on average over 5
+// requests of 31000 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, 172 MB
+// of records: 52 us, 3.3 TB/s of the 6.7 measured; a tile takes some 5000 cycles, of which
+// dequantising it is 2000 issue slots of each scheduler, and the first tile 20000, which is
+// mostly code that is not in the instruction cache yet.  One token of 16 heads over
+// 8192 rows: 9.6 us.
+//
+// Measured on the way, by cases as above (64 single tokens; last tokens; 4096 tokens):
+//  * each role walking the sequence by itself, one warp for queries and columns: 76, 536, 1784;
+//  * columns prepared by four warps: 103, 314, 1253; a planning warp: 67, 211, 1029;
+//  * pairs, with a release of the cluster's scope on each hand-over: 69, 344, 1054, and
+//    without: 69, 191, 935; stages of 128 dims instead of 64: 66, 186, 895;
+//  * 16 dequantising warps instead of 8: 69 with the loops of the other roles unrolled,
+//    as each passes its code once a tile and finds it gone from the instruction cache; 58 with
+//    short loops and one barrier per block of all parts.
 #include <cuda.h>
 
 #include <atomic>
@@ -1250,8 +1274,9 @@ bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
 
 constexpr int kMostShared = 227 * 1024;
 
-// Two CTAs share a tile of 256 rows, and the queries of each column tile, where requests
-// bring many columns: half the bytes of queries per row, and a ring twice as deep.
+// Pairs from this many columns a request on.  64 requests of 8192 rows, pairs against single
+// CTAs: 64 columns 101 us against 81 (a pair has half the dequantising warps), 128 99.8 against
+// 101.7 (head_dim 256: 64 against 83), 256 120 against 151, 512 190 against 245.
 constexpr int64_t kPairColumns = 128;
 
 LaunchShape make_shape(const WeightParams& p) {

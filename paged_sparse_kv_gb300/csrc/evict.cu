@@ -20,6 +20,11 @@ namespace {
 // rows in order come from counts per warp, each of which owns a run of neighbouring rows.
 // A cluster of CTAs shares a long request; they add up histograms and counts through
 // distributed shared memory.
+//
+// Latency bounds it: two reads of the rows, three histograms with their sums and three passes
+// in order follow one another, each behind barriers of 1024 threads (and of the cluster).
+// 64 requests of 2049 rows 8.8 us, 16 of up to 32768 rows in clusters of four 24.4 us, 3 of
+// 131071 rows in clusters of eight 41 us, where bytes alone would take 0.3, 1 and 0.5.
 constexpr int kThreads = 1024, kWarps = kThreads / kWarp;
 constexpr int kBins = 2048;  // of the first two digits; the third has half as many
 constexpr int kMostCtas = 8;
@@ -305,6 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
 //
 // A CTA takes kMoves moves of a request at a time: their addresses are looked up side by
 // side, then all threads copy 16-byte pieces of data (and the scales) of all of them.
+// 57000 records of 584 bytes: 14.9 us, 4.5 TB/s read and written, of the 6.7 measured; a
+// chain of three reads (count, move, table entry) precedes each tile's copies, with eight
+// CTAs an SM to cover it.  One record in each of 64 requests: 2.9 us.
 constexpr int kMoves = 32, kMoveThreads = 256;
 
 template <typename Unit>  // of the scales
@@ -381,8 +389,9 @@ constexpr int kMostKeys = 48 * 1024;  // of a CTA's rows in shared memory
 }  // namespace
 
 cudaError_t launch_select_evictions(const SelectParams& p, cudaStream_t stream) {
-    // 4096 rows or more a CTA, and clusters that run at the same time (a CTA fills an SM, and what a
-    // GPC has left over cannot take part: 16 clusters of eight took two rounds)
+    // 4096 rows or more a CTA, and clusters that run at the same time: a CTA fills an SM, and what a
+    // GPC has left over cannot take part (16 requests of up to 32768 rows: clusters of eight, which
+    // take two rounds, 42.5 us, of four 24.4)
     int ctas = 1;
     while (ctas < kMostCtas && (int64_t)ctas * 4096 < p.width && 3 * ctas * (int64_t)p.num_reqs <= sm_count()) ctas *= 2;
     const int32_t groups = (p.width + kWarp - 1) / kWarp, warps = ctas * kWarps;

@@ -16,6 +16,11 @@ constexpr int kThreads = 256;
 // so a far position costs no accuracy and no binary64 arithmetic (of which this part does
 // little).  An eighth of a turn to either side of the nearest quarter is left for the
 // series of sine and cosine.
+//
+// 1048576 positions of 64 dims (268 MB written) take 47.4 us, 5.7 TB/s of the 6.7 measured; the
+// issue slots are 81 % in use, so the arithmetic weighs as much as the stores.  One pair a
+// thread with its own product took 234 us; stores of 512 contiguous bytes by exchange between
+// threads 57.7, as without (the conversion below held both up).
 
 // sin and cos of a fraction of a turn: quarters off, then Taylor's series on
 // [-pi/4, pi/4], whose first dropped terms (x^11/11!, x^12/12!) are below 2^-28.
@@ -23,7 +28,7 @@ __device__ __forceinline__ void sincos_turn(uint64_t u, float& s, float& c) {
     const uint32_t quarter = (uint32_t)((u + (1ull << 61)) >> 62);
     constexpr float kRadians = (float)(6.283185307179586 / 18446744073709551616.0);  // 2 pi / 2^64
     const uint64_t rest = u - ((uint64_t)quarter << 62);
-    // in two halves: a conversion of 64 bits runs at the rate of binary64
+    // in two halves: with one conversion of 64 bits the table above took 57.4 us
     const float x = fmaf(__int2float_rn((int32_t)(rest >> 32)), 4294967296.0f, __uint2float_rn((uint32_t)rest)) * kRadians;
     const float y = x * x;
     float a = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
@@ -89,6 +94,13 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
 // two times 16 bytes of the half layout, or 16 bytes to copy; single pairs and elements
 // where sizes, strides or addresses allow no 16-byte accesses.  A thread keeps its unit
 // for all the heads it visits, so a token's cosines and sines are read once per CTA.
+//
+// Bound by memory where it is large: 4096 tokens, the 64 rope dims of 128 heads of 512 in
+// bf16 (134 MB in pieces of 128 bytes): 27.5 us, 4.9 TB/s of the 6.7 measured, with eight CTAs
+// an SM (five: 30.3).  The half layout holds two packs and spills with eight: 1901 tokens of
+// 36 heads of 256 dims (70 MB, in part from L2) 15.4 us with five, 20.6 with eight.  Several
+// heads in flight a thread cost more CTAs than they gain (two 33.7, four 46 us against 30.3).
+// 64 tokens of 64 heads take 1.9 us: launch and two dependent reads.
 
 template <int kType> struct Elem;
 template <> struct Elem<PSK_DTYPE_BF16> {
@@ -140,7 +152,7 @@ struct RotaryShape {
 };
 
 template <int kType, bool kHalf, bool kWide>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p, const RotaryShape sh) {
+__global__ void __launch_bounds__(kThreads, kHalf ? 5 : 8) rotary_kernel(const RotaryParams p, const RotaryShape sh) {
     using Raw = typename Elem<kType>::Raw;
     constexpr int V = per_access<kType, kWide>();
     // pairs of a unit; interleaved single elements make no pair, so two are taken
