@@ -37,8 +37,8 @@
 // What bounds it.  4096 tokens of 128 heads (1.1 TFLOP): 859 us, 1285 TFLOP/s; the tensor pipe is
 // 71 % in use at the 1.6 GHz that the power limit leaves (cuBLAS: 1734 TFLOP/s sustained).  The
 // rest is queries: 4.3 GB of them pass through L2 and 4.0 GB come from memory, at 4.7 TB/s, as
-// CTAs are at different columns at a time.  41 tokens of 40 heads on average over 5
-// requests of 31000 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, 172 MB
+// CTAs are at different columns at a time.  203 tokens of 40 heads of 5 requests, over
+// 11061 to 30023 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, 172 MB
 // of records: 52 us, 3.3 TB/s of the 6.7 measured; a tile takes some 5000 cycles, of which
 // dequantising it is 2000 issue slots of each scheduler, and the first tile 20000, which is
 // mostly code that is not in the instruction cache yet.  One token of 16 heads over
