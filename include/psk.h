@@ -1002,7 +1002,8 @@ psk_status accumulate_attention_weights(
  *                  moves_stride (elements, even; 8-byte aligned): entries [0,
  *                  num_moves[r]) are written.  from >= m > to, so moves may be made in
  *                  any order.
- *   num_moves, seq_lens_out  int32 [num_reqs].  seq_lens_out may be seq_lens.
+ *   num_moves, seq_lens_out  int32 [num_reqs].  seq_lens_out may be seq_lens; they must
+ *                  not overlap the other arrays or each other.
  *   The pages past ceil(m / block_size) of a request hold nothing any more.
  *   0 <= width <= 2^30; num_reqs <= 2^27.
  */

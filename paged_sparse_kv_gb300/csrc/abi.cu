@@ -1350,7 +1350,9 @@ psk_status select_cache_evictions(
           "weights in place need equal strides");
     CHECK(positions_out != row_positions || row_positions == nullptr || po_stride == pos_stride,
           "positions in place need equal strides");
-    CHECK(num_moves != seq_lens_out && num_moves != seq_lens && num_moves != keep_lens && seq_lens_out != keep_lens,
+    const auto overlap = [&](const int32_t* a, const int32_t* b) { return a < b + num_reqs && b < a + num_reqs; };
+    CHECK(!overlap(num_moves, seq_lens_out) && !overlap(num_moves, seq_lens) && !overlap(num_moves, keep_lens) &&
+              !overlap(seq_lens_out, keep_lens) && (seq_lens_out == seq_lens || !overlap(seq_lens_out, seq_lens)),
           "num_moves and seq_lens_out must not overlap the inputs or each other");
     psk::SelectParams p{weights, w_stride, seq_lens, keep_lens, num_reqs, width, row_positions, pos_stride,
                         num_first, num_recent, weights_out, wo_stride, positions_out, po_stride,

@@ -35,7 +35,7 @@ struct SelectShared {
     uint32_t warp[kWarps];
     uint32_t ties[kWarps], holes[kWarps], movers[kWarps];  // of the rows of a warp
     uint32_t total[3];   // of this CTA: ties, holes, movers
-    uint32_t found[2];   // the digit, and how many of its keys stay
+    uint32_t found[3];   // the digit, how many of its keys stay, and how many it has
     int32_t newest;      // of this CTA
 };
 
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
         for (int digit = 0; digit < 3; ++digit) {
             const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
             const uint32_t bins = digit == 2 ? kBins / 2 : kBins;
+#pragma unroll 4
             for (int32_t j0 = first; j0 < end; j0 += kWarp) {
                 const int32_t j = j0 + lane;
                 uint32_t key = 0;
@@ -205,24 +206,29 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
                 const bool second = left > above + x[0];
                 sh.found[0] = bins - 1 - (2 * tid + (second ? 1 : 0));
                 sh.found[1] = left - above - (second ? x[0] : 0);
+                sh.found[2] = second ? x[1] : x[0];
             }
             __syncthreads();
             threshold |= sh.found[0] << shift;
             left = sh.found[1];
         }
-        // ---- of the keys equal to it the lowest rows stay
-        uint32_t count = 0;
-        for (int32_t j0 = first; j0 < end; j0 += kWarp) {
-            const int32_t j = j0 + lane;
-            count += __popc(__ballot_sync(0xFFFFFFFFu, j < end && key_at(j) == threshold));
+        // ---- of the keys equal to it the lowest rows stay (mostly all do, and need no ranks)
+        uint32_t tied = 0;
+        if (left < sh.found[2]) {  // the same in all CTAs
+            uint32_t count = 0, all;
+#pragma unroll 4
+            for (int32_t j0 = first; j0 < end; j0 += kWarp) {
+                const int32_t j = j0 + lane;
+                count += __popc(__ballot_sync(0xFFFFFFFFu, j < end && key_at(j) == threshold));
+            }
+            if (lane == 0) sh.ties[warp] = count;
+            __syncthreads();
+            tied = below_warp(sh.ties, all);
+            if (tid == 0) sh.total[0] = all;
+            sync_all(ctas);
+            if (ctas > 1)
+                for_ctas(&sh.total[0], ctas, [&](int c, uint32_t v) { tied += c < rank ? v : 0; });
         }
-        if (lane == 0) sh.ties[warp] = count;
-        __syncthreads();
-        uint32_t all, tied = below_warp(sh.ties, all);
-        if (tid == 0) sh.total[0] = all;
-        sync_all(ctas);
-        if (ctas > 1)
-            for_ctas(&sh.total[0], ctas, [&](int c, uint32_t v) { tied += c < rank ? v : 0; });
 
         // ---- holes and movers: counts first, then their places
         uint32_t seen = tied, holes = 0, movers = 0;
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
             ties += __popc(t);
             return j;
         };
+#pragma unroll 4
         for (int32_t j0 = first; j0 < end; j0 += kWarp) {
             bool stays;
             const int32_t j = group(j0, seen, stays);
@@ -266,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
         const bool copy_w = p.weights_out && p.weights_out != p.weights;
         const bool copy_p = p.positions_out && p.positions_out != p.positions;
         seen = tied;
+#pragma unroll 4
         for (int32_t j0 = first; j0 < end; j0 += kWarp) {
             bool stays;
             const int32_t j = group(j0, seen, stays);

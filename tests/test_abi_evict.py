@@ -25,7 +25,7 @@ def _select(**kw):
     dict(w=None), dict(w=A + 2), dict(ws=98), dict(seq=None), dict(keep=None), dict(R=-1), dict(R=2**27 + 1), dict(W=-1),
     dict(W=2**30 + 1, ws=2**31, ps=2**31, wos=2**31, pos_=2**31, ms=2**32), dict(ps=98), dict(pos=C + 1), dict(first=-1),
     dict(recent=-1), dict(wos=98), dict(pos_=98), dict(wo=A + 1), dict(po=C + 2), dict(mv=None), dict(mv=D + 4), dict(ms=97),
-    dict(ms=96), dict(nm=None), dict(so=None), dict(nm=B + 1024), dict(so=B + 256), dict(nm=B), dict(wo=A, wos=101),
+    dict(ms=96), dict(nm=None), dict(so=None), dict(nm=B + 1024), dict(so=B + 256), dict(nm=B), dict(wo=A, wos=101), dict(nm=B + 1028), dict(so=B + 8), dict(so=B + 260), dict(nm=B + 4),
     dict(po=C, pos_=100), dict(err=B + 2), dict(so=B + 1)])
 def test_select_rejects_bad_arguments(psk_lib, kw):
     assert _select(**kw) == INV
