@@ -66,13 +66,15 @@ namespace {
 
 constexpr int kTile = 128;          // rows of a CTA's part of a tile
 constexpr int kCols = 128;          // columns of a column tile, at most
-// Warps by role.  A CTA of its own has few columns per row and many tiles: 16 warps
-// dequantise and 4 sum up; a pair has many columns: 8 and 8.
+// Warps by role.  A CTA of its own has few columns per row and many tiles: at head_dim 512 16
+// warps dequantise and 4 sum up (64 single tokens of 64 heads over 8192 rows 81 us, 8 and 4 92,
+// 16 and 8 91), at 256 8 and 4 (60 us, 16 and 4 68).  A pair has many columns: 8 and 8 (203 tokens
+// of 40 heads of 5 requests 165 us, 16 and 8 184, 16 and 4 237).
 template <int kHeadDim, bool kTwo>
 struct Roles {
     static constexpr int D = kHeadDim;
     static constexpr bool kPair = kTwo;
-    static constexpr int kWorkers = kPair || D == 128 ? 8 : 16, kParts = kWorkers / 4;  // each has D / kParts dims
+    static constexpr int kWorkers = !kPair && D == 512 ? 16 : 8, kParts = kWorkers / 4;  // each has D / kParts dims
     static constexpr int kSummers = kPair ? 8 : 4, kShares = kSummers / 4;              // of the columns
     static constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kCols / kWarp;
     static constexpr int kMmaWarp = kQueryWarp + 1, kPlanWarp = kMmaWarp + 1;
@@ -553,9 +555,15 @@ struct Tiles {
 
 // ---- workers: records to tensor memory -----------------------------------------------------
 
-// 16-byte copy global -> shared; `bytes` 0 writes zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16-byte copy global -> shared.  Records are read once: they leave L2 first, before the
+// queries and the kernel's own code.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint64_t read_once() {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -611,6 +619,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
     uint32_t mine = staging + quad * kWarp * stride;
     for (int i = 0; i < part; ++i) mine += 4 * kWarp * ls.stride[i];
     const uint32_t own = mine + lane * stride;
+    const uint64_t policy = read_once();
 
     const auto load_scales = [&](const uint8_t* at) {
         uint2 s = make_uint2(0, 0);
@@ -631,12 +640,12 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
             const int first = lane / 8, piece = lane % 8 * 16;
             const uint32_t dst = mine + first * stride + (at - byte0) + piece;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) copy16(dst + i * 4 * stride, row[first + i * 4].data + at + piece, 16);
+            for (int i = 0; i < 8; ++i) copy16(dst + i * 4 * stride, row[first + i * 4].data + at + piece, policy);
         } else {
             const int first = lane / 4, piece = lane % 4 * 16;
             const uint32_t dst = mine + first * stride + (at - byte0) + piece;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) copy16(dst + i * 8 * stride, row[first + i * 8].data + at + piece, 16);
+            for (int i = 0; i < 4; ++i) copy16(dst + i * 8 * stride, row[first + i * 8].data + at + piece, policy);
         }
     };
     const auto hand_over = [&](int b) {
@@ -1320,7 +1329,7 @@ LaunchShape make_shape(const WeightParams& p) {
     }
     ls.by_tokens = divisor(ls.tokens);
     ls.by_groups = divisor(ls.head_groups);
-    const int nope = p.head_dim - p.rope_dim, parts = ls.ranks == 2 || p.head_dim == 128 ? 2 : 4;
+    const int nope = p.head_dim - p.rope_dim, parts = ls.ranks == 1 && p.head_dim == 512 ? 4 : 2;
     const auto byte_of = [&](int d) { return d <= nope ? d : nope + 2 * (d - nope); };
     for (int i = 0; i < parts; ++i) {
         ls.stride[i] = byte_of((i + 1) * p.head_dim / parts) - byte_of(i * p.head_dim / parts) + 16;
