@@ -38,11 +38,13 @@
 // 71 % in use at the 1.6 GHz that the power limit leaves (cuBLAS: 1734 TFLOP/s sustained).  The
 // rest is queries: 4.3 GB of them pass through L2 and 4.0 GB come from memory, at 4.7 TB/s, as
 // CTAs are at different columns at a time.  203 tokens of 40 heads of 5 requests, over
-// 11061 to 30023 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, 172 MB
-// of records: 52 us, 3.3 TB/s of the 6.7 measured; a tile takes some 5000 cycles, of which
-// dequantising it is 2000 issue slots of each scheduler, and the first tile 20000, which is
-// mostly code that is not in the instruction cache yet.  One token of 16 heads over
-// 8192 rows: 9.6 us.
+// 11061 to 30023 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, over
+// up to 8192 rows: 52 to 60 us from one machine to another for 177 MB, over 8192 rows each 78 us
+// for 306 MB, 3.9 TB/s of the 6.7 measured.  A tile takes some 5000 cycles, of which
+// dequantising it is 2000 issue slots of each scheduler; the first one's sums come after 30000:
+// 17000 until the planning warp has found the range and published two tiles, mostly code that
+// is not in the instruction cache yet, then all SMs' first records at once.  One token
+// of 16 heads over 8192 rows: 9.6 us.
 //
 // Measured on the way, by cases as above (64 single tokens; last tokens; 4096 tokens):
 //  * each role walking the sequence by itself, one warp for queries and columns: 76, 536, 1784;
@@ -1284,8 +1286,8 @@ bool query_map(const WeightParams& p, const LaunchShape& ls, CUtensorMap& map) {
 constexpr int kMostShared = 227 * 1024;
 
 // Pairs from this many columns a request on.  64 requests of 8192 rows, pairs against single
-// CTAs: 64 columns 101 us against 81 (a pair has half the dequantising warps), 128 99.8 against
-// 101.7 (head_dim 256: 64 against 83), 256 120 against 151, 512 190 against 245.
+// CTAs: 64 columns 92 us against 78 (a pair has half the dequantising warps), 128 89 against 96
+// (head_dim 256: 64 against 69), 256 120 against 147, 512 194 against 241.
 constexpr int64_t kPairColumns = 128;
 
 LaunchShape make_shape(const WeightParams& p) {
