@@ -948,7 +948,7 @@ psk_status apply_rotary_embedding(
  *
  *   q, softmax_scale, cache, head_dim, rope_dim, sink, the metadata and the block
  *   table as in chunk_mla_attention, but q_stride_t and q_stride_h must be at least
- *   head_dim where there is more than one token or head.
+ *   head_dim where there is more than one token or head, and at most 2^38.
  *   lse            binary32; (t, h) at lse + t*lse_stride_t + h; -infinity (with no
  *                  sink) marks a (t, h) that saw nothing and gives no weight.
  *   weights        binary32 [num_reqs, width], row stride w_stride.  decay finite and

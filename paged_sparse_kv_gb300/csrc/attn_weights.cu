@@ -126,7 +126,7 @@ struct Row {
 
 // A step of the walk with columns, as the planning warp publishes it.
 struct Tile {
-    int32_t request, tile;    // request -1: the end
+    int32_t request;          // -1: the end
     int32_t first_row, end;   // its first row; the rows of the request that have a weight
     int32_t first, total;     // first token group and number of its column tiles
     int32_t c0, c1;           // those of them that are this CTA's
@@ -507,7 +507,6 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, W
             }
             if (lane == 0) {
                 t.request = x.r;
-                t.tile = x.k;
                 t.first_row = row_at(x, 0);  // lane 0's
                 t.end = x.q.end;
                 t.first = x.first;
