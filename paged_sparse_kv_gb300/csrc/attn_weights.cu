@@ -78,7 +78,8 @@ struct Roles {
     static constexpr bool kPair = kTwo;
     static constexpr int kWorkers = !kPair && D == 512 ? 16 : 8, kParts = kWorkers / 4;  // each has D / kParts dims
     static constexpr int kSummers = kPair ? 8 : 4, kShares = kSummers / 4;              // of the columns
-    static constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kCols / kWarp;
+    static constexpr int kColumnWarps = kPair ? 4 : 2;
+    static constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps;
     static constexpr int kMmaWarp = kQueryWarp + 1, kPlanWarp = kMmaWarp + 1;
     static constexpr int kThreads = (kPlanWarp + 1) * kWarp;
 };
@@ -115,7 +116,7 @@ struct Record {
 struct Columns {
     float log[kCols];                 // log2 units
     int32_t lo[kCols], hi[kCols];     // rows a column sees
-    // by column warp: rows that every column in use sees, and whether all are in use
+    // by 32 columns: rows that every one in use sees, and which are in use
     int4 all_lo, all_hi, all_used;
 };
 
@@ -794,15 +795,20 @@ __device__ bool fetch_queries(const WeightParams& p, const LaunchShape& ls, cons
     return false;
 }
 
-// The logarithms and bounds of the columns, one a thread.  The next column tile's lse is in
+// The logarithms and bounds of the columns, one or two a thread.  The next column tile's lse is in
 // flight while this one's is worked on.
 template <class R>
 __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh) {
-    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - R::kColumnWarp, col = warp * kWarp + lane;
-    const int32_t rank = col / ls.box_cols, at = col - rank * ls.box_cols;
-    const int32_t token = at / ls.box_heads + (ls.by_heads ? 0 : rank * ls.box_tokens);
-    const int32_t head = at % ls.box_heads + (ls.by_heads ? rank * ls.box_heads : 0);
-    const bool in_box = at < ls.box_heads * ls.box_tokens && rank < ls.ranks;
+    constexpr int kPer = kCols / kWarp / R::kColumnWarps;  // columns of a thread
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp - R::kColumnWarp;
+    int32_t token[kPer], head[kPer];  // in the column tile; token -1: not in the box
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int col = (u * R::kColumnWarps + warp) * kWarp + lane, rank = col / ls.box_cols, at = col - rank * ls.box_cols;
+        const bool in_box = at < ls.box_heads * ls.box_tokens && rank < ls.ranks;
+        token[u] = in_box ? at / ls.box_heads + (ls.by_heads ? 0 : rank * ls.box_tokens) : -1;
+        head[u] = at % ls.box_heads + (ls.by_heads ? rank * ls.box_heads : 0);
+    }
     struct Column {
         bool used;
         int32_t pos, rows_from;
@@ -811,18 +817,22 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
     Tiles tiles;
     int32_t c = 0, c1 = 0, group = 0, part = 0, tokens = 0, token0 = 0, row0 = 0, replay = 0;
     bool end = false;
-    // this thread's column of the column tile at hand
+    // this thread's columns of the column tile at hand
+    Column next[kPer];
     const auto load = [&]() {
-        Column x{false, 0, replay, 0.0f, -INFINITY};
-        const int32_t i = group * ls.tokens + token, h = part * ls.heads + head;
-        if (in_box && i < tokens && h < p.num_heads) {
-            const int64_t t = (int64_t)token0 + i;
-            x.used = p.valid == nullptr || p.valid[t] != 0;
-            x.pos = row0 + i;
-            x.lse = p.lse[t * p.lse_stride_t + h];
-            if (p.sink) x.sink = p.sink[h];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            Column x{false, 0, replay, 0.0f, -INFINITY};
+            const int32_t i = group * ls.tokens + token[u], h = part * ls.heads + head[u];
+            if (token[u] >= 0 && i < tokens && h < p.num_heads) {
+                const int64_t t = (int64_t)token0 + i;
+                x.used = p.valid == nullptr || p.valid[t] != 0;
+                x.pos = row0 + i;
+                x.lse = p.lse[t * p.lse_stride_t + h];
+                if (p.sink) x.sink = p.sink[h];
+            }
+            next[u] = x;
         }
-        return x;
     };
     // moves on to the first column tile of a later tile
     const auto next_tile = [&]() {
@@ -847,11 +857,12 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
         }
     };
     if (!next_tile()) return false;
-    Column next{};
-    if (!end) next = load();
+    if (!end) load();
     for (uint32_t seq = 0; !end; ++seq) {
-        const Column x = next;
-        // the next column is read ahead where that waits for no other role, which may be
+        Column now[kPer];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) now[u] = next[u];
+        // the next column tile is read ahead where that waits for no other role, which may be
         // waiting for this one
         const bool ahead = ++c < c1;
         if (ahead) {
@@ -859,31 +870,36 @@ __device__ bool columns(const WeightParams& p, const LaunchShape& ls, Shared& sh
                 part = 0;
                 ++group;
             }
-            next = load();
+            load();
         }
-        const float a = x.lse * kLog2e, b = x.sink * kLog2e, top = fmaxf(a, b);
-        const float log = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
-        const bool used = x.used && log != -INFINITY;  // else a token that saw nothing
-        const int32_t lo = max(p.window > 0 && x.pos >= p.window ? x.pos - p.window + 1 : 0, x.rows_from);
-        const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, used ? lo : INT32_MIN);
-        const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, used ? x.pos : INT32_MAX);
-        const uint32_t in_use = __ballot_sync(0xFFFFFFFFu, used);
         const uint32_t slot = seq % kColSlots;
         if (seq >= kColSlots && !wait_all(&sh.col_free[slot], (seq / kColSlots - 1) & 1)) return false;
         Columns& co = sh.columns[slot];
-        co.log[col] = used ? log : 0.0f;
-        co.lo[col] = used ? lo : INT32_MAX;
-        co.hi[col] = used ? x.pos : -1;
-        if (lane == 0) {
-            (&co.all_lo.x)[warp] = all_lo;
-            (&co.all_hi.x)[warp] = all_hi;
-            (&co.all_used.x)[warp] = (int32_t)in_use;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const Column& x = now[u];
+            const int group32 = u * R::kColumnWarps + warp, col = group32 * kWarp + lane;
+            const float a = x.lse * kLog2e, b = x.sink * kLog2e, top = fmaxf(a, b);
+            const float log = a != a || b != b ? NAN : isinf(top) ? top : top + log2f(1.0f + exp2f(-fabsf(a - b)));
+            const bool used = x.used && log != -INFINITY;  // else a token that saw nothing
+            const int32_t lo = max(p.window > 0 && x.pos >= p.window ? x.pos - p.window + 1 : 0, x.rows_from);
+            const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, used ? lo : INT32_MIN);
+            const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, used ? x.pos : INT32_MAX);
+            const uint32_t in_use = __ballot_sync(0xFFFFFFFFu, used);
+            co.log[col] = used ? log : 0.0f;
+            co.lo[col] = used ? lo : INT32_MAX;
+            co.hi[col] = used ? x.pos : -1;
+            if (lane == 0) {
+                (&co.all_lo.x)[group32] = all_lo;
+                (&co.all_hi.x)[group32] = all_hi;
+                (&co.all_used.x)[group32] = (int32_t)in_use;
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.col_full[slot]);
         if (!ahead) {
             if (!next_tile()) return false;
-            if (!end) next = load();
+            if (!end) load();
         }
     }
     return true;
@@ -1159,7 +1175,7 @@ __global__ void __launch_bounds__(R::kThreads, 1)
             mbar_init(&sh.q_free[i], 1);
         }
         for (int i = 0; i < kColSlots; ++i) {
-            mbar_init(&sh.col_full[i], kCols / kWarp);
+            mbar_init(&sh.col_full[i], R::kColumnWarps);
             mbar_init(&sh.col_free[i], R::kSummers);
         }
         for (int i = 0; i < 2; ++i) {
