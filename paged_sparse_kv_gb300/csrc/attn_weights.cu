@@ -39,8 +39,8 @@
 // rest is queries: 4.3 GB of them pass through L2 and 4.0 GB come from memory, at 4.7 TB/s, as
 // CTAs are at different columns at a time.  203 tokens of 40 heads of 5 requests, over
 // 11061 to 30023 rows: 166 us, 1350 TFLOP/s.  64 single tokens of 64 heads, over
-// up to 8192 rows: 52 to 60 us from one machine to another for 177 MB, over 8192 rows each 78 us
-// for 306 MB, 3.9 TB/s of the 6.7 measured.  A tile takes some 5000 cycles, of which
+// up to 8192 rows: 50 to 55 us from one machine to another for 177 MB, over 8192 rows each 75 us
+// for 306 MB, 4.1 TB/s of the 6.7 measured.  A tile takes some 5000 cycles, of which
 // dequantising it is 2000 issue slots of each scheduler; the first one's sums come after 30000:
 // 17000 until the planning warp has found the range and published two tiles, mostly code that
 // is not in the instruction cache yet, then all SMs' first records at once.  One token
@@ -71,14 +71,16 @@ constexpr int kCols = 128;          // columns of a column tile, at most
 // Warps by role.  A CTA of its own has few columns per row and many tiles: at head_dim 512 16
 // warps dequantise and 4 sum up (64 single tokens of 64 heads over 8192 rows 81 us, 8 and 4 92,
 // 16 and 8 91), at 256 8 and 4 (60 us, 16 and 4 68).  A pair has many columns: 8 and 8 (203 tokens
-// of 40 heads of 5 requests 165 us, 16 and 8 184, 16 and 4 237).
+// of 40 heads of 5 requests 165 us, 16 and 8 184, 16 and 4 237).  Few warps for the columns leave
+// the others registers: at head_dim 512 one instead of two or four 75, 76 and 79 us (up to 8192
+// rows 55, 57 and 60), at 256 57, 53 and 53.
 template <int kHeadDim, bool kTwo>
 struct Roles {
     static constexpr int D = kHeadDim;
     static constexpr bool kPair = kTwo;
     static constexpr int kWorkers = !kPair && D == 512 ? 16 : 8, kParts = kWorkers / 4;  // each has D / kParts dims
     static constexpr int kSummers = kPair ? 8 : 4, kShares = kSummers / 4;              // of the columns
-    static constexpr int kColumnWarps = kPair ? 4 : 2;
+    static constexpr int kColumnWarps = kPair ? 4 : D == 512 ? 1 : 2;
     static constexpr int kColumnWarp = kWorkers + kSummers, kQueryWarp = kColumnWarp + kColumnWarps;
     static constexpr int kMmaWarp = kQueryWarp + 1, kPlanWarp = kMmaWarp + 1;
     static constexpr int kThreads = (kPlanWarp + 1) * kWarp;
