@@ -24,7 +24,7 @@
 // their rows into a ring.  Worker warps bring records into shared memory by
 // asynchronous copies (32 rows and a part of the dims each, a copy of the next tile issued as
 // soon as a block of 64 dims is read), dequantise them and write them to tensor memory; one
-// warp fetches queries by TMA into a ring of 128-dim stages, four prepare the columns'
+// warp fetches queries by TMA into a ring of 128-dim stages, one to four prepare the columns'
 // logarithms and bounds; one issues the MMAs; others turn scores into sums.  Queries stay in
 // the ring while the column tile does not change (a decode batch: one column tile per
 // request).  Every wait is bounded (2 s of wall time, counted in psk_device_wait_timeouts).
