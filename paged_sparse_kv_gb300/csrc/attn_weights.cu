@@ -18,7 +18,10 @@
 // Work.  Tiles and their column tiles stand in one sequence over all requests (a tile
 // counts kTileCost column tiles besides, its dequantisation), which is cut into one
 // equal range per CTA whatever the lengths are.  A tile cut between CTAs has its partial
-// sums written to the workspace; a second kernel adds them up in order.
+// sums written to the workspace; a second kernel adds them up in order.  Tiles that no token sees
+// rows of (before the windows, or of requests without tokens) go as runs to the warps that
+// sum up, which fade their rows: 1048576 rows 9.3 us, where the planning warp took 77 and
+// held the others up (for as long as a wait lasts from 75 GB of weights on).
 //
 // Roles.  One warp plans: it walks the CTA's range and puts tiles with the addresses of
 // their rows into a ring.  Worker warps bring records into shared memory by
@@ -127,12 +130,12 @@ struct Row {
     const uint8_t* scales;
 };
 
-// A step of the walk with columns, as the planning warp publishes it.
+// A step of the walk, as the planning warp publishes it.
 struct Tile {
     int32_t request;          // -1: the end
     int32_t first_row, end;   // its first row; the rows of the request that have a weight
     int32_t first, total;     // first token group and number of its column tiles
-    int32_t c0, c1;           // those of them that are this CTA's
+    int32_t c0, c1;           // those of them that are this CTA's; both 0: rows first_row to end have none
     int32_t tokens, token0, row0, replay;  // of the request
     int32_t kept, keeps;      // the first column tile is at hand; the last one is the next tile's first
     uint32_t there[4];        // rows with a page
@@ -284,23 +287,33 @@ __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const La
     return sum;
 }
 
-// A walk over the tiles of a range of the sequence.
+// A walk over the tiles of a range of the sequence.  A step is a tile with columns, or a run
+// of neighbouring ones that no token sees rows of.
 struct Walk {
     int64_t from, to;        // the range
     int64_t at;              // place of the current tile in the sequence
     int32_t r, k, tiles;     // request and tile; r < 0: past the end; tiles of the request
+    int32_t count;           // tiles of this step
     int32_t first, total;    // its token groups start at `first`; its column tiles
     int32_t c0, c1;          // those of them in the range
     Request q;
 
     __device__ __forceinline__ bool done() const { return r < 0; }
 
-    // Moves to the next tile of which something lies in the range; from a `tiles` of -1 to the
+    // Past the last tile of the run without columns that tile k is in: the first ones, before
+    // every window, or the last ones, behind all tokens of the call.
+    __device__ __forceinline__ int32_t run_end(const WeightParams& p, const LaunchShape& ls) const {
+        if (((int64_t)k << ls.row_shift) >= (int64_t)q.row0 + q.tokens) return tiles;
+        const int64_t n = ((int64_t)q.row0 - p.window + 1) >> ls.row_shift;
+        return q.tokens == 0 || n > tiles ? tiles : (int32_t)n;
+    }
+
+    // Moves to the next step of which something lies in the range; from a `tiles` of -1 to the
     // first, which lies in request r at place `at` or behind it.
     __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
         if (tiles >= 0) {
-            at += kTileCost + total;
-            ++k;
+            at += kTileCost * count + total;
+            k += count;
         }
         for (;;) {
             if (at >= to) {
@@ -330,10 +343,21 @@ struct Walk {
             int32_t groups;
             column_tiles(p, ls, q, k, first, groups);
             total = groups * ls.head_groups;
+            if (total == 0) {
+                const int32_t n = run_end(p, ls) - k;
+                const int32_t skip = from > at ? (int32_t)min(from - at, (int64_t)n) : 0;
+                count = (int32_t)min(to - at, (int64_t)n) - skip;
+                at += skip;
+                k += skip;
+                c0 = c1 = 0;
+                if (count > 0) return;
+                continue;
+            }
+            count = 1;
             const int64_t a = from - at - kTileCost, b = to - at - kTileCost;
             c0 = a > 0 ? (int32_t)(a < total ? a : total) : 0;
             c1 = b > 0 ? (int32_t)(b < total ? b : total) : 0;
-            if (total == 0 ? at >= from : c0 < c1) return;
+            if (c0 < c1) return;
             at += kTileCost + total;
             ++k;
         }
@@ -464,8 +488,9 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, W
     x.r = -1;
     int32_t page[kPer];  // of x
     bool kept = false, started = false;
+    const bool fades = p.decay != 1.0f || p.out != p.weights;  // else rows that no token sees stay as they are
     for (uint32_t n = 0;;) {
-        // on to the next tile with columns; those no token sees rows of are dealt with here
+        // on to the next tile with columns
         for (;;) {
             w.next(p, ls);
             if (!started) {
@@ -477,14 +502,22 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, W
                 }
             }
             if (w.done() || w.total > 0) break;
-            if (p.decay == 1.0f && p.out == p.weights) continue;
-#pragma unroll 1
-            for (int i = 0; i < kPer; ++i) {
-                const int32_t j = row_at(w, i);
-                if (j >= w.q.end) continue;
-                const float old = p.decay == 0.0f ? 0.0f : p.decay * p.weights[(int64_t)w.r * p.w_stride + j];
-                p.out[(int64_t)w.r * p.out_stride + j] = old;
+            if (!fades) continue;
+            const uint32_t slot = n % kTiles;
+            if (n >= kTiles && !wait_all(&sh.tile_free[slot], (n / kTiles - 1) & 1)) return false;
+            if (lane == 0) {
+                Tile& t = sh.tile[slot];
+                // a pair halves the rows
+                const int64_t from = (int64_t)w.k << ls.row_shift;
+                const int64_t to = min((int64_t)w.q.end, from + ((int64_t)w.count << ls.row_shift));
+                const int64_t half = (to - from + 1) / 2, rank = blockIdx.x % ls.ranks;
+                t.request = w.r;
+                t.first_row = (int32_t)(from + rank * half);
+                t.end = (int32_t)(rank + 1 < ls.ranks ? from + half : to);
+                t.c0 = t.c1 = t.kept = 0;
+                mbar_arrive(&sh.tile_full[slot]);
             }
+            ++n;
         }
         if (!x.done()) {
             const uint32_t slot = n % kTiles;
@@ -549,6 +582,14 @@ struct Tiles {
     uint32_t n = 0;
     __device__ __forceinline__ bool wait(Shared& sh) const { return wait_all(&sh.tile_full[n % kTiles], (n / kTiles) & 1); }
     __device__ __forceinline__ const Tile& at(const Shared& sh) const { return sh.tile[n % kTiles]; }
+    // The next one with columns, or the end.
+    __device__ __forceinline__ bool wait_columns(Shared& sh) {
+        for (;;) {
+            if (!wait(sh)) return false;
+            if (at(sh).request < 0 || at(sh).c0 < at(sh).c1) return true;
+            next(sh);
+        }
+    }
     // The tile has been read (by this warp).
     __device__ __forceinline__ void next(Shared& sh) {
         __syncwarp();
@@ -659,7 +700,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
         if (lane == 0) arrive_leader<kPair>(&sh.k_full[b]);
     };
     Tiles tiles;
-    if (!tiles.wait(sh)) return false;
+    if (!tiles.wait_columns(sh)) return false;
     if (tiles.at(sh).request < 0) return true;
     for (int b = 0; b < kBlocks; ++b) {
         fetch(tiles.at(sh), b);
@@ -668,7 +709,7 @@ __device__ bool work(const WeightParams& p, const LaunchShape& ls, Shared& sh, u
     uint2 scales = load_scales(tiles.at(sh).row[quad * kWarp + lane].scales);
     tiles.next(sh);
     for (uint32_t step = 0;; ++step) {
-        if (!tiles.wait(sh)) return false;
+        if (!tiles.wait_columns(sh)) return false;
         const bool more = tiles.at(sh).request >= 0;
         uint2 next_scales = make_uint2(0, 0);
         if (more) next_scales = load_scales(tiles.at(sh).row[quad * kWarp + lane].scales);
@@ -966,7 +1007,7 @@ __device__ bool issue(const LaunchShape& ls, Shared& sh, uint32_t ring, uint32_t
     uint32_t stage = 0, round = 0, step = 0, tile = 0;
     Tiles tiles;
     for (;;) {
-        if (!tiles.wait(sh)) return false;
+        if (!tiles.wait_columns(sh)) return false;
         const Tile& t = tiles.at(sh);
         if (t.request < 0) return true;
         const int32_t c0 = t.c0, c1 = t.c1, first = t.first, tokens = t.tokens;
@@ -1023,6 +1064,22 @@ struct Sum {
     }
 };
 
+// Rows [j, end) of a request that no token of the call sees: every `step`-th is this thread's.
+__device__ __forceinline__ void fade(const WeightParams& p, int32_t request, int64_t j, int32_t end, int32_t step) {
+    constexpr int kAtOnce = 4;
+    const float* from = p.weights + (int64_t)request * p.w_stride;
+    float* to = p.out + (int64_t)request * p.out_stride;
+#pragma unroll 1
+    for (; j < end; j += kAtOnce * step) {
+        float v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) v[i] = p.decay != 0.0f && j + i * step < end ? p.decay * from[j + i * step] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (j + i * step < end) to[j + i * step] = v[i];
+    }
+}
+
 template <class R>
 __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& sh, uint32_t tmem_s) {
     constexpr bool kPair = R::kPair;
@@ -1031,11 +1088,17 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
     uint32_t step = 0, seq = 0, tile = 0;
     bool loaded = false;
     Tiles tiles;
-    for (;; ++tile) {
+    for (;;) {
         if (!tiles.wait(sh)) return false;
         const Tile& t = tiles.at(sh);
         const int32_t request = t.request;
         if (request < 0) return true;
+        if (t.c0 == t.c1) {
+            const int32_t first_row = t.first_row, end = t.end;
+            tiles.next(sh);
+            fade(p, request, (int64_t)first_row + warp * kWarp + lane, end, R::kSummers * kWarp);
+            continue;
+        }
         const int32_t c0 = t.c0, c1 = t.c1, first = t.first, tokens = t.tokens;
         const bool ok = t.there[quad] >> lane & 1, whole = c0 == 0 && c1 == t.total, keeps = t.keeps;
         const int32_t j = t.first_row + quad * kWarp + lane;
@@ -1127,6 +1190,7 @@ __device__ bool summarise(const WeightParams& p, const LaunchShape& ls, Shared& 
                 ls.parts[((int64_t)blockIdx.x * 2 + (c0 > 0 ? 0 : 1)) * kTile + quad * kWarp + lane] = total;
             }
         }
+        ++tile;
     }
 }
 
