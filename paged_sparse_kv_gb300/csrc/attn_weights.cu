@@ -232,24 +232,29 @@ __device__ __forceinline__ void column_tiles(const WeightParams& p, const Launch
     groups = i1 > i0 ? divide(i1 - 1, ls.by_tokens) + 1 - first : 0;
 }
 
-// The first `count` tiles of a request that cost the same, and that cost.  The others are
-// few (rows of the new tokens, and of their windows) and are counted one by one.
-__device__ __forceinline__ void even_tiles(const WeightParams& p, const LaunchShape& ls, const Request& q, int32_t tiles,
-                                           int32_t& count, int64_t& cost) {
-    int64_t n;
-    if (p.window > 0) {  // tiles before every window
-        n = ((int64_t)q.row0 - p.window + 1) >> ls.row_shift;
-        cost = kTileCost;
-    } else {             // tiles all tokens see
-        const int64_t x = (int64_t)q.row0 + min(ls.tokens, q.tokens) - 1;
-        n = (x >> ls.row_shift) + 1;
-        cost = kTileCost + (int64_t)(q.tokens > 0 ? divide(q.tokens - 1, ls.by_tokens) + 1 : 0) * ls.head_groups;
+// Tiles of a request that cost the same: the first `blind`, which no token sees rows of, and
+// those from `first` to `end`, which all column tiles see rows of, at even_cost each.  The others are
+// few (rows of the new tokens, and where their windows begin) and are counted one by one: with
+// all tiles of a windowed request one token over 1048576 rows took 1355 us, where 131 do.
+struct Even {
+    int32_t blind, first, end;
+};
+
+__device__ __forceinline__ int64_t even_cost(const LaunchShape& ls, const Request& q) {
+    return kTileCost + (int64_t)(q.tokens > 0 ? divide(q.tokens - 1, ls.by_tokens) + 1 : 0) * ls.head_groups;
+}
+
+__device__ __forceinline__ Even even_tiles(const WeightParams& p, const LaunchShape& ls, const Request& q, int32_t tiles) {
+    if (q.tokens == 0) return {tiles, tiles, tiles};
+    const auto bounded = [](int64_t n, int32_t lo, int32_t hi) { return n < lo ? lo : n > hi ? hi : (int32_t)n; };
+    Even e{0, 0, 0};
+    if (p.window > 0) {
+        e.blind = bounded(((int64_t)q.row0 - p.window + 1) >> ls.row_shift, 0, tiles);
+        e.first = bounded(((int64_t)q.row0 + q.tokens - p.window) >> ls.row_shift, e.blind, tiles);
     }
-    count = n < 0 || q.tokens == 0 ? 0 : n > tiles ? tiles : (int32_t)n;
-    if (q.tokens == 0) {
-        count = tiles;
-        cost = kTileCost;
-    }
+    const int64_t last = (int64_t)q.row0 + min(ls.tokens, q.tokens) - 1;  // of the first token group
+    e.end = bounded((last >> ls.row_shift) + 1, e.first, tiles);
+    return e;
 }
 
 __device__ __forceinline__ int32_t tiles_of(const LaunchShape& ls, const Request& q) {
@@ -260,24 +265,28 @@ __device__ __forceinline__ int32_t tiles_of(const LaunchShape& ls, const Request
 __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const LaunchShape& ls, int32_t r) {
     const int lane = threadIdx.x % kWarp;
     Request q{};
-    int32_t tiles = 0, even = 0;
-    int64_t cost = 0, sum = 0;
+    int32_t uneven = 0;
+    Even e{};
+    int64_t sum = 0;
     if (r < p.num_reqs) {
         q = load_request(p, r);
-        tiles = tiles_of(ls, q);
-        even_tiles(p, ls, q, tiles, even, cost);
-        sum = cost * even;
+        const int32_t tiles = tiles_of(ls, q);
+        e = even_tiles(p, ls, q, tiles);
+        uneven = tiles - e.blind - (e.end - e.first);
+        sum = (int64_t)kTileCost * e.blind + even_cost(ls, q) * (e.end - e.first);
     }
     // the uneven tiles of a request, 32 at a time
-    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, even < tiles); rest; rest &= rest - 1) {
+    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, uneven > 0); rest; rest &= rest - 1) {
         const int src = __ffs(rest) - 1;
         Request x{};
         x.tokens = __shfl_sync(0xFFFFFFFFu, q.tokens, src);
         x.row0 = __shfl_sync(0xFFFFFFFFu, q.row0, src);
-        const int32_t a = __shfl_sync(0xFFFFFFFFu, even, src), b = __shfl_sync(0xFFFFFFFFu, tiles, src);
+        const int32_t blind = __shfl_sync(0xFFFFFFFFu, e.blind, src), n = __shfl_sync(0xFFFFFFFFu, uneven, src);
+        const int32_t from = __shfl_sync(0xFFFFFFFFu, e.first, src), even = __shfl_sync(0xFFFFFFFFu, e.end, src) - from;
         int64_t mine = 0;
-        for (int32_t k = a + lane; k < b; k += kWarp) {
-            int32_t first, groups;
+        for (int32_t i = lane; i < n; i += kWarp) {
+            int32_t first, groups, k = blind + i;
+            if (k >= from) k += even;
             column_tiles(p, ls, x, k, first, groups);
             mine += kTileCost + (int64_t)groups * ls.head_groups;
         }
@@ -290,8 +299,7 @@ __device__ __forceinline__ int64_t request_costs(const WeightParams& p, const La
 // A walk over the tiles of a range of the sequence.  A step is a tile with columns, or a run
 // of neighbouring ones that no token sees rows of.
 struct Walk {
-    int64_t from, to;        // the range
-    int64_t at;              // place of the current tile in the sequence
+    int64_t ahead, left;     // from the current tile to the range's start and to its end
     int32_t r, k, tiles;     // request and tile; r < 0: past the end; tiles of the request
     int32_t count;           // tiles of this step
     int32_t first, total;    // its token groups start at `first`; its column tiles
@@ -308,36 +316,57 @@ struct Walk {
         return q.tokens == 0 || n > tiles ? tiles : (int32_t)n;
     }
 
-    // Moves to the next step of which something lies in the range; from a `tiles` of -1 to the
-    // first, which lies in request r at place `at` or behind it.
-    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
-        if (tiles >= 0) {
-            at += kTileCost * count + total;
-            k += count;
+    __device__ __forceinline__ void pass(int64_t cost) {
+        ahead -= cost;
+        left -= cost;
+    }
+
+    __device__ __forceinline__ void load(const WeightParams& p, const LaunchShape& ls) {
+        q = load_request(p, r);
+        tiles = tiles_of(ls, q);
+        k = 0;
+    }
+
+    // Takes up the walk at the start of request r, in which the range starts, and passes over whole
+    // tiles before it.
+    __device__ __forceinline__ void start(const WeightParams& p, const LaunchShape& ls) {
+        count = total = tiles = k = 0;
+        if (left <= 0) return;
+        load(p, ls);
+        const Even e = even_tiles(p, ls, q, tiles);
+        k = (int32_t)min(ahead / kTileCost, (int64_t)e.blind);
+        pass((int64_t)kTileCost * k);
+        if (k < e.blind) return;
+#pragma unroll 1
+        for (; k < e.first; ++k) {
+            int32_t groups;
+            column_tiles(p, ls, q, k, first, groups);
+            const int32_t cost = kTileCost + groups * ls.head_groups;
+            if (ahead < cost) return;
+            pass(cost);
         }
+        const int64_t cost = even_cost(ls, q);
+        const int64_t skip = (ahead | cost) >> 32 == 0 ? (int64_t)((uint32_t)ahead / (uint32_t)cost) : ahead / cost;
+        const int32_t n = (int32_t)min(skip, (int64_t)(e.end - e.first));
+        k += n;
+        pass(cost * n);
+    }
+
+    // Moves to the next step of which something lies in the range.
+    __device__ __forceinline__ void next(const WeightParams& p, const LaunchShape& ls) {
+        pass(kTileCost * count + total);
+        k += count;
         for (;;) {
-            if (at >= to) {
+            if (left <= 0) {
                 r = -1;
                 return;
             }
             if (k >= tiles) {
-                if (tiles >= 0 && ++r >= p.num_reqs) {
+                if (++r >= p.num_reqs) {
                     r = -1;
                     return;
                 }
-                const bool first_of_all = tiles < 0;
-                q = load_request(p, r);
-                tiles = tiles_of(ls, q);
-                k = 0;
-                if (first_of_all) {
-                    int32_t even;
-                    int64_t cost;
-                    even_tiles(p, ls, q, tiles, even, cost);
-                    const int64_t ahead = from - at;
-                    const int64_t skip = (ahead | cost) >> 32 == 0 ? (int64_t)((uint32_t)ahead / (uint32_t)cost) : ahead / cost;
-                    k = skip < even ? (int32_t)skip : even;
-                    at += cost * k;
-                }
+                load(p, ls);
                 continue;
             }
             int32_t groups;
@@ -345,20 +374,20 @@ struct Walk {
             total = groups * ls.head_groups;
             if (total == 0) {
                 const int32_t n = run_end(p, ls) - k;
-                const int32_t skip = from > at ? (int32_t)min(from - at, (int64_t)n) : 0;
-                count = (int32_t)min(to - at, (int64_t)n) - skip;
-                at += skip;
+                const int32_t skip = ahead > 0 ? (int32_t)min(ahead, (int64_t)n) : 0;
+                count = (int32_t)min(left, (int64_t)n) - skip;
+                pass(skip);
                 k += skip;
                 c0 = c1 = 0;
                 if (count > 0) return;
                 continue;
             }
             count = 1;
-            const int64_t a = from - at - kTileCost, b = to - at - kTileCost;
+            const int64_t a = ahead - kTileCost, b = left - kTileCost;
             c0 = a > 0 ? (int32_t)(a < total ? a : total) : 0;
             c1 = b > 0 ? (int32_t)(b < total ? b : total) : 0;
             if (c0 < c1) return;
-            at += kTileCost + total;
+            pass(kTileCost + total);
             ++k;
         }
     }
@@ -398,17 +427,17 @@ __device__ __forceinline__ void find_range_of_few(const WeightParams& p, const L
         all = __shfl_sync(0xFFFFFFFFu, all + sum, kWarp - 1);
     }
     const int64_t b = blockIdx.x / ls.ranks, n = gridDim.x / ls.ranks;
-    w.from = share(all, b, n);
-    w.to = share(all, b + 1, n);
+    const int64_t from = share(all, b, n);
     w.r = 0;
-    w.at = 0;
+    w.ahead = from;
+    w.left = share(all, b + 1, n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t here = __ballot_sync(0xFFFFFFFFu, at[i] <= w.from && w.from < at[i] + cost[i]);
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, at[i] <= from && from < at[i] + cost[i]);
         if (here) {
             const int src = __ffs(here) - 1;
             w.r = i * kWarp + src;
-            w.at = __shfl_sync(0xFFFFFFFFu, at[i], src);
+            w.pass(__shfl_sync(0xFFFFFFFFu, at[i], src));
         }
     }
 }
@@ -483,8 +512,8 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, W
     // row i * 32 + lane of this CTA's part of the tile
     const int32_t mine = (int32_t)(blockIdx.x % ls.ranks) * kTile + lane;
     const auto row_at = [&](const Walk& x, int i) { return (int32_t)min(((int64_t)x.k << ls.row_shift) + mine + i * kWarp, (int64_t)INT32_MAX); };
+    w.start(p, ls);
     Walk x;  // the tile before the walk's, which is to be published
-    w.tiles = -1;
     x.r = -1;
     int32_t page[kPer];  // of x
     bool kept = false, started = false;
@@ -496,7 +525,7 @@ __device__ bool plan(const WeightParams& p, const LaunchShape& ls, Shared& sh, W
             if (!started) {
                 started = true;
                 if (lane == 0) {
-                    Record rec{w.from >= w.to ? kEmptyRange : kNone, 0, 0, 0};
+                    Record rec{w.ahead >= w.left ? kEmptyRange : kNone, 0, 0, 0};
                     if (!w.done() && w.c0 > 0) rec = {w.c1 == w.total ? kEnds : kMiddle, w.r, w.k, 0};
                     ls.records[blockIdx.x] = rec;
                 }
@@ -1266,9 +1295,9 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     pdl_launch_dependents();
     Walk walk{};
     if (p.num_reqs > kFewRequests) {
-        find_range<R::kThreads>(p, ls, sh, walk.from, walk.to);
+        find_range<R::kThreads>(p, ls, sh, walk.ahead, walk.left);
         walk.r = sh.first_request;
-        walk.at = sh.first_at;
+        walk.pass(sh.first_at);
     } else if (warp == kPlanWarp) {
         find_range_of_few(p, ls, walk);
     }

@@ -19,6 +19,14 @@ def test_long_contexts_short_windows(cuda_device, q_lens, prefix, H, D, window, 
     _run(cuda_device, sum(prefix), q_lens, prefix, H, D, window=window, decay=decay, place=place)
 
 
+@pytest.mark.parametrize("q_lens,prefix,H,D,window", [
+    ([1], [40000], 16, 128, 20000), ([1, 2, 1], [30000, 12345, 700], 8, 128, 12000), ([300], [20000], 4, 128, 9000),
+    ([5, 1], [17000, 9000], 40, 128, 16900), ([40], [9000], 16, 256, 9041), ([3], [9000], 129, 128, 8000), ([2], [100], 1, 128, 2**31 - 1)])
+@pytest.mark.parametrize("decay,place", [(0.5, "in"), (1.0, "out")])
+def test_long_windows(cuda_device, q_lens, prefix, H, D, window, decay, place):
+    _run(cuda_device, window % 1000, q_lens, prefix, H, D, window=window, decay=decay, place=place)
+
+
 def _no_tokens(dev, w, seq, decay, out, tokens=0, H=1, window=0):
     """The call over rows without a page; `tokens` new ones of the last request."""
     R = len(seq)
@@ -46,24 +54,42 @@ def test_millions_of_rows(cuda_device, tokens, H, window, decay, place):
     assert torch.equal(big[:, 0], left) and torch.equal(big[:, 1 + W:], right)
 
 
+def _best(call, times=4):
+    """Least time of a call, in ms."""
+    res = []
+    for _ in range(times):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        res.append(a.elapsed_time(b))
+    return min(res)
+
+
 def test_fading_holds_no_other_role_up(cuda_device):
     """What waits for the walk over such rows waits 2 s at most, so the walk must not do the
     fading itself: 2^28 rows took it 80 times what a plain product takes."""
     d, n = cuda_device, 1 << 28
     w = torch.ones((1, n), device=d)
 
-    def best(call):
-        times = []
-        for _ in range(4):
-            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            a.record()
-            call()
-            b.record()
-            torch.cuda.synchronize()
-            times.append(a.elapsed_time(b))
-        return min(times)
-
-    product = best(lambda: w.mul_(0.5))
-    own = best(lambda: _no_tokens(d, w, [n], 0.5, None))
+    product = _best(lambda: w.mul_(0.5))
+    own = _best(lambda: _no_tokens(d, w, [n], 0.5, None))
     assert own < 25 * product, (own, product)
     assert bool((w == 2.0 ** -8).all())
+
+
+def test_a_window_past_the_context_is_none(cuda_device):
+    """The same bits as without one, and no walk over each tile by itself (10 times the time)."""
+    d, n, pages = cuda_device, 1 << 20, 1024
+    g = torch.Generator("cuda").manual_seed(2)
+    cache = torch.zeros((pages, 64 * 194), dtype=torch.uint8, device=d)
+    cache[:, :64 * 192:2] = torch.randint(0, 0x40, (pages, 64 * 96), generator=g, device=d, dtype=torch.uint8)
+    cache[:, 64 * 192:] = 127
+    table = torch.randint(0, pages, (1, n // 64), generator=g, device=d, dtype=torch.int32)
+    q, lse = torch.randn((1, 16, 128), generator=g, device=d).to(BF16), torch.full((1, 16), 9.0, device=d)
+    args = (q, lse, cache, _i32([0, 1], d), _i32([n], d), table, 64)
+    out = [torch.zeros((1, n), device=d) for _ in range(2)]
+    times = [_best(lambda: ops.accumulate_attention_weights(*args, o.zero_(), window_size=w)) for o, w in zip(out, (0, n))]
+    assert torch.equal(*out) and bool((out[0] > 0).all())
+    assert times[1] < 3 * times[0], times
