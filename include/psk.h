@@ -869,7 +869,7 @@ psk_status chunk_mla_attention(
  *   cos_sin_cache  binary32 [num_pos, rope_dim], row stride cs_stride (written):
  *                  with n = rope_dim / 2, i < n and pos = first_pos + row,
  *                    row[i] = m cos(pos f_i),  row[n + i] = m sin(pos f_i).
- *                  Angles are reduced exactly; a value is off by at most m 2^-22.
+ *                  A value is off by at most m 2^-22, at every position.
  *   first_pos, num_pos  0 <= first_pos, first_pos + num_pos <= 2^31.
  *   rope_dim       even, in [2, 512].
  *   theta          base > 1: f_i = theta^(-2i / rope_dim) where unscaled.
@@ -882,7 +882,7 @@ psk_status chunk_mla_attention(
  *                  their frequency, those that make fewer than beta_slow are stretched.
  *   factor         >= 1 (not used unscaled); original_max_pos >= 1 and
  *                  beta_fast >= beta_slow > 0 (used by PSK_ROPE_YARN alone).
- *   attention_factor  m, finite and > 0.
+ *   attention_factor  m is this in binary32, finite and > 0.
  */
 psk_status build_rope_cos_sin_cache(
     float* cos_sin_cache, int64_t cs_stride, int64_t first_pos, int64_t num_pos,

@@ -126,6 +126,53 @@ psk_status check_rotary(const void* in, int64_t it, int64_t ih, const void* out,
     return PSK_OK;
 }
 
+// A number as the unevaluated sum of two doubles, |lo| <= ulp(hi) / 2: 106 bits (Dekker's sums, Knuth's
+// error of a sum, the error of a product by a fused multiply-add).
+struct Wide {
+    double hi, lo;
+};
+
+Wide normal(double a, double b) {
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+
+Wide operator+(Wide a, Wide b) {
+    const double s = a.hi + b.hi, v = s - a.hi;
+    return normal(s, ((a.hi - (s - v)) + (b.hi - v)) + (a.lo + b.lo));
+}
+
+Wide operator*(Wide a, Wide b) {
+    const double p = a.hi * b.hi;
+    return normal(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+Wide operator/(Wide a, double b) {
+    const double q = a.hi / b;
+    return normal(q, (std::fma(-q, b, a.hi) + a.lo) / b);
+}
+
+// theta^(-1/n), n <= 256: Newton's step from the nearest double.  The powers are of a number in [1/2, 1),
+// with the exponents of two apart, so that none underflows.
+Wide inverse_root(double theta, int32_t n) {
+    int e0, e1;
+    const double x = std::frexp(std::pow(theta, -1.0 / n), &e0), t = std::frexp(theta, &e1);
+    Wide power = {t, 0.0}, square = {x, 0.0};
+    for (int32_t bits = n; bits != 0; bits /= 2, square = square * square)
+        if (bits % 2 != 0) power = power * square;
+    const int e = e0 * n + e1;
+    power = {std::ldexp(power.hi, e), std::ldexp(power.lo, e)};  // x^n theta, nearly 1
+    const double off = (power.hi - 1.0) + power.lo;
+    const Wide root = normal(x, -x * off / n);
+    return {std::ldexp(root.hi, e0), std::ldexp(root.lo, e0)};
+}
+
+// 2^64 w, rounded; 0 <= w < 1.
+uint64_t fraction64(Wide w) {
+    const double a = std::ldexp(w.hi, 64), whole = std::floor(a);
+    return (uint64_t)whole + (uint64_t)(int64_t)std::floor((a - whole) + std::ldexp(w.lo, 64) + 0.5);
+}
+
 // The largest number of positions a token of a call can see.
 int64_t chunk_max_keys(int32_t bt_width, int32_t block_size, int32_t window) {
     const int64_t all = (int64_t)bt_width * block_size;
@@ -1150,6 +1197,8 @@ psk_status build_rope_cos_sin_cache(float* cos_sin_cache, int64_t cs_stride, int
     if (num_pos == 0) return ok();
     CHECK(cos_sin_cache != nullptr && aligned(cos_sin_cache, 4), "cos_sin_cache must be non-null and 4-byte aligned");
     constexpr double kTwoPi = 6.283185307179586476925286766559;
+    // 1 / (2 pi): the double next to it, and what that leaves
+    const Wide per_radian = {0.15915494309189535, -9.8393383375912430e-18};
     psk::RopeTableParams p{};
     p.out = cos_sin_cache;
     p.stride = cs_stride;
@@ -1165,12 +1214,19 @@ psk_status build_rope_cos_sin_cache(float* cos_sin_cache, int64_t cs_stride, int
         lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
         span = std::fmax(std::fmin(std::ceil(pair_of(beta_slow)), rope_dim - 1.0) - lo, 0.001);
     }
-    for (int32_t i = 0; i < p.pairs; ++i) {
-        const double f = std::pow(theta, -2.0 * i / rope_dim);
-        const double g = scaling == PSK_ROPE_YARN ? std::fmin(std::fmax((i - lo) / span, 0.0), 1.0)
-                                                  : scaling == PSK_ROPE_LINEAR ? 1.0 : 0.0;
-        const double turns = (scaling == PSK_ROPE_UNSCALED ? f : f * (1.0 - g) + f / factor * g) / kTwoPi;
-        p.turn[i] = (uint64_t)std::ldexp(turns, 64);
+    // A position of 2^31 turns by the error of a frequency 2^31 times over: in doubles that came to
+    // 3.1e-7 of an angle, more than binary32 gives away.
+    const Wide ratio = inverse_root(theta, p.pairs);
+    Wide f = {1.0, 0.0};  // theta^(-2 i / rope_dim)
+    for (int32_t i = 0; i < p.pairs; ++i, f = f * ratio) {
+        Wide scaled = f;
+        if (scaling == PSK_ROPE_LINEAR || (scaling == PSK_ROPE_YARN && i - lo >= span)) {
+            scaled = f / factor;
+        } else if (scaling == PSK_ROPE_YARN && i > lo) {
+            const Wide g = Wide{i - lo, 0.0} / span, rest = Wide{1.0, 0.0} + Wide{-g.hi, -g.lo};
+            scaled = f * (rest + g / factor);
+        }
+        p.turn[i] = fraction64(scaled * per_radian);
     }
     return cuda_status(psk::launch_rope_table(p, reinterpret_cast<cudaStream_t>(stream)),
                        "build_rope_cos_sin_cache launch");
