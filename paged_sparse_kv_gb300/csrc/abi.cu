@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 #include <string>
+#include <utility>
 
 #include "attention.h"
 #include "attn_weights.h"
@@ -110,6 +111,22 @@ psk_status check_attention(const psk::AttnParams& p, bool work, int64_t workspac
     return PSK_OK;
 }
 
+// Whether rows of `dim` elements share memory, `rows` of them t apart in each of `heads` groups that are h
+// apart; both at least dim.
+bool rows_overlap(int64_t rows, int64_t t, int64_t heads, int64_t h, int64_t dim) {
+    if (rows <= 1 || heads <= 1 || t >= (heads - 1) * h + dim || h >= (rows - 1) * t + dim) return false;
+    if (rows < heads) {
+        std::swap(rows, heads);
+        std::swap(t, h);
+    }
+    for (int64_t b = 1; b < heads; ++b) {  // b groups on, the nearest rows: a and a + 1
+        const int64_t a = b * h / t, rest = b * h % t;
+        if (a >= rows) break;
+        if ((a >= 1 && rest < dim) || (a + 1 < rows && t - rest < dim)) return true;
+    }
+    return false;
+}
+
 // The strides of one of apply_rotary_embedding's tensors, in elements of `size` bytes.
 psk_status check_rotary(const void* in, int64_t it, int64_t ih, const void* out, int64_t ot, int64_t oh,
                         int32_t heads, int64_t num_tokens, int32_t head_dim, int32_t size, const char* name) {
@@ -118,9 +135,11 @@ psk_status check_rotary(const void* in, int64_t it, int64_t ih, const void* out,
     CHECK(aligned(in, size) && aligned(out, size), "%s and its output must be aligned to their elements", name);
     CHECK(it >= 0 && ih >= 0 && ot >= 0 && oh >= 0, "strides of %s must not be negative", name);
     const int64_t most = INT64_MAX / 8;
-    CHECK(it <= most && ih <= most && ot <= most && oh <= most, "strides of %s overflow", name);
+    const int64_t most_t = num_tokens > 1 ? most / (num_tokens - 1) : most, most_h = heads > 1 ? most / (heads - 1) : most;
+    CHECK(it <= most_t && ih <= most_h && ot <= most_t && oh <= most_h, "strides of %s overflow", name);
     CHECK((num_tokens <= 1 || ot >= head_dim) && (heads <= 1 || oh >= head_dim),
           "output strides of %s must be at least head_dim", name);
+    CHECK(!rows_overlap(num_tokens, ot, heads, oh, head_dim), "output rows of %s must not overlap", name);
     CHECK(in != out || ((num_tokens <= 1 || it == ot) && (heads <= 1 || ih == oh)),
           "%s in place needs equal strides", name);
     return PSK_OK;
