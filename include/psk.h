@@ -943,6 +943,9 @@ psk_status apply_rotary_embedding(
  *   [max(replay_start[r], pos - window + 1, 0), pos] that have a page; none where
  *   is_valid_token[t] is 0.  A row nobody sees has the sum 0.  Other entries of out
  *   are left as they were.
+ *   The rows of the chunk's own tokens are rows like the others: what weights holds for
+ *   them is added to, so the caller sets it to 0 before.  After an eviction it is what a
+ *   row that has moved or gone has left there.
  *   Products are exact in bf16 operands, sums are binary32; a row's sum is formed in
  *   an order that depends on the sizes and the device alone.
  *
@@ -1004,7 +1007,14 @@ psk_status accumulate_attention_weights(
  *                  any order.
  *   num_moves, seq_lens_out  int32 [num_reqs].  seq_lens_out may be seq_lens; they must
  *                  not overlap the other arrays or each other.
- *   The pages past ceil(m / block_size) of a request hold nothing any more.
+ *   The pages past ceil(m / block_size) of a request hold nothing any more.  Entries
+ *   [m, seq_lens[r]) of weights and row_positions are those of rows that have moved or
+ *   gone: before the next accumulation and selection the caller writes the entries of
+ *   the rows that new tokens take there (weight 0, and their position).
+ *   Rows stand in no order of positions afterwards.  chunk_mla_attention and
+ *   accumulate_attention_weights over all rows are right over such a cache, as a new
+ *   token's row still is the last; window and replay_start, the index builders for sliding
+ *   windows and top-k rows, and the positions of compute_slot_mappings count rows.
  *   0 <= width <= 2^30; num_reqs <= 2^27.
  */
 psk_status select_cache_evictions(

@@ -1016,7 +1016,10 @@ def accumulate_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torc
     """``decay * weights`` [R, W] plus the attention each cached row got from the new tokens ``q``
     [T, H, D], summed over tokens and heads: a chunk as chunk_mla_attention took it, with the
     ``lse`` [T, H] it returned.  In place unless ``out`` is given; entries past ``seq_lens`` are left
-    as they were.  ``workspace`` (uint8) is scratch; two calls that can run at once need one each."""
+    as they were.  The new tokens' own rows add to what ``weights`` holds there like any other, so the
+    caller sets them to 0 first (see select_cache_evictions).  ``window_size`` and ``replay_start`` count
+    rows, which after an eviction are not positions.  ``workspace`` (uint8) is scratch; two calls that
+    can run at once need one each."""
     i, i32 = _index(q), torch.int32
     qa = _heads(q, "q", i)
     T, H, D = q.shape
@@ -1066,7 +1069,27 @@ def select_cache_evictions(weights: torch.Tensor, seq_lens: torch.Tensor, keep_l
     first ``num_first`` positions and the ``num_recent`` newest ones protected) and the moves that
     bring them below the new length.  ``weights`` and ``row_positions`` are updated in place unless
     ``weights_out`` / ``positions_out`` are given.  Returns (moves [R, W // 2, 2] of which
-    ``num_moves`` are set, num_moves [R], seq_lens [R], weights, row_positions)."""
+    ``num_moves`` are set, num_moves [R], seq_lens [R], weights, row_positions).
+
+    Entries from the new length on keep what they held, weights and positions of rows that have moved
+    or gone: the caller writes those of the rows that new tokens take there.  Rows then stand in no
+    order of positions, so calls that take a row for its position (windows, replay starts, top-k and
+    sliding-window indices, the positions of compute_slot_mappings) see rows.  A step over a cache of
+    at most ``keep`` [R] rows a request, ``lens`` [R] of which are there, with new tokens at ``positions``
+    (none of them padding)::
+
+        ops.apply_rotary_embedding(positions, q, cos_sin, k, q_out=q, k_out=k)  # the last 64 dims
+        seq_lens = lens + qsl.diff()
+        rows, req, slots, _ = ops.compute_slot_mappings(qsl, seq_lens, table, 64, q.shape[0])
+        ops.quantize_and_insert_k_cache(k, cache, slots, 64)
+        at = req.long(), rows  # of the new rows, over what an evicted row may have left there
+        weights[at], row_positions[at] = 0.0, positions.int()
+        out, lse = ops.chunk_mla_attention(q, cache, qsl, seq_lens, req, table, 64)
+        ops.accumulate_attention_weights(q, lse, cache, qsl, seq_lens, table, 64, weights)
+        moves, counts, lens, _, _ = ops.select_cache_evictions(
+            weights, seq_lens, keep, row_positions=row_positions, num_first=4, num_recent=64)
+        ops.move_cache_rows(cache, table, moves, counts, 64, 512)
+    """
     i, i32 = _index(weights), torch.int32
     dev, R = weights.device, seq_lens.numel()
     width = weights.shape[1] if weights.dim() == 2 else 0
