@@ -323,13 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
 // CTAs an SM to cover it.  One record in each of 64 requests: 2.9 us.
 constexpr int kMoves = 32, kMoveThreads = 256;
 
+// Of a request; max_moves may be all 31 bits.
+__host__ __device__ __forceinline__ int32_t move_tiles(const MoveParams& p) {
+    return p.max_moves / kMoves + (p.max_moves % kMoves != 0);
+}
+
 template <typename Unit>  // of the scales
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
     __shared__ int64_t s_at[kMoves][4];  // data from, data to, scales from, scales to; -1: no page
     pdl_wait();
     const int32_t pieces = p.data_bytes / 16, scales = p.scale_bytes / (int32_t)sizeof(Unit);
     const int32_t per = pieces + scales;
-    const int32_t tiles = (p.max_moves + kMoves - 1) / kMoves;
+    const int32_t tiles = move_tiles(p);
     // the first tiles of all requests come first: the filled ones spread evenly over the CTAs
     for (int64_t id = blockIdx.x; id < (int64_t)tiles * p.num_reqs; id += gridDim.x) {
         const int32_t r = (int32_t)(id % p.num_reqs), first = (int32_t)(id / p.num_reqs) * kMoves;
@@ -417,7 +422,7 @@ cudaError_t launch_select_evictions(const SelectParams& p, cudaStream_t stream) 
 
 cudaError_t launch_move_rows(MoveParams p, cudaStream_t stream) {
     p.shift = log2_if_pow2(p.block_size);
-    const int64_t tiles = (int64_t)((p.max_moves + kMoves - 1) / kMoves) * p.num_reqs, most = (int64_t)sm_count() * 8;
+    const int64_t tiles = (int64_t)move_tiles(p) * p.num_reqs, most = (int64_t)sm_count() * 8;
     const dim3 grid((unsigned)(tiles < most ? tiles : most));
     auto* k = p.scale_bytes >= 16  ? move_kernel<uint4>
               : p.scale_bytes == 8 ? move_kernel<uint2>
