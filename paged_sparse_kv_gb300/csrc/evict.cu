@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
     // the first tiles of all requests come first: the filled ones spread evenly over the CTAs
     for (int64_t id = blockIdx.x; id < (int64_t)tiles * p.num_reqs; id += gridDim.x) {
         const int32_t r = (int32_t)(id % p.num_reqs), first = (int32_t)(id / p.num_reqs) * kMoves;
-        const int32_t count = min(min(p.num_moves[r], p.max_moves) - first, kMoves);
+        const int32_t count = min(min(max(p.num_moves[r], 0), p.max_moves) - first, kMoves);
         if (count <= 0) continue;
         __syncthreads();  // the last tile's addresses have been read
         if (threadIdx.x < 2 * count) {

@@ -27,3 +27,16 @@ def test_room_for_the_most_moves(cuda_device, room):
                         record=ops.PSK_REC_MXFP4)
     want, _ = plain.move(host, 16, 64, 4, table, [few], [40])
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_counts_below_zero(cuda_device):
+    """The least count of all, from which the moves before a tile cannot be taken off."""
+    d, rng = cuda_device, np.random.default_rng(2)
+    host, cache = _cache(rng, 32, d)
+    table = np.arange(32).reshape(4, 8)
+    moves = np.stack([np.tile(np.arange(64, 128), (4, 1)), np.tile(np.arange(64), (4, 1))], 2)
+    counts = [-2**31, -1, 64, 3 - 2**31]
+    ops.move_cache_rows(cache, torch.from_numpy(table.astype(np.int32)).to(d), torch.from_numpy(moves.astype(np.int32)).to(d),
+                        torch.tensor(counts, dtype=I32, device=d), 16, 128, record=ops.PSK_REC_MXFP4)
+    want, _ = plain.move(host, 16, 64, 4, table, moves, counts)
+    assert np.array_equal(cache.cpu().numpy(), want)
