@@ -899,7 +899,7 @@ psk_status build_rope_cos_sin_cache(
  *
  *   q              [num_tokens, num_heads, head_dim] of `dtype`; (t, h) at q +
  *                  t*q_stride_t + h*q_stride_h (elements).  k: the same with
- *                  num_k_heads heads, or NULL.
+ *                  num_k_heads heads, or NULL; at most 2^31 - 1 - 2^20 heads of both.
  *   q_out, k_out   as q and k.  q_out == q (with equal strides) rotates in place
  *                  and touches nothing else; otherwise the dims outside
  *                  [rope_offset, rope_offset + rope_dim) are copied.  Rows of an

@@ -1269,7 +1269,8 @@ psk_status apply_rotary_embedding(
     CHECK(inverse == 0 || inverse == 1, "inverse must be 0 or 1");
     CHECK(max_pos >= 0 && cs_stride >= rope_dim, "need max_pos >= 0 and cs_stride >= rope_dim");
     CHECK(num_heads >= 1 && (k == nullptr || num_k_heads >= 1), "numbers of heads must be >= 1");
-    CHECK((int64_t)num_heads + (k == nullptr ? 0 : num_k_heads) <= (int64_t)INT32_MAX, "too many heads");
+    // 32 bits hold a row index and a step of the whole grid
+    CHECK((int64_t)num_heads + (k == nullptr ? 0 : num_k_heads) <= psk::kMostRotaryHeads, "too many heads");
     if (num_tokens == 0) return ok();
     const int32_t size = dtype == PSK_DTYPE_FP32 ? 4 : 2;
     psk_status st = check_rotary(q, q_stride_t, q_stride_h, q_out, q_out_stride_t, q_out_stride_h, num_heads,

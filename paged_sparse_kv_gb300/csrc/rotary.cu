@@ -243,6 +243,7 @@ cudaError_t launch(const RotaryParams& p, cudaStream_t stream) {
     const int64_t x = (p.num_tokens + sh.tokens - 1) / sh.tokens;
     // few tokens: their rows are spread over CTAs until there are two per SM
     int64_t y = (2 * (int64_t)sm_count() + x - 1) / x;
+    if (y * sh.rows_at_once > (1 << 20)) y = (1 << 20) / sh.rows_at_once;  // kMostRotaryHeads counts on that
     const int64_t most = sh.tokens > 1 ? 1 : (p.all_heads + sh.rows_at_once - 1) / sh.rows_at_once;
     if (y > most) y = most;
     return launch_pdl(rotary_kernel<kType, kHalf, kWide>, dim3((unsigned)x, (unsigned)y), dim3(kThreads), 0, stream, p, sh);

@@ -6,6 +6,7 @@
 namespace psk {
 
 constexpr int kMaxTablePairs = 256;  // rope_dim up to 512
+constexpr int32_t kMostRotaryHeads = 0x7FFFFFFF - (1 << 20);  // of queries and keys together
 
 struct RopeTableParams {
     float* out;

@@ -52,3 +52,17 @@ def test_far_strides_are_refused(psk_lib):
     """Rows whose address passes 64 bits."""
     assert "overflow" in _error(2**31 - 1, 2, 64, 2**40, 64)
     assert "overflow" in _error(2, 2**30, 64, 2**60 - 8, 2**40)
+
+
+@pytest.mark.parametrize("heads,keys", [(2**31 - 1, 0), (2**31 - 2**20, 0), (2**31 - 77825, 0), (2**30, 2**30), (1, 2**31 - 2**20 - 1)])
+def test_heads_past_32_bits_with_a_step(psk_lib, heads, keys):
+    """A row index plus a step of all CTAs would wrap around."""
+    def call(heads, keys):
+        k = (B, 2 * 2**31, 2) if keys else (None, 0, 0)
+        ko = (B + 2**36, *k[1:]) if keys else k
+        status = _abi.status("apply_rotary_embedding", A, 2 * 2**31, 2, heads, *k, keys, 1, _abi.PSK_DTYPE_BF16, 2, 0, 2, 1, 0, None, None, 2,
+                             0, A + 2**35, 2 * 2**31, 2, *ko, None, None)
+        assert status == _abi.PSK_ERR_INVALID_ARGUMENT
+        return _abi.last_error()
+    assert "heads" in call(heads, keys)
+    assert "positions" in call(2**31 - 1 - 2**20, 0) and "positions" in call(2**31 - 2**20 - 2, 1)
