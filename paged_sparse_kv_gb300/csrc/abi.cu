@@ -3,8 +3,9 @@
 // Each entry point validates its arguments on the host, returns
 // PSK_ERR_INVALID_ARGUMENT before touching the GPU when they are wrong,
 // returns PSK_OK without a launch when there is no work, and otherwise
-// launches one kernel (the attention calls one or two) on the caller's stream.  Nothing here
-// allocates, synchronises or keeps state beyond the per-thread error text.
+// launches one kernel (the attention calls and the accumulation of their weights one or two)
+// on the caller's stream.  Nothing here allocates, synchronises or keeps state beyond the
+// per-thread error text.
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>

@@ -318,9 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
 //
 // A CTA takes kMoves moves of a request at a time: their addresses are looked up side by
 // side, then all threads copy 16-byte pieces of data (and the scales) of all of them.
-// 57000 records of 584 bytes: 14.9 us, 4.5 TB/s read and written, of the 6.7 measured; a
-// chain of three reads (count, move, table entry) precedes each tile's copies, with eight
-// CTAs an SM to cover it.  One record in each of 64 requests: 2.9 us.
+// 53500 records of 584 bytes: 14.8 us, 4.2 TB/s read and written, of the 6.7 measured; a
+// chain of three reads (count, move, table entry) precedes each tile's copies, and only three
+// CTAs an SM cover it (70 to 80 registers a thread, for the five accesses in flight; the grid has
+// eight an SM).  57600 MXFP4 records of 68 bytes: 9.9 us; a tile of them has 160 pieces for 256
+// threads.  One record in each of 64 requests: 2.9 us.
 constexpr int kMoves = 32, kMoveThreads = 256;
 
 // Of a request; max_moves may be all 31 bits.
@@ -403,8 +405,11 @@ constexpr int kMostKeys = 48 * 1024;  // of a CTA's rows in shared memory
 
 cudaError_t launch_select_evictions(const SelectParams& p, cudaStream_t stream) {
     // 4096 rows or more a CTA, and clusters that run at the same time: a CTA fills an SM, and what a
-    // GPC has left over cannot take part (16 requests of up to 32768 rows: clusters of eight, which
-    // take two rounds, 42.5 us, of four 24.4)
+    // GPC has left over cannot take part.  us at 32768 rows a request in clusters of 1, 2, 4 and 8:
+    // 8 requests 39.8, 27.1, 18.8, 18.7; 12 39.8, 27.1, 18.9, 19.3; 16 39.8, 27.1, 18.9, 35.7;
+    // 25 40.0, 27.1, 19.4, 38.3; 32 40.0, 27.2, 19.5, 54.5; 40 40.0, 27.3, 37.5, 56.9; 64 40.2,
+    // 27.3, 38.5, 91.3; 100 40.3, 53.7, 57.4, 130.  The rule takes the best up to 25 requests and
+    // is careful past that: 26 to 38 requests could have clusters of four, 51 to 76 of two.
     int ctas = 1;
     while (ctas < kMostCtas && (int64_t)ctas * 4096 < p.width && 3 * ctas * (int64_t)p.num_reqs <= sm_count()) ctas *= 2;
     const int32_t groups = (p.width + kWarp - 1) / kWarp, warps = ctas * kWarps;

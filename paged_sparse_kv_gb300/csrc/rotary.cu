@@ -101,9 +101,12 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
 // Bound by memory where it is large: 4096 tokens, the 64 rope dims of 128 heads of 512 in
 // bf16 (134 MB in pieces of 128 bytes): 27.5 us, 4.9 TB/s of the 6.7 measured, with eight CTAs
 // an SM (five: 30.3).  The half layout holds two packs and spills with eight: 1901 tokens of
-// 36 heads of 256 dims (70 MB, in part from L2) 15.4 us with five, 20.6 with eight.  Several
+// 36 heads of 256 dims (70 MB, in part from L2) 14 to 15.4 us with five, 20.6 with eight.  Several
 // heads in flight a thread cost more CTAs than they gain (two 33.7, four 46 us against 30.3).
-// 64 tokens of 64 heads take 1.9 us: launch and two dependent reads.
+// These limits are bf16's.  The fp16 forms spill 8 bytes a thread at them, which does not show:
+// in place on the last 64 of 512 dims, 4096 tokens of 129 heads, data in L2 (67.6 MB), 21.0 us in
+// either type, half layout 22.6; binary32 (135 MB) 47.6 and 63.4.  Whole heads out of place, 1.08
+// GB, 174 us.  64 tokens of 64 heads take 1.9 us: launch and two dependent reads.
 
 template <int kType> struct Elem;
 template <> struct Elem<PSK_DTYPE_BF16> {
@@ -267,7 +270,7 @@ cudaError_t launch_type(const RotaryParams& p, cudaStream_t stream) {
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream) {
     const bool wide = p.pairs % 4 == 0 && p.stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
     const int32_t groups = p.pairs / (wide ? 4 : 1), at_once = groups < kThreads ? kThreads / groups : 1;
-    // eight CTAs an SM, each with whole turns of its threads
+    // a grid of eight CTAs an SM (three run at a time), each with whole turns of its threads
     const int64_t turns = (p.num_pos + at_once - 1) / at_once, most = (int64_t)sm_count() * 8;
     const int64_t rows = (turns + most - 1) / most * at_once, ctas = (p.num_pos + rows - 1) / rows;
     return launch_pdl(wide ? rope_table_kernel<4> : rope_table_kernel<1>, dim3((unsigned)ctas), dim3(kThreads), 0, stream, p,
