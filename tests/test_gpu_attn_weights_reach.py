@@ -27,6 +27,14 @@ def test_long_windows(cuda_device, q_lens, prefix, H, D, window, decay, place):
     _run(cuda_device, window % 1000, q_lens, prefix, H, D, window=window, decay=decay, place=place)
 
 
+@pytest.mark.parametrize("R", [60, 128, 129, 300])
+def test_many_requests(cuda_device, R):
+    """Tiles and rows that only fade in turn, ranges found by one warp and by all."""
+    rng = np.random.default_rng(R)
+    _run(cuda_device, R, rng.integers(0, 3, size=R) + (np.arange(R) == 0), rng.integers(0, 700, size=R), 16, 128, bs=16, window=40,
+         decay=0.5, place="out" if R % 2 else "in")
+
+
 def _no_tokens(dev, w, seq, decay, out, tokens=0, H=1, window=0):
     """The call over rows without a page; `tokens` new ones of the last request."""
     R = len(seq)
